@@ -42,6 +42,19 @@ cudaError_t launch_attn_decode(const void *q, const void *k_cache, const void *v
                                const void *z, void *out, int B, int Lmax, void *ws, gdn_dtype out_dt,
                                cudaStream_t s);
 void *attn_error_word();
+cudaError_t launch_qk_norm_rope(const gdn_attn_params *p, const void *q, long long q_row, long long q_head,
+                                const void *k, long long k_row, long long k_head, const int32_t *positions, int M,
+                                void *q_out, void *k_out, gdn_dtype act, gdn_dtype out_dt, cudaStream_t s);
+cudaError_t launch_kv_append(const gdn_attn_params *p, const gdn_paged_batch *b, const gdn_kv_cache *c, const void *k,
+                             long long k_row, long long k_head, const void *v, long long v_row, long long v_head,
+                             const void *q, long long q_row, long long q_head, void *q_out, const int32_t *positions,
+                             gdn_dtype act, cudaStream_t s);
+cudaError_t launch_kv_gather(const gdn_paged_batch *b, const gdn_kv_cache *c, void *k_out, void *v_out,
+                             gdn_dtype out_dt, cudaStream_t s);
+size_t paged_workspace_bytes(const gdn_paged_batch *b, const gdn_kv_cache *c);
+cudaError_t launch_attn_paged(const gdn_paged_batch *b, const gdn_kv_cache *c, const void *q, const void *gate,
+                              long long gate_row, long long gate_head, void *out, void *ws, gdn_dtype out_dt,
+                              cudaStream_t s);
 cudaError_t launch_wait_timeout(cudaStream_t s);
 void *selftest_error_word();
 }  // namespace gdn
@@ -83,6 +96,84 @@ constexpr int MAX_B = 65535;
 constexpr int MAX_N = 65535;
 constexpr int MAX_T = 1 << 24;
 constexpr size_t WS_HEADER = 256;   // keeps the workspace body 256-byte aligned
+
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Do [a, a + an) and [b, b + bn) share a byte?
+bool overlap(const void *a, size_t an, const void *b, size_t bn)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return an > 0 && bn > 0 && x < y + bn && y < x + an;
+}
+
+// A head tensor [M][heads][256] with element strides: the strides keep every row
+// 16-byte aligned, and rows and heads do not run into each other.
+struct Heads {
+    const void *p;
+    long long row, head;
+    int heads;
+    gdn_dtype dt;
+    size_t bytes(int M) const
+    {
+        return ((size_t)(M - 1) * (size_t)row + (size_t)(heads - 1) * (size_t)head + GDN_ATTN_HEAD_DIM) *
+               (dt == GDN_F32 ? 4 : 2);
+    }
+    bool dense() const { return head == GDN_ATTN_HEAD_DIM && row == (long long)heads * GDN_ATTN_HEAD_DIM; }
+};
+gdn_status check_heads(const Heads &t)
+{
+    const long long q = t.dt == GDN_F32 ? 4 : 8;
+    if (!ok_ptr(t.p)) return fail(GDN_ERR_INVALID_ARG, "a tensor pointer is NULL or not 16-byte aligned");
+    if (t.head < GDN_ATTN_HEAD_DIM || t.row < 0 || t.row % q || t.head % q || t.row > (1ll << 32) ||
+        t.head > (1ll << 32))
+        return fail(GDN_ERR_INVALID_ARG, "a stride is negative, below the head dim, above 2^32 or not a multiple of 16 bytes");
+    return GDN_OK;
+}
+
+gdn_status check_attn_params(const gdn_attn_params *p)
+{
+    if (p == nullptr) return fail(GDN_ERR_INVALID_ARG, "attention params is NULL");
+    if (!ok_opt_ptr(p->q_norm_w) || !ok_opt_ptr(p->k_norm_w) || !ok_opt_ptr(p->rope))
+        return fail(GDN_ERR_INVALID_ARG, "a parameter pointer is not 16-byte aligned");
+    if (!(p->norm_eps >= 0.0f)) return fail(GDN_ERR_INVALID_ARG, "norm_eps must be >= 0");
+    if (p->rope != nullptr && p->n_pos < 1) return fail(GDN_ERR_INVALID_ARG, "n_pos must be >= 1 with a rotation table");
+    return GDN_OK;
+}
+
+size_t kv_cache_bytes(const gdn_kv_cache *c)
+{
+    const size_t rows = (size_t)c->num_pages * GDN_ATTN_KV_HEADS * (size_t)c->page_size;
+    return c->format == GDN_KV_Q4 ? rows / GDN_KV_RECORD_ROWS * GDN_KV_RECORD_BYTES : rows * GDN_ATTN_HEAD_DIM * 2;
+}
+
+gdn_status check_batch_sizes(const gdn_paged_batch *b, const gdn_kv_cache *c)
+{
+    if (b == nullptr || c == nullptr) return fail(GDN_ERR_INVALID_ARG, "batch or cache is NULL");
+    if (c->format != GDN_KV_BF16 && c->format != GDN_KV_Q4) return fail(GDN_ERR_INVALID_ARG, "unknown cache format");
+    if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
+        return fail(GDN_ERR_INVALID_ARG, "page_size must be 16, 32, 64 or 128");
+    if (c->num_pages < 1 || (long long)c->num_pages * GDN_ATTN_KV_HEADS * c->page_size > (1ll << 30))
+        return fail(GDN_ERR_INVALID_ARG, "num_pages out of range: need 1 <= num_pages and num_pages * 2 * page_size <= 2^30");
+    if (b->B < 0 || b->B > MAX_B) return fail(GDN_ERR_INVALID_ARG, "B out of range [0, 65535]");
+    if (b->M < 0 || b->M > MAX_T) return fail(GDN_ERR_INVALID_ARG, "M out of range [0, 2^24]");
+    if (b->max_pages < 1 || (long long)b->max_pages * c->page_size > (1ll << 30))
+        return fail(GDN_ERR_INVALID_ARG, "max_pages out of range: need 1 <= max_pages and max_pages * page_size <= 2^30");
+    if (b->cu_q == nullptr && (b->max_q != 1 || b->M < b->B))
+        return fail(GDN_ERR_INVALID_ARG, "without cu_q, max_q must be 1 and M at least B");
+    if (b->max_q < 1 || b->max_q > MAX_T) return fail(GDN_ERR_INVALID_ARG, "max_q out of range [1, 2^24]");
+    return GDN_OK;
+}
+
+gdn_status check_batch(const gdn_paged_batch *b, const gdn_kv_cache *c)
+{
+    const gdn_status st = check_batch_sizes(b, c);
+    if (st != GDN_OK || b->B == 0 || b->M == 0) return st;
+    if (!ok_ptr(c->k) || (c->format == GDN_KV_BF16 && !ok_ptr(c->v)) || (c->format == GDN_KV_Q4 && c->v != nullptr))
+        return fail(GDN_ERR_INVALID_ARG, "a cache pointer is NULL or not 16-byte aligned, or a 4-bit cache has a v");
+    if (!b->page_table || !b->ctx_len || !aligned4(b->page_table) || !aligned4(b->ctx_len) || !aligned4(b->cu_q))
+        return fail(GDN_ERR_INVALID_ARG, "page_table, ctx_len or cu_q is NULL or not 4-byte aligned");
+    return GDN_OK;
+}
 
 // chunk_size 0 = library choice: the exact scan for fp32 activations, the
 // chunked tensor-core form for bf16 activations.
@@ -273,6 +364,118 @@ gdn_status gdn_attn_decode(const void *q, const void *k_cache, const void *v_cac
     cudaError_t e = launch_attn_decode(q, k_cache, v_cache, ctx_len, z, out, B, Lmax, workspace, out_dt,
                                        (cudaStream_t)stream);
     return e == cudaSuccess ? GDN_OK : cuda_fail(e, "gdn_attn_decode");
+}
+
+gdn_status gdn_attn_qk_norm_rope(const gdn_attn_params *p, const void *q, long long q_row_stride,
+                                 long long q_head_stride, const void *k, long long k_row_stride,
+                                 long long k_head_stride, const int32_t *positions, int M, void *q_out, void *k_out,
+                                 gdn_dtype act, gdn_dtype out_dt, void *stream)
+{
+    if (!ok_dtype(act) || !ok_dtype(out_dt)) return fail(GDN_ERR_INVALID_ARG, "unknown activation or output dtype");
+    if (M < 0 || M > MAX_T) return fail(GDN_ERR_INVALID_ARG, "M out of range [0, 2^24]");
+    gdn_status st = check_attn_params(p);
+    if (st != GDN_OK || M == 0) return st;
+    const Heads hq = {q, q_row_stride, q_head_stride, GDN_ATTN_Q_HEADS, act};
+    const Heads hk = {k, k_row_stride, k_head_stride, GDN_ATTN_KV_HEADS, act};
+    if ((st = check_heads(hq)) != GDN_OK) return st;
+    if (k != nullptr && (st = check_heads(hk)) != GDN_OK) return st;
+    if (!ok_ptr(q_out) || (k != nullptr) != (k_out != nullptr) || !ok_opt_ptr(k_out))
+        return fail(GDN_ERR_INVALID_ARG, "an output is NULL or not 16-byte aligned, or only one of k and k_out is given");
+    if (p->rope != nullptr && (positions == nullptr || !aligned4(positions)))
+        return fail(GDN_ERR_INVALID_ARG, "positions is NULL or not 4-byte aligned");
+    const size_t es = out_dt == GDN_F32 ? 4 : 2, qo = (size_t)M * GDN_ATTN_Q_HEADS * GDN_ATTN_HEAD_DIM * es,
+                 ko = (size_t)M * GDN_ATTN_KV_HEADS * GDN_ATTN_HEAD_DIM * es;
+    const bool q_same = q_out == q && hq.dense() && act == out_dt, k_same = k_out == k && hk.dense() && act == out_dt;
+    if ((!q_same && overlap(q_out, qo, q, hq.bytes(M))) ||
+        (k != nullptr && ((!k_same && overlap(k_out, ko, k, hk.bytes(M))) || overlap(q_out, qo, k, hk.bytes(M)) ||
+                          overlap(k_out, ko, q, hq.bytes(M)) || overlap(q_out, qo, k_out, ko))))
+        return fail(GDN_ERR_INVALID_ARG, "an output overlaps an input or the other output");
+    cudaError_t e = launch_qk_norm_rope(p, q, q_row_stride, q_head_stride, k, k_row_stride, k_head_stride, positions,
+                                        M, q_out, k_out, act, out_dt, (cudaStream_t)stream);
+    return e == cudaSuccess ? GDN_OK : cuda_fail(e, "gdn_attn_qk_norm_rope");
+}
+
+gdn_status gdn_kv_append(const gdn_attn_params *p, const gdn_paged_batch *batch, const gdn_kv_cache *cache,
+                         const void *k, long long k_row_stride, long long k_head_stride, const void *v,
+                         long long v_row_stride, long long v_head_stride, const void *q, long long q_row_stride,
+                         long long q_head_stride, void *q_out, const int32_t *positions, gdn_dtype act,
+                         void *stream)
+{
+    if (!ok_dtype(act)) return fail(GDN_ERR_INVALID_ARG, "unknown activation dtype");
+    gdn_status st = check_attn_params(p);
+    if (st == GDN_OK) st = check_batch(batch, cache);
+    if (st != GDN_OK || batch->B == 0 || batch->M == 0) return st;
+    const int M = batch->M;
+    const Heads hk = {k, k_row_stride, k_head_stride, GDN_ATTN_KV_HEADS, act};
+    const Heads hv = {v, v_row_stride, v_head_stride, GDN_ATTN_KV_HEADS, act};
+    const Heads hq = {q, q_row_stride, q_head_stride, GDN_ATTN_Q_HEADS, act};
+    if ((st = check_heads(hk)) != GDN_OK || (st = check_heads(hv)) != GDN_OK) return st;
+    if (q != nullptr && (st = check_heads(hq)) != GDN_OK) return st;
+    if ((q != nullptr) != (q_out != nullptr) || !ok_opt_ptr(q_out))
+        return fail(GDN_ERR_INVALID_ARG, "q_out is not 16-byte aligned, or only one of q and q_out is given");
+    if (!aligned4(positions)) return fail(GDN_ERR_INVALID_ARG, "positions is not 4-byte aligned");
+    const size_t cb = kv_cache_bytes(cache), qo = (size_t)M * GDN_ATTN_Q_HEADS * GDN_ATTN_HEAD_DIM * 2;
+    const Heads ins[3] = {hk, hv, hq};
+    for (const Heads &t : ins) {
+        if (t.p == nullptr) continue;
+        const bool same = q_out != nullptr && t.p == q && q_out == q && hq.dense() && act == GDN_BF16;
+        if (overlap(cache->k, cb, t.p, t.bytes(M)) || (cache->v && overlap(cache->v, cb, t.p, t.bytes(M))) ||
+            (q_out != nullptr && !same && overlap(q_out, qo, t.p, t.bytes(M))))
+            return fail(GDN_ERR_INVALID_ARG, "the cache or q_out overlaps an input");
+    }
+    if (q_out != nullptr && (overlap(cache->k, cb, q_out, qo) || (cache->v && overlap(cache->v, cb, q_out, qo))))
+        return fail(GDN_ERR_INVALID_ARG, "the cache overlaps q_out");
+    cudaError_t e = launch_kv_append(p, batch, cache, k, k_row_stride, k_head_stride, v, v_row_stride, v_head_stride,
+                                     q, q_row_stride, q_head_stride, q_out, positions, act, (cudaStream_t)stream);
+    return e == cudaSuccess ? GDN_OK : cuda_fail(e, "gdn_kv_append");
+}
+
+gdn_status gdn_kv_gather(const gdn_paged_batch *batch, const gdn_kv_cache *cache, void *k_out, void *v_out,
+                         gdn_dtype out_dt, void *stream)
+{
+    if (!ok_dtype(out_dt)) return fail(GDN_ERR_INVALID_ARG, "unknown output dtype");
+    gdn_status st = check_batch(batch, cache);
+    if (st != GDN_OK || batch->B == 0 || batch->M == 0) return st;
+    if (!ok_opt_ptr(k_out) || !ok_opt_ptr(v_out)) return fail(GDN_ERR_INVALID_ARG, "an output is not 16-byte aligned");
+    if (k_out == nullptr && v_out == nullptr) return GDN_OK;
+    const size_t n = (size_t)batch->M * GDN_ATTN_KV_HEADS * GDN_ATTN_HEAD_DIM * (out_dt == GDN_F32 ? 4 : 2);
+    const size_t cb = kv_cache_bytes(cache);
+    void *const outs[2] = {k_out, v_out};
+    for (void *o : outs)
+        if (o && (overlap(o, n, cache->k, cb) || (cache->v && overlap(o, n, cache->v, cb))))
+            return fail(GDN_ERR_INVALID_ARG, "an output overlaps the cache");
+    if (k_out && v_out && overlap(k_out, n, v_out, n)) return fail(GDN_ERR_INVALID_ARG, "k_out and v_out overlap");
+    cudaError_t e = launch_kv_gather(batch, cache, k_out, v_out, out_dt, (cudaStream_t)stream);
+    return e == cudaSuccess ? GDN_OK : cuda_fail(e, "gdn_kv_gather");
+}
+
+size_t gdn_attn_paged_workspace_size(const gdn_paged_batch *batch, const gdn_kv_cache *cache)
+{
+    if (check_batch_sizes(batch, cache) != GDN_OK) return 0;
+    return paged_workspace_bytes(batch, cache);
+}
+
+gdn_status gdn_attn_paged(const gdn_paged_batch *batch, const gdn_kv_cache *cache, const void *q, const void *gate,
+                          long long gate_row_stride, long long gate_head_stride, void *out, void *workspace,
+                          size_t workspace_bytes, gdn_dtype out_dt, void *stream)
+{
+    if (!ok_dtype(out_dt)) return fail(GDN_ERR_INVALID_ARG, "unknown output dtype");
+    gdn_status st = check_batch(batch, cache);
+    if (st != GDN_OK || batch->B == 0 || batch->M == 0) return st;
+    if (!ok_ptr(q) || !ok_ptr(out)) return fail(GDN_ERR_INVALID_ARG, "a tensor pointer is NULL or not 16-byte aligned");
+    const Heads hg = {gate, gate_row_stride, gate_head_stride, GDN_ATTN_Q_HEADS, GDN_BF16};
+    if (gate != nullptr && (st = check_heads(hg)) != GDN_OK) return st;
+    const size_t n = (size_t)batch->M * GDN_ATTN_Q_HEADS * GDN_ATTN_HEAD_DIM, no = n * (out_dt == GDN_F32 ? 4 : 2);
+    const size_t cb = kv_cache_bytes(cache);
+    if (overlap(out, no, q, n * 2) || (gate && overlap(out, no, gate, hg.bytes(batch->M))) ||
+        overlap(out, no, cache->k, cb) || (cache->v && overlap(out, no, cache->v, cb)))
+        return fail(GDN_ERR_INVALID_ARG, "out overlaps an input");
+    if (!ok_ptr(workspace)) return fail(GDN_ERR_WORKSPACE, "workspace is NULL or not 16-byte aligned");
+    if (workspace_bytes < paged_workspace_bytes(batch, cache))
+        return fail(GDN_ERR_WORKSPACE, "workspace smaller than gdn_attn_paged_workspace_size(batch, cache)");
+    cudaError_t e = launch_attn_paged(batch, cache, q, gate, gate_row_stride, gate_head_stride, out, workspace, out_dt,
+                                      (cudaStream_t)stream);
+    return e == cudaSuccess ? GDN_OK : cuda_fail(e, "gdn_attn_paged");
 }
 
 size_t gdn_prefill_workspace_size(int N, int T_total, gdn_dtype act, int chunk_size)

@@ -37,6 +37,21 @@ class gdn_params(ctypes.Structure):
                 ("norm_w", ctypes.c_void_p), ("norm_eps", ctypes.c_float), ("l2_eps", ctypes.c_float)]
 
 
+class gdn_attn_params(ctypes.Structure):
+    _fields_ = [("q_norm_w", ctypes.c_void_p), ("k_norm_w", ctypes.c_void_p), ("rope", ctypes.c_void_p),
+                ("n_pos", ctypes.c_int), ("norm_eps", ctypes.c_float)]
+
+
+class gdn_kv_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("num_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("format", ctypes.c_int)]
+
+
+class gdn_paged_batch(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("ctx_len", ctypes.c_void_p), ("cu_q", ctypes.c_void_p),
+                ("B", ctypes.c_int), ("M", ctypes.c_int), ("max_q", ctypes.c_int), ("max_pages", ctypes.c_int)]
+
+
 _lib = None
 _vp, _int, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
 
@@ -77,6 +92,17 @@ def lib() -> ctypes.CDLL:
         L.gdn_attn_decode.argtypes = [_vp] * 6 + [_int, _int, _vp, _sz, _int, _vp]
         L.gdn_attn_decode_workspace_size.restype = _sz
         L.gdn_attn_decode_workspace_size.argtypes = [_int, _int]
+        _ll = ctypes.c_longlong
+        L.gdn_attn_qk_norm_rope.restype = _int
+        L.gdn_attn_qk_norm_rope.argtypes = [_vp, _vp, _ll, _ll, _vp, _ll, _ll, _vp, _int, _vp, _vp, _int, _int, _vp]
+        L.gdn_kv_append.restype = _int
+        L.gdn_kv_append.argtypes = [_vp, _vp, _vp] + [_vp, _ll, _ll] * 3 + [_vp, _vp, _int, _vp]
+        L.gdn_kv_gather.restype = _int
+        L.gdn_kv_gather.argtypes = [_vp, _vp, _vp, _vp, _int, _vp]
+        L.gdn_attn_paged.restype = _int
+        L.gdn_attn_paged.argtypes = [_vp, _vp, _vp, _vp, _ll, _ll, _vp, _vp, _sz, _int, _vp]
+        L.gdn_attn_paged_workspace_size.restype = _sz
+        L.gdn_attn_paged_workspace_size.argtypes = [_vp, _vp]
         L.gdn_prefill_workspace_size.restype = _sz
         L.gdn_prefill_workspace_size.argtypes = [_int, _int, _int, _int]
         L.gdn_selftest_wait_timeout.restype = _int
@@ -311,6 +337,187 @@ def attn_decode(q, k_cache, v_cache, ctx_len, z, out, workspace=None, stream=Non
                                _ptr(out, "out", (B, ATTN_HQ, ATTN_D)), B, Lmax, _ptr(workspace, "workspace"),
                                workspace.numel() * workspace.element_size(), od, _stream(stream))
     _check(st, "gdn_attn_decode")
+    return workspace
+
+
+# ---- the full-attention layers' input side and paged cache
+
+GDN_KV_BF16, GDN_KV_Q4 = 0, 1
+ATTN_ROT = 64                    # GDN_ATTN_ROT_DIM
+KV_RECORD_ROWS, KV_RECORD_BYTES = 16, 4608
+
+
+def make_attn_params(q_norm_w=None, k_norm_w=None, rope=None, norm_eps: float = 1e-6) -> gdn_attn_params:
+    """gdn_attn_params from fp32 CUDA tensors: the RMSNorm weights [256] of
+    queries and keys (None: no norm) and the rotation table [n_pos][64], 32
+    cosines then 32 sines per position (None: no rotation). The struct keeps the
+    tensors alive."""
+    n_pos = rope.shape[0] if rope is not None else 0
+    p = gdn_attn_params(_ptr(q_norm_w, "q_norm_w", (ATTN_D,), torch.float32),
+                        _ptr(k_norm_w, "k_norm_w", (ATTN_D,), torch.float32),
+                        _ptr(rope, "rope", (n_pos, ATTN_ROT), torch.float32), n_pos, float(norm_eps))
+    p._keep_alive = (q_norm_w, k_norm_w, rope)
+    p._device = _one_device(q_norm_w, k_norm_w, rope)
+    p._ref = ctypes.addressof(p)
+    return p
+
+
+def make_kv_cache(k, v=None) -> gdn_kv_cache:
+    """gdn_kv_cache over caller-owned tensors: bf16 k and v
+    [num_pages][2][page_size][256], or for the 4-bit format one uint8 tensor
+    [num_pages][2][page_size / 16][4608] (zeroed: rows of zeros). The struct
+    keeps the tensors alive."""
+    if v is None:
+        pages, recs = k.shape[0], k.shape[2] if k.dim() == 4 else 0
+        c = gdn_kv_cache(_ptr(k, "k", (pages, ATTN_HKV, recs, KV_RECORD_BYTES), torch.uint8), None, pages,
+                         recs * KV_RECORD_ROWS, GDN_KV_Q4)
+    else:
+        pages, page = k.shape[0], k.shape[2] if k.dim() == 4 else 0
+        shape = (pages, ATTN_HKV, page, ATTN_D)
+        c = gdn_kv_cache(_ptr(k, "k", shape, torch.bfloat16), _ptr(v, "v", shape, torch.bfloat16, k.device), pages,
+                         page, GDN_KV_BF16)
+    c._keep_alive = (k, v)
+    c._device = k.device
+    c._ref = ctypes.addressof(c)
+    return c
+
+
+def make_paged_batch(page_table, ctx_len, M: int, cu_q=None, max_q: int = 1) -> gdn_paged_batch:
+    """gdn_paged_batch from int32 CUDA tensors: page_table [B][max_pages],
+    ctx_len [B] (the new tokens included), cu_q [B+1] packed row offsets (None:
+    one token per sequence). M packed rows, at most max_q of one sequence. The
+    struct reads the tensors at every call (update them in place from step to
+    step) and keeps them alive."""
+    B, mp = page_table.shape
+    b = gdn_paged_batch(_ptr(page_table, "page_table", (B, mp), torch.int32),
+                        _ptr(ctx_len, "ctx_len", (B,), torch.int32, page_table.device),
+                        _ptr(cu_q, "cu_q", (B + 1,), torch.int32, page_table.device), B, int(M), int(max_q), mp)
+    b._keep_alive = (page_table, ctx_len, cu_q)
+    b._device = page_table.device
+    b._ref = ctypes.addressof(b)
+    return b
+
+
+def _one_device(*tensors):
+    devs = {t.device for t in tensors if t is not None}
+    if len(devs) > 1:
+        raise ValueError(f"tensors on different devices: {sorted(map(str, devs))}")
+    return devs.pop() if devs else None
+
+
+def _on_current(device, where: str) -> torch.device:
+    """The library launches on the current device: tensors of another one are refused."""
+    if device.type != "cuda":
+        raise ValueError(f"{where}: tensors must be on a CUDA device, not {device}")
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"{where}: tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+    return device
+
+
+def _heads(t, name: str, M: int, heads: int, device, dtype=None):
+    """(pointer, row stride, head stride) of a [M][heads][256] tensor whose last
+    dim is dense; other strides are free (multiples of 16 bytes, checked by the
+    library)."""
+    if t is None:
+        return None, 0, 0
+    if t.shape != (M, heads, ATTN_D):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(M, heads, ATTN_D)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    row, head, last = t.stride()
+    if last != 1:
+        raise ValueError(f"{name} must be dense in its last dimension")
+    return t.data_ptr(), row, head
+
+
+def _dense(t, name: str, M: int, heads: int, device, dtype=None):
+    ptr, row, head = _heads(t, name, M, heads, device, dtype)
+    if ptr is not None and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return ptr
+
+
+def _raw_stream(stream, device) -> int:
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return _stream(stream)
+
+
+def attn_qk_norm_rope(params: gdn_attn_params, q, positions, q_out, k=None, k_out=None, stream=None):
+    """gdn_attn_qk_norm_rope: per-head RMSNorm and rotation of q [M][16][256] and
+    optionally k [M][2][256] (fp32 or bf16, strided views allowed, e.g. the query
+    half of a joint query+gate projection) into dense q_out and k_out (fp32 or
+    bf16). positions [M] int32: rows of the rotation table (None without one)."""
+    M, dev = q.shape[0], _on_current(q.device, "attn_qk_norm_rope")
+    if params._device is not None and params._device != dev:
+        raise ValueError(f"the parameters are on {params._device}, expected {dev}")
+    qp, qr, qh = _heads(q, "q", M, ATTN_HQ, dev)
+    kp, kr, kh = _heads(k, "k", M, ATTN_HKV, dev, q.dtype)
+    st = lib().gdn_attn_qk_norm_rope(params._ref, qp, qr, qh, kp, kr, kh,
+                                     _ptr(positions, "positions", (M,), torch.int32, dev), M,
+                                     _dense(q_out, "q_out", M, ATTN_HQ, dev),
+                                     _dense(k_out, "k_out", M, ATTN_HKV, dev, q_out.dtype), _act_dtype(q),
+                                     _act_dtype(q_out), _raw_stream(stream, dev))
+    _check(st, "gdn_attn_qk_norm_rope")
+
+
+def _on_batch(batch, cache, where: str, params=None):
+    dev = _on_current(batch._device, where)
+    if cache._device != dev or (params is not None and params._device not in (None, dev)):
+        raise ValueError(f"{where}: batch, cache and parameters are on different devices")
+    return dev
+
+
+def kv_append(params: gdn_attn_params, batch: gdn_paged_batch, cache: gdn_kv_cache, k, v, q=None, q_out=None,
+              positions=None, stream=None):
+    """gdn_kv_append: the batch's new keys (normed and rotated on the way) and
+    values [M][2][256] (fp32 or bf16, strided views allowed) into the paged
+    cache. With q [M][16][256] and q_out (dense bf16) the queries are normed and
+    rotated in the same launch. positions [M] int32 overrides the rows of the
+    rotation table (default: the token's position in its context)."""
+    M, dev = batch.M, _on_batch(batch, cache, "kv_append", params)
+    kp, kr, kh = _heads(k, "k", M, ATTN_HKV, dev)
+    vp, vr, vh = _heads(v, "v", M, ATTN_HKV, dev, k.dtype)
+    qp, qr, qh = _heads(q, "q", M, ATTN_HQ, dev, k.dtype)
+    st = lib().gdn_kv_append(params._ref, batch._ref, cache._ref, kp, kr, kh, vp, vr, vh, qp, qr, qh,
+                             _dense(q_out, "q_out", M, ATTN_HQ, dev, torch.bfloat16),
+                             _ptr(positions, "positions", (M,), torch.int32, dev), _act_dtype(k),
+                             _raw_stream(stream, dev))
+    _check(st, "gdn_kv_append")
+
+
+def kv_gather(batch: gdn_paged_batch, cache: gdn_kv_cache, k_out, v_out, stream=None):
+    """gdn_kv_gather: the cached rows of the batch's new tokens as values, into
+    dense k_out and v_out [M][2][256] (fp32 or bf16; either may be None)."""
+    M, dev = batch.M, _on_batch(batch, cache, "kv_gather")
+    some = k_out if k_out is not None else v_out
+    if some is None:
+        return
+    st = lib().gdn_kv_gather(batch._ref, cache._ref, _dense(k_out, "k_out", M, ATTN_HKV, dev, some.dtype),
+                             _dense(v_out, "v_out", M, ATTN_HKV, dev, some.dtype), _act_dtype(some),
+                             _raw_stream(stream, dev))
+    _check(st, "gdn_kv_gather")
+
+
+def attn_paged_workspace_size(batch: gdn_paged_batch, cache: gdn_kv_cache) -> int:
+    return int(lib().gdn_attn_paged_workspace_size(batch._ref, cache._ref))
+
+
+def attn_paged(batch: gdn_paged_batch, cache: gdn_kv_cache, q, out, gate=None, workspace=None, stream=None):
+    """gdn_attn_paged: causal attention of the batch's new tokens over the paged
+    cache. q [M][16][256] dense bf16 (normed and rotated), out dense fp32 or
+    bf16, gate [M][16][256] bf16 (strided views allowed; None: no output gate).
+    Allocates the workspace through torch when none is given and returns it."""
+    M, dev = batch.M, _on_batch(batch, cache, "attn_paged")
+    gp, gr, gh = _heads(gate, "gate", M, ATTN_HQ, dev, torch.bfloat16)
+    if workspace is None:
+        workspace = torch.empty(max(attn_paged_workspace_size(batch, cache), 256), dtype=torch.uint8, device=dev)
+    st = lib().gdn_attn_paged(batch._ref, cache._ref, _dense(q, "q", M, ATTN_HQ, dev, torch.bfloat16), gp, gr, gh,
+                              _dense(out, "out", M, ATTN_HQ, dev), _ptr(workspace, "workspace", device=dev),
+                              workspace.nbytes, _act_dtype(out), _raw_stream(stream, dev))
+    _check(st, "gdn_attn_paged")
     return workspace
 
 

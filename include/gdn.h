@@ -372,6 +372,159 @@ gdn_status gdn_attn_decode(const void *q, const void *k_cache, const void *v_cac
  * range. Pure host arithmetic. */
 size_t gdn_attn_decode_workspace_size(int B, int Lmax);
 
+/* ---------------------------------------------------------------------------
+ * The full-attention layers' input side and paged cache (steps 2-6 of section
+ * "Full-attention block"): per-head RMSNorm of q and k, partial rotation (RoPE)
+ * of the first GDN_ATTN_ROT_DIM dims, the key/value cache in pages, and the
+ * attention of new tokens over it.
+ * ------------------------------------------------------------------------- */
+#define GDN_ATTN_ROT_DIM 64
+#define GDN_KV_RECORD_ROWS 16      /* rows of one 4-bit record */
+#define GDN_KV_RECORD_BYTES 4608   /* bytes of one 4-bit record */
+
+/* Formats of the paged cache.
+ * GDN_KV_BF16: two tensors k, v [num_pages][2][page_size][256] bf16.
+ * GDN_KV_Q4:   one tensor k [num_pages][2][page_size / 16][4608] bytes (v is
+ *   NULL). A row of 256 values is 4 groups of 64 dims; with lo = min and
+ *   hi = max of the group (real numbers), zero z = bf16(lo), step
+ *   s = bf16((hi - lo) / 15), code = clamp(round_to_even((x - z) / s), 0, 15)
+ *   (0 where s = 0), and it stands for z + s * code. A group that holds an
+ *   infinity or a NaN reads back as NaN. One record holds 16 rows: key codes
+ *   [16][128 B], value codes [16][128 B], key (s, z) [16][4][2] bf16, value
+ *   (s, z). Byte 16 c + 4 g + b of a row's codes holds dims 64 g + 8 c + 2 b
+ *   (low nibble) and 64 g + 8 c + 2 b + 1 (high nibble): the 16 bytes c are the
+ *   c-th 8 dims of each group. */
+typedef enum { GDN_KV_BF16 = 0, GDN_KV_Q4 = 1 } gdn_kv_format;
+
+typedef struct {
+    void *k, *v;            /* device, 16-byte aligned                         */
+    int num_pages;          /* num_pages * 2 * page_size <= 2^30               */
+    int page_size;          /* 16, 32, 64 or 128 rows                          */
+    gdn_kv_format format;
+} gdn_kv_cache;
+
+/* The new tokens of B sequences. Sequence b has n_b new tokens, the packed rows
+ * [cu_q[b], cu_q[b+1]), at positions ctx_len[b] - n_b ... ctx_len[b] - 1 of its
+ * context, and position p lives in row p % page_size of page
+ * page_table[b][p / page_size].
+ *   page_table  device int32 [B][max_pages]; entries of pages that no position
+ *               below ctx_len reaches are not used. An entry outside
+ *               [0, num_pages) never touches memory outside the cache: what
+ *               would be stored there is dropped, and it reads as zeros
+ *   ctx_len     device int32 [B]: cached positions, the new tokens included.
+ *               Positions past max_pages * page_size or below 0 do not exist:
+ *               they are neither stored nor read
+ *   cu_q        device int32 [B+1], 0 = cu[0] <= ... <= cu[B] <= M; NULL: one
+ *               new token per sequence, row b
+ *   M           packed rows; rows at or past cu_q[B] (B without cu_q) are
+ *               padding, neither read nor written
+ *   max_q       at least the largest n_b (1 without cu_q). It chooses kernels
+ *               and workspace; rows of a sequence with more tokens than this
+ *               are unspecified
+ * B <= 65535, M <= 2^24, max_pages * page_size <= 2^30. */
+typedef struct {
+    const int32_t *page_table, *ctx_len, *cu_q;
+    int B, M, max_q, max_pages;
+} gdn_paged_batch;
+
+/* Layer parameters of the input side, device fp32, each may be NULL:
+ *   q_norm_w, k_norm_w [256]  RMSNorm weights, applied as w (NULL: no norm)
+ *   rope [n_pos][64]          per position 32 cosines, then 32 sines (NULL: no
+ *                             rotation). Dims i and i + 32 (i < 32) turn into
+ *                             (x_i c_i - x_{i+32} s_i, x_{i+32} c_i + x_i s_i) */
+typedef struct {
+    const float *q_norm_w, *k_norm_w, *rope;
+    int n_pos;
+    float norm_eps;
+} gdn_attn_params;
+
+/*
+ * gdn_attn_qk_norm_rope -- steps 2-4 for M tokens in one pass:
+ *   out = rotate(x * (mean(x^2) + norm_eps)^-1/2 * w, rope[positions[m]])
+ * per head of 256 dims, fp32 arithmetic, one rounding at the end.
+ *   q           [M][16][256] act with element strides q_row_stride and
+ *               q_head_stride (the last dim dense; e.g. 8192 and 512 for the
+ *               joint query+gate projection)
+ *   k           [M][2][256] act with its strides, or NULL (then k_out is NULL)
+ *   positions   device int32 [M]: rows of `rope`; a token whose position is
+ *               outside [0, n_pos) is padding, left as it is in q_out and k_out.
+ *               Not read when rope is NULL (may be NULL then)
+ *   q_out, k_out dense [M][16][256], [M][2][256] out_dt. An output may be its
+ *               own input (same pointer, dense strides, same dtype) and must not
+ *               overlap an input otherwise
+ * Strides are multiples of 16 bytes. 0 <= M <= 2^24. Errors:
+ * GDN_ERR_INVALID_ARG, GDN_ERR_CUDA.
+ */
+gdn_status gdn_attn_qk_norm_rope(const gdn_attn_params *p, const void *q, long long q_row_stride,
+                                 long long q_head_stride, const void *k, long long k_row_stride,
+                                 long long k_head_stride, const int32_t *positions, int M, void *q_out, void *k_out,
+                                 gdn_dtype act, gdn_dtype out_dt, void *stream);
+
+/*
+ * gdn_kv_append -- the new tokens' keys (normed by k_norm_w and rotated on the
+ * way) and values into the paged cache, each (token, KV head) row written once,
+ * in the cache's format. Optionally also the tokens' queries, normed and rotated
+ * into q_out, so that one launch does the whole input side of gdn_attn_paged.
+ *   k, v        [M][2][256] act with their strides (as above)
+ *   q           [M][16][256] act with its strides, or NULL (then q_out is NULL)
+ *   q_out       dense [M][16][256] bf16; must not overlap the inputs, except
+ *               that it may be q itself (dense bf16)
+ *   positions   device int32 [M]: rows of `rope`, or NULL: the token's position
+ *               in its context. A token whose row is outside [0, n_pos) is
+ *               neither stored nor written to q_out (not read without rope)
+ * Keys are rounded once, from fp32 to bf16 or, in the 4-bit format, as the
+ * format defines it from the unrounded keys: codes, steps and zeros that fp32
+ * cannot decide are settled in 64 bits. Two tokens that name the same cache row
+ * (a page listed for two sequences) leave that row unspecified.
+ * Errors: GDN_ERR_INVALID_ARG, GDN_ERR_CUDA.
+ */
+gdn_status gdn_kv_append(const gdn_attn_params *p, const gdn_paged_batch *batch, const gdn_kv_cache *cache,
+                         const void *k, long long k_row_stride, long long k_head_stride, const void *v,
+                         long long v_row_stride, long long v_head_stride, const void *q, long long q_row_stride,
+                         long long q_head_stride, void *q_out, const int32_t *positions, gdn_dtype act,
+                         void *stream);
+
+/*
+ * gdn_kv_gather -- the cached rows of the batch's new tokens, in packed order,
+ * as values: k_out, v_out dense [M][2][256] out_dt (either may be NULL). With
+ * n_b = ctx_len[b] it reads whole contexts back (to move a cache to another
+ * format or store). Rows that do not exist (positions out of range, page ids
+ * out of range) read as zeros; padding rows are left as they are.
+ * Errors: GDN_ERR_INVALID_ARG, GDN_ERR_CUDA.
+ */
+gdn_status gdn_kv_gather(const gdn_paged_batch *batch, const gdn_kv_cache *cache, void *k_out, void *v_out,
+                         gdn_dtype out_dt, void *stream);
+
+/*
+ * gdn_attn_paged -- causal attention of the batch's new tokens over the paged
+ * cache, their own rows included (append them first), and the output gate:
+ *   out[m][h] = sigmoid(gate[m][h]) * sum_{p <= pos(m)} w_p v[p][h / 8],
+ *   w = softmax_p(k[p][h / 8] . q[m][h] / 16)
+ * for one token per sequence (decode), a few (draft tokens) or whole prompts.
+ *   q           dense [M][16][256] bf16, normed and rotated
+ *   gate        [M][16][256] bf16 with element strides (multiples of 8), or NULL:
+ *               no gate
+ *   out         dense [M][16][256] out_dt; a token that sees no position gives
+ *               zeros. Must not overlap the inputs
+ *   workspace   device scratch, 16-byte aligned, of
+ *               gdn_attn_paged_workspace_size(batch, cache) bytes; contents need
+ *               no initialisation. Calls that share one must be ordered on a
+ *               stream
+ * Rows of the cache at or past ctx_len are never used, whatever they hold. The
+ * softmax weights enter the value product rounded to bf16 (fp32 sums).
+ * Errors: GDN_ERR_INVALID_ARG, GDN_ERR_WORKSPACE, GDN_ERR_CUDA (also when the
+ * driver's tensor-map encoder is unavailable). A bounded device wait that gives
+ * up is reported afterwards by gdn_device_error.
+ */
+gdn_status gdn_attn_paged(const gdn_paged_batch *batch, const gdn_kv_cache *cache, const void *q, const void *gate,
+                          long long gate_row_stride, long long gate_head_stride, void *out, void *workspace,
+                          size_t workspace_bytes, gdn_dtype out_dt, void *stream);
+
+/* Bytes of workspace gdn_attn_paged needs: a function of the batch's B, M and
+ * max_q and the cache's format. 0 if the arguments are out of range. Pure host
+ * arithmetic. */
+size_t gdn_attn_paged_workspace_size(const gdn_paged_batch *batch, const gdn_kv_cache *cache);
+
 /* Bytes of workspace gdn_prefill needs for these sizes (0 if the arguments are
  * invalid; never 0 for valid ones). Pure host arithmetic. */
 size_t gdn_prefill_workspace_size(int N, int T_total, gdn_dtype act, int chunk_size);

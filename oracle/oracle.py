@@ -229,6 +229,70 @@ def attn_decode(q, k_cache, v_cache, ctx_len, z):
     return out
 
 
+def bf16_of(x):
+    """fp64 values rounded to the nearest bf16 (ties to even), as fp64: 8
+    significant bits, exponents down to 2^-133 (the subnormals' last place)."""
+    x = _f64(x)
+    _, e = np.frexp(x)
+    step = np.ldexp(1.0, np.maximum(e - 8, -133))
+    return np.rint(x / step) * step
+
+
+def norm_rope(x, w, rows, eps=1e-6):
+    """Steps 2-4 of section "Full-attention block" for heads x [M][H][256]:
+    RMSNorm with weight w (applied as w; None: left out), then the rotation of
+    dims i and i + 32 (i < 32) by the cosines rows[m][i] and sines
+    rows[m][32 + i] (rows None: no rotation)."""
+    x = _f64(x)
+    if w is not None:
+        x = x / np.sqrt((x * x).mean(-1, keepdims=True) + eps) * _f64(w)
+    if rows is None:
+        return x
+    c, s = _f64(rows)[:, None, :32], _f64(rows)[:, None, 32:]
+    y = x.copy()
+    y[..., :32] = x[..., :32] * c - x[..., 32:64] * s
+    y[..., 32:64] = x[..., 32:64] * c + x[..., :32] * s
+    return y
+
+
+def kv4(x):
+    """The 4-bit form of rows x [..][256]: (codes [..][4][64], steps, zeros
+    [..][4], values [..][256]). Per group of 64 dims: zero = bf16(min), step =
+    bf16((max - min) / 15), code = round_to_even((x - zero) / step) in 0..15 (0
+    where the step is 0), value = zero + step * code; a group with a non-finite
+    element has the values NaN."""
+    v = _f64(x)
+    v = v.reshape(*v.shape[:-1], 4, 64)
+    fin = np.isfinite(v).all(-1)
+    v0 = np.where(fin[..., None], v, 0.0)
+    lo, hi = v0.min(-1), v0.max(-1)
+    z, s = bf16_of(lo), bf16_of((hi - lo) / 15.0)
+    with np.errstate(divide="ignore", invalid="ignore"):
+        c = np.clip(np.rint((v0 - z[..., None]) / s[..., None]), 0, 15)
+    c = np.where(s[..., None] > 0, c, 0.0)
+    val = np.where(fin[..., None], z[..., None] + s[..., None] * c, np.nan)
+    return c, s, np.where(fin, z, np.nan), val.reshape(*v.shape[:-2], 256)
+
+
+def attn_causal(q, k, v, gate, first):
+    """Causal attention of n new tokens of one sequence: token t (q [n][16][256])
+    sees positions 0 .. first + t of k, v [2][L][256], scale 1/16, query head h
+    reading KV head h // 8; then the gate sigmoid(gate) (None: none). A token that
+    sees no position gives zeros."""
+    q, k, v = _f64(q), _f64(k), _f64(v)
+    n, Hq, D = q.shape
+    L = k.shape[1]
+    out = np.zeros((n, Hq, D))
+    see = np.arange(L)[None, :] <= (first + np.arange(n))[:, None]
+    some = see.any(1)
+    if some.any():
+        for h in range(Hq):
+            s = np.where(see, q[:, h] @ k[h // 8].T / np.sqrt(D), -np.inf)[some]
+            p = np.exp(s - s.max(1, keepdims=True))
+            out[some, h] = (p / p.sum(1, keepdims=True)) @ v[h // 8]
+    return out if gate is None else out / (1.0 + np.exp(-_f64(gate)))
+
+
 @dataclass
 class Params:
     """One layer's parameters as fp64 arrays (the page's tensor roles:
