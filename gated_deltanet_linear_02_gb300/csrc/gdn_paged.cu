@@ -1,21 +1,522 @@
-// gdn_paged.cu -- causal attention of new tokens over the paged cache (bf16 or
-// 4 bits), steps 5-6 of section "Full-attention block" of "qwen35moe --
-// Forward-Pass Design (Pantheon port)".
+// gdn_paged.cu -- causal attention of new tokens over the paged cache, steps 5-6
+// of section "Full-attention block" of "qwen35moe -- Forward-Pass Design
+// (Pantheon port)", on 5th-generation tensor cores. gdn_paged.cuh describes how
+// the work is shared out: pieces of up to 128 query rows (16 tokens x the 8
+// heads of a KV head) over 128-position tiles of the context.
 //
-// One warp per (token, query head): 8 dims per lane, one pass over the context
-// with the running maximum and sum of the softmax.
+// Per unit (one tile), with M = 128 query rows:
+//   S = Q K^T (N = 128 positions, K = 256 dims), fp32 in tensor memory;
+//   P = 2^((S - m) log2 e / 16), rounded to bf16, over S's own columns;
+//   O += P V (N = 256 dims, K = 128 positions), fp32 in tensor memory,
+// m the row's reference maximum and l its sum of P. O is rescaled only when a
+// row's maximum passes m by more than 8 (in powers of two): P then stays below
+// 2^8, l and O lose nothing in fp32, and the rescale, a round trip of the whole
+// accumulator, happens a few times per context instead of at every tile.
+//
+// Roles in a CTA (one per SM, 256 threads):
+//  - warp 0, TMA producer: 32 KiB stages of 128 positions x 128 dims (keys low,
+//    high, values low, high), one box per page and 64 dims, in a ring of five;
+//    the next tile's keys ahead of this tile's values, as the MMAs use them;
+//  - warp 1, one lane, MMA issuer: S of unit u + 1 is issued before O += P V of
+//    unit u, so the tensor core has work while P is formed;
+//  - warps 4-7, one thread per query row: softmax, rescale, and the epilogue
+//    (normalise and gate, or store the piece's unnormalised output).
+// Tensor memory: two S buffers (P over their first half) and O, all 512 columns.
+//
+// Bound: for one token per sequence by HBM (1 KiB of keys and values per position
+// and KV head; the 120 unused rows cost tensor time that hides behind it), for
+// prompts by the shared-memory port, which carries Q, K, V and the TMA writes of
+// a tile in about 2,500 cycles against 2,048 of tensor work.
+#include <cuda.h>
+
+#include <mutex>
+
 #include "gdn_async.cuh"
-#include "gdn_kv.cuh"
+#include "gdn_paged.cuh"
+#include "gdn_tc.cuh"
+#include "gdn_tma.cuh"
 
 namespace gdn {
 
-struct PagedArgs {
-    PagedBatch b;
-    const void *ck, *cv;
-    const bf16 *q, *gate;
-    long long gate_row, gate_head;
-    void *out;
+__device__ unsigned int g_paged_error;            // GDN_ERR_TIMEOUT if a bounded wait gave up
+
+constexpr int FA_THREADS = 256;
+constexpr int FA_STAGES = 5;
+constexpr uint32_t FA_BOX = PG_TILE * 128;        // 128 rows x 64 dims of bf16: 16 KiB
+constexpr uint32_t FA_STAGE_BYTES = 2 * FA_BOX;   // 128 dims: 32 KiB
+constexpr uint32_t FA_Q = 0;                      // Q: 4 boxes of 64 dims
+constexpr uint32_t FA_RING = 4 * FA_BOX;
+constexpr uint32_t FA_SMALL = FA_RING + FA_STAGES * FA_STAGE_BYTES;
+constexpr uint32_t FA_S = 0, FA_O = 256;          // tensor memory columns: S buffers at 0 and 128, O at 256
+constexpr float SCORE_SCALE = 1.4426950408889634f / 16.0f;   // log2 e / sqrt(256)
+constexpr float RESCALE_AT = 8.0f;                // powers of two a maximum may pass the reference by
+
+struct FaSmall {
+    uint64_t full[FA_STAGES], empty[FA_STAGES];
+    uint64_t q_full, q_empty, s_full[2], p_full[2], pv_done, o_empty, done;
+    long long scan[FA_THREADS / 32 + 1];
+    PagedStart start;
+    uint32_t tmem;
+    int abort;
 };
+constexpr size_t FA_SMEM = FA_SMALL + sizeof(FaSmall) + 1024;   // + slack to align the block
+static_assert(FA_SMEM <= 232448, "shared memory of one CTA");
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3, %4}], [%5];"
+                 ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void load8_bf16(const bf16 *p, float (&x)[8])
+{
+    const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float((i & 1) ? (w[i >> 1] & 0xFFFF0000u) : (w[i >> 1] << 16));
+}
+__device__ __forceinline__ void store8_out(float *p, const float (&x)[8])
+{
+    reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ void store8_out(bf16 *p, const float (&x)[8])
+{
+    *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                                               pack_bf16(x[6], x[7]));
+}
+// Normalised output times the gate, 8 dims from dim d of (packed row m, head h).
+template <typename TO>
+__device__ __forceinline__ void finish8(const PagedArgs &a, int m, int h, int d, float (&o)[8], float inv)
+{
+    if (a.gate != nullptr) {
+        float g[8];
+        load8_bf16(a.gate + m * a.gate_row + h * a.gate_head + d, g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] *= __fdividef(inv, 1.0f + __expf(-g[i]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] *= inv;
+    }
+    store8_out(static_cast<TO *>(a.out) + ((size_t)m * KV_HQ + h) * KV_D + d, o);
+}
+
+// A walk over the units of a range, one at a time.
+struct UnitWalk {
+    PieceWalk w;
+    int j;
+    __device__ __forceinline__ void begin(const PagedBatch &b, const PagedStart &s, long long count)
+    {
+        w.begin(b, s, count);
+        j = 0;
+    }
+    __device__ __forceinline__ bool last() const { return j + 1 >= w.len && w.left == 0; }
+    __device__ __forceinline__ void next(const PagedBatch &b)
+    {
+        if (++j == w.len) {
+            w.next(b);
+            j = 0;
+        }
+    }
+};
+
+template <typename TO>
+__global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_constant__ CUtensorMap qmap,
+                                                                   const __grid_constant__ CUtensorMap kmap,
+                                                                   const __grid_constant__ CUtensorMap vmap,
+                                                                   const PagedArgs a)
+{
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *blk = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    FaSmall &ss = *reinterpret_cast<FaSmall *>(blk + FA_SMALL);
+    const uint32_t sb = smem_u32(blk);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const PagedBatch &b = a.b;
+    const int cap = b.max_pages << b.page_log2;
+
+    if (tid == 0) {
+        for (int s = 0; s < FA_STAGES; ++s) {
+            mbar_init(smem_u32(&ss.full[s]), 1);
+            mbar_init(smem_u32(&ss.empty[s]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&ss.s_full[i]), 1);
+            mbar_init(smem_u32(&ss.p_full[i]), 128);
+        }
+        mbar_init(smem_u32(&ss.q_full), 1);
+        mbar_init(smem_u32(&ss.q_empty), 1);
+        mbar_init(smem_u32(&ss.pv_done), 1);
+        mbar_init(smem_u32(&ss.o_empty), 128);
+        mbar_init(smem_u32(&ss.done), 1);
+        ss.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 2) {
+        tc::tmem_alloc(smem_u32(&ss.tmem), 512);
+        tc::tmem_relinquish();
+    }
+    grid_dep_wait();
+    grid_dep_launch();
+    find_start<FA_THREADS>(b, blockIdx.x, a.ranges, ss.scan, &ss.start);   // ends in a CTA barrier
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tm = ss.tmem;
+    const PagedStart st = ss.start;
+    if (tid == 0) a.start[blockIdx.x] = st;
+    const long long count = range_begin(st.total, blockIdx.x + 1, a.ranges) - range_begin(st.total, blockIdx.x, a.ranges);
+    const volatile int &aborted = ss.abort;
+    auto stage = [&](uint32_t i) { return sb + FA_RING + (i % FA_STAGES) * FA_STAGE_BYTES; };
+    auto wait_full = [&](uint32_t i) {
+        return mbar_wait_bounded(smem_u32(&ss.full[i % FA_STAGES]), (i / FA_STAGES) & 1);
+    };
+
+    if (count > 0) {
+        if (warp == 0) {
+            // ---- TMA producer. Stage order: K(0), then K(u + 1), V(u) for each u.
+            UnitWalk kw;
+            kw.begin(b, st, count);
+            const int seg = lane >> 1, box = lane & 1, nseg = PG_TILE >> b.page_log2;
+            const uint32_t seg_dst = (uint32_t)seg * ((uint32_t)b.page * 128) + box * FA_BOX;
+            uint32_t i = 0, piece = 0;
+            bool ok = true;
+            // row of the cache tensors where this lane's segment of the unit starts; segments past
+            // what the item sees are not loaded, bad page ids load past the end (zeros)
+            auto segment = [&](int &row, int &loaded) {
+                const int p = (kw.w.unit + kw.j) * PG_TILE;
+                const int sees = tile_sees(b, kw.w.t, kw.w.tile);
+                loaded = min(nseg, max(0, (sees - p + b.page - 1) >> b.page_log2));
+                row = 0;
+                if (seg < loaded) {
+                    const int page = cache_page(b, kw.w.seq, p + seg * b.page);
+                    row = page < 0 ? (b.num_pages * KV_H) << b.page_log2 : ((page * KV_H + kw.w.head) << b.page_log2);
+                }
+            };
+            auto load = [&](const CUtensorMap *m, int row, int loaded) {
+                for (int half = 0; half < 2 && ok; ++half, ++i) {
+                    if (i >= FA_STAGES)
+                        ok = mbar_wait_bounded(smem_u32(&ss.empty[i % FA_STAGES]), (i / FA_STAGES - 1) & 1);
+                    ok = __all_sync(0xffffffffu, ok && !aborted);
+                    if (!ok) break;
+                    const uint32_t bar = smem_u32(&ss.full[i % FA_STAGES]);
+                    if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)loaded * b.page * 256);
+                    __syncwarp();
+                    if (seg < loaded) tma_load_2d(stage(i) + seg_dst, m, half * 128 + box * 64, row, bar);
+                }
+            };
+            auto load_q = [&]() {
+                if (piece > 0) ok = mbar_wait_bounded(smem_u32(&ss.q_empty), (piece - 1) & 1);
+                ok = __all_sync(0xffffffffu, ok && !aborted);
+                if (ok && lane == 0) {
+                    const uint32_t bar = smem_u32(&ss.q_full);
+                    mbar_arrive_expect_tx(bar, 4 * FA_BOX);
+                    for (int c = 0; c < 4; ++c)
+                        tma_load_3d(sb + FA_Q + c * FA_BOX, &qmap, 64 * c, KV_G * kw.w.head,
+                                    kw.w.t.row0 + PG_TOK * kw.w.tile, bar);
+                }
+                ++piece;
+            };
+            int row, loaded;
+            segment(row, loaded);
+            load_q();
+            if (ok) load(&kmap, row, loaded);
+            while (ok) {
+                const int vrow = row, vloaded = loaded;
+                const bool more = !kw.last();
+                if (more) {
+                    kw.next(b);
+                    segment(row, loaded);
+                    if (kw.j == 0) load_q();
+                    if (ok) load(&kmap, row, loaded);
+                }
+                if (ok) load(&vmap, vrow, vloaded);
+                if (!more) break;
+            }
+            if (!ok) {                             // copies in flight land before the CTA exits
+                if (lane == 0) ss.abort = 1;
+                for (uint32_t k = i > FA_STAGES ? i - FA_STAGES : 0; k < i; ++k) wait_full(k);
+                if (piece > 0) mbar_wait_bounded(smem_u32(&ss.q_full), (piece - 1) & 1);
+            }
+        } else if (warp == 1) {
+            // ---- MMA issuer
+            if (lane == 0) {
+                const uint32_t id_s = tc::instr_desc(tc::FMT_BF16, 128, PG_TILE);
+                const uint32_t id_o = id_s | tc::IDESC_B_MN;
+                UnitWalk qk, pv;
+                qk.begin(b, st, count);
+                pv = qk;
+                uint32_t i = 0, piece_q = 0, piece_o = 0;
+                bool ok = true;
+                auto scores = [&](uint32_t u) {    // S(u) = Q K^T
+                    if (qk.j == 0) {
+                        ok = mbar_wait_bounded(smem_u32(&ss.q_full), piece_q & 1);
+                        ++piece_q;
+                    }
+                    for (int half = 0; half < 2 && ok; ++half, ++i) {
+                        ok = wait_full(i);
+                        if (!ok) break;
+                        tc::fence_after_sync();
+                        for (int kk = 0; kk < 8; ++kk)
+                            tc::mma_f16(tm + FA_S + (u & 1) * 128,
+                                        tc::sw128_desc(sb + FA_Q + (2 * half + (kk >> 2)) * FA_BOX + (kk & 3) * 32),
+                                        tc::sw128_desc(stage(i) + (kk >> 2) * FA_BOX + (kk & 3) * 32), id_s,
+                                        half + kk > 0 ? 1u : 0u);
+                        tc::mma_commit(smem_u32(&ss.empty[i % FA_STAGES]));
+                    }
+                    if (!ok) return;
+                    tc::mma_commit(smem_u32(&ss.s_full[u & 1]));
+                    if (qk.j + 1 == qk.w.len) tc::mma_commit(smem_u32(&ss.q_empty));
+                };
+                scores(0);
+                for (uint32_t u = 0; ok; ++u) {
+                    const bool more = !qk.last();
+                    if (more) {
+                        qk.next(b);
+                        scores(u + 1);
+                        if (!ok) break;
+                    }
+                    if (pv.j == 0) {
+                        if (piece_o > 0) ok = mbar_wait_bounded(smem_u32(&ss.o_empty), (piece_o - 1) & 1);
+                        ++piece_o;
+                    }
+                    ok = ok && mbar_wait_bounded(smem_u32(&ss.p_full[u & 1]), (u >> 1) & 1) && !aborted;
+                    if (!ok) break;
+                    for (int half = 0; half < 2 && ok; ++half, ++i) {
+                        ok = wait_full(i);
+                        if (!ok) break;
+                        tc::fence_after_sync();
+                        for (int kk = 0; kk < 8; ++kk)
+                            tc::mma_f16_tmem_a(tm + FA_O + half * 128, tm + FA_S + (u & 1) * 128 + kk * 8,
+                                               tc::sw128_mn_desc(stage(i) + kk * 2048, FA_BOX), id_o,
+                                               pv.j + kk > 0 ? 1u : 0u);
+                        tc::mma_commit(smem_u32(&ss.empty[i % FA_STAGES]));
+                    }
+                    if (!ok) break;
+                    tc::mma_commit(smem_u32(&ss.pv_done));
+                    if (!more) break;
+                    pv.next(b);
+                }
+                if (!ok) ss.abort = 1;
+                tc::mma_commit(smem_u32(&ss.done));    // every MMA completes before tensor memory is freed
+                mbar_wait_bounded(smem_u32(&ss.done), 0u);
+            }
+        } else if (warp >= 4) {
+            // ---- softmax and epilogue: thread r is query row r of the item
+            const int r = tid - 128, q4 = warp & 3;
+            const uint32_t lbase = tm + ((uint32_t)(32 * q4) << 16);
+            PieceWalk w;
+            w.begin(b, st, count);
+            uint32_t u = 0;
+            bool ok = true;
+            for (;;) {
+                const int rows = KV_G * w.tokens(), sees = tile_sees(b, w.t, w.tile);
+                const int limit = min(w.t.first + PG_TOK * w.tile + (r >> 3) + 1, cap);   // positions this row sees
+                const bool live = 32 * q4 < rows;      // the warp has rows of the item
+                float m = -INFINITY, l = 0.0f;
+                for (int j = 0; j < w.len; ++j, ++u) {
+                    const int p0 = (w.unit + j) * PG_TILE;
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&ss.s_full[u & 1]), (u >> 1) & 1) && !aborted);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    if (live) {
+                        const uint32_t sc = lbase + FA_S + (u & 1) * 128;
+                        float x[4][32];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) tc::tmem_ld32(sc + 32 * c, x[c]);
+                        tc::wait_ld();
+                        if (__any_sync(0xffffffffu, p0 + PG_TILE > limit)) {
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    if (p0 + 32 * c + i >= limit) x[c][i] = -INFINITY;
+                        }
+                        float mx[4];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            mx[c] = fmaxf(x[c][0], x[c][1]);
+#pragma unroll
+                            for (int i = 2; i < 32; i += 2) mx[c] = fmaxf(mx[c], fmaxf(x[c][i], x[c][i + 1]));
+                        }
+                        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                        const bool move = (top - m) * SCORE_SCALE > RESCALE_AT;   // also from m = -inf; never for top = -inf
+                        if (__any_sync(0xffffffffu, move)) {
+                            const float f = !move ? 1.0f : (m == -INFINITY ? 0.0f : ex2((m - top) * SCORE_SCALE));
+                            if (j > 0) {
+                                ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&ss.pv_done), (u - 1) & 1));
+                                if (!ok) break;
+                                tc::fence_after_sync();
+                                for (int c = 0; c < 8; ++c) {
+                                    float o[32];
+                                    tc::tmem_ld32(lbase + FA_O + 32 * c, o);
+                                    tc::wait_ld();
+#pragma unroll
+                                    for (int i = 0; i < 32; ++i) o[i] = f > 0.0f ? o[i] * f : 0.0f;
+                                    tc::tmem_st32(lbase + FA_O + 32 * c, o);
+                                }
+                                tc::wait_st();
+                            }
+                            l *= f;
+                            m = move ? top : m;
+                        }
+                        const float off = m == -INFINITY ? 0.0f : m * SCORE_SCALE;
+                        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t pk[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const float e0 = ex2(fmaf(x[c][2 * i], SCORE_SCALE, -off));
+                                const float e1 = ex2(fmaf(x[c][2 * i + 1], SCORE_SCALE, -off));
+                                sum[c] += e0 + e1;
+                                pk[i] = pack_bf16(e0, e1);
+                            }
+                            tc::tmem_st16_u32(sc + 16 * c, pk);
+                        }
+                        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                        tc::wait_st();
+                    }
+                    if (p0 + PG_TILE > sees) {
+                        // the tile's positions that no token of the item sees: their value rows become
+                        // zeros, whatever the cache (or an earlier tile) left there (0 * NaN is NaN). The
+                        // previous unit's products are waited for first: they free the stages' earlier use,
+                        // without which the phase of `full` would be ambiguous.
+                        const uint32_t vi = w.left == 0 && j + 1 == w.len ? 4 * u + 2 : 4 * u + 4;
+                        ok = u == 0 || mbar_wait_bounded(smem_u32(&ss.pv_done), (u - 1) & 1);
+                        ok = __all_sync(0xffffffffu, ok && wait_full(vi) && wait_full(vi + 1) && !aborted);
+                        if (!ok) break;
+                        if (p0 + r >= sees) {
+                            const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                uint4 *row = reinterpret_cast<uint4 *>(blk + (stage(vi + (k >> 1)) - sb) + (k & 1) * FA_BOX + r * 128);
+#pragma unroll
+                                for (int c = 0; c < 8; ++c) row[c] = zero;
+                            }
+                        }
+                        fence_proxy_async_smem();
+                    }
+                    tc::fence_before_sync();           // P stored, S read
+                    mbar_arrive(smem_u32(&ss.p_full[u & 1]));
+                }
+                if (!ok) break;
+                // O is complete. Two products may still be under way here, so both phases are waited for
+                // in turn: one phase behind, the parity alone could be mistaken.
+                ok = u < 2 || mbar_wait_bounded(smem_u32(&ss.pv_done), u & 1);
+                ok = __all_sync(0xffffffffu, ok && mbar_wait_bounded(smem_u32(&ss.pv_done), (u - 1) & 1) && !aborted);
+                if (!ok) break;
+                tc::fence_after_sync();
+                if (live) {
+                    const bool mine = r < rows, whole = w.whole();
+                    const int mrow = w.t.row0 + PG_TOK * w.tile + (r >> 3), h = KV_G * w.head + (r & 7);
+                    const size_t slot = ((size_t)2 * blockIdx.x + (w.first ? 0 : 1)) * a.rows + r;
+                    const float inv = l != 0.0f ? 1.0f / l : 0.0f;   // 0: the row saw nothing
+                    for (int c = 0; c < 8; ++c) {
+                        float o[32];
+                        tc::tmem_ld32(lbase + FA_O + 32 * c, o);
+                        tc::wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float e[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) e[k] = l != 0.0f ? o[8 * i + k] : 0.0f;
+                            if (mine && whole) finish8<TO>(a, mrow, h, 32 * c + 8 * i, e, inv);
+                            else if (mine) store8_out(a.part_o + slot * KV_D + 32 * c + 8 * i, e);
+                        }
+                        __syncwarp();
+                    }
+                    if (mine && !whole) *reinterpret_cast<float2 *>(a.part_ml + slot * 2) = make_float2(m * SCORE_SCALE, l);
+                }
+                tc::fence_before_sync();
+                mbar_arrive(smem_u32(&ss.o_empty));
+                if (w.left == 0) break;
+                w.next(b);
+            }
+            if (!ok && lane == 0) ss.abort = 1;
+        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 2) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tm, 512);
+    }
+    if (tid == 0 && ss.abort) atomicExch(&g_paged_error, (unsigned int)GDN_ERR_TIMEOUT);
+}
+
+// Joins the pieces of every item that spans ranges. CTA (x, y): the range
+// boundary x + 1, if it is the first one inside an item, and row y of that item;
+// 8 warps take the pieces in turn, 8 dims per lane, and meet in shared memory:
+// with block maxima m_s (powers of two), sums l_s and unnormalised outputs o_s,
+//   M = max m_s, out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s * sigmoid(gate).
+template <typename TO>
+__global__ void __launch_bounds__(256) attn_paged_join_kernel(const PagedArgs a)
+{
+    __shared__ float so[8][KV_D], sml[8][2];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c = blockIdx.x + 1, r = blockIdx.y;
+    grid_dep_wait();
+    grid_dep_launch();
+    const PagedStart st = a.start[c];
+    const long long u = range_begin(st.total, c, a.ranges), begin = u - st.unit;
+    if (u >= st.total || st.unit == 0 || range_begin(st.total, c - 1, a.ranges) > begin) return;
+    const SeqTokens t = seq_tokens(a.b, st.seq);
+    const int tokens = min(PG_TOK, t.n - PG_TOK * st.tile);
+    if (r >= KV_G * tokens) return;
+    const long long end = begin + tile_units(a.b, t, st.tile);
+    int last = c;                                      // the last range with a piece of the item
+    while (last + 1 < a.ranges && range_begin(st.total, last + 1, a.ranges) < end) ++last;
+    float M = -INFINITY, l = 0.0f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int k = c - 1 + warp; k <= last; k += 8) {
+        const long long k0 = range_begin(st.total, k, a.ranges), k1 = range_begin(st.total, k + 1, a.ranges);
+        if (k1 == k0) continue;
+        const size_t slot = ((size_t)2 * k + (k0 >= begin ? 0 : 1)) * a.rows + r;
+        const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + slot * 2);
+        const float4 *src = reinterpret_cast<const float4 *>(a.part_o + slot * KV_D) + 2 * lane;
+        const float4 x = src[0], y = src[1];
+        if (ml.y != 0.0f) {
+            const float Mn = fmaxf(M, ml.x), f = ex2(M - Mn), g = ex2(ml.x - Mn);
+            M = Mn;
+            l = l * f + ml.y * g;
+            o[0] = o[0] * f + x.x * g; o[1] = o[1] * f + x.y * g; o[2] = o[2] * f + x.z * g; o[3] = o[3] * f + x.w * g;
+            o[4] = o[4] * f + y.x * g; o[5] = o[5] * f + y.y * g; o[6] = o[6] * f + y.z * g; o[7] = o[7] * f + y.w * g;
+        }
+    }
+    store8_out(&so[warp][8 * lane], o);
+    if (lane == 0) {
+        sml[warp][0] = M;
+        sml[warp][1] = l;
+    }
+    __syncthreads();
+    if (warp != 0) return;
+    float Ma = sml[0][0];
+#pragma unroll
+    for (int k = 1; k < 8; ++k) Ma = fmaxf(Ma, sml[k][0]);
+    float la = 0.0f, e[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        if (sml[k][1] == 0.0f) continue;
+        const float g = ex2(sml[k][0] - Ma);
+        la += g * sml[k][1];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] += g * so[k][8 * lane + i];
+    }
+    finish8<TO>(a, t.row0 + PG_TOK * st.tile + (r >> 3), KV_G * st.head + (r & 7), 8 * lane, e,
+                la != 0.0f ? 1.0f / la : 0.0f);
+}
 
 template <bool Q4>
 __device__ __forceinline__ void load_row(const PagedArgs &a, int page, int head, int off, bool isv, int lane, float (&x)[8])
@@ -43,7 +544,7 @@ __device__ __forceinline__ void load_row(const PagedArgs &a, int page, int head,
 }
 
 template <typename TO, bool Q4>
-__global__ void __launch_bounds__(256) attn_paged_kernel(const PagedArgs a)
+__global__ void __launch_bounds__(256) attn_paged_simple_kernel(const PagedArgs a)
 {
     const int lane = threadIdx.x & 31;
     const long long item = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -86,19 +587,103 @@ __global__ void __launch_bounds__(256) attn_paged_kernel(const PagedArgs a)
     }
 }
 
-size_t paged_workspace_bytes(const gdn_paged_batch *, const gdn_kv_cache *) { return 16; }
+// ------------------------------------------------------------------ launcher
+
+// The driver's tensor-map encoder, looked up once.
+static bool encode_q_map(CUtensorMap *map, const void *q, int M)
+{
+    typedef CUresult (*Fn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                           const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                           CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const Fn fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r);
+        return e == cudaSuccess && r == cudaDriverEntryPointSuccess ? reinterpret_cast<Fn>(p) : nullptr;
+    }();
+    if (!fn) return false;
+    // [M][16][256] in boxes of 16 tokens x 8 heads x 64 dims, 128-byte swizzle; tokens past M read as zeros
+    const cuuint64_t dims[3] = {KV_D, KV_HQ, (cuuint64_t)M}, strides[2] = {KV_D * 2, KV_HQ * KV_D * 2};
+    const cuuint32_t box[3] = {64, KV_G, PG_TOK}, one[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dims, strides, box, one,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int FA_RANGES = 152;                    // one CTA per SM
+constexpr size_t START_BYTES = (PG_MAX_CTAS * sizeof(PagedStart) + 255) / 256 * 256;
+
+static int piece_rows(int max_q) { return KV_G * (max_q < PG_TOK ? max_q : PG_TOK); }
+
+size_t paged_workspace_bytes(const gdn_paged_batch *b, const gdn_kv_cache *)
+{
+    return START_BYTES + (size_t)2 * FA_RANGES * piece_rows(b->max_q) * (KV_D + 2) * sizeof(float);
+}
+
+template <auto KERNEL> static cudaError_t smem_attr_once(size_t bytes)
+{
+    static std::mutex mu;
+    static bool done[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev < 0 || dev >= 64 || !done[dev]) {
+        e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
+    }
+    return e;
+}
+
+template <typename TO>
+static cudaError_t launch_join(const PagedArgs &a, cudaStream_t s)
+{
+    return launch_pdl(attn_paged_join_kernel<TO>, dim3(a.ranges - 1, a.rows), dim3(256), 0, s, a);
+}
+
+template <typename TO>
+static cudaError_t launch_bf16(const PagedArgs &a, cudaStream_t s)
+{
+    CUtensorMap qm, km, vm;
+    const long long rows = (long long)a.b.num_pages * KV_H * a.b.page;
+    if (!encode_q_map(&qm, a.q, a.b.M) || !make_bf16_sw128_map(&km, a.ck, rows, KV_D, a.b.page) ||
+        !make_bf16_sw128_map(&vm, a.cv, rows, KV_D, a.b.page))
+        return cudaErrorInvalidValue;
+    cudaError_t e = smem_attr_once<attn_paged_kernel<TO>>(FA_SMEM);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(attn_paged_kernel<TO>, dim3(a.ranges), dim3(FA_THREADS), FA_SMEM, s, qm, km, vm, a);
+    return e == cudaSuccess ? launch_join<TO>(a, s) : e;
+}
 
 cudaError_t launch_attn_paged(const gdn_paged_batch *b, const gdn_kv_cache *c, const void *q, const void *gate,
-                              long long gate_row, long long gate_head, void *out, void *, gdn_dtype out_dt,
+                              long long gate_row, long long gate_head, void *out, void *ws, gdn_dtype out_dt,
                               cudaStream_t s)
 {
-    PagedArgs a = {paged_batch(*b, *c), c->k, c->v, (const bf16 *)q, (const bf16 *)gate, gate_row, gate_head, out};
+    PagedArgs a = {};
+    a.b = paged_batch(*b, *c);
+    a.ck = c->k;
+    a.cv = c->v;
+    a.q = (const bf16 *)q;
+    a.gate = (const bf16 *)gate;
+    a.gate_row = gate_row;
+    a.gate_head = gate_head;
+    a.out = out;
+    a.rows = piece_rows(b->max_q);
+    a.ranges = FA_RANGES;
+    a.start = (PagedStart *)ws;
+    a.part_o = (float *)((char *)ws + START_BYTES);
+    a.part_ml = a.part_o + (size_t)2 * a.ranges * a.rows * KV_D;
+    if (c->format == GDN_KV_BF16) return out_dt == GDN_F32 ? launch_bf16<float>(a, s) : launch_bf16<bf16>(a, s);
     const dim3 grid((unsigned)(((long long)b->M * KV_HQ + 7) / 8)), block(256);
-    if (c->format == GDN_KV_Q4)
-        return out_dt == GDN_F32 ? launch_pdl(attn_paged_kernel<float, true>, grid, block, 0, s, a)
-                                 : launch_pdl(attn_paged_kernel<bf16, true>, grid, block, 0, s, a);
-    return out_dt == GDN_F32 ? launch_pdl(attn_paged_kernel<float, false>, grid, block, 0, s, a)
-                             : launch_pdl(attn_paged_kernel<bf16, false>, grid, block, 0, s, a);
+    return out_dt == GDN_F32 ? launch_pdl(attn_paged_simple_kernel<float, true>, grid, block, 0, s, a)
+                             : launch_pdl(attn_paged_simple_kernel<bf16, true>, grid, block, 0, s, a);
+}
+
+// Device address of this file's error word, for gdn_device_error.
+void *paged_error_word()
+{
+    void *p = nullptr;
+    return cudaGetSymbolAddress(&p, g_paged_error) == cudaSuccess ? p : nullptr;
 }
 
 }  // namespace gdn
