@@ -53,7 +53,7 @@ constexpr float RESCALE_AT = 8.0f;                // powers of two a maximum may
 
 struct FaSmall {
     uint64_t full[FA_STAGES], empty[FA_STAGES];
-    uint64_t q_full, q_empty, s_full[2], p_full[2], pv_done, o_empty, done;
+    uint64_t q_full, q_empty, s_full[2], p_full[2], pv_done[2], o_empty, done;
     long long scan[FA_THREADS / 32 + 1];
     PagedStart start;
     uint32_t tmem;
@@ -81,13 +81,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
                  ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
 }
 
-__device__ __forceinline__ void load8_bf16(const bf16 *p, float (&x)[8])
-{
-    const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float((i & 1) ? (w[i >> 1] & 0xFFFF0000u) : (w[i >> 1] << 16));
-}
 __device__ __forceinline__ void store8_out(float *p, const float (&x)[8])
 {
     reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
@@ -98,40 +91,25 @@ __device__ __forceinline__ void store8_out(bf16 *p, const float (&x)[8])
     *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
                                                pack_bf16(x[6], x[7]));
 }
+__device__ __forceinline__ void gate8(const uint4 u, float (&o)[8], float inv)
+{
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        o[i] *= __fdividef(inv, 1.0f + __expf(-__uint_as_float((i & 1) ? (w[i >> 1] & 0xFFFF0000u) : (w[i >> 1] << 16))));
+}
 // Normalised output times the gate, 8 dims from dim d of (packed row m, head h).
 template <typename TO>
 __device__ __forceinline__ void finish8(const PagedArgs &a, int m, int h, int d, float (&o)[8], float inv)
 {
     if (a.gate != nullptr) {
-        float g[8];
-        load8_bf16(a.gate + m * a.gate_row + h * a.gate_head + d, g);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] *= __fdividef(inv, 1.0f + __expf(-g[i]));
+        gate8(__ldg(reinterpret_cast<const uint4 *>(a.gate + m * a.gate_row + h * a.gate_head + d)), o, inv);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] *= inv;
     }
     store8_out(static_cast<TO *>(a.out) + ((size_t)m * KV_HQ + h) * KV_D + d, o);
 }
-
-// A walk over the units of a range, one at a time.
-struct UnitWalk {
-    PieceWalk w;
-    int j;
-    __device__ __forceinline__ void begin(const PagedBatch &b, const PagedStart &s, long long count)
-    {
-        w.begin(b, s, count);
-        j = 0;
-    }
-    __device__ __forceinline__ bool last() const { return j + 1 >= w.len && w.left == 0; }
-    __device__ __forceinline__ void next(const PagedBatch &b)
-    {
-        if (++j == w.len) {
-            w.next(b);
-            j = 0;
-        }
-    }
-};
 
 template <typename TO>
 __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_constant__ CUtensorMap qmap,
@@ -155,10 +133,10 @@ __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&ss.s_full[i]), 1);
             mbar_init(smem_u32(&ss.p_full[i]), 128);
+            mbar_init(smem_u32(&ss.pv_done[i]), 1);
         }
         mbar_init(smem_u32(&ss.q_full), 1);
         mbar_init(smem_u32(&ss.q_empty), 1);
-        mbar_init(smem_u32(&ss.pv_done), 1);
         mbar_init(smem_u32(&ss.o_empty), 128);
         mbar_init(smem_u32(&ss.done), 1);
         ss.abort = 0;
@@ -170,7 +148,7 @@ __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_
     }
     grid_dep_wait();
     grid_dep_launch();
-    find_start<FA_THREADS>(b, blockIdx.x, a.ranges, ss.scan, &ss.start);   // ends in a CTA barrier
+    find_start<FA_THREADS>(a, blockIdx.x, ss.scan, &ss.start);   // ends in a CTA barrier
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
@@ -184,11 +162,13 @@ __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_
         return mbar_wait_bounded(smem_u32(&ss.full[i % FA_STAGES]), (i / FA_STAGES) & 1);
     };
 
-    if (count > 0) {
+    PieceWalk first;
+    if (count > 0) first.begin(a, st, count);
+    if (count > 0 && first.len > 0) {
         if (warp == 0) {
             // ---- TMA producer. Stage order: K(0), then K(u + 1), V(u) for each u.
             UnitWalk kw;
-            kw.begin(b, st, count);
+            kw.begin(a, st, count);
             const int seg = lane >> 1, box = lane & 1, nseg = PG_TILE >> b.page_log2;
             const uint32_t seg_dst = (uint32_t)seg * ((uint32_t)b.page * 128) + box * FA_BOX;
             uint32_t i = 0, piece = 0;
@@ -235,9 +215,9 @@ __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_
             if (ok) load(&kmap, row, loaded);
             while (ok) {
                 const int vrow = row, vloaded = loaded;
-                const bool more = !kw.last();
+                const bool more = !kw.last(a);
                 if (more) {
-                    kw.next(b);
+                    kw.next(a);
                     segment(row, loaded);
                     if (kw.j == 0) load_q();
                     if (ok) load(&kmap, row, loaded);
@@ -256,7 +236,7 @@ __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_
                 const uint32_t id_s = tc::instr_desc(tc::FMT_BF16, 128, PG_TILE);
                 const uint32_t id_o = id_s | tc::IDESC_B_MN;
                 UnitWalk qk, pv;
-                qk.begin(b, st, count);
+                qk.begin(a, st, count);
                 pv = qk;
                 uint32_t i = 0, piece_q = 0, piece_o = 0;
                 bool ok = true;
@@ -282,9 +262,9 @@ __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_
                 };
                 scores(0);
                 for (uint32_t u = 0; ok; ++u) {
-                    const bool more = !qk.last();
+                    const bool more = !qk.last(a);
                     if (more) {
-                        qk.next(b);
+                        qk.next(a);
                         scores(u + 1);
                         if (!ok) break;
                     }
@@ -305,9 +285,9 @@ __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_
                         tc::mma_commit(smem_u32(&ss.empty[i % FA_STAGES]));
                     }
                     if (!ok) break;
-                    tc::mma_commit(smem_u32(&ss.pv_done));
+                    tc::mma_commit(smem_u32(&ss.pv_done[u & 1]));
                     if (!more) break;
-                    pv.next(b);
+                    pv.next(a);
                 }
                 if (!ok) ss.abort = 1;
                 tc::mma_commit(smem_u32(&ss.done));    // every MMA completes before tensor memory is freed
@@ -317,14 +297,22 @@ __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_
             // ---- softmax and epilogue: thread r is query row r of the item
             const int r = tid - 128, q4 = warp & 3;
             const uint32_t lbase = tm + ((uint32_t)(32 * q4) << 16);
-            PieceWalk w;
-            w.begin(b, st, count);
+            PieceWalk w = first;
             uint32_t u = 0;
             bool ok = true;
+            // O += P V of unit v is complete. Two barriers in turn: S of unit u, which this thread has
+            // seen, was issued after the product of unit u - 2, so each is one phase behind at most.
+            auto wait_pv = [&](uint32_t v) { return mbar_wait_bounded(smem_u32(&ss.pv_done[v & 1]), (v >> 1) & 1); };
             for (;;) {
                 const int rows = KV_G * w.tokens(), sees = tile_sees(b, w.t, w.tile);
                 const int limit = min(w.t.first + PG_TOK * w.tile + (r >> 3) + 1, cap);   // positions this row sees
                 const bool live = 32 * q4 < rows;      // the warp has rows of the item
+                if (r < rows && w.whole() && a.gate != nullptr) {
+                    const bf16 *g = a.gate + (w.t.row0 + PG_TOK * w.tile + (r >> 3)) * a.gate_row +
+                                    (KV_G * w.head + (r & 7)) * a.gate_head;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) asm volatile("prefetch.global.L2 [%0];" ::"l"(g + 64 * i));
+                }
                 float m = -INFINITY, l = 0.0f;
                 for (int j = 0; j < w.len; ++j, ++u) {
                     const int p0 = (w.unit + j) * PG_TILE;
@@ -356,9 +344,10 @@ __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_
                         if (__any_sync(0xffffffffu, move)) {
                             const float f = !move ? 1.0f : (m == -INFINITY ? 0.0f : ex2((m - top) * SCORE_SCALE));
                             if (j > 0) {
-                                ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&ss.pv_done), (u - 1) & 1));
+                                ok = __all_sync(0xffffffffu, wait_pv(u - 1));
                                 if (!ok) break;
                                 tc::fence_after_sync();
+#pragma unroll 1
                                 for (int c = 0; c < 8; ++c) {
                                     float o[32];
                                     tc::tmem_ld32(lbase + FA_O + 32 * c, o);
@@ -394,8 +383,8 @@ __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_
                         // zeros, whatever the cache (or an earlier tile) left there (0 * NaN is NaN). The
                         // previous unit's products are waited for first: they free the stages' earlier use,
                         // without which the phase of `full` would be ambiguous.
-                        const uint32_t vi = w.left == 0 && j + 1 == w.len ? 4 * u + 2 : 4 * u + 4;
-                        ok = u == 0 || mbar_wait_bounded(smem_u32(&ss.pv_done), (u - 1) & 1);
+                        const uint32_t vi = j + 1 == w.len && !w.more(a) ? 4 * u + 2 : 4 * u + 4;
+                        ok = u == 0 || wait_pv(u - 1);
                         ok = __all_sync(0xffffffffu, ok && wait_full(vi) && wait_full(vi + 1) && !aborted);
                         if (!ok) break;
                         if (p0 + r >= sees) {
@@ -413,28 +402,47 @@ __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_
                     mbar_arrive(smem_u32(&ss.p_full[u & 1]));
                 }
                 if (!ok) break;
-                // O is complete. Two products may still be under way here, so both phases are waited for
-                // in turn: one phase behind, the parity alone could be mistaken.
-                ok = u < 2 || mbar_wait_bounded(smem_u32(&ss.pv_done), u & 1);
-                ok = __all_sync(0xffffffffu, ok && mbar_wait_bounded(smem_u32(&ss.pv_done), (u - 1) & 1) && !aborted);
+                // The loop below stays rolled: it runs once per piece, and unrolled it was tens of KB of
+                // cold instructions (15 us per piece, most of it instruction fetch). The gate's next 64
+                // bytes are read a round ahead, the first while the last product runs.
+                const bool mine = r < rows, whole = w.whole(), gated = mine && whole && a.gate != nullptr;
+                const int mrow = w.t.row0 + PG_TOK * w.tile + (r >> 3), h = KV_G * w.head + (r & 7);
+                uint4 gate[4] = {};
+                const uint4 *gsrc = reinterpret_cast<const uint4 *>(a.gate + mrow * a.gate_row + h * a.gate_head);
+                if (gated)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) gate[i] = __ldg(gsrc + i);
+                ok = __all_sync(0xffffffffu, wait_pv(u - 1) && !aborted);
                 if (!ok) break;
                 tc::fence_after_sync();
                 if (live) {
-                    const bool mine = r < rows, whole = w.whole();
-                    const int mrow = w.t.row0 + PG_TOK * w.tile + (r >> 3), h = KV_G * w.head + (r & 7);
                     const size_t slot = ((size_t)2 * blockIdx.x + (w.first ? 0 : 1)) * a.rows + r;
-                    const float inv = l != 0.0f ? 1.0f / l : 0.0f;   // 0: the row saw nothing
+                    const float inv = l == 0.0f ? 0.0f : (whole ? 1.0f / l : 1.0f);   // l = 0: the row saw nothing
+                    TO *orow = static_cast<TO *>(a.out) + ((size_t)mrow * KV_HQ + h) * KV_D;
+                    float *prow = a.part_o + slot * KV_D;
+#pragma unroll 1
                     for (int c = 0; c < 8; ++c) {
                         float o[32];
                         tc::tmem_ld32(lbase + FA_O + 32 * c, o);
+                        uint4 next[4] = {};
+                        if (gated && c < 7)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) next[i] = __ldg(gsrc + 4 * c + 4 + i);
                         tc::wait_ld();
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             float e[8];
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) e[k] = l != 0.0f ? o[8 * i + k] : 0.0f;
-                            if (mine && whole) finish8<TO>(a, mrow, h, 32 * c + 8 * i, e, inv);
-                            else if (mine) store8_out(a.part_o + slot * KV_D + 32 * c + 8 * i, e);
+                            for (int k = 0; k < 8; ++k) e[k] = l == 0.0f ? 0.0f : o[8 * i + k];
+                            if (gated) {
+                                gate8(gate[i], e, inv);
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) e[k] *= inv;
+                            }
+                            if (mine && whole) store8_out(orow + 32 * c + 8 * i, e);
+                            else if (mine) store8_out(prow + 32 * c + 8 * i, e);
+                            gate[i] = next[i];
                         }
                         __syncwarp();
                     }
@@ -442,8 +450,8 @@ __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_
                 }
                 tc::fence_before_sync();
                 mbar_arrive(smem_u32(&ss.o_empty));
-                if (w.left == 0) break;
-                w.next(b);
+                if (!w.more(a)) break;
+                w.next(a);
             }
             if (!ok && lane == 0) ss.abort = 1;
         }
@@ -471,18 +479,19 @@ __global__ void __launch_bounds__(256) attn_paged_join_kernel(const PagedArgs a)
     grid_dep_wait();
     grid_dep_launch();
     const PagedStart st = a.start[c];
-    const long long u = range_begin(st.total, c, a.ranges), begin = u - st.unit;
-    if (u >= st.total || st.unit == 0 || range_begin(st.total, c - 1, a.ranges) > begin) return;
+    // the item's first step, and the step of its first unit: a cut at or before that one cuts nothing
+    const long long u = range_begin(st.total, c, a.ranges), begin = u - st.step, unit0 = begin + a.lead;
+    if (u >= st.total || u <= unit0 || range_begin(st.total, c - 1, a.ranges) > unit0) return;
     const SeqTokens t = seq_tokens(a.b, st.seq);
     const int tokens = min(PG_TOK, t.n - PG_TOK * st.tile);
     if (r >= KV_G * tokens) return;
-    const long long end = begin + tile_units(a.b, t, st.tile);
+    const long long end = unit0 + tile_units(a.b, t, st.tile);
     int last = c;                                      // the last range with a piece of the item
     while (last + 1 < a.ranges && range_begin(st.total, last + 1, a.ranges) < end) ++last;
     float M = -INFINITY, l = 0.0f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     for (int k = c - 1 + warp; k <= last; k += 8) {
         const long long k0 = range_begin(st.total, k, a.ranges), k1 = range_begin(st.total, k + 1, a.ranges);
-        if (k1 == k0) continue;
+        if (k1 == k0) continue;                    // an empty range
         const size_t slot = ((size_t)2 * k + (k0 >= begin ? 0 : 1)) * a.rows + r;
         const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + slot * 2);
         const float4 *src = reinterpret_cast<const float4 *>(a.part_o + slot * KV_D) + 2 * lane;
@@ -670,6 +679,8 @@ cudaError_t launch_attn_paged(const gdn_paged_batch *b, const gdn_kv_cache *c, c
     a.out = out;
     a.rows = piece_rows(b->max_q);
     a.ranges = FA_RANGES;
+    // measured with 16 and 8 query rows: about 9 and 4 us per item against 2.5 and 2.9 per unit
+    a.lead = b->max_q >= PG_TOK ? 4 : b->max_q > 1 ? 3 : 2;
     a.start = (PagedStart *)ws;
     a.part_o = (float *)((char *)ws + START_BYTES);
     a.part_ml = a.part_o + (size_t)2 * a.ranges * a.rows * KV_D;

@@ -33,12 +33,13 @@ struct PagedArgs {
     float *part_ml;                               // [2 * ranges][rows][2]
     int rows;                                     // rows per piece in the workspace: 8 min(max_q, 16)
     int ranges;
+    int lead;                                     // leading steps of an item
 };
 
-// Where a range starts; `total` is the number of units of the whole call.
+// Where a range starts; `total` is the number of steps of the whole call.
 struct PagedStart {
     long long total;
-    int seq, tile, head, unit;
+    int seq, tile, head, step;
 };
 
 // One sequence's new tokens: packed rows [row0, row0 + n) at positions first,
@@ -91,6 +92,11 @@ __device__ __forceinline__ long long units_before(const PagedBatch &b, const Seq
     return u;
 }
 __device__ __forceinline__ int seq_tiles(const SeqTokens &t) { return (t.n + PG_TOK - 1) / PG_TOK; }
+// Steps of tiles 0 .. i-1, both heads.
+__device__ __forceinline__ long long steps_before(const PagedArgs &a, const SeqTokens &t, int i)
+{
+    return KV_H * (units_before(a.b, t, i) + (long long)a.lead * i);
+}
 
 __device__ __forceinline__ long long range_begin(long long total, int c, int ranges)
 {
@@ -101,14 +107,15 @@ __device__ __forceinline__ long long range_begin(long long total, int c, int ran
 // a stretch of sequences, a block scan, then the owner of the range's first unit
 // walks its stretch. `scan` is shared scratch of THREADS / 32 + 1 values.
 template <int THREADS>
-__device__ __forceinline__ void find_start(const PagedBatch &b, int c, int ranges, long long *scan, PagedStart *out)
+__device__ __forceinline__ void find_start(const PagedArgs &a, int c, long long *scan, PagedStart *out)
 {
+    const PagedBatch &b = a.b;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (b.B + THREADS - 1) / THREADS, s0 = min(tid * per, b.B), s1 = min(s0 + per, b.B);
     long long mine = 0;
     for (int s = s0; s < s1; ++s) {
         const SeqTokens t = seq_tokens(b, s);
-        mine += KV_H * units_before(b, t, seq_tiles(t));
+        mine += steps_before(a, t, seq_tiles(t));
     }
     long long incl = mine;
 #pragma unroll
@@ -129,10 +136,10 @@ __device__ __forceinline__ void find_start(const PagedBatch &b, int c, int range
     }
     __syncthreads();
     const long long total = scan[THREADS / 32 - 1], before = incl - mine + (warp > 0 ? scan[warp - 1] : 0);
-    const long long u = range_begin(total, c, ranges);
+    const long long u = range_begin(total, c, a.ranges);
     if (tid == 0) {
         out->total = total;
-        out->seq = out->tile = out->head = out->unit = 0;
+        out->seq = out->tile = out->head = out->step = 0;
     }
     __syncthreads();
     if (mine > 0 && u >= before && u < before + mine) {
@@ -140,73 +147,97 @@ __device__ __forceinline__ void find_start(const PagedBatch &b, int c, int range
         int s = s0;
         SeqTokens t = seq_tokens(b, s);
         for (;;) {
-            const long long n = KV_H * units_before(b, t, seq_tiles(t));
+            const long long n = steps_before(a, t, seq_tiles(t));
             if (left < n) break;
             left -= n;
             t = seq_tokens(b, ++s);
         }
-        int lo = 0, hi = seq_tiles(t) - 1;         // the tile: largest i with 2 units_before(i) <= left
+        int lo = 0, hi = seq_tiles(t) - 1;         // the tile: largest i with steps_before(i) <= left
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (KV_H * units_before(b, t, mid) <= left) lo = mid;
+            if (steps_before(a, t, mid) <= left) lo = mid;
             else hi = mid - 1;
         }
-        left -= KV_H * units_before(b, t, lo);
-        const int n = tile_units(b, t, lo);
+        left -= steps_before(a, t, lo);
+        const int n = tile_units(b, t, lo) + a.lead;
         out->seq = s;
         out->tile = lo;
         out->head = (int)(left / n);
-        out->unit = (int)(left % n);
+        out->step = (int)(left % n);
     }
     __syncthreads();
 }
 
 // Walks a range piece by piece: units [unit, unit + len) of item (seq, tile, head).
+// A walk that has found no (further) piece has len = 0.
 struct PieceWalk {
     int seq, tile, head, unit, len, units;        // units of the whole item
-    long long left;                               // units of the range after this piece
+    long long left;                               // steps of the range after this piece
     SeqTokens t;
     bool first;                                   // the range's first piece
 
-    __device__ __forceinline__ void cut(const PagedBatch &b, long long avail)
+    // The piece from step `from` of the current item; empty if only leading steps are left of the range.
+    __device__ __forceinline__ void cut(const PagedArgs &a, int from, long long avail)
     {
-        units = tile_units(b, t, tile);
-        len = (int)min((long long)(units - unit), avail);
-        left = avail - len;
+        units = tile_units(a.b, t, tile);
+        const int to = (int)min((long long)(units + a.lead), from + avail);
+        left = avail - (to - from);
+        unit = max(from - a.lead, 0);
+        len = max(to - a.lead, 0) - unit;
     }
-    __device__ __forceinline__ void begin(const PagedBatch &b, const PagedStart &s, long long count)
+    __device__ __forceinline__ void begin(const PagedArgs &a, const PagedStart &s, long long count)
     {
         seq = s.seq;
         tile = s.tile;
         head = s.head;
-        unit = s.unit;
         first = true;
-        t = seq_tokens(b, seq);
-        cut(b, count);
+        t = seq_tokens(a.b, seq);
+        cut(a, s.step, count);                    // ends inside the leading steps: no piece, and left = 0
     }
-    // Moves to the next piece; only while left > 0.
-    __device__ __forceinline__ void next(const PagedBatch &b)
+    // Whether the range has a piece after this one: what is left reaches past the
+    // next item's leading steps.
+    __device__ __forceinline__ bool more(const PagedArgs &a) const { return left > a.lead; }
+    // Moves to the next piece; only if there is one.
+    __device__ __forceinline__ void next(const PagedArgs &a)
     {
         first = false;
-        unit = 0;
         if (++head == KV_H) {
             head = 0;
             if (++tile >= seq_tiles(t)) {
                 tile = 0;
                 do {
-                    if (seq + 1 >= b.B) {          // not while left > 0, unless the lengths changed during the call
+                    if (seq + 1 >= a.b.B) {        // not while steps are left, unless the lengths changed during the call
                         len = 0;
                         left = 0;
                         return;
                     }
-                    t = seq_tokens(b, ++seq);
+                    t = seq_tokens(a.b, ++seq);
                 } while (t.n == 0);
             }
         }
-        cut(b, left);
+        cut(a, 0, left);
     }
     __device__ __forceinline__ bool whole() const { return unit == 0 && len == units; }
     __device__ __forceinline__ int tokens() const { return min(PG_TOK, t.n - PG_TOK * tile); }
+};
+
+// A walk over the units of a range, one at a time.
+struct UnitWalk {
+    PieceWalk w;
+    int j;
+    __device__ __forceinline__ void begin(const PagedArgs &a, const PagedStart &s, long long count)
+    {
+        w.begin(a, s, count);
+        j = 0;
+    }
+    __device__ __forceinline__ bool last(const PagedArgs &a) const { return j + 1 >= w.len && !w.more(a); }
+    __device__ __forceinline__ void next(const PagedArgs &a)
+    {
+        if (++j == w.len) {
+            w.next(a);
+            j = 0;
+        }
+    }
 };
 
 }  // namespace gdn
