@@ -52,6 +52,7 @@ cudaError_t launch_kv_append(const gdn_attn_params *p, const gdn_paged_batch *b,
 cudaError_t launch_kv_gather(const gdn_paged_batch *b, const gdn_kv_cache *c, void *k_out, void *v_out,
                              gdn_dtype out_dt, cudaStream_t s);
 void *paged_error_word();
+void *paged_q4_error_word();
 size_t paged_workspace_bytes(const gdn_paged_batch *b, const gdn_kv_cache *c);
 cudaError_t launch_attn_paged(const gdn_paged_batch *b, const gdn_kv_cache *c, const void *q, const void *gate,
                               long long gate_row, long long gate_head, void *out, void *ws, gdn_dtype out_dt,
@@ -192,7 +193,7 @@ namespace gdn {
 // clears all of them with one small kernel (an atomic exchange each, so a word
 // set while the call runs is either reported now or kept for the next call)
 // and one copy of the OR back to the host.
-constexpr int N_ERROR_WORDS = 9;
+constexpr int N_ERROR_WORDS = 10;
 struct ErrorWords {
     unsigned int *p[N_ERROR_WORDS];
 };
@@ -222,7 +223,8 @@ static bool error_words(ErrorWords *out)
     if (!have[dev]) {
         void *(*const fns[N_ERROR_WORDS])() = {decode_error_word, chunk_error_word,    multi_error_word,
                                                gemm_error_word,   attn_error_word,     selftest_error_word,
-                                               gproj_error_word,  inconv_error_word,   paged_error_word};
+                                               gproj_error_word,  inconv_error_word,   paged_error_word,
+                                               paged_q4_error_word};
         for (int i = 0; i < N_ERROR_WORDS; ++i) {
             cache[dev].p[i] = static_cast<unsigned int *>(fns[i]());
             if (cache[dev].p[i] == nullptr) return false;

@@ -29,12 +29,9 @@
 // a tile in about 2,500 cycles against 2,048 of tensor work.
 #include <cuda.h>
 
-#include <mutex>
-
 #include "gdn_async.cuh"
 #include "gdn_paged.cuh"
 #include "gdn_tc.cuh"
-#include "gdn_tma.cuh"
 
 namespace gdn {
 
@@ -48,8 +45,6 @@ constexpr uint32_t FA_Q = 0;                      // Q: 4 boxes of 64 dims
 constexpr uint32_t FA_RING = 4 * FA_BOX;
 constexpr uint32_t FA_SMALL = FA_RING + FA_STAGES * FA_STAGE_BYTES;
 constexpr uint32_t FA_S = 0, FA_O = 256;          // tensor memory columns: S buffers at 0 and 128, O at 256
-constexpr float SCORE_SCALE = 1.4426950408889634f / 16.0f;   // log2 e / sqrt(256)
-constexpr float RESCALE_AT = 8.0f;                // powers of two a maximum may pass the reference by
 
 struct FaSmall {
     uint64_t full[FA_STAGES], empty[FA_STAGES];
@@ -61,55 +56,6 @@ struct FaSmall {
 };
 constexpr size_t FA_SMEM = FA_SMALL + sizeof(FaSmall) + 1024;   // + slack to align the block
 static_assert(FA_SMEM <= 232448, "shared memory of one CTA");
-
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar)
-{
-    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-                 "[%0], [%1, {%2, %3, %4}], [%5];"
-                 ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
-}
-
-__device__ __forceinline__ void store8_out(float *p, const float (&x)[8])
-{
-    reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-}
-__device__ __forceinline__ void store8_out(bf16 *p, const float (&x)[8])
-{
-    *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
-                                               pack_bf16(x[6], x[7]));
-}
-__device__ __forceinline__ void gate8(const uint4 u, float (&o)[8], float inv)
-{
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        o[i] *= __fdividef(inv, 1.0f + __expf(-__uint_as_float((i & 1) ? (w[i >> 1] & 0xFFFF0000u) : (w[i >> 1] << 16))));
-}
-// Normalised output times the gate, 8 dims from dim d of (packed row m, head h).
-template <typename TO>
-__device__ __forceinline__ void finish8(const PagedArgs &a, int m, int h, int d, float (&o)[8], float inv)
-{
-    if (a.gate != nullptr) {
-        gate8(__ldg(reinterpret_cast<const uint4 *>(a.gate + m * a.gate_row + h * a.gate_head + d)), o, inv);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] *= inv;
-    }
-    store8_out(static_cast<TO *>(a.out) + ((size_t)m * KV_HQ + h) * KV_D + d, o);
-}
 
 template <typename TO>
 __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_constant__ CUtensorMap qmap,
@@ -155,7 +101,7 @@ __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_
     const uint32_t tm = ss.tmem;
     const PagedStart st = ss.start;
     if (tid == 0) a.start[blockIdx.x] = st;
-    const long long count = range_begin(st.total, blockIdx.x + 1, a.ranges) - range_begin(st.total, blockIdx.x, a.ranges);
+    const long long count = range_begin(st, blockIdx.x + 1, a.ranges) - range_begin(st, blockIdx.x, a.ranges);
     const volatile int &aborted = ss.abort;
     auto stage = [&](uint32_t i) { return sb + FA_RING + (i % FA_STAGES) * FA_STAGE_BYTES; };
     auto wait_full = [&](uint32_t i) {
@@ -177,7 +123,7 @@ __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_
             // what the item sees are not loaded, bad page ids load past the end (zeros)
             auto segment = [&](int &row, int &loaded) {
                 const int p = (kw.w.unit + kw.j) * PG_TILE;
-                const int sees = tile_sees(b, kw.w.t, kw.w.tile);
+                const int sees = tile_sees(a, kw.w.t, kw.w.tile);
                 loaded = min(nseg, max(0, (sees - p + b.page - 1) >> b.page_log2));
                 row = 0;
                 if (seg < loaded) {
@@ -304,7 +250,7 @@ __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_
             // seen, was issued after the product of unit u - 2, so each is one phase behind at most.
             auto wait_pv = [&](uint32_t v) { return mbar_wait_bounded(smem_u32(&ss.pv_done[v & 1]), (v >> 1) & 1); };
             for (;;) {
-                const int rows = KV_G * w.tokens(), sees = tile_sees(b, w.t, w.tile);
+                const int rows = KV_G * w.tokens(a), sees = tile_sees(a, w.t, w.tile);
                 const int limit = min(w.t.first + PG_TOK * w.tile + (r >> 3) + 1, cap);   // positions this row sees
                 const bool live = 32 * q4 < rows;      // the warp has rows of the item
                 if (r < rows && w.whole() && a.gate != nullptr) {
@@ -480,28 +426,41 @@ __global__ void __launch_bounds__(256) attn_paged_join_kernel(const PagedArgs a)
     grid_dep_launch();
     const PagedStart st = a.start[c];
     // the item's first step, and the step of its first unit: a cut at or before that one cuts nothing
-    const long long u = range_begin(st.total, c, a.ranges), begin = u - st.step, unit0 = begin + a.lead;
-    if (u >= st.total || u <= unit0 || range_begin(st.total, c - 1, a.ranges) > unit0) return;
+    const long long u = range_begin(st, c, a.ranges), begin = u - st.step, unit0 = begin + a.lead;
+    if (u >= range_begin(st, a.ranges, a.ranges) || u <= unit0 || range_begin(st, c - 1, a.ranges) > unit0) return;
     const SeqTokens t = seq_tokens(a.b, st.seq);
-    const int tokens = min(PG_TOK, t.n - PG_TOK * st.tile);
+    const int tokens = min(a.tok, t.n - (st.tile << a.tok_log2));
     if (r >= KV_G * tokens) return;
-    const long long end = unit0 + tile_units(a.b, t, st.tile);
-    int last = c;                                      // the last range with a piece of the item
-    while (last + 1 < a.ranges && range_begin(st.total, last + 1, a.ranges) < end) ++last;
+    const long long end = unit0 + tile_units(a, t, st.tile);
+    int last = c + (int)((end - u - 1) / (st.quot + 1));   // the last range with a piece of the item, at least
+    while (last + 1 < a.ranges && range_begin(st, last + 1, a.ranges) < end) ++last;
     float M = -INFINITY, l = 0.0f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int k = c - 1 + warp; k <= last; k += 8) {
-        const long long k0 = range_begin(st.total, k, a.ranges), k1 = range_begin(st.total, k + 1, a.ranges);
-        if (k1 == k0) continue;                    // an empty range
-        const size_t slot = ((size_t)2 * k + (k0 >= begin ? 0 : 1)) * a.rows + r;
-        const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + slot * 2);
-        const float4 *src = reinterpret_cast<const float4 *>(a.part_o + slot * KV_D) + 2 * lane;
-        const float4 x = src[0], y = src[1];
-        if (ml.y != 0.0f) {
-            const float Mn = fmaxf(M, ml.x), f = ex2(M - Mn), g = ex2(ml.x - Mn);
+    for (int k0 = c - 1 + warp; k0 <= last; k0 += 32) {    // four pieces' loads at a time
+        float2 ml[4];
+        float4 x[4], y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int k = k0 + 8 * i;
+            ml[i] = make_float2(-INFINITY, 0.0f);
+            x[i] = y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            const long long from = range_begin(st, k, a.ranges);
+            if (k > last || range_begin(st, k + 1, a.ranges) == from) continue;   // past the item, or an empty range
+            const size_t slot = ((size_t)2 * k + (from >= begin ? 0 : 1)) * a.rows + r;
+            ml[i] = *reinterpret_cast<const float2 *>(a.part_ml + slot * 2);
+            const float4 *src = reinterpret_cast<const float4 *>(a.part_o + slot * KV_D) + 2 * lane;
+            x[i] = src[0];
+            y[i] = src[1];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (ml[i].y == 0.0f) continue;             // a piece that saw nothing
+            const float Mn = fmaxf(M, ml[i].x), f = ex2(M - Mn), g = ex2(ml[i].x - Mn);
             M = Mn;
-            l = l * f + ml.y * g;
-            o[0] = o[0] * f + x.x * g; o[1] = o[1] * f + x.y * g; o[2] = o[2] * f + x.z * g; o[3] = o[3] * f + x.w * g;
-            o[4] = o[4] * f + y.x * g; o[5] = o[5] * f + y.y * g; o[6] = o[6] * f + y.z * g; o[7] = o[7] * f + y.w * g;
+            l = l * f + ml[i].y * g;
+            o[0] = o[0] * f + x[i].x * g; o[1] = o[1] * f + x[i].y * g;
+            o[2] = o[2] * f + x[i].z * g; o[3] = o[3] * f + x[i].w * g;
+            o[4] = o[4] * f + y[i].x * g; o[5] = o[5] * f + y[i].y * g;
+            o[6] = o[6] * f + y[i].z * g; o[7] = o[7] * f + y[i].w * g;
         }
     }
     store8_out(&so[warp][8 * lane], o);
@@ -523,83 +482,16 @@ __global__ void __launch_bounds__(256) attn_paged_join_kernel(const PagedArgs a)
 #pragma unroll
         for (int i = 0; i < 8; ++i) e[i] += g * so[k][8 * lane + i];
     }
-    finish8<TO>(a, t.row0 + PG_TOK * st.tile + (r >> 3), KV_G * st.head + (r & 7), 8 * lane, e,
+    finish8<TO>(a, t.row0 + (st.tile << a.tok_log2) + (r >> 3), KV_G * st.head + (r & 7), 8 * lane, e,
                 la != 0.0f ? 1.0f / la : 0.0f);
-}
-
-template <bool Q4>
-__device__ __forceinline__ void load_row(const PagedArgs &a, int page, int head, int off, bool isv, int lane, float (&x)[8])
-{
-    if (page < 0) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = 0.0f;
-        return;
-    }
-    if (!Q4) {
-        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(static_cast<const bf16 *>(isv ? a.cv : a.ck) +
-                                                              row_bf16(a.b, page, head, off)) + lane);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = __uint_as_float((i & 1) ? (w[i >> 1] & 0xFFFF0000u) : (w[i >> 1] << 16));
-    } else {
-        const unsigned char *rec = static_cast<const unsigned char *>(a.ck) + record_of(a.b, page, head, off);
-        const int r = off & (REC_ROWS - 1), g = lane >> 3, c = lane & 7;
-        const uint32_t w = *reinterpret_cast<const uint32_t *>(rec + (isv ? REC_V : 0u) + r * 128 + c * 16 + g * 4);
-        const uint32_t sz = *reinterpret_cast<const uint32_t *>(rec + (isv ? REC_VSZ : REC_KSZ) + r * 16 + g * 4);
-        const float s = __uint_as_float(sz << 16), z = __uint_as_float(sz & 0xFFFF0000u);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = fmaf(s, (float)((w >> (4 * i)) & 15u), z);
-    }
-}
-
-template <typename TO, bool Q4>
-__global__ void __launch_bounds__(256) attn_paged_simple_kernel(const PagedArgs a)
-{
-    const int lane = threadIdx.x & 31;
-    const long long item = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int m = (int)(item / KV_HQ), h = (int)(item % KV_HQ);
-    grid_dep_wait();
-    grid_dep_launch();
-    if (m >= a.b.M) return;
-    const TokenPlace at = token_place(a.b, m, lane);
-    if (at.seq < 0) return;
-    const int n = min(at.pos + 1, a.b.max_pages << a.b.page_log2);
-    float q[8], acc[8], M = -INFINITY, l = 0.0f;
-    const uint4 u = __ldg(reinterpret_cast<const uint4 *>(a.q + ((size_t)m * KV_HQ + h) * KV_D) + lane);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        q[i] = 0.0625f * __uint_as_float((i & 1) ? (w[i >> 1] & 0xFFFF0000u) : (w[i >> 1] << 16));
-        acc[i] = 0.0f;
-    }
-    for (int p = 0; p < n; ++p) {
-        const int page = cache_page(a.b, at.seq, p), off = p & (a.b.page - 1);
-        float k[8], v[8], s = 0.0f;
-        load_row<Q4>(a, page, h / KV_G, off, false, lane, k);
-        load_row<Q4>(a, page, h / KV_G, off, true, lane, v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s = fmaf(q[i], k[i], s);
-        s = warp_sum(s);
-        const float Mn = fmaxf(M, s), f = expf(M - Mn), e = expf(s - Mn);
-        M = Mn;
-        l = l * f + e;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = acc[i] * f + e * v[i];
-    }
-    const float inv = n > 0 ? 1.0f / l : 0.0f;
-    TO *out = static_cast<TO *>(a.out) + ((size_t)m * KV_HQ + h) * KV_D + 8 * lane;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        float o = acc[i] * inv;
-        if (a.gate != nullptr) o /= 1.0f + expf(-to_f(a.gate[m * a.gate_row + h * a.gate_head + 8 * lane + i]));
-        out[i] = from_f<TO>(o);
-    }
 }
 
 // ------------------------------------------------------------------ launcher
 
-// The driver's tensor-map encoder, looked up once.
-static bool encode_q_map(CUtensorMap *map, const void *q, int M)
+// A tensor map with unit element strides and zero fill, through the driver's
+// encoder (looked up once); false if that is missing or rejects the arguments.
+bool encode_tiled(CUtensorMap *map, CUtensorMapDataType dt, int rank, const void *base, const cuuint64_t *dims,
+                  const cuuint64_t *strides, const cuuint32_t *box, CUtensorMapSwizzle swizzle)
 {
     typedef CUresult (*Fn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                            const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
@@ -610,13 +502,24 @@ static bool encode_q_map(CUtensorMap *map, const void *q, int M)
         const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r);
         return e == cudaSuccess && r == cudaDriverEntryPointSuccess ? reinterpret_cast<Fn>(p) : nullptr;
     }();
-    if (!fn) return false;
-    // [M][16][256] in boxes of 16 tokens x 8 heads x 64 dims, 128-byte swizzle; tokens past M read as zeros
+    const cuuint32_t one[3] = {1, 1, 1};
+    return fn && fn(map, dt, rank, const_cast<void *>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t launch_paged_join(const PagedArgs &a, gdn_dtype out_dt, cudaStream_t s)
+{
+    const dim3 grid(a.ranges - 1, a.rows), block(256);
+    return out_dt == GDN_F32 ? launch_pdl(attn_paged_join_kernel<float>, grid, block, 0, s, a)
+                             : launch_pdl(attn_paged_join_kernel<bf16>, grid, block, 0, s, a);
+}
+
+// [M][16][256] in boxes of 16 tokens x 8 heads x 64 dims, 128-byte swizzle; tokens past M read as zeros.
+static bool encode_q_map(CUtensorMap *map, const void *q, int M)
+{
     const cuuint64_t dims[3] = {KV_D, KV_HQ, (cuuint64_t)M}, strides[2] = {KV_D * 2, KV_HQ * KV_D * 2};
-    const cuuint32_t box[3] = {64, KV_G, PG_TOK}, one[3] = {1, 1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dims, strides, box, one,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const cuuint32_t box[3] = {64, KV_G, PG_TOK};
+    return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 constexpr int FA_RANGES = 152;                    // one CTA per SM
@@ -627,27 +530,6 @@ static int piece_rows(int max_q) { return KV_G * (max_q < PG_TOK ? max_q : PG_TO
 size_t paged_workspace_bytes(const gdn_paged_batch *b, const gdn_kv_cache *)
 {
     return START_BYTES + (size_t)2 * FA_RANGES * piece_rows(b->max_q) * (KV_D + 2) * sizeof(float);
-}
-
-template <auto KERNEL> static cudaError_t smem_attr_once(size_t bytes)
-{
-    static std::mutex mu;
-    static bool done[64] = {};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    std::lock_guard<std::mutex> lock(mu);
-    if (dev < 0 || dev >= 64 || !done[dev]) {
-        e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-        if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
-    }
-    return e;
-}
-
-template <typename TO>
-static cudaError_t launch_join(const PagedArgs &a, cudaStream_t s)
-{
-    return launch_pdl(attn_paged_join_kernel<TO>, dim3(a.ranges - 1, a.rows), dim3(256), 0, s, a);
 }
 
 template <typename TO>
@@ -661,7 +543,7 @@ static cudaError_t launch_bf16(const PagedArgs &a, cudaStream_t s)
     cudaError_t e = smem_attr_once<attn_paged_kernel<TO>>(FA_SMEM);
     if (e != cudaSuccess) return e;
     e = launch_pdl(attn_paged_kernel<TO>, dim3(a.ranges), dim3(FA_THREADS), FA_SMEM, s, qm, km, vm, a);
-    return e == cudaSuccess ? launch_join<TO>(a, s) : e;
+    return e;
 }
 
 cudaError_t launch_attn_paged(const gdn_paged_batch *b, const gdn_kv_cache *c, const void *q, const void *gate,
@@ -680,14 +562,23 @@ cudaError_t launch_attn_paged(const gdn_paged_batch *b, const gdn_kv_cache *c, c
     a.rows = piece_rows(b->max_q);
     a.ranges = FA_RANGES;
     // measured with 16 and 8 query rows: about 9 and 4 us per item against 2.5 and 2.9 per unit
+    a.tok = PG_TOK;
+    a.tok_log2 = 4;
     a.lead = b->max_q >= PG_TOK ? 4 : b->max_q > 1 ? 3 : 2;
     a.start = (PagedStart *)ws;
     a.part_o = (float *)((char *)ws + START_BYTES);
     a.part_ml = a.part_o + (size_t)2 * a.ranges * a.rows * KV_D;
-    if (c->format == GDN_KV_BF16) return out_dt == GDN_F32 ? launch_bf16<float>(a, s) : launch_bf16<bf16>(a, s);
-    const dim3 grid((unsigned)(((long long)b->M * KV_HQ + 7) / 8)), block(256);
-    return out_dt == GDN_F32 ? launch_pdl(attn_paged_simple_kernel<float, true>, grid, block, 0, s, a)
-                             : launch_pdl(attn_paged_simple_kernel<bf16, true>, grid, block, 0, s, a);
+    cudaError_t e;
+    if (c->format == GDN_KV_Q4) {
+        a.tok = 1;
+        a.tok_log2 = 0;
+        a.rows = KV_G;
+        a.lead = 2;
+        e = launch_paged_q4(a, out_dt, s);
+    } else {
+        e = out_dt == GDN_F32 ? launch_bf16<float>(a, s) : launch_bf16<bf16>(a, s);
+    }
+    return e == cudaSuccess ? launch_paged_join(a, out_dt, s) : e;
 }
 
 // Device address of this file's error word, for gdn_device_error.

@@ -1,8 +1,8 @@
 // gdn_paged.cuh -- how the paged attention kernels share out their work.
 //
 // An item is 16 consecutive new tokens of one sequence (the last one may have
-// fewer) and one KV head: up to 128 query rows (8 heads x 16 tokens) that read
-// the same keys and values. Its units are the 128-position tiles of the context
+// fewer), or a single token, and one KV head: up to 128 query rows (8 heads x 16
+// tokens) that read the same keys and values. Its units are the 128-position tiles of the context
 // that its last token sees, at least one. The units of all items, in order of
 // sequence, tokens, head and position, are cut into one even range per CTA,
 // wherever that falls: contexts of any mix of lengths and batches of any size
@@ -13,7 +13,13 @@
 // device, so a captured call follows them from replay to replay.
 #pragma once
 
+#include <cuda.h>
+
+#include <mutex>
+
+#include "gdn_async.cuh"
 #include "gdn_kv.cuh"
+#include "gdn_tma.cuh"
 
 namespace gdn {
 
@@ -21,6 +27,9 @@ constexpr int PG_TOK = 16;                        // tokens per item, at most
 constexpr int PG_TILE = 128;                      // positions per unit
 constexpr int PG_ROWS = PG_TOK * KV_G;            // 128 query rows
 constexpr int PG_MAX_CTAS = 304;                  // ranges, at most (two per SM of 152)
+
+constexpr float SCORE_SCALE = 1.4426950408889634f / 16.0f;   // log2 e / sqrt(256)
+constexpr float RESCALE_AT = 8.0f;                // powers of two a maximum may pass the reference by
 
 struct PagedArgs {
     PagedBatch b;
@@ -34,11 +43,13 @@ struct PagedArgs {
     int rows;                                     // rows per piece in the workspace: 8 min(max_q, 16)
     int ranges;
     int lead;                                     // leading steps of an item
+    int tok, tok_log2;                            // tokens per item: 16 or 1
 };
 
-// Where a range starts; `total` is the number of steps of the whole call.
+// Where a range starts; the whole call has quot * ranges + rem steps.
 struct PagedStart {
-    long long total;
+    long long quot;
+    int rem;
     int seq, tile, head, step;
 };
 
@@ -64,43 +75,46 @@ __device__ __forceinline__ SeqTokens seq_tokens(const PagedBatch &b, int s)
 }
 
 // Positions the last token of tile i sees, and the tile's units.
-__device__ __forceinline__ int tile_sees(const PagedBatch &b, const SeqTokens &t, int i)
+__device__ __forceinline__ int tile_sees(const PagedArgs &a, const SeqTokens &t, int i)
 {
-    return min(t.first + min(PG_TOK * (i + 1), t.n), b.max_pages << b.page_log2);
+    return min(t.first + min((i + 1) << a.tok_log2, t.n), a.b.max_pages << a.b.page_log2);
 }
-__device__ __forceinline__ int tile_units(const PagedBatch &b, const SeqTokens &t, int i)
+__device__ __forceinline__ int tile_units(const PagedArgs &a, const SeqTokens &t, int i)
 {
-    return max((tile_sees(b, t, i) + PG_TILE - 1) / PG_TILE, 1);
+    return max((tile_sees(a, t, i) + PG_TILE - 1) / PG_TILE, 1);
 }
+__device__ __forceinline__ int seq_tiles(const PagedArgs &a, const SeqTokens &t) { return (t.n + a.tok - 1) >> a.tok_log2; }
 
-// Units of tiles 0 .. i-1, per head. With x = floor((first + 127) / 16), whole
-// tile j (from 1) has floor((x + j) / 8) units, and the sum of floor(m / 8) over
-// m = 0 .. 8 q + r is 4 q (q - 1) + q (r + 1). Contexts that start below 0 or
-// end past the table are summed term by term.
-__device__ __forceinline__ long long units_before(const PagedBatch &b, const SeqTokens &t, int i)
+// Units of tiles 0 .. i-1, per head. With x = floor((first + 127) / tok) and
+// D = 128 / tok, whole tile j (from 1) has floor((x + j) / D) units, and the sum
+// of floor(m / D) over m = 0 .. D q + r is D q (q - 1) / 2 + q (r + 1). Contexts
+// that start below 0 or end past the table are summed term by term.
+__device__ __forceinline__ long long units_before(const PagedArgs &a, const SeqTokens &t, int i)
 {
-    if (t.first < 0 || t.first + t.n > (b.max_pages << b.page_log2)) {
+    if (t.first < 0 || t.first + t.n > (a.b.max_pages << a.b.page_log2)) {
         long long u = 0;
-        for (int j = 0; j < i; ++j) u += tile_units(b, t, j);
+        for (int j = 0; j < i; ++j) u += tile_units(a, t, j);
         return u;
     }
-    const int tiles = (t.n + PG_TOK - 1) / PG_TOK, whole = min(i, t.n / PG_TOK);
-    auto sum = [](long long m) { const long long q = m >> 3; return 4 * q * (q - 1) + q * ((m & 7) + 1); };
-    const int x = (t.first + PG_TILE - 1) / PG_TOK;
+    const int tiles = seq_tiles(a, t), whole = min(i, t.n >> a.tok_log2), dl = 7 - a.tok_log2;
+    auto sum = [dl](long long m) {
+        const long long q = m >> dl;
+        return ((q * (q - 1)) << dl >> 1) + q * ((m & ((1 << dl) - 1)) + 1);
+    };
+    const int x = (t.first + PG_TILE - 1) >> a.tok_log2;
     long long u = sum(x + whole) - sum(x);
-    if (i == tiles && whole < tiles) u += tile_units(b, t, tiles - 1);
+    if (i == tiles && whole < tiles) u += tile_units(a, t, tiles - 1);
     return u;
 }
-__device__ __forceinline__ int seq_tiles(const SeqTokens &t) { return (t.n + PG_TOK - 1) / PG_TOK; }
 // Steps of tiles 0 .. i-1, both heads.
 __device__ __forceinline__ long long steps_before(const PagedArgs &a, const SeqTokens &t, int i)
 {
-    return KV_H * (units_before(a.b, t, i) + (long long)a.lead * i);
+    return KV_H * (units_before(a, t, i) + (long long)a.lead * i);
 }
 
-__device__ __forceinline__ long long range_begin(long long total, int c, int ranges)
+__device__ __forceinline__ long long range_begin(const PagedStart &s, int c, int ranges)
 {
-    return total / ranges * c + total % ranges * c / ranges;
+    return s.quot * c + s.rem * c / ranges;
 }
 
 // The start of range c, by all THREADS threads of the CTA: per-thread sums over
@@ -115,7 +129,7 @@ __device__ __forceinline__ void find_start(const PagedArgs &a, int c, long long 
     long long mine = 0;
     for (int s = s0; s < s1; ++s) {
         const SeqTokens t = seq_tokens(b, s);
-        mine += steps_before(a, t, seq_tiles(t));
+        mine += steps_before(a, t, seq_tiles(a, t));
     }
     long long incl = mine;
 #pragma unroll
@@ -136,9 +150,13 @@ __device__ __forceinline__ void find_start(const PagedArgs &a, int c, long long 
     }
     __syncthreads();
     const long long total = scan[THREADS / 32 - 1], before = incl - mine + (warp > 0 ? scan[warp - 1] : 0);
-    const long long u = range_begin(total, c, a.ranges);
+    PagedStart cuts;
+    cuts.quot = total / a.ranges;
+    cuts.rem = (int)(total % a.ranges);
+    const long long u = range_begin(cuts, c, a.ranges);
     if (tid == 0) {
-        out->total = total;
+        out->quot = cuts.quot;
+        out->rem = cuts.rem;
         out->seq = out->tile = out->head = out->step = 0;
     }
     __syncthreads();
@@ -147,19 +165,19 @@ __device__ __forceinline__ void find_start(const PagedArgs &a, int c, long long 
         int s = s0;
         SeqTokens t = seq_tokens(b, s);
         for (;;) {
-            const long long n = steps_before(a, t, seq_tiles(t));
+            const long long n = steps_before(a, t, seq_tiles(a, t));
             if (left < n) break;
             left -= n;
             t = seq_tokens(b, ++s);
         }
-        int lo = 0, hi = seq_tiles(t) - 1;         // the tile: largest i with steps_before(i) <= left
+        int lo = 0, hi = seq_tiles(a, t) - 1;         // the tile: largest i with steps_before(i) <= left
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
             if (steps_before(a, t, mid) <= left) lo = mid;
             else hi = mid - 1;
         }
         left -= steps_before(a, t, lo);
-        const int n = tile_units(b, t, lo) + a.lead;
+        const int n = tile_units(a, t, lo) + a.lead;
         out->seq = s;
         out->tile = lo;
         out->head = (int)(left / n);
@@ -179,7 +197,7 @@ struct PieceWalk {
     // The piece from step `from` of the current item; empty if only leading steps are left of the range.
     __device__ __forceinline__ void cut(const PagedArgs &a, int from, long long avail)
     {
-        units = tile_units(a.b, t, tile);
+        units = tile_units(a, t, tile);
         const int to = (int)min((long long)(units + a.lead), from + avail);
         left = avail - (to - from);
         unit = max(from - a.lead, 0);
@@ -203,7 +221,7 @@ struct PieceWalk {
         first = false;
         if (++head == KV_H) {
             head = 0;
-            if (++tile >= seq_tiles(t)) {
+            if (++tile >= seq_tiles(a, t)) {
                 tile = 0;
                 do {
                     if (seq + 1 >= a.b.B) {        // not while steps are left, unless the lengths changed during the call
@@ -218,7 +236,7 @@ struct PieceWalk {
         cut(a, 0, left);
     }
     __device__ __forceinline__ bool whole() const { return unit == 0 && len == units; }
-    __device__ __forceinline__ int tokens() const { return min(PG_TOK, t.n - PG_TOK * tile); }
+    __device__ __forceinline__ int tokens(const PagedArgs &a) const { return min(a.tok, t.n - (tile << a.tok_log2)); }
 };
 
 // A walk over the units of a range, one at a time.
@@ -239,5 +257,78 @@ struct UnitWalk {
         }
     }
 };
+
+// ---- small device helpers of the paged kernels
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3, %4}], [%5];"
+                 ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void store8_out(float *p, const float (&x)[8])
+{
+    reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ void store8_out(bf16 *p, const float (&x)[8])
+{
+    *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                                               pack_bf16(x[6], x[7]));
+}
+__device__ __forceinline__ void gate8(const uint4 u, float (&o)[8], float inv)
+{
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        o[i] *= __fdividef(inv, 1.0f + __expf(-__uint_as_float((i & 1) ? (w[i >> 1] & 0xFFFF0000u) : (w[i >> 1] << 16))));
+}
+// Normalised output times the gate, 8 dims from dim d of (packed row m, head h).
+template <typename TO>
+__device__ __forceinline__ void finish8(const PagedArgs &a, int m, int h, int d, float (&o)[8], float inv)
+{
+    if (a.gate != nullptr) {
+        gate8(__ldg(reinterpret_cast<const uint4 *>(a.gate + m * a.gate_row + h * a.gate_head + d)), o, inv);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] *= inv;
+    }
+    store8_out(static_cast<TO *>(a.out) + ((size_t)m * KV_HQ + h) * KV_D + d, o);
+}
+
+// ---- host side, gdn_paged.cu and gdn_paged_q4.cu
+
+bool encode_tiled(CUtensorMap *map, CUtensorMapDataType dt, int rank, const void *base, const cuuint64_t *dims,
+                  const cuuint64_t *strides, const cuuint32_t *box, CUtensorMapSwizzle swizzle);
+cudaError_t launch_paged_q4(const PagedArgs &a, gdn_dtype out_dt, cudaStream_t s);
+
+// The kernel's shared-memory attribute, set once per device.
+template <auto KERNEL> static cudaError_t smem_attr_once(size_t bytes)
+{
+    static std::mutex mu;
+    static bool done[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev < 0 || dev >= 64 || !done[dev]) {
+        e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
+    }
+    return e;
+}
 
 }  // namespace gdn
