@@ -6,36 +6,45 @@
 // for the 5th-generation tensor cores would write and read back 16 KiB per
 // record, more than the shared-memory port carries in that time (128 bytes per
 // cycle). So the codes go from shared memory to registers once and enter warp
-// matrix instructions (m16n8k16, 8 query heads as N) as they are: nibble c in
-// the low mantissa bits of 0x4300 is the bf16 number 128 + c, one logic
-// operation per two codes. Steps and zeros stay out of the products:
-//   q . k = sum_g s_g (sum_{d in g} q_d (128 + c_d)) + (z_g - 128 s_g) sum_{d in g} q_d,
-//   o_d   = sum_p w'_p (128 + c_d) + sum_p (w_p z_p - 128 w'_p),  w'_p = bf16(w_p s_p),
-// with the sums per group g of 64 dims in fp32. The one rounding to fewer bits is
-// w'. Products with 128 + c lose nothing that matters: the 128s are taken out
-// with the rounded w' they went in with.
+// matrix instructions (m16n8k16, 8 query heads as N) almost as they are, one logic
+// operation per two codes and few shifts:
+//  - keys in fp16: nibble c in bits 0-3 of 0x6400 is 1024 + c, in bits 4-7 1024 +
+//    16 c, so a word of eight codes needs one shift; q enters in fp16, scaled by a
+//    power of two per head (exact down to 2^-22 of the head's largest element) and
+//    by 1/16 where the code has its 16;
+//  - values in bf16: the sum runs over positions, so words of two positions are
+//    interleaved by halves, and nibble c in the low bits of 0x4300 is 128 + c.
+// (fp8 instructions would take the nibbles as they are, 0..15 being c 2^-9 in e4m3,
+// but they are carried out as conversions to fp16 here: measured 10% slower.)
+// Steps and zeros stay out of the products: with sums per group g of 64 dims,
+//   q . k = sum_g s_g (sum_{d in g} q_d (1024 + c_d) - 1024 sum q_d) + z_g sum_{d in g} q_d,
+//   o_d   = sum_p w'_p (128 + c_d) + sum_p (w_p z_p - 128 w'_p),  w'_p = bf16(w_p s_p).
+// The roundings to fewer bits are w' and q's elements below 2^-22 of the largest.
+// The 1024s and 128s are taken out with the rounded numbers they went in with.
 //
-// Work: gdn_paged.cuh with one token per item. A unit is 8 records, one per warp:
-// each of the 8 warps runs its own online softmax over its records, and the warps
-// meet once per piece. A ninth warp issues the copies, lane k for warp k: a
+// Work: gdn_paged.cuh with one token per item. The records of a piece go round the
+// 11 warps, each with its own online softmax, and the warps meet once per piece.
+// A twelfth warp issues the copies, lane k for warp k: a
 // record's 32 code rows as one tiled TMA box in the 128-byte swizzle (which makes
 // every operand read below free of bank conflicts) and its steps and zeros as
-// another, through a ring of four records per warp.
+// another, through a ring of three records per warp.
+#include <cuda_fp16.h>
+
 #include "gdn_paged.cuh"
 
 namespace gdn {
 
 __device__ unsigned int g_paged_q4_error;         // GDN_ERR_TIMEOUT if a bounded wait gave up
 
-constexpr int DQ_WARPS = 8;
+constexpr int DQ_WARPS = 11;                      // with the producer three warps per scheduler, 168 registers each
 constexpr int DQ_THREADS = 32 * (DQ_WARPS + 1);
-constexpr int DQ_STAGES = 4;
+constexpr int DQ_STAGES = 3;
 constexpr uint32_t DQ_CODES = 4096, DQ_SZ = 512;  // bytes of a record's codes; of its steps and zeros
 constexpr int DQ_OSTRIDE = KV_D + 8;              // floats per head of a warp's output in shared memory
 constexpr uint32_t DQ_RING = 0;
 constexpr uint32_t DQ_RING_SZ = DQ_WARPS * DQ_STAGES * DQ_CODES;
 constexpr uint32_t DQ_OUT = DQ_RING_SZ + DQ_WARPS * DQ_STAGES * DQ_SZ;
-constexpr uint32_t DQ_SMALL = DQ_OUT + DQ_WARPS * KV_G * DQ_OSTRIDE * 4;
+constexpr uint32_t DQ_SMALL = DQ_OUT + DQ_WARPS * (KV_G / 2) * DQ_OSTRIDE * 4;
 
 struct DqSmall {
     uint64_t full[DQ_WARPS][DQ_STAGES], empty[DQ_WARPS][DQ_STAGES];
@@ -51,19 +60,37 @@ static_assert(DQ_SMEM <= 232448, "shared memory of one CTA");
 __device__ __forceinline__ void mma_m16n8k16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                              uint32_t b0, uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The same with fp16 operands; mma_f16_from starts from the accumulator (c0, c1, c0, c1).
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1, float c0, float c1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
 }
 // 8 x 8 transpose of 16-bit elements across the warp.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x)
 {
     uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-// Codes t and t + 4 of a word as the bf16 pair (128 + c_t, 128 + c_{t+4}).
-__device__ __forceinline__ uint32_t code_pair(uint32_t w, int t) { return ((w >> (4 * t)) & 0x000F000Fu) | 0x43004300u; }
-
+// (w & mask) | magic in one logic operation; the masks are kept in registers.
+__device__ __forceinline__ uint32_t mask_or(uint32_t w, uint32_t mask, uint32_t magic)
+{
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(magic));
+    return r;
+}
 __device__ __forceinline__ float sz_step(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float sz_zero(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 __device__ __forceinline__ uint32_t word_of(const uint4 &v, int g) { return g == 0 ? v.x : g == 1 ? v.y : g == 2 ? v.z : v.w; }
@@ -73,6 +100,8 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr)
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
     return v;
 }
+
+__device__ __forceinline__ void consumer_bar() { asm volatile("bar.sync 1, %0;" ::"n"(32 * DQ_WARPS) : "memory"); }
 
 template <typename TO>
 __global__ void __launch_bounds__(DQ_THREADS, 1) attn_paged_q4_kernel(const __grid_constant__ CUtensorMap cmap,
@@ -102,46 +131,63 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) attn_paged_q4_kernel(const __gr
     if (count > 0) w.begin(a, st, count);
     if (count == 0 || w.len == 0) return;
     const volatile int &aborted = ss.abort;
-    auto codes_at = [&](int wp, uint32_t i) { return sb + DQ_RING + (wp * DQ_STAGES + i % DQ_STAGES) * DQ_CODES; };
-    auto sz_at = [&](int wp, uint32_t i) { return sb + DQ_RING_SZ + (wp * DQ_STAGES + i % DQ_STAGES) * DQ_SZ; };
+    auto codes_at = [&](int wp, uint32_t i) { return sb + DQ_RING + (wp * DQ_STAGES + i) * DQ_CODES; };
+    auto sz_at = [&](int wp, uint32_t i) { return sb + DQ_RING_SZ + (wp * DQ_STAGES + i) * DQ_SZ; };
+
+    // where the positions of a piece end
+    auto piece_end = [&](const PieceWalk &p) { return min(tile_sees(a, p.t, p.tile), (p.unit + p.len) * PG_TILE); };
 
     if (warp == DQ_WARPS) {
         // ---- producer: lane k feeds warp k
-        UnitWalk u;
-        u.w = w;
-        u.j = 0;
         const int recs = (b.num_pages * KV_H) << b.page_log2 >> 4;
-        // this lane's record of the walk's unit: -1 if the item does not see it, past the end for a bad page
-        auto record = [&]() {
-            const int p = (u.w.unit + u.j) * PG_TILE + 16 * lane;
-            if (lane >= DQ_WARPS || p >= tile_sees(a, u.w.t, u.w.tile)) return -1;
-            const int page = cache_page(b, u.w.seq, p);
-            return page < 0 ? recs : ((((page * KV_H + u.w.head) << b.page_log2) + (p & (b.page - 1))) >> 4);
+        int base = 0;                              // first record of the round, from the piece's first position
+        bool more = true;
+        // A round's record of this lane: whether it has one, its page table entry (a load that is two
+        // rounds old when its value is first needed) and its place in the page.
+        struct Rec {
+            bool round, mine;
+            int page, in_page;
+        };
+        auto fetch = [&]() {
+            Rec r = {more, false, 0, 0};
+            if (!more) return r;
+            const int p = w.unit * PG_TILE + 16 * (base + lane), end = piece_end(w);
+            if (lane < DQ_WARPS && p < end) {
+                r.mine = true;
+                r.page = __ldg(b.table + (size_t)w.seq * b.max_pages + (p >> b.page_log2));
+                r.in_page = (w.head << b.page_log2) + (p & (b.page - 1));
+            }
+            base += DQ_WARPS;
+            if (w.unit * PG_TILE + 16 * base >= end) {
+                more = w.more(a);
+                if (more) w.next(a);
+                base = 0;
+            }
+            return r;
         };
         uint32_t i = 0;
         bool ok = true;
-        int rec = record();
-        for (;;) {
-            const bool more = !u.last(a);
-            int next = -1;
-            if (more) {                            // the next unit's page is looked up before this one waits
-                u.next(a);
-                next = record();
-            }
-            if (rec >= 0 && ok) {
+        Rec r0 = fetch(), r1 = fetch();
+        while (r0.round) {
+            const Rec r2 = fetch();
+            if (r0.mine) {
                 if (i >= DQ_STAGES)
                     ok = mbar_wait_bounded(smem_u32(&ss.empty[lane][i % DQ_STAGES]), (i / DQ_STAGES - 1) & 1);
                 if (ok) {
+                    // a page id outside the cache reads past its end: zeros
+                    const int rec = (unsigned)r0.page < (unsigned)b.num_pages
+                                        ? (((r0.page * KV_H) << b.page_log2) + r0.in_page) >> 4 : recs;
                     const uint32_t bar = smem_u32(&ss.full[lane][i % DQ_STAGES]);
                     mbar_arrive_expect_tx(bar, DQ_CODES + DQ_SZ);
-                    tma_load_3d(codes_at(lane, i), &cmap, 0, 0, rec, bar);
-                    tma_load_2d(sz_at(lane, i), &smap, 0, rec, bar);
+                    tma_load_3d(codes_at(lane, i % DQ_STAGES), &cmap, 0, 0, rec, bar);
+                    tma_load_2d(sz_at(lane, i % DQ_STAGES), &smap, 0, rec, bar);
                     ++i;
                 }
             }
             ok = __all_sync(0xffffffffu, ok && !aborted);
-            if (!more || !ok) break;
-            rec = next;
+            if (!ok) break;
+            r0 = r1;
+            r1 = r2;
         }
         if (!ok) {                                 // copies in flight land before the CTA exits
             ss.abort = 1;
@@ -152,34 +198,72 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) attn_paged_q4_kernel(const __gr
     } else {
         // ---- consumers. Fragment coordinates: i = lane / 4, j = lane % 4.
         const int i4 = lane >> 2, j4 = lane & 3;
-        uint32_t n = 0;                            // records consumed
+        uint32_t slot = 0, phase = 0;              // of the warp's ring
+        uint32_t mask, magic, mask16, one;         // not constants to the compiler, so that they stay in registers
+        asm volatile("mov.u32 %0, 0x000F000F;\n\tmov.u32 %1, 0x43004300;" : "=r"(mask), "=r"(magic));
+        asm volatile("mov.u32 %0, 0x00F000F0;\n\tmov.u32 %1, 0x64006400;" : "=r"(mask16), "=r"(one));
         bool ok = true;
         for (;;) {
             const int sees = tile_sees(a, w.t, w.tile);
             const int mrow = w.t.row0 + w.tile;
-            // Q^T operand: head i, dims of chunks 2 j and 2 j + 1 of each group, paired as code_pair
-            // pairs the codes; and the sums of q over each group for heads 2 j, 2 j + 1
+            // Q^T operand: head i, dims of chunks 2 j and 2 j + 1 of each group, in fp16, scaled by a power
+            // of two per head that brings its largest element to 128..256, and the odd codes' dims by
+            // 1/16 more; paired as the codes unpack: (0, 4), (1, 5) / 16, (2, 6), (3, 7) / 16. For heads 2 j
+            // and 2 j + 1: the sums of q over each group, what the 1024s add to a product, the scale back.
             uint32_t qf[4][2][4];
-            float qs[4][2];
+            float qs[4][2], off[4][2], back[2];
             {
-                const bf16 *q = a.q + ((size_t)mrow * KV_HQ + KV_G * w.head + i4) * KV_D;
+                const uint4 *q = reinterpret_cast<const uint4 *>(a.q + ((size_t)mrow * KV_HQ + KV_G * w.head + i4) * KV_D) + 2 * j4;
+                float top = 0.0f;
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
                     float sum = 0.0f;
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(q + 64 * g + 8 * (2 * j4 + c)));
-                        qf[g][c][0] = __byte_perm(v.x, v.z, 0x5410);   // dims 0, 4
-                        qf[g][c][1] = __byte_perm(v.x, v.z, 0x7632);   // 1, 5
-                        qf[g][c][2] = __byte_perm(v.y, v.w, 0x5410);   // 2, 6
-                        qf[g][c][3] = __byte_perm(v.y, v.w, 0x7632);   // 3, 7
+                        const uint4 v = __ldg(q + 8 * g + c);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) sum += sz_step(word_of(v, k)) + sz_zero(word_of(v, k));
+                        for (int k = 0; k < 4; ++k) {
+                            qf[g][c][k] = word_of(v, k);
+                            sum += sz_step(word_of(v, k)) + sz_zero(word_of(v, k));
+                            top = fmaxf(top, fmaxf(fabsf(sz_step(word_of(v, k))), fabsf(sz_zero(word_of(v, k)))));
+                        }
                     }
                     sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                     sum += __shfl_xor_sync(0xffffffffu, sum, 2);
                     qs[g][0] = __shfl_sync(0xffffffffu, sum, 8 * j4);
                     qs[g][1] = __shfl_sync(0xffffffffu, sum, 8 * j4 + 4);
+                }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const int ex = min(max((int)(__float_as_uint(top) >> 23), 24), 253);   // top in [2^(ex-127), 2^(ex-126))
+                const float up = __uint_as_float((uint32_t)(261 - ex) << 23);         // 2^(134 - ex)
+                const float down = __uint_as_float((uint32_t)(ex - 7) << 23);          // 2^(ex - 134)
+                back[0] = __shfl_sync(0xffffffffu, down, 8 * j4);
+                back[1] = __shfl_sync(0xffffffffu, down, 8 * j4 + 4);
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float d[8];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            d[2 * k] = sz_step(qf[g][c][k]) * up;
+                            d[2 * k + 1] = sz_zero(qf[g][c][k]) * (up * 0.0625f);
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const __half2 h = __floats2half2_rn(d[k], d[k + 4]);
+                            qf[g][c][k] = *reinterpret_cast<const uint32_t *>(&h);
+                            const float2 f = __half22float2(h);
+                            sum += f.x + f.y;
+                        }
+                    }
+                    sum *= -1024.0f;
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                    off[g][0] = __shfl_sync(0xffffffffu, sum, 8 * j4);
+                    off[g][1] = __shfl_sync(0xffffffffu, sum, 8 * j4 + 4);
                 }
             }
             float o[4][4][4], bias[4][2], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
@@ -191,10 +275,11 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) attn_paged_q4_kernel(const __gr
 #pragma unroll
                     for (int k = 0; k < 4; ++k) o[g][t][k] = 0.0f;
             }
-            for (int p0 = w.unit * PG_TILE + 16 * warp; p0 < min(sees, (w.unit + w.len) * PG_TILE); p0 += PG_TILE, ++n) {
-                ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&ss.full[warp][n % DQ_STAGES]), (n / DQ_STAGES) & 1));
+            const int end = piece_end(w);
+            for (int p0 = w.unit * PG_TILE + 16 * warp; p0 < end; p0 += 16 * DQ_WARPS) {
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&ss.full[warp][slot]), phase));
                 if (!ok) break;
-                const uint32_t cb = codes_at(warp, n), zb = sz_at(warp, n);
+                const uint32_t cb = codes_at(warp, slot), zb = sz_at(warp, slot);
                 // scores of positions p0 + i and p0 + 8 + i for heads 2 j, 2 j + 1
                 float s[4] = {0.f, 0.f, 0.f, 0.f};
                 {
@@ -202,28 +287,46 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) attn_paged_q4_kernel(const __gr
                     const uint4 ka[2] = {lds128(r0 + x0), lds128(r0 + x1)};
                     const uint4 kb[2] = {lds128(r0 + 1024 + x0), lds128(r0 + 1024 + x1)};
                     uint4 z0 = lds128(zb + i4 * 16), z1 = lds128(zb + 128 + i4 * 16);
-                    if (p0 + i4 >= sees) z0 = make_uint4(0u, 0u, 0u, 0u);        // rows past the context hold
-                    if (p0 + 8 + i4 >= sees) z1 = make_uint4(0u, 0u, 0u, 0u);    // anything; codes are finite
+                    if (p0 + 16 > sees) {          // rows past the context hold anything; codes are finite
+                        if (p0 + i4 >= sees) z0 = make_uint4(0u, 0u, 0u, 0u);
+                        if (p0 + 8 + i4 >= sees) z1 = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    float t[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
-                        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                        float acc[4];
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
                             const uint32_t u = word_of(ka[c], g), v = word_of(kb[c], g);
-                            mma_m16n8k16(acc, code_pair(u, 0), code_pair(v, 0), code_pair(u, 1), code_pair(v, 1),
-                                         qf[g][c][0], qf[g][c][1]);
-                            mma_m16n8k16(acc, code_pair(u, 2), code_pair(v, 2), code_pair(u, 3), code_pair(v, 3),
-                                         qf[g][c][2], qf[g][c][3]);
+                            const uint32_t x = u >> 8, y = v >> 8;
+                            if (c == 0)
+                                mma_f16_from(acc, mask_or(u, mask, one), mask_or(v, mask, one), mask_or(u, mask16, one),
+                                             mask_or(v, mask16, one), qf[g][c][0], qf[g][c][1], off[g][0], off[g][1]);
+                            else
+                                mma_f16(acc, mask_or(u, mask, one), mask_or(v, mask, one), mask_or(u, mask16, one),
+                                        mask_or(v, mask16, one), qf[g][c][0], qf[g][c][1]);
+                            mma_f16(acc, mask_or(x, mask, one), mask_or(y, mask, one), mask_or(x, mask16, one),
+                                    mask_or(y, mask16, one), qf[g][c][2], qf[g][c][3]);
                         }
                         const float s0 = sz_step(word_of(z0, g)), s1 = sz_step(word_of(z1, g));
-                        const float t0 = fmaf(-128.0f, s0, sz_zero(word_of(z0, g))), t1 = fmaf(-128.0f, s1, sz_zero(word_of(z1, g)));
-                        s[0] = fmaf(s0, acc[0], fmaf(t0, qs[g][0], s[0]));
-                        s[1] = fmaf(s0, acc[1], fmaf(t0, qs[g][1], s[1]));
-                        s[2] = fmaf(s1, acc[2], fmaf(t1, qs[g][0], s[2]));
-                        s[3] = fmaf(s1, acc[3], fmaf(t1, qs[g][1], s[3]));
+                        const float e0 = sz_zero(word_of(z0, g)), e1 = sz_zero(word_of(z1, g));
+                        t[0] = fmaf(s0, acc[0], t[0]);
+                        t[1] = fmaf(s0, acc[1], t[1]);
+                        t[2] = fmaf(s1, acc[2], t[2]);
+                        t[3] = fmaf(s1, acc[3], t[3]);
+                        s[0] = fmaf(e0, qs[g][0], s[0]);
+                        s[1] = fmaf(e0, qs[g][1], s[1]);
+                        s[2] = fmaf(e1, qs[g][0], s[2]);
+                        s[3] = fmaf(e1, qs[g][1], s[3]);
                     }
-                    if (p0 + i4 >= sees) s[0] = s[1] = -INFINITY;
-                    if (p0 + 8 + i4 >= sees) s[2] = s[3] = -INFINITY;
+                    s[0] = fmaf(t[0], back[0], s[0]);
+                    s[1] = fmaf(t[1], back[1], s[1]);
+                    s[2] = fmaf(t[2], back[0], s[2]);
+                    s[3] = fmaf(t[3], back[1], s[3]);
+                    if (p0 + 16 > sees) {
+                        if (p0 + i4 >= sees) s[0] = s[1] = -INFINITY;
+                        if (p0 + 8 + i4 >= sees) s[2] = s[3] = -INFINITY;
+                    }
                 }
                 const float t0 = fmaxf(s[0], s[2]), t1 = fmaxf(s[1], s[3]);
                 if (__any_sync(0xffffffffu, (t0 - m[0]) * SCORE_SCALE > RESCALE_AT || (t1 - m[1]) * SCORE_SCALE > RESCALE_AT)) {
@@ -264,8 +367,10 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) attn_paged_q4_kernel(const __gr
                     const uint4 v0 = lds128(va + x0), v1 = lds128(va + 128 + x1);
                     const uint4 v2 = lds128(va + 1024 + x0), v3 = lds128(va + 1152 + x1);
                     uint4 z0 = lds128(zb + 256 + i4 * 16), z1 = lds128(zb + 384 + i4 * 16);
-                    if (p0 + i4 >= sees) z0 = make_uint4(0u, 0u, 0u, 0u);
-                    if (p0 + 8 + i4 >= sees) z1 = make_uint4(0u, 0u, 0u, 0u);
+                    if (p0 + 16 > sees) {
+                        if (p0 + i4 >= sees) z0 = make_uint4(0u, 0u, 0u, 0u);
+                        if (p0 + 8 + i4 >= sees) z1 = make_uint4(0u, 0u, 0u, 0u);
+                    }
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
                         const float s0 = sz_step(word_of(z0, g)), s1 = sz_step(word_of(z1, g));
@@ -277,15 +382,19 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) attn_paged_q4_kernel(const __gr
                         const uint32_t lo = __byte_perm(word_of(v0, g), word_of(v1, g), 0x5410), hi = __byte_perm(word_of(v0, g), word_of(v1, g), 0x7632);
                         const uint32_t lo2 = __byte_perm(word_of(v2, g), word_of(v3, g), 0x5410), hi2 = __byte_perm(word_of(v2, g), word_of(v3, g), 0x7632);
                         // product t: rows 0-7 are dims 8 i + 2 t of the group, rows 8-15 dims 8 i + 2 t + 1
-                        mma_m16n8k16(o[g][0], code_pair(lo, 0), code_pair(lo, 1), code_pair(lo2, 0), code_pair(lo2, 1), b0, b1);
-                        mma_m16n8k16(o[g][1], code_pair(lo, 2), code_pair(lo, 3), code_pair(lo2, 2), code_pair(lo2, 3), b0, b1);
-                        mma_m16n8k16(o[g][2], code_pair(hi, 0), code_pair(hi, 1), code_pair(hi2, 0), code_pair(hi2, 1), b0, b1);
-                        mma_m16n8k16(o[g][3], code_pair(hi, 2), code_pair(hi, 3), code_pair(hi2, 2), code_pair(hi2, 3), b0, b1);
+                        mma_m16n8k16(o[g][0], mask_or(lo, mask, magic), mask_or(lo >> 4, mask, magic), mask_or(lo2, mask, magic), mask_or(lo2 >> 4, mask, magic), b0, b1);
+                        mma_m16n8k16(o[g][1], mask_or(lo >> 8, mask, magic), mask_or(lo >> 12, mask, magic), mask_or(lo2 >> 8, mask, magic), mask_or(lo2 >> 12, mask, magic), b0, b1);
+                        mma_m16n8k16(o[g][2], mask_or(hi, mask, magic), mask_or(hi >> 4, mask, magic), mask_or(hi2, mask, magic), mask_or(hi2 >> 4, mask, magic), b0, b1);
+                        mma_m16n8k16(o[g][3], mask_or(hi >> 8, mask, magic), mask_or(hi >> 12, mask, magic), mask_or(hi2 >> 8, mask, magic), mask_or(hi2 >> 12, mask, magic), b0, b1);
                     }
                 }
-                mbar_arrive(smem_u32(&ss.empty[warp][n % DQ_STAGES]));
+                mbar_arrive(smem_u32(&ss.empty[warp][slot]));
+                if (++slot == DQ_STAGES) {
+                    slot = 0;
+                    phase ^= 1;
+                }
             }
-            // the warps' outputs, maxima and sums meet in shared memory
+            // the warps' outputs, maxima and sums meet in shared memory, four heads at a time
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) {
 #pragma unroll
@@ -295,15 +404,6 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) attn_paged_q4_kernel(const __gr
                     for (int g = 0; g < 4; ++g) bias[g][k] += __shfl_xor_sync(0xffffffffu, bias[g][k], d);
                 }
             }
-            float *os = reinterpret_cast<float *>(blk + DQ_OUT) + warp * KV_G * DQ_OSTRIDE;
-#pragma unroll
-            for (int g = 0; g < 4; ++g)
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    float4 *dst = reinterpret_cast<float4 *>(os + (2 * j4 + k) * DQ_OSTRIDE + 64 * g + 8 * i4);
-                    dst[0] = make_float4(o[g][0][k] + bias[g][k], o[g][0][2 + k] + bias[g][k], o[g][1][k] + bias[g][k], o[g][1][2 + k] + bias[g][k]);
-                    dst[1] = make_float4(o[g][2][k] + bias[g][k], o[g][2][2 + k] + bias[g][k], o[g][3][k] + bias[g][k], o[g][3][2 + k] + bias[g][k]);
-                }
             if (i4 == 0)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
@@ -311,33 +411,48 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) attn_paged_q4_kernel(const __gr
                     ss.ml[warp][2 * j4 + k][1] = l[k];
                 }
             if (!ok) ss.abort = ss.stop = 1;
-            asm volatile("bar.sync 1, 256;" ::: "memory");
-            {
-                const int h = warp, d = 8 * lane;
-                float M = -INFINITY, L = 0.0f, e[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int k = 0; k < DQ_WARPS; ++k) M = fmaxf(M, ss.ml[k][h][0]);
-                const float *src = reinterpret_cast<const float *>(blk + DQ_OUT) + h * DQ_OSTRIDE + d;
+            float *const all = reinterpret_cast<float *>(blk + DQ_OUT);
 #pragma unroll 1
-                for (int k = 0; k < DQ_WARPS; ++k) {
-                    if (ss.ml[k][h][1] == 0.0f) continue;      // no records of this piece
-                    const float f = ex2(ss.ml[k][h][0] - M);
-                    const float4 x = *reinterpret_cast<const float4 *>(src + k * KV_G * DQ_OSTRIDE);
-                    const float4 y = *reinterpret_cast<const float4 *>(src + k * KV_G * DQ_OSTRIDE + 4);
-                    L += f * ss.ml[k][h][1];
-                    e[0] += f * x.x; e[1] += f * x.y; e[2] += f * x.z; e[3] += f * x.w;
-                    e[4] += f * y.x; e[5] += f * y.y; e[6] += f * y.z; e[7] += f * y.w;
+            for (int half = 0; half < 2; ++half) {
+                if (j4 >> 1 == half) {
+                    float *os = all + (warp * (KV_G / 2) + 2 * (j4 & 1)) * DQ_OSTRIDE + 8 * i4;
+#pragma unroll
+                    for (int g = 0; g < 4; ++g)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            float4 *dst = reinterpret_cast<float4 *>(os + k * DQ_OSTRIDE + 64 * g);
+                            dst[0] = make_float4(o[g][0][k] + bias[g][k], o[g][0][2 + k] + bias[g][k], o[g][1][k] + bias[g][k], o[g][1][2 + k] + bias[g][k]);
+                            dst[1] = make_float4(o[g][2][k] + bias[g][k], o[g][2][2 + k] + bias[g][k], o[g][3][k] + bias[g][k], o[g][3][2 + k] + bias[g][k]);
+                        }
                 }
-                if (w.whole()) {
-                    finish8<TO>(a, mrow, KV_G * w.head + h, d, e, L != 0.0f ? 1.0f / L : 0.0f);
-                } else {
-                    const size_t slot = ((size_t)2 * blockIdx.x + (w.first ? 0 : 1)) * a.rows + h;
-                    store8_out(a.part_o + slot * KV_D + d, e);
-                    if (lane == 0) *reinterpret_cast<float2 *>(a.part_ml + slot * 2) = make_float2(M, L);
+                consumer_bar();
+                if (tid < 128) {                   // one head per warp, 8 dims per lane
+                    const int hl = warp, h = 4 * half + hl, d = 8 * lane;
+                    float M = -INFINITY, L = 0.0f, e[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int k = 0; k < DQ_WARPS; ++k) M = fmaxf(M, ss.ml[k][h][0]);
+                    const float *src = all + hl * DQ_OSTRIDE + d;
+#pragma unroll
+                    for (int k = 0; k < DQ_WARPS; ++k) {
+                        const float lk = ss.ml[k][h][1], f = lk != 0.0f ? ex2(ss.ml[k][h][0] - M) : 0.0f;   // 0: no records
+                        const float4 x = *reinterpret_cast<const float4 *>(src + k * (KV_G / 2) * DQ_OSTRIDE);
+                        const float4 y = *reinterpret_cast<const float4 *>(src + k * (KV_G / 2) * DQ_OSTRIDE + 4);
+                        L = fmaf(f, lk, L);
+                        e[0] = fmaf(f, x.x, e[0]); e[1] = fmaf(f, x.y, e[1]); e[2] = fmaf(f, x.z, e[2]); e[3] = fmaf(f, x.w, e[3]);
+                        e[4] = fmaf(f, y.x, e[4]); e[5] = fmaf(f, y.y, e[5]); e[6] = fmaf(f, y.z, e[6]); e[7] = fmaf(f, y.w, e[7]);
+                    }
+                    if (w.whole()) {
+                        finish8<TO>(a, mrow, KV_G * w.head + h, d, e, L != 0.0f ? 1.0f / L : 0.0f);
+                    } else {
+                        const size_t slot = ((size_t)2 * blockIdx.x + (w.first ? 0 : 1)) * a.rows + h;
+                        store8_out(a.part_o + slot * KV_D + d, e);
+                        if (lane == 0) *reinterpret_cast<float2 *>(a.part_ml + slot * 2) = make_float2(M, L);
+                    }
                 }
+                if (half == 0) consumer_bar();
             }
             const bool stop = *const_cast<const volatile int *>(&ss.stop) != 0;
-            asm volatile("bar.sync 1, 256;" ::: "memory");
+            consumer_bar();
             if (stop || !w.more(a)) break;
             w.next(a);
         }
