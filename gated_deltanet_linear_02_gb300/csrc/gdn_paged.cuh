@@ -309,6 +309,22 @@ __device__ __forceinline__ void finish8(const PagedArgs &a, int m, int h, int d,
     store8_out(static_cast<TO *>(a.out) + ((size_t)m * KV_HQ + h) * KV_D + d, o);
 }
 
+// The same for 4 dims.
+template <typename TO>
+__device__ __forceinline__ void finish4(const PagedArgs &a, int m, int h, int d, float4 o, float inv)
+{
+    float s[4] = {inv, inv, inv, inv};
+    if (a.gate != nullptr) {
+        const float4 g = load4(a.gate + m * a.gate_row + h * a.gate_head + d);
+        s[0] = __fdividef(inv, 1.0f + __expf(-g.x));
+        s[1] = __fdividef(inv, 1.0f + __expf(-g.y));
+        s[2] = __fdividef(inv, 1.0f + __expf(-g.z));
+        s[3] = __fdividef(inv, 1.0f + __expf(-g.w));
+    }
+    store4(static_cast<TO *>(a.out) + ((size_t)m * KV_HQ + h) * KV_D + d,
+           make_float4(o.x * s[0], o.y * s[1], o.z * s[2], o.w * s[3]));
+}
+
 // ---- host side, gdn_paged.cu and gdn_paged_q4.cu
 
 bool encode_tiled(CUtensorMap *map, CUtensorMapDataType dt, int rank, const void *base, const cuuint64_t *dims,

@@ -46,7 +46,17 @@ constexpr uint32_t DQ_RING_SZ = DQ_WARPS * DQ_STAGES * DQ_CODES;
 constexpr uint32_t DQ_OUT = DQ_RING_SZ + DQ_WARPS * DQ_STAGES * DQ_SZ;
 constexpr uint32_t DQ_SMALL = DQ_OUT + DQ_WARPS * (KV_G / 2) * DQ_OSTRIDE * 4;
 
+// A piece's queries as its warps take them, made by the producer warp.
+struct DqQuery {
+    uint4 frag[8][32];                            // [2 g + c][lane]: B operands of the key products
+    float4 aux[4][4];                             // [g][j]: what the 1024s add, negated, and the sums of q, for heads 2 j, 2 j + 1
+    float2 back[4];                               // [j]: the scale back
+};
+constexpr int DQ_QUERIES = 4;                     // short pieces run up to three ahead
+
 struct DqSmall {
+    DqQuery query[DQ_QUERIES];
+    uint64_t q_full[DQ_QUERIES], q_empty[DQ_QUERIES];
     uint64_t full[DQ_WARPS][DQ_STAGES], empty[DQ_WARPS][DQ_STAGES];
     long long scan[DQ_THREADS / 32 + 1];
     PagedStart start;
@@ -101,6 +111,70 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr)
     return v;
 }
 
+// Queries of one item into shared memory, by one warp with the fragment coordinates
+// i = lane / 4, j = lane % 4. B operand of the key products: head i, dims of chunks
+// 2 j and 2 j + 1 of each group, in fp16, scaled by a power of two per head that
+// brings its largest element to 128..256, and by 1/16 more where the code has its
+// 16; paired as the codes unpack: (0, 4), (1, 5) / 16, (2, 6), (3, 7) / 16.
+__device__ __noinline__ void make_query(const uint4 *q, DqQuery &out, int lane)
+{
+    const int j4 = lane & 3;
+    uint32_t qf[4][2][4];
+    float qs[4][2], top = 0.0f;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const uint4 v = __ldg(q + 8 * g + c);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                qf[g][c][k] = word_of(v, k);
+                sum += sz_step(word_of(v, k)) + sz_zero(word_of(v, k));
+                top = fmaxf(top, fmaxf(fabsf(sz_step(word_of(v, k))), fabsf(sz_zero(word_of(v, k)))));
+            }
+        }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        qs[g][0] = __shfl_sync(0xffffffffu, sum, 8 * j4);
+        qs[g][1] = __shfl_sync(0xffffffffu, sum, 8 * j4 + 4);
+    }
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const int ex = min(max((int)(__float_as_uint(top) >> 23), 24), 253);   // top in [2^(ex-127), 2^(ex-126))
+    const float up = __uint_as_float((uint32_t)(261 - ex) << 23);         // 2^(134 - ex)
+    const float down = __uint_as_float((uint32_t)(ex - 7) << 23);          // 2^(ex - 134)
+    const float back0 = __shfl_sync(0xffffffffu, down, 8 * j4), back1 = __shfl_sync(0xffffffffu, down, 8 * j4 + 4);
+    if (lane < 4) out.back[lane] = make_float2(back0, back1);
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            float d[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                d[2 * k] = sz_step(qf[g][c][k]) * up;
+                d[2 * k + 1] = sz_zero(qf[g][c][k]) * (up * 0.0625f);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const __half2 h = __floats2half2_rn(d[k], d[k + 4]);
+                qf[g][c][k] = *reinterpret_cast<const uint32_t *>(&h);
+                const float2 f = __half22float2(h);
+                sum += f.x + f.y;
+            }
+        }
+        sum *= -1024.0f;
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        const float off0 = __shfl_sync(0xffffffffu, sum, 8 * j4), off1 = __shfl_sync(0xffffffffu, sum, 8 * j4 + 4);
+        if (lane < 4) out.aux[g][lane] = make_float4(off0, off1, qs[g][0], qs[g][1]);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) out.frag[2 * g + c][lane] = make_uint4(qf[g][c][0], qf[g][c][1], qf[g][c][2], qf[g][c][3]);
+    }
+}
+
 __device__ __forceinline__ void consumer_bar() { asm volatile("bar.sync 1, %0;" ::"n"(32 * DQ_WARPS) : "memory"); }
 
 template <typename TO>
@@ -118,6 +192,10 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) attn_paged_q4_kernel(const __gr
     if (tid < DQ_WARPS * DQ_STAGES) {
         mbar_init(smem_u32(&ss.full[0][0] + tid), 1);
         mbar_init(smem_u32(&ss.empty[0][0] + tid), 32);
+    }
+    if (tid < DQ_QUERIES) {
+        mbar_init(smem_u32(&ss.q_full[tid]), 32);
+        mbar_init(smem_u32(&ss.q_empty[tid]), DQ_WARPS);
     }
     if (tid == 0) ss.abort = ss.stop = 0;
     fence_mbar_init();
@@ -148,9 +226,27 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) attn_paged_q4_kernel(const __gr
             bool round, mine;
             int page, in_page;
         };
+        uint32_t piece = 0;
+        bool ok = true;
         auto fetch = [&]() {
             Rec r = {more, false, 0, 0};
             if (!more) return r;
+            if (base == 0) {                       // a piece begins: its queries
+                const uint32_t qb = piece % DQ_QUERIES;
+                if (piece >= DQ_QUERIES)
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&ss.q_empty[qb]), (piece / DQ_QUERIES - 1) & 1));
+                if (!ok) {
+                    r.round = false;
+                    return r;
+                }
+                const int m = w.t.row0 + w.tile;
+                make_query(reinterpret_cast<const uint4 *>(a.q + ((size_t)m * KV_HQ + KV_G * w.head + (lane >> 2)) * KV_D) + 2 * (lane & 3),
+                           ss.query[qb], lane);
+                mbar_arrive(smem_u32(&ss.q_full[qb]));
+                ++piece;
+                if (a.gate != nullptr && w.whole())    // and its gates, for the epilogue: 128 bytes per lane
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(a.gate + m * a.gate_row + (KV_G * w.head + (lane >> 2)) * a.gate_head + 64 * (lane & 3)));
+            }
             const int p = w.unit * PG_TILE + 16 * (base + lane), end = piece_end(w);
             if (lane < DQ_WARPS && p < end) {
                 r.mine = true;
@@ -166,11 +262,10 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) attn_paged_q4_kernel(const __gr
             return r;
         };
         uint32_t i = 0;
-        bool ok = true;
         Rec r0 = fetch(), r1 = fetch();
-        while (r0.round) {
+        while (r0.round && ok) {
             const Rec r2 = fetch();
-            if (r0.mine) {
+            if (r0.mine && ok) {
                 if (i >= DQ_STAGES)
                     ok = mbar_wait_bounded(smem_u32(&ss.empty[lane][i % DQ_STAGES]), (i / DQ_STAGES - 1) & 1);
                 if (ok) {
@@ -198,7 +293,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) attn_paged_q4_kernel(const __gr
     } else {
         // ---- consumers. Fragment coordinates: i = lane / 4, j = lane % 4.
         const int i4 = lane >> 2, j4 = lane & 3;
-        uint32_t slot = 0, phase = 0;              // of the warp's ring
+        uint32_t slot = 0, phase = 0, piece = 0;   // of the warp's ring; pieces begun
         uint32_t mask, magic, mask16, one;         // not constants to the compiler, so that they stay in registers
         asm volatile("mov.u32 %0, 0x000F000F;\n\tmov.u32 %1, 0x43004300;" : "=r"(mask), "=r"(magic));
         asm volatile("mov.u32 %0, 0x00F000F0;\n\tmov.u32 %1, 0x64006400;" : "=r"(mask16), "=r"(one));
@@ -206,66 +301,9 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) attn_paged_q4_kernel(const __gr
         for (;;) {
             const int sees = tile_sees(a, w.t, w.tile);
             const int mrow = w.t.row0 + w.tile;
-            // Q^T operand: head i, dims of chunks 2 j and 2 j + 1 of each group, in fp16, scaled by a power
-            // of two per head that brings its largest element to 128..256, and the odd codes' dims by
-            // 1/16 more; paired as the codes unpack: (0, 4), (1, 5) / 16, (2, 6), (3, 7) / 16. For heads 2 j
-            // and 2 j + 1: the sums of q over each group, what the 1024s add to a product, the scale back.
-            uint32_t qf[4][2][4];
-            float qs[4][2], off[4][2], back[2];
-            {
-                const uint4 *q = reinterpret_cast<const uint4 *>(a.q + ((size_t)mrow * KV_HQ + KV_G * w.head + i4) * KV_D) + 2 * j4;
-                float top = 0.0f;
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    float sum = 0.0f;
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const uint4 v = __ldg(q + 8 * g + c);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            qf[g][c][k] = word_of(v, k);
-                            sum += sz_step(word_of(v, k)) + sz_zero(word_of(v, k));
-                            top = fmaxf(top, fmaxf(fabsf(sz_step(word_of(v, k))), fabsf(sz_zero(word_of(v, k)))));
-                        }
-                    }
-                    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                    qs[g][0] = __shfl_sync(0xffffffffu, sum, 8 * j4);
-                    qs[g][1] = __shfl_sync(0xffffffffu, sum, 8 * j4 + 4);
-                }
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const int ex = min(max((int)(__float_as_uint(top) >> 23), 24), 253);   // top in [2^(ex-127), 2^(ex-126))
-                const float up = __uint_as_float((uint32_t)(261 - ex) << 23);         // 2^(134 - ex)
-                const float down = __uint_as_float((uint32_t)(ex - 7) << 23);          // 2^(ex - 134)
-                back[0] = __shfl_sync(0xffffffffu, down, 8 * j4);
-                back[1] = __shfl_sync(0xffffffffu, down, 8 * j4 + 4);
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    float sum = 0.0f;
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        float d[8];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            d[2 * k] = sz_step(qf[g][c][k]) * up;
-                            d[2 * k + 1] = sz_zero(qf[g][c][k]) * (up * 0.0625f);
-                        }
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const __half2 h = __floats2half2_rn(d[k], d[k + 4]);
-                            qf[g][c][k] = *reinterpret_cast<const uint32_t *>(&h);
-                            const float2 f = __half22float2(h);
-                            sum += f.x + f.y;
-                        }
-                    }
-                    sum *= -1024.0f;
-                    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                    off[g][0] = __shfl_sync(0xffffffffu, sum, 8 * j4);
-                    off[g][1] = __shfl_sync(0xffffffffu, sum, 8 * j4 + 4);
-                }
-            }
+            const uint32_t qb = piece % DQ_QUERIES;
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&ss.q_full[qb]), (piece / DQ_QUERIES) & 1));
+            ++piece;
             float o[4][4][4], bias[4][2], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
@@ -276,7 +314,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) attn_paged_q4_kernel(const __gr
                     for (int k = 0; k < 4; ++k) o[g][t][k] = 0.0f;
             }
             const int end = piece_end(w);
-            for (int p0 = w.unit * PG_TILE + 16 * warp; p0 < end; p0 += 16 * DQ_WARPS) {
+            for (int p0 = w.unit * PG_TILE + 16 * warp; p0 < end && ok; p0 += 16 * DQ_WARPS) {
                 ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&ss.full[warp][slot]), phase));
                 if (!ok) break;
                 const uint32_t cb = codes_at(warp, slot), zb = sz_at(warp, slot);
@@ -295,18 +333,20 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) attn_paged_q4_kernel(const __gr
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
                         float acc[4];
+                        const float4 aux = ss.query[qb].aux[g][j4];
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
                             const uint32_t u = word_of(ka[c], g), v = word_of(kb[c], g);
+                            const uint4 qf = ss.query[qb].frag[2 * g + c][lane];
                             const uint32_t x = u >> 8, y = v >> 8;
                             if (c == 0)
                                 mma_f16_from(acc, mask_or(u, mask, one), mask_or(v, mask, one), mask_or(u, mask16, one),
-                                             mask_or(v, mask16, one), qf[g][c][0], qf[g][c][1], off[g][0], off[g][1]);
+                                             mask_or(v, mask16, one), qf.x, qf.y, aux.x, aux.y);
                             else
                                 mma_f16(acc, mask_or(u, mask, one), mask_or(v, mask, one), mask_or(u, mask16, one),
-                                        mask_or(v, mask16, one), qf[g][c][0], qf[g][c][1]);
+                                        mask_or(v, mask16, one), qf.x, qf.y);
                             mma_f16(acc, mask_or(x, mask, one), mask_or(y, mask, one), mask_or(x, mask16, one),
-                                    mask_or(y, mask16, one), qf[g][c][2], qf[g][c][3]);
+                                    mask_or(y, mask16, one), qf.z, qf.w);
                         }
                         const float s0 = sz_step(word_of(z0, g)), s1 = sz_step(word_of(z1, g));
                         const float e0 = sz_zero(word_of(z0, g)), e1 = sz_zero(word_of(z1, g));
@@ -314,15 +354,16 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) attn_paged_q4_kernel(const __gr
                         t[1] = fmaf(s0, acc[1], t[1]);
                         t[2] = fmaf(s1, acc[2], t[2]);
                         t[3] = fmaf(s1, acc[3], t[3]);
-                        s[0] = fmaf(e0, qs[g][0], s[0]);
-                        s[1] = fmaf(e0, qs[g][1], s[1]);
-                        s[2] = fmaf(e1, qs[g][0], s[2]);
-                        s[3] = fmaf(e1, qs[g][1], s[3]);
+                        s[0] = fmaf(e0, aux.z, s[0]);
+                        s[1] = fmaf(e0, aux.w, s[1]);
+                        s[2] = fmaf(e1, aux.z, s[2]);
+                        s[3] = fmaf(e1, aux.w, s[3]);
                     }
-                    s[0] = fmaf(t[0], back[0], s[0]);
-                    s[1] = fmaf(t[1], back[1], s[1]);
-                    s[2] = fmaf(t[2], back[0], s[2]);
-                    s[3] = fmaf(t[3], back[1], s[3]);
+                    const float2 back = ss.query[qb].back[j4];
+                    s[0] = fmaf(t[0], back.x, s[0]);
+                    s[1] = fmaf(t[1], back.y, s[1]);
+                    s[2] = fmaf(t[2], back.x, s[2]);
+                    s[3] = fmaf(t[3], back.y, s[3]);
                     if (p0 + 16 > sees) {
                         if (p0 + i4 >= sees) s[0] = s[1] = -INFINITY;
                         if (p0 + 8 + i4 >= sees) s[2] = s[3] = -INFINITY;
@@ -394,6 +435,8 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) attn_paged_q4_kernel(const __gr
                     phase ^= 1;
                 }
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&ss.q_empty[qb]));
             // the warps' outputs, maxima and sums meet in shared memory, four heads at a time
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) {
@@ -426,9 +469,10 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) attn_paged_q4_kernel(const __gr
                         }
                 }
                 consumer_bar();
-                if (tid < 128) {                   // one head per warp, 8 dims per lane
-                    const int hl = warp, h = 4 * half + hl, d = 8 * lane;
-                    float M = -INFINITY, L = 0.0f, e[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                if (warp < 8) {                    // two warps per head, 4 dims per lane
+                    const int hl = warp >> 1, h = 4 * half + hl, d = 128 * (warp & 1) + 4 * lane;
+                    float M = -INFINITY, L = 0.0f;
+                    float4 e = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                     for (int k = 0; k < DQ_WARPS; ++k) M = fmaxf(M, ss.ml[k][h][0]);
                     const float *src = all + hl * DQ_OSTRIDE + d;
@@ -436,17 +480,15 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) attn_paged_q4_kernel(const __gr
                     for (int k = 0; k < DQ_WARPS; ++k) {
                         const float lk = ss.ml[k][h][1], f = lk != 0.0f ? ex2(ss.ml[k][h][0] - M) : 0.0f;   // 0: no records
                         const float4 x = *reinterpret_cast<const float4 *>(src + k * (KV_G / 2) * DQ_OSTRIDE);
-                        const float4 y = *reinterpret_cast<const float4 *>(src + k * (KV_G / 2) * DQ_OSTRIDE + 4);
                         L = fmaf(f, lk, L);
-                        e[0] = fmaf(f, x.x, e[0]); e[1] = fmaf(f, x.y, e[1]); e[2] = fmaf(f, x.z, e[2]); e[3] = fmaf(f, x.w, e[3]);
-                        e[4] = fmaf(f, y.x, e[4]); e[5] = fmaf(f, y.y, e[5]); e[6] = fmaf(f, y.z, e[6]); e[7] = fmaf(f, y.w, e[7]);
+                        e.x = fmaf(f, x.x, e.x); e.y = fmaf(f, x.y, e.y); e.z = fmaf(f, x.z, e.z); e.w = fmaf(f, x.w, e.w);
                     }
                     if (w.whole()) {
-                        finish8<TO>(a, mrow, KV_G * w.head + h, d, e, L != 0.0f ? 1.0f / L : 0.0f);
+                        finish4<TO>(a, mrow, KV_G * w.head + h, d, e, L != 0.0f ? 1.0f / L : 0.0f);
                     } else {
-                        const size_t slot = ((size_t)2 * blockIdx.x + (w.first ? 0 : 1)) * a.rows + h;
-                        store8_out(a.part_o + slot * KV_D + d, e);
-                        if (lane == 0) *reinterpret_cast<float2 *>(a.part_ml + slot * 2) = make_float2(M, L);
+                        const size_t at = ((size_t)2 * blockIdx.x + (w.first ? 0 : 1)) * a.rows + h;
+                        *reinterpret_cast<float4 *>(a.part_o + at * KV_D + d) = e;
+                        if (lane == 0) *reinterpret_cast<float2 *>(a.part_ml + at * 2) = make_float2(M, L);
                     }
                 }
                 if (half == 0) consumer_bar();
