@@ -30,6 +30,8 @@
 // another, through a ring of three records per warp.
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "gdn_paged.cuh"
 
 namespace gdn {
@@ -318,6 +320,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) attn_paged_q4_kernel(const __gr
                 ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&ss.full[warp][slot]), phase));
                 if (!ok) break;
                 const uint32_t cb = codes_at(warp, slot), zb = sz_at(warp, slot);
+                auto record = [&](auto tail) {     // tail: the context ends inside the record
                 // scores of positions p0 + i and p0 + 8 + i for heads 2 j, 2 j + 1
                 float s[4] = {0.f, 0.f, 0.f, 0.f};
                 {
@@ -325,7 +328,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) attn_paged_q4_kernel(const __gr
                     const uint4 ka[2] = {lds128(r0 + x0), lds128(r0 + x1)};
                     const uint4 kb[2] = {lds128(r0 + 1024 + x0), lds128(r0 + 1024 + x1)};
                     uint4 z0 = lds128(zb + i4 * 16), z1 = lds128(zb + 128 + i4 * 16);
-                    if (p0 + 16 > sees) {          // rows past the context hold anything; codes are finite
+                    if (tail.value) {              // rows past the context hold anything; codes are finite
                         if (p0 + i4 >= sees) z0 = make_uint4(0u, 0u, 0u, 0u);
                         if (p0 + 8 + i4 >= sees) z1 = make_uint4(0u, 0u, 0u, 0u);
                     }
@@ -364,10 +367,19 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) attn_paged_q4_kernel(const __gr
                     s[1] = fmaf(t[1], back.y, s[1]);
                     s[2] = fmaf(t[2], back.x, s[2]);
                     s[3] = fmaf(t[3], back.y, s[3]);
-                    if (p0 + 16 > sees) {
+                    if (tail.value) {
                         if (p0 + i4 >= sees) s[0] = s[1] = -INFINITY;
                         if (p0 + 8 + i4 >= sees) s[2] = s[3] = -INFINITY;
                     }
+                }
+                // V^T operand: dims on rows, so words of two positions are interleaved by halves
+                const uint32_t va = cb + 2048 + 2 * j4 * 128, x0 = (i4 ^ (2 * j4)) << 4, x1 = (i4 ^ (2 * j4 + 1)) << 4;
+                const uint4 v0 = lds128(va + x0), v1 = lds128(va + 128 + x1);
+                const uint4 v2 = lds128(va + 1024 + x0), v3 = lds128(va + 1152 + x1);
+                uint4 z0 = lds128(zb + 256 + i4 * 16), z1 = lds128(zb + 384 + i4 * 16);
+                if (tail.value) {
+                    if (p0 + i4 >= sees) z0 = make_uint4(0u, 0u, 0u, 0u);
+                    if (p0 + 8 + i4 >= sees) z1 = make_uint4(0u, 0u, 0u, 0u);
                 }
                 const float t0 = fmaxf(s[0], s[2]), t1 = fmaxf(s[1], s[3]);
                 if (__any_sync(0xffffffffu, (t0 - m[0]) * SCORE_SCALE > RESCALE_AT || (t1 - m[1]) * SCORE_SCALE > RESCALE_AT)) {
@@ -403,15 +415,6 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) attn_paged_q4_kernel(const __gr
                 l[0] += p[0] + p[2];
                 l[1] += p[1] + p[3];
                 {
-                    // V^T operand: dims on rows, so words of two positions are interleaved by halves
-                    const uint32_t va = cb + 2048 + 2 * j4 * 128, x0 = (i4 ^ (2 * j4)) << 4, x1 = (i4 ^ (2 * j4 + 1)) << 4;
-                    const uint4 v0 = lds128(va + x0), v1 = lds128(va + 128 + x1);
-                    const uint4 v2 = lds128(va + 1024 + x0), v3 = lds128(va + 1152 + x1);
-                    uint4 z0 = lds128(zb + 256 + i4 * 16), z1 = lds128(zb + 384 + i4 * 16);
-                    if (p0 + 16 > sees) {
-                        if (p0 + i4 >= sees) z0 = make_uint4(0u, 0u, 0u, 0u);
-                        if (p0 + 8 + i4 >= sees) z1 = make_uint4(0u, 0u, 0u, 0u);
-                    }
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
                         const float s0 = sz_step(word_of(z0, g)), s1 = sz_step(word_of(z1, g));
@@ -429,6 +432,9 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) attn_paged_q4_kernel(const __gr
                         mma_m16n8k16(o[g][3], mask_or(hi >> 8, mask, magic), mask_or(hi >> 12, mask, magic), mask_or(hi2 >> 8, mask, magic), mask_or(hi2 >> 12, mask, magic), b0, b1);
                     }
                 }
+                };
+                if (p0 + 16 > sees) record(std::true_type());
+                else record(std::false_type());
                 mbar_arrive(smem_u32(&ss.empty[warp][slot]));
                 if (++slot == DQ_STAGES) {
                     slot = 0;
