@@ -3,15 +3,17 @@
 // and the cache writes that go with them: per-head RMSNorm of q and k, rotation
 // of the first 64 of 256 dims, and the rows of the paged cache in bf16 or 4 bits.
 //
-// One warp per (token, head) row of 256 values, 8 consecutive dims per lane: a
-// row is one coalesced 512-byte access, the mean of squares one warp reduction,
-// and the rotation's partner dim + 32 is the same register four lanes away. A
-// 4-bit group of 64 dims is 8 lanes, whose 8 codes each pack into one 32-bit
-// word; a row's 32 words are one 128-byte line of the record.
+// A (token, head) row of 256 values is one warp's, 8 consecutive dims per lane: a
+// row is one coalesced 512-byte access, the mean of squares one warp reduction, and
+// the rotation's partner dim + 32 is the same register four lanes away. A 4-bit
+// group of 64 dims is 8 lanes, whose 8 codes each pack into one 32-bit word; a
+// row's 32 words are one 128-byte line of the record.
 //
-// The kernels are bound by HBM (or, for a few tokens, by launch latency): per
-// token and head 512 bytes in, 512 (bf16) or 144 (4 bits) out, and the rotation
-// table's 256 bytes per token, shared by its heads through L1.
+// The kernels are bound by HBM (or, for a few tokens, by latency): per token and
+// head 512 bytes in, 512 (bf16) or 144 (4 bits) out, and the rotation table's 256
+// bytes per token. With many tokens a warp takes four rows of one token, whose
+// loads all start before the token's place in the cache is looked up (a chain of
+// dependent reads); with few, one row, so that more SMs share them.
 #include "gdn_async.cuh"
 #include "gdn_kv.cuh"
 
@@ -79,12 +81,12 @@ __device__ __forceinline__ void norm_rotate(float (&x)[8], const float *__restri
 {
     tame = true;
     if (w != nullptr) {
-        float ss = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-        ss = warp_sum(ss);
+        const float s0 = fmaf(x[1], x[1], x[0] * x[0]), s1 = fmaf(x[3], x[3], x[2] * x[2]);
+        const float s2 = fmaf(x[5], x[5], x[4] * x[4]), s3 = fmaf(x[7], x[7], x[6] * x[6]);
+        const float ss = warp_sum((s0 + s1) + (s2 + s3));
         tame = ss < 1e30f;
-        const float r = rsqrtf(fmaf(ss, 1.0f / KV_D, eps));
+        const float v = fmaf(ss, 1.0f / KV_D, eps), r0 = rsqrtf(v);
+        const float r = fmaf(r0 * 0.5f, fmaf(-v * r0, r0, 1.0f), r0);   // one Newton step: the last bit
         float wv[8];
         load8(w + 8 * lane, wv);
 #pragma unroll
@@ -140,8 +142,85 @@ __device__ __forceinline__ void norm_rotate_f64(const float (&in)[8], double (&x
     }
 }
 
-// A real number to bf16 in one rounding: to fp32 with the discarded part kept as
-// a sticky low bit, then to nearest.
+// ---- pairs of fp32 numbers (h + l, |l| at most half a last place of h): 48 bits
+// by Dekker's and Knuth's exact sums and products, several times as fast as 64-bit
+// arithmetic here (2 fused multiply-adds per cycle and SM). For magnitudes whose
+// low parts stay normal; others take the 64-bit form below.
+struct Pair {
+    float h, l;
+};
+__device__ __forceinline__ Pair two_sum(float a, float b)
+{
+    const float s = a + b, bb = s - a;
+    return Pair{s, (a - (s - bb)) + (b - bb)};
+}
+__device__ __forceinline__ Pair quick_sum(float a, float b)   // |a| >= |b|
+{
+    const float s = a + b;
+    return Pair{s, b - (s - a)};
+}
+__device__ __forceinline__ Pair add(Pair x, Pair y)
+{
+    const Pair s = two_sum(x.h, y.h), t = two_sum(x.l, y.l), u = quick_sum(s.h, s.l + t.h);
+    return quick_sum(u.h, u.l + t.l);
+}
+__device__ __forceinline__ Pair mul(Pair x, float f)
+{
+    const float p = x.h * f;
+    return quick_sum(p, fmaf(x.l, f, fmaf(x.h, f, -p)));
+}
+__device__ __forceinline__ Pair mul(Pair x, Pair y)
+{
+    const float p = x.h * y.h;
+    return quick_sum(p, fmaf(x.l, y.h, fmaf(x.h, y.l, fmaf(x.h, y.h, -p))));
+}
+__device__ __forceinline__ Pair shfl_xor(Pair x, int o)
+{
+    return Pair{__shfl_xor_sync(0xffffffffu, x.h, o), __shfl_xor_sync(0xffffffffu, x.l, o)};
+}
+__device__ __forceinline__ bool below(Pair x, Pair y) { return x.h < y.h || (x.h == y.h && x.l < y.l); }
+// To bf16 in one rounding: toward zero to fp32 with the rest as a sticky low bit, then to nearest.
+__device__ __forceinline__ float round_bf16(Pair x)
+{
+    uint32_t u = __float_as_uint(x.h);
+    if (x.l != 0.0f) u = (u - ((x.l > 0.0f) != (x.h > 0.0f) ? 1u : 0u)) | 1u;
+    return to_f(__float2bfloat16_rn(__uint_as_float(u)));
+}
+
+// RMSNorm and rotation of a row in pairs, from the row as it came.
+__device__ __forceinline__ void norm_rotate_pair(const float (&in)[8], Pair (&x)[8], const float *w, const float *rope,
+                                                 float eps, int lane)
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = Pair{in[i], 0.0f};
+    if (w != nullptr) {
+        Pair ss = {0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = add(ss, mul(x[i], in[i]));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) ss = add(ss, shfl_xor(ss, o));
+        const Pair v = add(mul(ss, 1.0f / KV_D), Pair{eps, 0.0f});
+        // v^-1/2: one step of r (1 + e / 2 + 3 e^2 / 8) with e = 1 - v r^2 from the hardware's r
+        const float r0 = rsqrtf(v.h);
+        const Pair t = mul(mul(v, r0), r0);
+        const float e = (1.0f - t.h) - t.l;
+        const Pair r = quick_sum(r0, r0 * fmaf(0.375f * e, e, 0.5f * e));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = mul(mul(r, __ldg(w + 8 * lane + i)), in[i]);
+    }
+    if (rope != nullptr) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const Pair y = shfl_xor(x[i], 4);
+            if (lane < 8) {
+                const float c = __ldg(rope + 8 * (lane & 3) + i), s = __ldg(rope + 32 + 8 * (lane & 3) + i);
+                x[i] = add(mul(x[i], c), mul(y, lane < 4 ? -s : s));
+            }
+        }
+    }
+}
+
+// A real number to bf16 in one rounding, as above.
 __device__ __forceinline__ float round_bf16(double v)
 {
     float f = __double2float_rz(v);
@@ -155,54 +234,100 @@ struct Quant {
 };
 
 // A lane's 8 codes and its group's step and zero, in fp32. `err` bounds the
-// distance of every x of the group from the real value it stands for (0: the x
-// are exact). Returns whether that error can change nothing: the zero and the
-// step round to the same bf16 at both ends of their error intervals, and no
-// code's distance from a rounding border is within the error.
-__device__ __forceinline__ bool quantise_f32(const float (&x)[8], float err, Quant &q)
+// distance of every x of the group from the real value it stands for. Returns
+// whether neither that nor the arithmetic's own error can change anything: the
+// zero and the step round to the same bf16 at both ends of their error intervals,
+// (`range`) and every x is further from a border between two codes than all errors
+// together (those of x - z and its product with 1 / s: 3 roundings of at most 16 s).
+// Rounding to an integer is adding 1.5 2^23; four codes are joined in fp32, whose
+// 24 bits hold them exactly.
+__device__ __forceinline__ bool quantise_f32(const float (&x)[8], float err, Quant &q, bool &range)
 {
-    float lo = x[0], hi = x[0];
-#pragma unroll
-    for (int i = 1; i < 8; ++i) {
-        lo = fminf(lo, x[i]);
-        hi = fmaxf(hi, x[i]);
-    }
+    float lo = fminf(fminf(fminf(x[0], x[1]), fminf(x[2], x[3])), fminf(fminf(x[4], x[5]), fminf(x[6], x[7])));
+    float hi = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) {
         lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
         hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
     }
     q.z = to_f(__float2bfloat16_rn(lo));
-    bool sure = to_f(__float2bfloat16_rn(lo - err)) == to_f(__float2bfloat16_rn(lo + err));
-    const float t = (hi - lo) / 15.0f, et = err * (2.0f / 15.0f) + t * 3e-7f;
+    const float t = (hi - lo) * (1.0f / 15.0f), et = err * (2.0f / 15.0f) + t * 3e-7f;
     q.s = to_f(__float2bfloat16_rn(t));
-    sure = sure && to_f(__float2bfloat16_rn(t - et)) == to_f(__float2bfloat16_rn(t + et));
     q.codes = 0;
     if (hi == lo && err == 0.0f) {                 // a constant group: s = 0
         q.s = 0.0f;
-        return sure;
+        return range = true;
     }
-    sure = sure && q.s > 1e-30f && q.s < 1e30f;    // away from under- and overflow of 1 / s
-    const float inv = 1.0f / q.s;
+    const float inv = __fdividef(1.0f, q.s), half = 0.5f * q.s, magic = 12582912.0f;
+    float nearest = q.s, n[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        // d = x - z and the exact rounding error of that subtraction
+        const float d = x[i] - q.z;
+        n[i] = fminf(fmaxf(fmaf(d, inv, magic), magic), magic + 15.0f) - magic;
+        nearest = fminf(nearest, fabsf(fabsf(fmaf(-q.s, n[i], d)) - half));
+    }
+    const float a = fmaf(4096.0f, n[3], fmaf(256.0f, n[2], fmaf(16.0f, n[1], n[0])));
+    const float b = fmaf(4096.0f, n[7], fmaf(256.0f, n[6], fmaf(16.0f, n[5], n[4])));
+    q.codes = __byte_perm(__float_as_uint(a + 8388608.0f), __float_as_uint(b + 8388608.0f), 0x5410);   // low 16 bits of each
+    range = to_f(__float2bfloat16_rn(lo - err)) == to_f(__float2bfloat16_rn(lo + err)) &&
+            to_f(__float2bfloat16_rn(t - et)) == to_f(__float2bfloat16_rn(t + et)) && q.s > 1e-30f && q.s < 1e30f;
+    return range && nearest > fmaf(q.s, 4e-6f, err);
+}
+
+// Exact x (err = 0) next to a border: the same with every comparison exact in fp32,
+// ties to the even code. Returns whether that was possible.
+__device__ __forceinline__ bool quantise_exact(const float (&x)[8], Quant &q)
+{
+    const float inv = 1.0f / q.s, half = 0.5f * q.s;
+    bool sure = true;
+    q.codes = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        // d = x - z and the exact rounding error of that subtraction, which has to be nothing
         const float d = x[i] - q.z, bb = d - x[i];
-        const float lost = (x[i] - (d - bb)) + (-q.z - bb);
-        const float ed = err + (err > 0.0f || lost != 0.0f ? fabsf(d) * 6e-8f : 0.0f);
+        const bool exact = (x[i] - (d - bb)) + (-q.z - bb) == 0.0f;
         float n = fminf(fmaxf(rintf(d * inv), 0.0f), 15.0f);
-        float r = fmaf(-q.s, n, d);                // exact
-        // the quotient's own error can leave n one off next to a border
-        const float up = r > 0.0f ? 1.0f : -1.0f;
-        const float over = fabsf(r) - 0.5f * q.s;
+        const float r = fmaf(-q.s, n, d), over = fabsf(r) - half;   // both exact
         const bool end = (n == 0.0f && r < 0.0f) || (n == 15.0f && r > 0.0f);
-        if (!end) {
-            if (over > ed || (over == 0.0f && ed == 0.0f && ((int)n & 1))) n += up;
-            else if (!(over < -ed || (over == 0.0f && ed == 0.0f))) sure = false;
-        }
+        if (!end && (over > 0.0f || (over == 0.0f && ((int)n & 1)))) n += r > 0.0f ? 1.0f : -1.0f;
+        sure = sure && (exact || fabsf(over) > 1e-6f * fabsf(d));
         q.codes |= (uint32_t)(int)n << (4 * i);
     }
     return sure;
+}
+
+// The definition in pairs.
+__device__ __noinline__ void quantise_pair(const Pair (&x)[8], Quant &q)
+{
+    Pair lo = x[0], hi = x[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+        if (below(x[i], lo)) lo = x[i];
+        if (below(hi, x[i])) hi = x[i];
+    }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) {
+        const Pair a = shfl_xor(lo, o), b = shfl_xor(hi, o);
+        if (below(a, lo)) lo = a;
+        if (below(hi, b)) hi = b;
+    }
+    q.z = round_bf16(lo);
+    const Pair d = add(hi, Pair{-lo.h, -lo.l});
+    const float t = d.h / 15.0f;
+    q.s = round_bf16(quick_sum(t, (fmaf(-15.0f, t, d.h) + d.l) / 15.0f));
+    q.codes = 0;
+    if (q.s == 0.0f) return;
+    const float inv = 1.0f / q.s, half = 0.5f * q.s;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const Pair a = add(x[i], Pair{-q.z, 0.0f});
+        float n = fminf(fmaxf(rintf(a.h * inv), 0.0f), 15.0f);
+        const Pair r = two_sum(fmaf(-q.s, n, a.h), a.l);
+        const float up = r.h > 0.0f ? 1.0f : -1.0f, over = (fabsf(r.h) - half) + up * r.l;
+        const bool end = (n == 0.0f && r.h < 0.0f) || (n == 15.0f && r.h > 0.0f);
+        if (!end && (over > 0.0f || (over == 0.0f && ((int)n & 1)))) n += up;
+        q.codes |= (uint32_t)(int)n << (4 * i);
+    }
 }
 
 // The definition in 64 bits; a group that holds no finite range reads as NaN.
@@ -239,22 +364,70 @@ __device__ __noinline__ void quantise_f64(const double (&x)[8], Quant &q)
     }
 }
 
-// Warp item: head h of token m; heads 0..15 are queries, 16..17 keys, 18..19
-// values. The kernel is instantiated for the heads a call has: NQ queries (0 or
-// 16) and NKV (0; 2: keys to k_out; 4: keys and values to the cache).
+// One K or V row in registers to its 4-bit place: fp32 where its error can change
+// nothing, else in pairs, or in 64 bits where pairs leave their range.
+__device__ __forceinline__ void store_row_q4(const InputArgs &a, const float (&in)[8], bool isv, const float *rope, int page,
+                                             int head, int off, int lane)
+{
+    float x[8], err = 0.0f, big = 0.0f;
+    bool tame = true;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = in[i];
+    if (!isv && (a.k_w != nullptr || rope != nullptr)) {
+        // Error of a normed and rotated value, in units of 2^-24 relative: the mean of squares 9 (a
+        // tree of 8 additions on rounded squares, and eps), halved by the root, the refined root 1.5,
+        // two products 2: 8; in the rotated group three roundings more, of a sum of two terms that is
+        // at most sqrt 2 times the larger: 16 of `big`, 1e-6.
+        norm_rotate(x, a.k_w, rope, a.eps, lane, big, tame);
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+        err = 1e-6f * big;
+    }
+    float all = 0.0f;                              // of the row as it came; infinities and NaN are the 64-bit form's
+#pragma unroll
+    for (int i = 0; i < 8; ++i) all += fabsf(in[i]);
+    Quant q;
+    bool range, sure = quantise_f32(x, err, q, range) && tame && all < 1e30f;
+    // Exact values that are next to a border are mostly ties, which fp32 can settle.
+    if (err == 0.0f && !__all_sync(0xffffffffu, sure)) sure = sure || (range && all < 1e30f && quantise_exact(x, q));
+    if (!__all_sync(0xffffffffu, sure)) {
+        const bool mid = all < 1e12f && (all > 1e-10f || all == 0.0f) && big < 1e12f && (big > 1e-10f || big == 0.0f) &&
+                         q.s < 1e12f && (q.s > 1e-12f || q.s == 0.0f);
+        if (__all_sync(0xffffffffu, mid)) {
+            Pair xp[8];
+            norm_rotate_pair(in, xp, isv ? nullptr : a.k_w, isv ? nullptr : rope, a.eps, lane);
+            quantise_pair(xp, q);
+        } else {
+            double xd[8];
+            norm_rotate_f64(in, xd, isv ? nullptr : a.k_w, isv ? nullptr : rope, a.eps, lane);
+            quantise_f64(xd, q);
+        }
+    }
+    unsigned char *rec = static_cast<unsigned char *>(a.cache_k) + record_of(a.b, page, head, off);
+    const int r = off & (REC_ROWS - 1), g = lane >> 3, c = lane & 7;
+    *reinterpret_cast<uint32_t *>(rec + (isv ? REC_V : 0u) + r * 128 + c * 16 + g * 4) = q.codes;
+    if (c == 0)
+        *reinterpret_cast<uint32_t *>(rec + (isv ? REC_VSZ : REC_KSZ) + r * 16 + g * 4) =
+            (__float_as_uint(q.s) >> 16) | (__float_as_uint(q.z) & 0xFFFF0000u);
+}
+
+// Few rows: one warp per row. Heads 0..15 of a token are queries (NQ 0 or 16), then
+// NKV rows: 2, its keys for k_out, or 4, its keys and values for the cache.
 template <typename TI, typename TO, int NQ, int NKV, bool Q4>
-__global__ void __launch_bounds__(KV_WARPS * 32) attn_input_kernel(const InputArgs a)
+__global__ void __launch_bounds__(KV_WARPS * 32) attn_input_few_kernel(const InputArgs a)
 {
     constexpr int NH = NQ + NKV;
     const int lane = threadIdx.x & 31;
-    const long long item = (long long)blockIdx.x * KV_WARPS + (threadIdx.x >> 5);
-    const int m = (int)(item / NH), h = (int)(item % NH) + (NQ ? 0 : KV_HQ);
+    const int item = blockIdx.x * KV_WARPS + (threadIdx.x >> 5);   // below 2^31: the host sends more rows to the other kernel
+    const int m = item / NH, u = item % NH;
     grid_dep_wait();
     grid_dep_launch();
     if (m >= a.M) return;
-    const bool isq = h < KV_HQ, isv = h >= KV_HQ + KV_H;
-    const int hh = isq ? h : (isv ? h - KV_HQ - KV_H : h - KV_HQ);
-
+    const bool isq = u < NQ, isv = u >= NQ + KV_H;
+    const int h = isq ? u : (isv ? u - NQ - KV_H : u - NQ);
+    const RowSrc src = isq ? a.q : (isv ? a.v : a.k);
+    float x[8];
+    load8_in(static_cast<const TI *>(src.p) + m * src.row + h * src.head + 8 * lane, x);
     TokenPlace at = {0, 0};
     if (NKV == 4) {
         at = token_place(a.b, m, lane);
@@ -266,69 +439,192 @@ __global__ void __launch_bounds__(KV_WARPS * 32) attn_input_kernel(const InputAr
         if ((unsigned)rp >= (unsigned)a.n_pos) return;
         rope = a.rope + (size_t)rp * GDN_ATTN_ROT_DIM;
     }
-    const RowSrc &src = isq ? a.q : (isv ? a.v : a.k);
-    float x[8];
-    load8_in(static_cast<const TI *>(src.p) + m * src.row + hh * src.head + 8 * lane, x);
-
-    if (isq || NKV == 2) {
-        float big;
-        bool tame;
-        norm_rotate(x, isq ? a.q_w : a.k_w, rope, a.eps, lane, big, tame);
-        TO *out = isq ? static_cast<TO *>(a.q_out) + ((size_t)m * KV_HQ + hh) * KV_D
-                      : static_cast<TO *>(a.k_out) + ((size_t)m * KV_H + hh) * KV_D;
-        store8(out + 8 * lane, x);
-        return;
-    }
-    const int page = cache_page(a.b, at.seq, at.pos);
-    if (page < 0) return;
-    const int off = at.pos & (a.b.page - 1);
-    if (!Q4) {
+    if (NKV == 4 && !isq) {
+        const int page = cache_page(a.b, at.seq, at.pos), off = at.pos & (a.b.page - 1);
+        if (page < 0) return;
+        if (Q4) {
+            store_row_q4(a, x, isv, rope, page, h, off, lane);
+            return;
+        }
         float big;
         bool tame;
         if (!isv) norm_rotate(x, a.k_w, rope, a.eps, lane, big, tame);
-        bf16 *dst = static_cast<bf16 *>(isv ? a.cache_v : a.cache_k) + row_bf16(a.b, page, hh, off);
-        store8(dst + 8 * lane, x);
+        store8(static_cast<bf16 *>(isv ? a.cache_v : a.cache_k) + row_bf16(a.b, page, h, off) + 8 * lane, x);
         return;
     }
-    float in[8], err = 0.0f;
-    bool sure = true;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) in[i] = x[i];
-    if (!isv && (a.k_w != nullptr || rope != nullptr)) {
-        // Error of a normed and rotated value: the mean of squares (8 + 5
-        // additions, halved by the root), rsqrt (2 ulp), two products, and the
-        // rotation's two products and one sum, each relative to `big`: below
-        // 7e-7 big in all. 2e-6 big leaves a factor of two and a half.
-        float big;
-        norm_rotate(x, a.k_w, rope, a.eps, lane, big, sure);
-#pragma unroll
-        for (int o = 4; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-        err = 2e-6f * big;
-    }
-    float far = 0.0f;                              // infinities and NaN are the 64-bit form's
-#pragma unroll
-    for (int i = 0; i < 8; ++i) far += fabsf(x[i]);
-    Quant q;
-    sure = quantise_f32(x, err, q) && sure && far < 1e30f;
-    if (!__all_sync(0xffffffffu, sure)) {
-        double xd[8];
-        norm_rotate_f64(in, xd, isv ? nullptr : a.k_w, isv ? nullptr : rope, a.eps, lane);
-        quantise_f64(xd, q);
-    }
-    unsigned char *rec = static_cast<unsigned char *>(a.cache_k) + record_of(a.b, page, hh, off);
-    const int r = off & (REC_ROWS - 1), g = lane >> 3, c = lane & 7;
-    *reinterpret_cast<uint32_t *>(rec + (isv ? REC_V : 0u) + r * 128 + c * 16 + g * 4) = q.codes;
-    if (c == 0)
-        *reinterpret_cast<uint32_t *>(rec + (isv ? REC_VSZ : REC_KSZ) + r * 16 + g * 4) =
-            (__float_as_uint(q.s) >> 16) | (__float_as_uint(q.z) & 0xFFFF0000u);
+    float big;
+    bool tame;
+    norm_rotate(x, isq ? a.q_w : a.k_w, rope, a.eps, lane, big, tame);
+    store8(isq ? static_cast<TO *>(a.q_out) + ((size_t)m * KV_HQ + h) * KV_D + 8 * lane
+               : static_cast<TO *>(a.k_out) + ((size_t)m * KV_H + h) * KV_D + 8 * lane, x);
 }
+
+// Many rows: a fixed grid whose warps each walk a stretch of tokens with one unit
+// of heads (QR queries, or the token's keys and values; one of those in 4 bits).
+// A warp looks up the places of 32 tokens at a time, one per lane, and starts the
+// next token's rows and rotation before it works on the current one's.
+template <typename TI> struct Raw8;
+template <> struct Raw8<bf16> {
+    uint4 v;
+    __device__ __forceinline__ void load(const bf16 *p) { v = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ void get(float (&x)[8]) const
+    {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __uint_as_float((i & 1) ? (w[i >> 1] & 0xFFFF0000u) : (w[i >> 1] << 16));
+    }
+};
+template <> struct Raw8<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float *p)
+    {
+        a = reinterpret_cast<const float4 *>(p)[0];
+        b = reinterpret_cast<const float4 *>(p)[1];
+    }
+    __device__ __forceinline__ void get(float (&x)[8]) const
+    {
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    }
+};
+
+// norm_rotate with the weights and the rotation (lanes 0-7's) in registers.
+__device__ __forceinline__ void norm_rotate_regs(float (&x)[8], bool norm, const float (&w)[8], bool rot, const float (&c)[8],
+                                                 const float (&s)[8], float eps, int lane)
+{
+    if (norm) {
+        float ss = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+        ss = warp_sum(ss);
+        const float r = rsqrtf(fmaf(ss, 1.0f / KV_D, eps));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
+    }
+    if (rot) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float y = __shfl_xor_sync(0xffffffffu, x[i], 4);
+            x[i] = lane < 8 ? fmaf(x[i], c[i], (lane < 4 ? -y : y) * s[i]) : x[i];
+        }
+    }
+}
+
+constexpr int QR = 4;                             // queries per warp and token
+
+// One unit over the tokens [m0, m1): N rows of each, `first` the first of them
+// (queries 0..15; k0, k1, v0, v1).
+template <typename TI, typename TO, int NKV, bool Q4, bool ISQ, int N>
+__device__ __forceinline__ void walk_tokens(const InputArgs &a, int first, int m0, int m1, int lane)
+{
+    const bool rot = a.rope != nullptr && !(NKV == 4 && !ISQ && N == 1 && first >= KV_H && !Q4);
+    const float *wp = ISQ ? a.q_w : a.k_w;
+    float w[8] = {}, c[8] = {}, s[8] = {};
+    if (wp != nullptr) load8(wp + 8 * lane, w);
+    Raw8<TI> cur[N], nxt[N];
+    auto load = [&](Raw8<TI> (&raw)[N], int m) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int r = first + i;
+            const RowSrc src = ISQ ? a.q : (r < KV_H ? a.k : a.v);
+            raw[i].load(static_cast<const TI *>(src.p) + m * src.row + (ISQ || r < KV_H ? r : r - KV_H) * src.head + 8 * lane);
+        }
+    };
+    load(nxt, m0);
+    for (int base = m0; base < m1; base += 32) {
+        // places of 32 tokens, one per lane: rotation row (-1: the token is padding), page (-1: none), row in the page
+        const int mine = min(base + lane, m1 - 1);
+        int seq = 0, pos = 0, page = 0, rp = 0;
+        if (NKV == 4) {
+            seq = mine < a.b.B || a.b.cu != nullptr ? mine : -1;
+            if (a.b.cu != nullptr) {               // the number of entries cu[1..B] at or below the row
+                int lo = 0, hi = a.b.B;
+                while (lo < hi) {
+                    const int mid = (lo + hi + 1) >> 1;
+                    if (__ldg(a.b.cu + mid) <= mine) lo = mid;
+                    else hi = mid - 1;
+                }
+                seq = lo < a.b.B ? lo : -1;
+            }
+            if (seq >= 0) {
+                pos = __ldg(a.b.ctx + seq) - (a.b.cu != nullptr ? __ldg(a.b.cu + seq + 1) - mine : 1);
+                page = ISQ ? 0 : cache_page(a.b, seq, pos);
+            }
+        }
+        if (a.rope != nullptr) rp = NKV == 4 && a.positions == nullptr ? pos : __ldg(a.positions + mine);
+        if (seq < 0 || (a.rope != nullptr && (unsigned)rp >= (unsigned)a.n_pos)) rp = -1;
+        const int n = min(32, m1 - base);
+        float cn[8] = {}, sn[8] = {};
+        auto turn = [&](int k) {                   // the rotation of token base + k
+            const int r = __shfl_sync(0xffffffffu, rp, k);
+            if (rot && r >= 0 && lane < 8) {
+                const float *row = a.rope + (size_t)r * GDN_ATTN_ROT_DIM + 8 * (lane & 3);
+                load8(row, cn);
+                load8(row + 32, sn);
+            }
+        };
+        turn(0);
+        for (int k = 0; k < n; ++k) {
+            const int m = base + k;
+#pragma unroll
+            for (int i = 0; i < N; ++i) cur[i] = nxt[i];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                c[i] = cn[i];
+                s[i] = sn[i];
+            }
+            if (m + 1 < m1) load(nxt, m + 1);
+            if (k + 1 < n) turn(k + 1);
+            const int r = __shfl_sync(0xffffffffu, rp, k), pg = __shfl_sync(0xffffffffu, page, k);
+            const int off = __shfl_sync(0xffffffffu, pos, k) & (a.b.page - 1);
+            if (r < 0 || pg < 0) continue;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int row = first + i, h = ISQ || row < KV_H ? row : row - KV_H;
+                const bool isv = !ISQ && row >= KV_H;
+                float x[8];
+                cur[i].get(x);
+                if (Q4 && !ISQ) {
+                    store_row_q4(a, x, isv, a.rope != nullptr ? a.rope + (size_t)r * GDN_ATTN_ROT_DIM : nullptr, pg, h, off, lane);
+                    continue;
+                }
+                if (!isv) norm_rotate_regs(x, wp != nullptr, w, rot, c, s, a.eps, lane);
+                if (ISQ) store8(static_cast<TO *>(a.q_out) + ((size_t)m * KV_HQ + h) * KV_D + 8 * lane, x);
+                else if (NKV == 2) store8(static_cast<TO *>(a.k_out) + ((size_t)m * KV_H + h) * KV_D + 8 * lane, x);
+                else store8(static_cast<bf16 *>(isv ? a.cache_v : a.cache_k) + row_bf16(a.b, pg, h, off) + 8 * lane, x);
+            }
+        }
+    }
+}
+
+template <typename TI, typename TO, int NQ, int NKV, bool Q4>
+__global__ void __launch_bounds__(KV_WARPS * 32, 2) attn_input_kernel(const InputArgs a)
+{
+    constexpr int UQ = NQ / QR, UK = Q4 ? NKV : NKV > 0 ? 1 : 0, U = UQ + UK;
+    const int lane = threadIdx.x & 31, gw = blockIdx.x * KV_WARPS + (threadIdx.x >> 5);
+    const int stretches = (int)gridDim.x * KV_WARPS / U, at = gw / U, u = gw % U;
+    grid_dep_wait();
+    grid_dep_launch();
+    const int per = (a.M + stretches - 1) / stretches;
+    const int m0 = min((long long)at * per, (long long)a.M), m1 = min(m0 + per, a.M);
+    if (at >= stretches || m0 >= m1) return;
+    if (u < UQ) walk_tokens<TI, TO, NKV, Q4, true, QR>(a, u * QR, m0, m1, lane);
+    else if (Q4) walk_tokens<TI, TO, NKV, Q4, false, 1>(a, u - UQ, m0, m1, lane);
+    else if (NKV > 0) walk_tokens<TI, TO, NKV, Q4, false, NKV == 4 ? 4 : 2>(a, 0, m0, m1, lane);
+}
+
+// Rows from which the walking kernel is used: two waves of one-row warps, 48 on each
+// of 152 SMs.
+constexpr long long FEW_ROWS = 2 * 152 * 48;
 
 template <typename TI, typename TO, int NQ, int NKV, bool Q4>
 static cudaError_t launch_input(const InputArgs &a, cudaStream_t s)
 {
-    const long long items = (long long)a.M * (NQ + NKV);
-    return launch_pdl(attn_input_kernel<TI, TO, NQ, NKV, Q4>, dim3((unsigned)((items + KV_WARPS - 1) / KV_WARPS)),
-                      dim3(KV_WARPS * 32), 0, s, a);
+    const long long rows = (long long)a.M * (NQ + NKV);
+    if (rows <= FEW_ROWS)
+        return launch_pdl(attn_input_few_kernel<TI, TO, NQ, NKV, Q4>, dim3((unsigned)((rows + KV_WARPS - 1) / KV_WARPS)),
+                          dim3(KV_WARPS * 32), 0, s, a);
+    return launch_pdl(attn_input_kernel<TI, TO, NQ, NKV, Q4>, dim3(2 * 152), dim3(KV_WARPS * 32), 0, s, a);
 }
 
 cudaError_t launch_qk_norm_rope(const gdn_attn_params *p, const void *q, long long q_row, long long q_head,
@@ -363,50 +659,71 @@ cudaError_t launch_kv_append(const gdn_attn_params *p, const gdn_paged_batch *b,
 }
 
 // Reads rows back: the same warp layout, values z + s c in fp32 (s c is exact:
-// 8 x 4 bits), one rounding to the output type.
-template <typename TO, bool Q4>
+// 8 x 4 bits), one rounding to the output type. R rows of k0, k1, v0, v1 per warp.
+template <typename TO, bool Q4, int R>
 __global__ void __launch_bounds__(KV_WARPS * 32) kv_gather_kernel(const PagedBatch b, const void *ck, const void *cv,
                                                                   TO *k_out, TO *v_out)
 {
     const int lane = threadIdx.x & 31;
     const long long item = (long long)blockIdx.x * KV_WARPS + (threadIdx.x >> 5);
-    const int m = (int)(item >> 2), h = (int)item & 1;
-    const bool isv = (item & 2) != 0;
+    const int m = (int)(item / (4 / R)), row0 = (int)(item % (4 / R)) * R;
     grid_dep_wait();
     grid_dep_launch();
-    TO *out = isv ? v_out : k_out;
-    if (m >= b.M || out == nullptr) return;
+    if (m >= b.M) return;
     const TokenPlace at = token_place(b, m, lane);
     if (at.seq < 0) return;
     const int page = cache_page(b, at.seq, at.pos), off = at.pos & (b.page - 1);
-    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (page >= 0) {
+    const int r = off & (REC_ROWS - 1), g = lane >> 3, c = lane & 7;
+    uint4 raw[R];
+    uint32_t sz[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const bool isv = row0 + i >= KV_H;
+        const int h = (row0 + i) & 1;
+        raw[i] = make_uint4(0u, 0u, 0u, 0u);
+        sz[i] = 0;
+        if (page < 0 || (isv ? v_out : k_out) == nullptr) continue;
         if (!Q4) {
-            load8(static_cast<const bf16 *>(isv ? cv : ck) + row_bf16(b, page, h, off) + 8 * lane, x);
+            raw[i] = *(reinterpret_cast<const uint4 *>(static_cast<const bf16 *>(isv ? cv : ck) + row_bf16(b, page, h, off)) + lane);
         } else {
             const unsigned char *rec = static_cast<const unsigned char *>(ck) + record_of(b, page, h, off);
-            const int r = off & (REC_ROWS - 1), g = lane >> 3, c = lane & 7;
-            const uint32_t w = *reinterpret_cast<const uint32_t *>(rec + (isv ? REC_V : 0u) + r * 128 + c * 16 + g * 4);
-            const uint32_t sz = *reinterpret_cast<const uint32_t *>(rec + (isv ? REC_VSZ : REC_KSZ) + r * 16 + g * 4);
-            const float s = __uint_as_float(sz << 16), z = __uint_as_float(sz & 0xFFFF0000u);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = fmaf(s, (float)((w >> (4 * i)) & 15u), z);
+            raw[i].x = *reinterpret_cast<const uint32_t *>(rec + (isv ? REC_V : 0u) + r * 128 + c * 16 + g * 4);
+            sz[i] = *reinterpret_cast<const uint32_t *>(rec + (isv ? REC_VSZ : REC_KSZ) + r * 16 + g * 4);
         }
     }
-    store8(out + ((size_t)m * KV_H + h) * KV_D + 8 * lane, x);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        TO *out = row0 + i >= KV_H ? v_out : k_out;
+        if (out == nullptr) continue;
+        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+        const float s = __uint_as_float(sz[i] << 16), z = __uint_as_float(sz[i] & 0xFFFF0000u);
+        float x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            x[k] = Q4 ? fmaf(s, (float)((w[0] >> (4 * k)) & 15u), z)
+                      : __uint_as_float((k & 1) ? (w[k >> 1] & 0xFFFF0000u) : (w[k >> 1] << 16));
+        store8(out + ((size_t)m * KV_H + ((row0 + i) & 1)) * KV_D + 8 * lane, x);
+    }
+}
+
+template <typename TO, bool Q4>
+static cudaError_t launch_gather(const PagedBatch &b, const gdn_kv_cache *c, void *k_out, void *v_out, cudaStream_t s)
+{
+    const bool few = (long long)b.M * 2 * KV_H <= FEW_ROWS;
+    const long long items = (long long)b.M * (few ? 2 * KV_H : 1);
+    const dim3 grid((unsigned)((items + KV_WARPS - 1) / KV_WARPS)), block(KV_WARPS * 32);
+    const void *ck = c->k, *cv = c->v;
+    return few ? launch_pdl(kv_gather_kernel<TO, Q4, 1>, grid, block, 0, s, b, ck, cv, (TO *)k_out, (TO *)v_out)
+               : launch_pdl(kv_gather_kernel<TO, Q4, 4>, grid, block, 0, s, b, ck, cv, (TO *)k_out, (TO *)v_out);
 }
 
 cudaError_t launch_kv_gather(const gdn_paged_batch *b, const gdn_kv_cache *c, void *k_out, void *v_out,
                              gdn_dtype out_dt, cudaStream_t s)
 {
     const PagedBatch pb = paged_batch(*b, *c);
-    const dim3 grid((unsigned)(((long long)b->M * 2 * KV_H + KV_WARPS - 1) / KV_WARPS)), block(KV_WARPS * 32);
-    const void *ck = c->k, *cv = c->v;
     if (c->format == GDN_KV_Q4)
-        return out_dt == GDN_F32 ? launch_pdl(kv_gather_kernel<float, true>, grid, block, 0, s, pb, ck, cv, (float *)k_out, (float *)v_out)
-                                 : launch_pdl(kv_gather_kernel<bf16, true>, grid, block, 0, s, pb, ck, cv, (bf16 *)k_out, (bf16 *)v_out);
-    return out_dt == GDN_F32 ? launch_pdl(kv_gather_kernel<float, false>, grid, block, 0, s, pb, ck, cv, (float *)k_out, (float *)v_out)
-                             : launch_pdl(kv_gather_kernel<bf16, false>, grid, block, 0, s, pb, ck, cv, (bf16 *)k_out, (bf16 *)v_out);
+        return out_dt == GDN_F32 ? launch_gather<float, true>(pb, c, k_out, v_out, s) : launch_gather<bf16, true>(pb, c, k_out, v_out, s);
+    return out_dt == GDN_F32 ? launch_gather<float, false>(pb, c, k_out, v_out, s) : launch_gather<bf16, false>(pb, c, k_out, v_out, s);
 }
 
 }  // namespace gdn
