@@ -597,8 +597,12 @@ __device__ __forceinline__ void walk_tokens(const InputArgs &a, int first, int m
     }
 }
 
+// CTAs per SM: two hold four queries a warp and the next token's; keys and values
+// alone into 4 bits are bound by instructions, and hide them better with more warps.
+constexpr int input_ctas(int nq, bool q4) { return nq == 0 && q4 ? 3 : 2; }
+
 template <typename TI, typename TO, int NQ, int NKV, bool Q4>
-__global__ void __launch_bounds__(KV_WARPS * 32, 2) attn_input_kernel(const InputArgs a)
+__global__ void __launch_bounds__(KV_WARPS * 32, input_ctas(NQ, Q4)) attn_input_kernel(const InputArgs a)
 {
     constexpr int UQ = NQ / QR, UK = Q4 ? NKV : NKV > 0 ? 1 : 0, U = UQ + UK;
     const int lane = threadIdx.x & 31, gw = blockIdx.x * KV_WARPS + (threadIdx.x >> 5);
@@ -624,7 +628,8 @@ static cudaError_t launch_input(const InputArgs &a, cudaStream_t s)
     if (rows <= FEW_ROWS)
         return launch_pdl(attn_input_few_kernel<TI, TO, NQ, NKV, Q4>, dim3((unsigned)((rows + KV_WARPS - 1) / KV_WARPS)),
                           dim3(KV_WARPS * 32), 0, s, a);
-    return launch_pdl(attn_input_kernel<TI, TO, NQ, NKV, Q4>, dim3(2 * 152), dim3(KV_WARPS * 32), 0, s, a);
+    return launch_pdl(attn_input_kernel<TI, TO, NQ, NKV, Q4>, dim3(input_ctas(NQ, Q4) * 152), dim3(KV_WARPS * 32),
+                      0, s, a);
 }
 
 cudaError_t launch_qk_norm_rope(const gdn_attn_params *p, const void *q, long long q_row, long long q_head,
