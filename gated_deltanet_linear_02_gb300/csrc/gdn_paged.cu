@@ -17,8 +17,9 @@
 //  - warp 0, TMA producer: 32 KiB stages of 128 positions x 128 dims (keys low,
 //    high, values low, high), one box per page and 64 dims, in a ring of five;
 //    the next tile's keys ahead of this tile's values, as the MMAs use them;
-//  - warp 1, one lane, MMA issuer: S of unit u + 1 is issued before O += P V of
-//    unit u, so the tensor core has work while P is formed;
+//  - warps 1 and 2, one lane each, issue the two products: each waits for its own
+//    operands while the other's instructions run (one issuer for both left the
+//    tensor core idle for half of every unit: 2.6 us instead of 1.6);
 //  - warps 4-7, one thread per query row: softmax, rescale, and the epilogue
 //    (normalise and gate, or store the piece's unnormalised output).
 // Tensor memory: two S buffers (P over their first half) and O, all 512 columns.
@@ -48,7 +49,7 @@ constexpr uint32_t FA_S = 0, FA_O = 256;          // tensor memory columns: S bu
 
 struct FaSmall {
     uint64_t full[FA_STAGES], empty[FA_STAGES];
-    uint64_t q_full, q_empty, s_full[2], p_full[2], pv_done[2], o_empty, done;
+    uint64_t q_full, q_empty, s_full[2], p_full[2], pv_done[2], o_empty, done[2];
     long long scan[FA_THREADS / 32 + 1];
     PagedStart start;
     uint32_t tmem;
@@ -80,15 +81,15 @@ __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_
             mbar_init(smem_u32(&ss.s_full[i]), 1);
             mbar_init(smem_u32(&ss.p_full[i]), 128);
             mbar_init(smem_u32(&ss.pv_done[i]), 1);
+            mbar_init(smem_u32(&ss.done[i]), 1);
         }
         mbar_init(smem_u32(&ss.q_full), 1);
         mbar_init(smem_u32(&ss.q_empty), 1);
         mbar_init(smem_u32(&ss.o_empty), 128);
-        mbar_init(smem_u32(&ss.done), 1);
         ss.abort = 0;
         fence_mbar_init();
     }
-    if (warp == 2) {
+    if (warp == 3) {
         tc::tmem_alloc(smem_u32(&ss.tmem), 512);
         tc::tmem_relinquish();
     }
@@ -177,67 +178,76 @@ __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_
                 if (piece > 0) mbar_wait_bounded(smem_u32(&ss.q_full), (piece - 1) & 1);
             }
         } else if (warp == 1) {
-            // ---- MMA issuer
+            // ---- issuer of S(u) = Q K^T
             if (lane == 0) {
-                const uint32_t id_s = tc::instr_desc(tc::FMT_BF16, 128, PG_TILE);
-                const uint32_t id_o = id_s | tc::IDESC_B_MN;
-                UnitWalk qk, pv;
-                qk.begin(a, st, count);
-                pv = qk;
-                uint32_t i = 0, piece_q = 0, piece_o = 0;
+                const uint32_t id = tc::instr_desc(tc::FMT_BF16, 128, PG_TILE);
+                UnitWalk w;
+                w.begin(a, st, count);
+                uint32_t i = 0, piece = 0;
                 bool ok = true;
-                auto scores = [&](uint32_t u) {    // S(u) = Q K^T
-                    if (qk.j == 0) {
-                        ok = mbar_wait_bounded(smem_u32(&ss.q_full), piece_q & 1);
-                        ++piece_q;
-                    }
+                for (uint32_t u = 0; ok; ++u) {
+                    if (w.j == 0) ok = mbar_wait_bounded(smem_u32(&ss.q_full), piece++ & 1);
+                    // the buffer holds P of unit u - 2 until its product is complete
+                    if (u >= 2) ok = ok && mbar_wait_bounded(smem_u32(&ss.pv_done[u & 1]), ((u - 2) >> 1) & 1);
+                    if (u == 1) i = 2;
                     for (int half = 0; half < 2 && ok; ++half, ++i) {
-                        ok = wait_full(i);
+                        ok = wait_full(i) && !aborted;
                         if (!ok) break;
                         tc::fence_after_sync();
+#pragma unroll
                         for (int kk = 0; kk < 8; ++kk)
                             tc::mma_f16(tm + FA_S + (u & 1) * 128,
                                         tc::sw128_desc(sb + FA_Q + (2 * half + (kk >> 2)) * FA_BOX + (kk & 3) * 32),
-                                        tc::sw128_desc(stage(i) + (kk >> 2) * FA_BOX + (kk & 3) * 32), id_s,
+                                        tc::sw128_desc(stage(i) + (kk >> 2) * FA_BOX + (kk & 3) * 32), id,
                                         half + kk > 0 ? 1u : 0u);
                         tc::mma_commit(smem_u32(&ss.empty[i % FA_STAGES]));
                     }
-                    if (!ok) return;
-                    tc::mma_commit(smem_u32(&ss.s_full[u & 1]));
-                    if (qk.j + 1 == qk.w.len) tc::mma_commit(smem_u32(&ss.q_empty));
-                };
-                scores(0);
-                for (uint32_t u = 0; ok; ++u) {
-                    const bool more = !qk.last(a);
-                    if (more) {
-                        qk.next(a);
-                        scores(u + 1);
-                        if (!ok) break;
-                    }
-                    if (pv.j == 0) {
-                        if (piece_o > 0) ok = mbar_wait_bounded(smem_u32(&ss.o_empty), (piece_o - 1) & 1);
-                        ++piece_o;
-                    }
-                    ok = ok && mbar_wait_bounded(smem_u32(&ss.p_full[u & 1]), (u >> 1) & 1) && !aborted;
                     if (!ok) break;
+                    tc::mma_commit(smem_u32(&ss.s_full[u & 1]));
+                    if (w.j + 1 == w.w.len) tc::mma_commit(smem_u32(&ss.q_empty));
+                    if (w.last(a)) break;
+                    w.next(a);
+                    if (u > 0) i += 2;             // the values of unit u - 1 come between
+                }
+                if (!ok) ss.abort = 1;
+                tc::mma_commit(smem_u32(&ss.done[0]));   // every MMA completes before tensor memory is freed
+                mbar_wait_bounded(smem_u32(&ss.done[0]), 0u);
+            }
+        } else if (warp == 2) {
+            // ---- issuer of O += P(u) V
+            if (lane == 0) {
+                const uint32_t id = tc::instr_desc(tc::FMT_BF16, 128, 128) | tc::IDESC_B_MN;
+                UnitWalk w;
+                w.begin(a, st, count);
+                uint32_t piece = 0;
+                bool ok = true;
+                for (uint32_t u = 0; ok; ++u) {
+                    const bool last = w.last(a);
+                    uint32_t i = last ? 4 * u + 2 : 4 * u + 4;   // the keys of unit u + 1 come before
+                    if (w.j == 0) {                // O of the piece before has been read
+                        if (piece > 0) ok = mbar_wait_bounded(smem_u32(&ss.o_empty), (piece - 1) & 1);
+                        ++piece;
+                    }
+                    ok = ok && mbar_wait_bounded(smem_u32(&ss.p_full[u & 1]), (u >> 1) & 1);
                     for (int half = 0; half < 2 && ok; ++half, ++i) {
-                        ok = wait_full(i);
+                        ok = wait_full(i) && !aborted;
                         if (!ok) break;
                         tc::fence_after_sync();
+#pragma unroll
                         for (int kk = 0; kk < 8; ++kk)
                             tc::mma_f16_tmem_a(tm + FA_O + half * 128, tm + FA_S + (u & 1) * 128 + kk * 8,
-                                               tc::sw128_mn_desc(stage(i) + kk * 2048, FA_BOX), id_o,
-                                               pv.j + kk > 0 ? 1u : 0u);
+                                               tc::sw128_mn_desc(stage(i) + kk * 2048, FA_BOX), id,
+                                               w.j + kk > 0 ? 1u : 0u);
                         tc::mma_commit(smem_u32(&ss.empty[i % FA_STAGES]));
                     }
                     if (!ok) break;
                     tc::mma_commit(smem_u32(&ss.pv_done[u & 1]));
-                    if (!more) break;
-                    pv.next(a);
+                    if (last) break;
+                    w.next(a);
                 }
                 if (!ok) ss.abort = 1;
-                tc::mma_commit(smem_u32(&ss.done));    // every MMA completes before tensor memory is freed
-                mbar_wait_bounded(smem_u32(&ss.done), 0u);
+                tc::mma_commit(smem_u32(&ss.done[1]));
+                mbar_wait_bounded(smem_u32(&ss.done[1]), 0u);
             }
         } else if (warp >= 4) {
             // ---- softmax and epilogue: thread r is query row r of the item
@@ -247,7 +257,7 @@ __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_
             uint32_t u = 0;
             bool ok = true;
             // O += P V of unit v is complete. Two barriers in turn: S of unit u, which this thread has
-            // seen, was issued after the product of unit u - 2, so each is one phase behind at most.
+            // seen, was issued after that of unit u - 2 completed, so each is one phase behind at most.
             auto wait_pv = [&](uint32_t v) { return mbar_wait_bounded(smem_u32(&ss.pv_done[v & 1]), (v >> 1) & 1); };
             for (;;) {
                 const int rows = KV_G * w.tokens(a), sees = tile_sees(a, w.t, w.tile);
@@ -404,7 +414,7 @@ __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_
     }
     tc::fence_before_sync();
     __syncthreads();
-    if (warp == 2) {
+    if (warp == 3) {
         tc::fence_after_sync();
         tc::tmem_dealloc(tm, 512);
     }
