@@ -13,15 +13,16 @@
 // 2^8, l and O lose nothing in fp32, and the rescale, a round trip of the whole
 // accumulator, happens a few times per context instead of at every tile.
 //
-// Roles in a CTA (one per SM, 256 threads):
+// Roles in a CTA (one per SM, 384 threads):
 //  - warp 0, TMA producer: 32 KiB stages of 128 positions x 128 dims (keys low,
-//    high, values low, high), one box per page and 64 dims, in a ring of five;
+//    high, values low, high), one box per page and 64 dims, in a ring of four;
 //    the next tile's keys ahead of this tile's values, as the MMAs use them;
 //  - warps 1 and 2, one lane each, issue the two products: each waits for its own
 //    operands while the other's instructions run (one issuer for both left the
 //    tensor core idle for half of every unit: 2.6 us instead of 1.6);
-//  - warps 4-7, one thread per query row: softmax, rescale, and the epilogue
-//    (normalise and gate, or store the piece's unnormalised output).
+//  - warps 4-11, two threads per query row, each with half of a tile's positions
+//    and half of the output's dims: softmax, rescale, and the epilogue (normalise
+//    and gate, or store the piece's unnormalised output).
 // Tensor memory: two S buffers (P over their first half) and O, all 512 columns.
 //
 // Bound: for one token per sequence by HBM (1 KiB of keys and values per position
@@ -38,24 +39,29 @@ namespace gdn {
 
 __device__ unsigned int g_paged_error;            // GDN_ERR_TIMEOUT if a bounded wait gave up
 
-constexpr int FA_THREADS = 256;
-constexpr int FA_STAGES = 5;
+constexpr int FA_THREADS = 384;
+constexpr int FA_STAGES = 4;
 constexpr uint32_t FA_BOX = PG_TILE * 128;        // 128 rows x 64 dims of bf16: 16 KiB
 constexpr uint32_t FA_STAGE_BYTES = 2 * FA_BOX;   // 128 dims: 32 KiB
 constexpr uint32_t FA_Q = 0;                      // Q: 4 boxes of 64 dims
 constexpr uint32_t FA_RING = 4 * FA_BOX;
-constexpr uint32_t FA_SMALL = FA_RING + FA_STAGES * FA_STAGE_BYTES;
+constexpr uint32_t FA_EPI = FA_RING + FA_STAGES * FA_STAGE_BYTES;   // 4 KiB for each softmax warp
+constexpr uint32_t FA_SMALL = FA_EPI + 8 * 4096;
 constexpr uint32_t FA_S = 0, FA_O = 256;          // tensor memory columns: S buffers at 0 and 128, O at 256
 
 struct FaSmall {
     uint64_t full[FA_STAGES], empty[FA_STAGES];
     uint64_t q_full, q_empty, s_full[2], p_full[2], pv_done[2], o_empty, done[2];
     long long scan[FA_THREADS / 32 + 1];
+    uint32_t top[2][2][128];                        // by unit parity and group: a row's maximum
     PagedStart start;
     uint32_t tmem;
     int abort;
 };
-constexpr size_t FA_SMEM = FA_SMALL + sizeof(FaSmall) + 1024;   // + slack to align the block
+// Slack to align the block to 1 KiB. Dynamic shared memory starts on such a boundary
+// as it is; the kernel checks that the slack is enough.
+constexpr uint32_t FA_SLACK = 512;
+constexpr size_t FA_SMEM = FA_SMALL + sizeof(FaSmall) + FA_SLACK;
 static_assert(FA_SMEM <= 232448, "shared memory of one CTA");
 
 template <typename TO>
@@ -65,7 +71,12 @@ __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_
                                                                    const PagedArgs a)
 {
     extern __shared__ unsigned char smem_raw[];
-    unsigned char *blk = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const uint32_t shift = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
+    if (shift > FA_SLACK) {
+        if (threadIdx.x == 0) atomicExch(&g_paged_error, (unsigned int)GDN_ERR_TIMEOUT);
+        return;
+    }
+    unsigned char *blk = smem_raw + shift;
     FaSmall &ss = *reinterpret_cast<FaSmall *>(blk + FA_SMALL);
     const uint32_t sb = smem_u32(blk);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -79,13 +90,13 @@ __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&ss.s_full[i]), 1);
-            mbar_init(smem_u32(&ss.p_full[i]), 128);
+            mbar_init(smem_u32(&ss.p_full[i]), 256);
             mbar_init(smem_u32(&ss.pv_done[i]), 1);
             mbar_init(smem_u32(&ss.done[i]), 1);
         }
         mbar_init(smem_u32(&ss.q_full), 1);
         mbar_init(smem_u32(&ss.q_empty), 1);
-        mbar_init(smem_u32(&ss.o_empty), 128);
+        mbar_init(smem_u32(&ss.o_empty), 256);
         ss.abort = 0;
         fence_mbar_init();
     }
@@ -250,8 +261,9 @@ __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_
                 mbar_wait_bounded(smem_u32(&ss.done[1]), 0u);
             }
         } else if (warp >= 4) {
-            // ---- softmax and epilogue: thread r is query row r of the item
-            const int r = tid - 128, q4 = warp & 3;
+            // ---- softmax and epilogue: threads r of both groups share query row r of the item; group 0
+            // has positions 0-63 of a tile and dims 0-127 of the output, group 1 the others
+            const int r = tid & 127, q4 = warp & 3, grp = (warp >> 2) - 1;
             const uint32_t lbase = tm + ((uint32_t)(32 * q4) << 16);
             PieceWalk w = first;
             uint32_t u = 0;
@@ -259,58 +271,64 @@ __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_
             // O += P V of unit v is complete. Two barriers in turn: S of unit u, which this thread has
             // seen, was issued after that of unit u - 2 completed, so each is one phase behind at most.
             auto wait_pv = [&](uint32_t v) { return mbar_wait_bounded(smem_u32(&ss.pv_done[v & 1]), (v >> 1) & 1); };
+            // barrier of the two warps that share rows
+            auto pair_bar = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + q4) : "memory"); };
             for (;;) {
                 const int rows = KV_G * w.tokens(a), sees = tile_sees(a, w.t, w.tile);
                 const int limit = min(w.t.first + PG_TOK * w.tile + (r >> 3) + 1, cap);   // positions this row sees
                 const bool live = 32 * q4 < rows;      // the warp has rows of the item
-                if (r < rows && w.whole() && a.gate != nullptr) {
-                    const bf16 *g = a.gate + (w.t.row0 + PG_TOK * w.tile + (r >> 3)) * a.gate_row +
-                                    (KV_G * w.head + (r & 7)) * a.gate_head;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) asm volatile("prefetch.global.L2 [%0];" ::"l"(g + 64 * i));
-                }
                 float m = -INFINITY, l = 0.0f;
                 for (int j = 0; j < w.len; ++j, ++u) {
-                    const int p0 = (w.unit + j) * PG_TILE;
+                    const int p0 = (w.unit + j) * PG_TILE, c0 = p0 + 64 * grp;
                     ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&ss.s_full[u & 1]), (u >> 1) & 1) && !aborted);
-                    if (!ok) break;
                     tc::fence_after_sync();
                     if (live) {
                         const uint32_t sc = lbase + FA_S + (u & 1) * 128;
-                        float x[4][32];
+                        float x[2][32];
+                        if (ok) {
+                            tc::tmem_ld32(sc + 64 * grp, x[0]);
+                            tc::tmem_ld32(sc + 64 * grp + 32, x[1]);
+                            tc::wait_ld();
+                        }
+                        if (__any_sync(0xffffffffu, c0 + 64 > limit)) {
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) tc::tmem_ld32(sc + 32 * c, x[c]);
-                        tc::wait_ld();
-                        if (__any_sync(0xffffffffu, p0 + PG_TILE > limit)) {
-#pragma unroll
-                            for (int c = 0; c < 4; ++c)
+                            for (int c = 0; c < 2; ++c)
 #pragma unroll
                                 for (int i = 0; i < 32; ++i)
-                                    if (p0 + 32 * c + i >= limit) x[c][i] = -INFINITY;
+                                    if (c0 + 32 * c + i >= limit) x[c][i] = -INFINITY;
                         }
                         float mx[4];
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
-                            mx[c] = fmaxf(x[c][0], x[c][1]);
+                            mx[c] = fmaxf(x[c >> 1][16 * (c & 1)], x[c >> 1][16 * (c & 1) + 1]);
 #pragma unroll
-                            for (int i = 2; i < 32; i += 2) mx[c] = fmaxf(mx[c], fmaxf(x[c][i], x[c][i + 1]));
+                            for (int i = 2; i < 16; i += 2)
+                                mx[c] = fmaxf(mx[c], fmaxf(x[c >> 1][16 * (c & 1) + i], x[c >> 1][16 * (c & 1) + i + 1]));
                         }
-                        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                        // the row's maximum over both groups; a stop is passed on as a NaN that no maximum is
+                        float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                        ss.top[u & 1][grp][r] = ok ? __float_as_uint(top) : 0xFFFFFFFFu;
+                        tc::fence_before_sync();
+                        pair_bar();                    // S has been read by both: P may go over it
+                        tc::fence_after_sync();
+                        const uint32_t other = ss.top[u & 1][grp ^ 1][r];
+                        ok = __all_sync(0xffffffffu, ok && other != 0xFFFFFFFFu);
+                        if (!ok) break;
+                        top = fmaxf(top, __uint_as_float(other));
                         const bool move = (top - m) * SCORE_SCALE > RESCALE_AT;   // also from m = -inf; never for top = -inf
                         if (__any_sync(0xffffffffu, move)) {
                             const float f = !move ? 1.0f : (m == -INFINITY ? 0.0f : ex2((m - top) * SCORE_SCALE));
                             if (j > 0) {
                                 ok = __all_sync(0xffffffffu, wait_pv(u - 1));
-                                if (!ok) break;
                                 tc::fence_after_sync();
 #pragma unroll 1
-                                for (int c = 0; c < 8; ++c) {
+                                for (int c = 0; c < 4 && ok; ++c) {
                                     float o[32];
-                                    tc::tmem_ld32(lbase + FA_O + 32 * c, o);
+                                    tc::tmem_ld32(lbase + FA_O + 128 * grp + 32 * c, o);
                                     tc::wait_ld();
 #pragma unroll
                                     for (int i = 0; i < 32; ++i) o[i] = f > 0.0f ? o[i] * f : 0.0f;
-                                    tc::tmem_st32(lbase + FA_O + 32 * c, o);
+                                    tc::tmem_st32(lbase + FA_O + 128 * grp + 32 * c, o);
                                 }
                                 tc::wait_st();
                             }
@@ -320,34 +338,35 @@ __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_
                         const float off = m == -INFINITY ? 0.0f : m * SCORE_SCALE;
                         float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
+                        for (int c = 0; c < 2; ++c) {
                             uint32_t pk[16];
 #pragma unroll
                             for (int i = 0; i < 16; ++i) {
                                 const float e0 = ex2(fmaf(x[c][2 * i], SCORE_SCALE, -off));
                                 const float e1 = ex2(fmaf(x[c][2 * i + 1], SCORE_SCALE, -off));
-                                sum[c] += e0 + e1;
+                                sum[2 * c + (i & 1)] += e0 + e1;
                                 pk[i] = pack_bf16(e0, e1);
                             }
-                            tc::tmem_st16_u32(sc + 16 * c, pk);
+                            tc::tmem_st16_u32(sc + 32 * grp + 16 * c, pk);
                         }
                         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                         tc::wait_st();
                     }
+                    if (!ok) break;
                     if (p0 + PG_TILE > sees) {
                         // the tile's positions that no token of the item sees: their value rows become
                         // zeros, whatever the cache (or an earlier tile) left there (0 * NaN is NaN). The
                         // previous unit's products are waited for first: they free the stages' earlier use,
                         // without which the phase of `full` would be ambiguous.
-                        const uint32_t vi = j + 1 == w.len && !w.more(a) ? 4 * u + 2 : 4 * u + 4;
+                        const uint32_t vi = (j + 1 == w.len && !w.more(a) ? 4 * u + 2 : 4 * u + 4) + grp;
                         ok = u == 0 || wait_pv(u - 1);
-                        ok = __all_sync(0xffffffffu, ok && wait_full(vi) && wait_full(vi + 1) && !aborted);
+                        ok = __all_sync(0xffffffffu, ok && wait_full(vi) && !aborted);
                         if (!ok) break;
                         if (p0 + r >= sees) {
                             const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                uint4 *row = reinterpret_cast<uint4 *>(blk + (stage(vi + (k >> 1)) - sb) + (k & 1) * FA_BOX + r * 128);
+                            for (int k = 0; k < 2; ++k) {
+                                uint4 *row = reinterpret_cast<uint4 *>(blk + (stage(vi) - sb) + k * FA_BOX + r * 128);
 #pragma unroll
                                 for (int c = 0; c < 8; ++c) row[c] = zero;
                             }
@@ -358,55 +377,99 @@ __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_
                     mbar_arrive(smem_u32(&ss.p_full[u & 1]));
                 }
                 if (!ok) break;
-                // The loop below stays rolled: it runs once per piece, and unrolled it was tens of KB of
-                // cold instructions (15 us per piece, most of it instruction fetch). The gate's next 64
-                // bytes are read a round ahead, the first while the last product runs.
-                const bool mine = r < rows, whole = w.whole(), gated = mine && whole && a.gate != nullptr;
-                const int mrow = w.t.row0 + PG_TOK * w.tile + (r >> 3), h = KV_G * w.head + (r & 7);
-                uint4 gate[4] = {};
-                const uint4 *gsrc = reinterpret_cast<const uint4 *>(a.gate + mrow * a.gate_row + h * a.gate_head);
-                if (gated)
+                // Epilogue: this group's 128 dims, 64 at a time. A thread's row lies 512 bytes from its
+                // neighbour's, so gates come in and outputs leave through 4 KiB of shared memory per warp,
+                // in whole 128-byte lines. The gates are read while the last product runs. The loop stays
+                // rolled: it runs once per piece, and cold instructions cost more than the branches.
+                const bool mine = r < rows, whole = w.whole(), gated = whole && a.gate != nullptr;
+                const int row0 = w.t.row0 + PG_TOK * w.tile, h0 = KV_G * w.head;
+                const int er = lane >> 3, ec = lane & 7;       // copy i of a lane: row 4 i + er of the warp's 32, chunk ec
+                unsigned char *box = blk + FA_EPI + (warp - 4) * 4096;
+                // row 32 q4 + 4 i + er is token 4 q4 + i / 2, head 4 (i & 1) + er
+                uint4 gate[2][8];
+                if (gated && live) {
+                    const bf16 *src = a.gate + (row0 + 4 * q4) * a.gate_row + (h0 + er) * a.gate_head + 128 * grp + 8 * ec;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) gate[i] = __ldg(gsrc + i);
+                    for (int i = 0; i < 8; ++i) {
+                        const bf16 *g = src + (i >> 1) * a.gate_row + 4 * (i & 1) * a.gate_head;
+                        const bool in = 4 * q4 + (i >> 1) < rows >> 3;
+                        gate[0][i] = in ? __ldg(reinterpret_cast<const uint4 *>(g)) : make_uint4(0u, 0u, 0u, 0u);
+                        gate[1][i] = in ? __ldg(reinterpret_cast<const uint4 *>(g + 64)) : make_uint4(0u, 0u, 0u, 0u);
+                    }
+                }
+                reinterpret_cast<float *>(box)[lane] = l;      // the row's sum over both groups
+                pair_bar();
+                const float l1 = reinterpret_cast<const float *>(blk + FA_EPI + ((warp - 4) ^ 4) * 4096)[lane];
+                l = grp == 0 ? l + l1 : l1 + l;
+                pair_bar();
                 ok = __all_sync(0xffffffffu, wait_pv(u - 1) && !aborted);
-                if (!ok) break;
                 tc::fence_after_sync();
-                if (live) {
+                if (live && ok) {
                     const size_t slot = ((size_t)2 * blockIdx.x + (w.first ? 0 : 1)) * a.rows + r;
                     const float inv = l == 0.0f ? 0.0f : (whole ? 1.0f / l : 1.0f);   // l = 0: the row saw nothing
-                    TO *orow = static_cast<TO *>(a.out) + ((size_t)mrow * KV_HQ + h) * KV_D;
-                    float *prow = a.part_o + slot * KV_D;
-#pragma unroll 1
-                    for (int c = 0; c < 8; ++c) {
-                        float o[32];
-                        tc::tmem_ld32(lbase + FA_O + 32 * c, o);
-                        uint4 next[4] = {};
-                        if (gated && c < 7)
+                    TO *out = static_cast<TO *>(a.out);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) next[i] = __ldg(gsrc + 4 * c + 4 + i);
-                        tc::wait_ld();
+                    for (int part = 0; part < 2; ++part) {
+                        if (gated) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float e[8];
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) e[k] = l == 0.0f ? 0.0f : o[8 * i + k];
-                            if (gated) {
-                                gate8(gate[i], e, inv);
-                            } else {
-#pragma unroll
-                                for (int k = 0; k < 8; ++k) e[k] *= inv;
-                            }
-                            if (mine && whole) store8_out(orow + 32 * c + 8 * i, e);
-                            else if (mine) store8_out(prow + 32 * c + 8 * i, e);
-                            gate[i] = next[i];
+                            for (int i = 0; i < 8; ++i)
+                                *reinterpret_cast<uint4 *>(box + (4 * i + er) * 128 + ((ec ^ ((4 * i + er) & 7)) << 4)) = gate[part][i];
+                            __syncwarp();
                         }
-                        __syncwarp();
+#pragma unroll 1
+                        for (int c = 0; c < 2; ++c) {
+                            float o[32];
+                            tc::tmem_ld32(lbase + FA_O + 128 * grp + 64 * part + 32 * c, o);
+                            uint4 *at[4], g[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                at[i] = reinterpret_cast<uint4 *>(box + lane * 128 + (((4 * c + i) ^ (lane & 7)) << 4));
+                                if (gated) g[i] = *at[i];
+                            }
+                            tc::wait_ld();
+                            float e[4][8];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) e[i][k] = l == 0.0f ? 0.0f : o[8 * i + k];
+                                if (gated) {
+                                    gate8(g[i], e[i], inv);
+                                } else {
+#pragma unroll
+                                    for (int k = 0; k < 8; ++k) e[i][k] *= inv;
+                                }
+                            }
+                            const int d = 128 * grp + 64 * part + 32 * c;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                if (!whole) {
+                                    if (mine) store8_out(a.part_o + slot * KV_D + d + 8 * i, e[i]);
+                                } else if (sizeof(TO) == 4) {
+                                    if (mine) store8_out(out + ((size_t)(row0 + (r >> 3)) * KV_HQ + h0 + (r & 7)) * KV_D + d + 8 * i, e[i]);
+                                } else {
+                                    store8_out(reinterpret_cast<bf16 *>(at[i]), e[i]);
+                                }
+                            }
+                            __syncwarp();
+                        }
+                        if (whole && sizeof(TO) == 2) {
+                            uint4 v[8];
+                            TO *dst = out + ((size_t)(row0 + 4 * q4) * KV_HQ + h0 + er) * KV_D + 128 * grp + 64 * part + 8 * ec;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                v[i] = *reinterpret_cast<const uint4 *>(box + (4 * i + er) * 128 + ((ec ^ ((4 * i + er) & 7)) << 4));
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                if (4 * q4 + (i >> 1) < rows >> 3)
+                                    *reinterpret_cast<uint4 *>(dst + ((i >> 1) * KV_HQ + 4 * (i & 1)) * KV_D) = v[i];
+                            __syncwarp();
+                        }
                     }
-                    if (mine && !whole) *reinterpret_cast<float2 *>(a.part_ml + slot * 2) = make_float2(m * SCORE_SCALE, l);
+                    if (mine && !whole && grp == 0) *reinterpret_cast<float2 *>(a.part_ml + slot * 2) = make_float2(m * SCORE_SCALE, l);
                 }
                 tc::fence_before_sync();
                 mbar_arrive(smem_u32(&ss.o_empty));
-                if (!w.more(a)) break;
+                if (!ok || !w.more(a)) break;
                 w.next(a);
             }
             if (!ok && lane == 0) ss.abort = 1;

@@ -289,12 +289,20 @@ __device__ __forceinline__ void store8_out(bf16 *p, const float (&x)[8])
     *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
                                                pack_bf16(x[6], x[7]));
 }
+// inv * sigmoid(g): two special-function operations (a few 2^-23 relative; a gate
+// below -126 ln 2 gives zero). Division and expf in full are four times as many
+// instructions, which an epilogue of one warp per scheduler waits for.
+__device__ __forceinline__ float gate1(float g, float inv)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.0f + ex2(-1.4426950408889634f * g)));
+    return y * inv;
+}
 __device__ __forceinline__ void gate8(const uint4 u, float (&o)[8], float inv)
 {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        o[i] *= __fdividef(inv, 1.0f + __expf(-__uint_as_float((i & 1) ? (w[i >> 1] & 0xFFFF0000u) : (w[i >> 1] << 16))));
+    for (int i = 0; i < 8; ++i) o[i] *= gate1(__uint_as_float((i & 1) ? (w[i >> 1] & 0xFFFF0000u) : (w[i >> 1] << 16)), inv);
 }
 // Normalised output times the gate, 8 dims from dim d of (packed row m, head h).
 template <typename TO>
@@ -316,10 +324,10 @@ __device__ __forceinline__ void finish4(const PagedArgs &a, int m, int h, int d,
     float s[4] = {inv, inv, inv, inv};
     if (a.gate != nullptr) {
         const float4 g = load4(a.gate + m * a.gate_row + h * a.gate_head + d);
-        s[0] = __fdividef(inv, 1.0f + __expf(-g.x));
-        s[1] = __fdividef(inv, 1.0f + __expf(-g.y));
-        s[2] = __fdividef(inv, 1.0f + __expf(-g.z));
-        s[3] = __fdividef(inv, 1.0f + __expf(-g.w));
+        s[0] = gate1(g.x, inv);
+        s[1] = gate1(g.y, inv);
+        s[2] = gate1(g.z, inv);
+        s[3] = gate1(g.w, inv);
     }
     store4(static_cast<TO *>(a.out) + ((size_t)m * KV_HQ + h) * KV_D + d,
            make_float4(o.x * s[0], o.y * s[1], o.z * s[2], o.w * s[3]));
