@@ -379,24 +379,24 @@ __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_
                 if (!ok) break;
                 // Epilogue: this group's 128 dims, 64 at a time. A thread's row lies 512 bytes from its
                 // neighbour's, so gates come in and outputs leave through 4 KiB of shared memory per warp,
-                // in whole 128-byte lines. The gates are read while the last product runs. The loop stays
-                // rolled: it runs once per piece, and cold instructions cost more than the branches.
+                // in whole 128-byte lines. The gates are read while the last product runs. The loops stay
+                // rolled: this runs once per piece, so its instructions are fetched anew each time, and
+                // unrolled it took 13,000 cycles per piece, most of them for that.
                 const bool mine = r < rows, whole = w.whole(), gated = whole && a.gate != nullptr;
                 const int row0 = w.t.row0 + PG_TOK * w.tile, h0 = KV_G * w.head;
                 const int er = lane >> 3, ec = lane & 7;       // copy i of a lane: row 4 i + er of the warp's 32, chunk ec
                 unsigned char *box = blk + FA_EPI + (warp - 4) * 4096;
                 // row 32 q4 + 4 i + er is token 4 q4 + i / 2, head 4 (i & 1) + er
-                uint4 gate[2][8];
-                if (gated && live) {
-                    const bf16 *src = a.gate + (row0 + 4 * q4) * a.gate_row + (h0 + er) * a.gate_head + 128 * grp + 8 * ec;
+                uint4 gate[8];
+                const bf16 *gsrc = a.gate + (row0 + 4 * q4) * a.gate_row + (h0 + er) * a.gate_head + 128 * grp + 8 * ec;
+                auto load_gate = [&](int part) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const bf16 *g = src + (i >> 1) * a.gate_row + 4 * (i & 1) * a.gate_head;
-                        const bool in = 4 * q4 + (i >> 1) < rows >> 3;
-                        gate[0][i] = in ? __ldg(reinterpret_cast<const uint4 *>(g)) : make_uint4(0u, 0u, 0u, 0u);
-                        gate[1][i] = in ? __ldg(reinterpret_cast<const uint4 *>(g + 64)) : make_uint4(0u, 0u, 0u, 0u);
-                    }
-                }
+                    for (int i = 0; i < 8; ++i)
+                        gate[i] = 4 * q4 + (i >> 1) < rows >> 3
+                                      ? __ldg(reinterpret_cast<const uint4 *>(gsrc + (i >> 1) * a.gate_row + 4 * (i & 1) * a.gate_head + 64 * part))
+                                      : make_uint4(0u, 0u, 0u, 0u);
+                };
+                if (gated && live) load_gate(0);
                 reinterpret_cast<float *>(box)[lane] = l;      // the row's sum over both groups
                 pair_bar();
                 const float l1 = reinterpret_cast<const float *>(blk + FA_EPI + ((warp - 4) ^ 4) * 4096)[lane];
@@ -408,46 +408,44 @@ __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_
                     const size_t slot = ((size_t)2 * blockIdx.x + (w.first ? 0 : 1)) * a.rows + r;
                     const float inv = l == 0.0f ? 0.0f : (whole ? 1.0f / l : 1.0f);   // l = 0: the row saw nothing
                     TO *out = static_cast<TO *>(a.out);
-#pragma unroll
+#pragma unroll 1
                     for (int part = 0; part < 2; ++part) {
                         if (gated) {
 #pragma unroll
                             for (int i = 0; i < 8; ++i)
-                                *reinterpret_cast<uint4 *>(box + (4 * i + er) * 128 + ((ec ^ ((4 * i + er) & 7)) << 4)) = gate[part][i];
+                                *reinterpret_cast<uint4 *>(box + (4 * i + er) * 128 + ((ec ^ ((4 * i + er) & 7)) << 4)) = gate[i];
                             __syncwarp();
+                            if (part == 0) load_gate(1);
                         }
 #pragma unroll 1
-                        for (int c = 0; c < 2; ++c) {
-                            float o[32];
-                            tc::tmem_ld32(lbase + FA_O + 128 * grp + 64 * part + 32 * c, o);
-                            uint4 *at[4], g[4];
+                        for (int c = 0; c < 4; ++c) {          // 16 dims
+                            const int d = 128 * grp + 64 * part + 16 * c;
+                            float o[16];
+                            tc::tmem_ld16(lbase + FA_O + d, o);
+                            uint4 *at[2], g[2];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                at[i] = reinterpret_cast<uint4 *>(box + lane * 128 + (((4 * c + i) ^ (lane & 7)) << 4));
-                                if (gated) g[i] = *at[i];
+                            for (int i = 0; i < 2; ++i) {
+                                at[i] = reinterpret_cast<uint4 *>(box + lane * 128 + (((2 * c + i) ^ (lane & 7)) << 4));
+                                g[i] = gated ? *at[i] : make_uint4(0u, 0u, 0u, 0u);
                             }
                             tc::wait_ld();
-                            float e[4][8];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
+                            for (int i = 0; i < 2; ++i) {
+                                float e[8];
 #pragma unroll
-                                for (int k = 0; k < 8; ++k) e[i][k] = l == 0.0f ? 0.0f : o[8 * i + k];
+                                for (int k = 0; k < 8; ++k) e[k] = l == 0.0f ? 0.0f : o[8 * i + k];
                                 if (gated) {
-                                    gate8(g[i], e[i], inv);
+                                    gate8(g[i], e, inv);
                                 } else {
 #pragma unroll
-                                    for (int k = 0; k < 8; ++k) e[i][k] *= inv;
+                                    for (int k = 0; k < 8; ++k) e[k] *= inv;
                                 }
-                            }
-                            const int d = 128 * grp + 64 * part + 32 * c;
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
                                 if (!whole) {
-                                    if (mine) store8_out(a.part_o + slot * KV_D + d + 8 * i, e[i]);
+                                    if (mine) store8_out(a.part_o + slot * KV_D + d + 8 * i, e);
                                 } else if (sizeof(TO) == 4) {
-                                    if (mine) store8_out(out + ((size_t)(row0 + (r >> 3)) * KV_HQ + h0 + (r & 7)) * KV_D + d + 8 * i, e[i]);
+                                    if (mine) store8_out(out + ((size_t)(row0 + (r >> 3)) * KV_HQ + h0 + (r & 7)) * KV_D + d + 8 * i, e);
                                 } else {
-                                    store8_out(reinterpret_cast<bf16 *>(at[i]), e[i]);
+                                    store8_out(reinterpret_cast<bf16 *>(at[i]), e);
                                 }
                             }
                             __syncwarp();
