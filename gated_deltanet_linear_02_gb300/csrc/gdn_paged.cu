@@ -406,7 +406,8 @@ __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_
                 tc::fence_after_sync();
                 if (live && ok) {
                     const size_t slot = ((size_t)2 * blockIdx.x + (w.first ? 0 : 1)) * a.rows + r;
-                    const float inv = l == 0.0f ? 0.0f : (whole ? 1.0f / l : 1.0f);   // l = 0: the row saw nothing
+                    const float inv = l == 0.0f ? 0.0f : (whole ? 1.0f / l : 1.0f);
+                    const bool blank = __any_sync(0xffffffffu, l == 0.0f);   // a row that saw nothing gives zeros
                     TO *out = static_cast<TO *>(a.out);
 #pragma unroll 1
                     for (int part = 0; part < 2; ++part) {
@@ -429,11 +430,14 @@ __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_
                                 g[i] = gated ? *at[i] : make_uint4(0u, 0u, 0u, 0u);
                             }
                             tc::wait_ld();
+                            if (blank)
+#pragma unroll
+                                for (int k = 0; k < 16; ++k) o[k] = l == 0.0f ? 0.0f : o[k];
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
                                 float e[8];
 #pragma unroll
-                                for (int k = 0; k < 8; ++k) e[k] = l == 0.0f ? 0.0f : o[8 * i + k];
+                                for (int k = 0; k < 8; ++k) e[k] = o[8 * i + k];
                                 if (gated) {
                                     gate8(g[i], e, inv);
                                 } else {

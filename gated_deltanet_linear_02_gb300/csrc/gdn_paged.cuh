@@ -289,17 +289,14 @@ __device__ __forceinline__ void store8_out(bf16 *p, const float (&x)[8])
     *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
                                                pack_bf16(x[6], x[7]));
 }
-// inv * sigmoid(g) with one special-function operation: e = exp(-|g|) is at most 1,
-// and 1 / d for d = 1 + e in [1, 2] is the quadratic of least relative error (1/99,
-// from the Chebyshev polynomial T3) and one cubic Newton step, 1e-6 in all. The
-// hardware's reciprocal was what an epilogue of 32,768 outputs waited for: 8,000
-// cycles with it.
+// inv * sigmoid(g) in four instructions, two of them special functions (a few 2^-23
+// relative). Epilogues wait for these: with expf and a division in full an item's
+// 32,768 outputs took three times as long, with a Newton reciprocal twice.
 __device__ __forceinline__ float gate1(float g, float inv)
 {
-    const float e = ex2(-1.4426950408889634f * fabsf(g)), d = 1.0f + e;
-    const float y = fmaf(fmaf(32.0f / 99.0f, d, -144.0f / 99.0f), d, 210.0f / 99.0f), t = fmaf(-d, y, 1.0f);
-    const float r = inv * fmaf(y, fmaf(t, t, t), y);
-    return g < 0.0f ? e * r : r;
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.0f + ex2(-1.4426950408889634f * g)));
+    return y * inv;
 }
 __device__ __forceinline__ void gate8(const uint4 u, float (&o)[8], float inv)
 {
