@@ -486,36 +486,43 @@ __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_
     if (tid == 0 && ss.abort) atomicExch(&g_paged_error, (unsigned int)GDN_ERR_TIMEOUT);
 }
 
-// Joins the pieces of every item that spans ranges. CTA (x, y): the range
-// boundary x + 1, if it is the first one inside an item, and row y of that item;
-// 8 warps take the pieces in turn, 8 dims per lane, and meet in shared memory:
-// with block maxima m_s (powers of two), sums l_s and unnormalised outputs o_s,
+// Joins the pieces of every item that spans ranges: with the pieces' maxima m_s
+// (powers of two), sums l_s and unnormalised outputs o_s,
 //   M = max m_s, out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s * sigmoid(gate).
+// There is one CTA for every cut between ranges and eight rows of an item. An item
+// of n + 1 pieces has n cuts, so its CTAs, numbered over cuts and row groups, share
+// its rows: eight to one each, as there are few or many pieces. The 8 warps of a CTA
+// divide over its rows, those of a row over its pieces (8 dims per lane, four
+// pieces' loads at a time), and meet in shared memory.
 template <typename TO>
 __global__ void __launch_bounds__(256) attn_paged_join_kernel(const PagedArgs a)
 {
     __shared__ float so[8][KV_D], sml[8][2];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int c = blockIdx.x + 1, r = blockIdx.y;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x + 1;
     grid_dep_wait();
     grid_dep_launch();
     const PagedStart st = a.start[c];
     // the item's first step, and the step of its first unit: a cut at or before that one cuts nothing
     const long long u = range_begin(st, c, a.ranges), begin = u - st.step, unit0 = begin + a.lead;
-    if (u >= range_begin(st, a.ranges, a.ranges) || u <= unit0 || range_begin(st, c - 1, a.ranges) > unit0) return;
+    if (u >= range_begin(st, a.ranges, a.ranges) || u <= unit0) return;
     const SeqTokens t = seq_tokens(a.b, st.seq);
-    const int tokens = min(a.tok, t.n - (st.tile << a.tok_log2));
-    if (r >= KV_G * tokens) return;
     const long long end = unit0 + tile_units(a, t, st.tile);
-    int last = c + (int)((end - u - 1) / (st.quot + 1));   // the last range with a piece of the item, at least
+    int head = c - (int)((u - unit0 - 1) / (st.quot + 1));   // the item's first cut, at most
+    while (range_begin(st, head - 1, a.ranges) > unit0) --head;
+    int last = c + (int)((end - u - 1) / (st.quot + 1));     // its last range, at least
     while (last + 1 < a.ranges && range_begin(st, last + 1, a.ranges) < end) ++last;
+    const int rows = KV_G * min(a.tok, t.n - (st.tile << a.tok_log2));
+    const int ctas = (last - head + 1) * gridDim.y, cta = (c - head) * gridDim.y + blockIdx.y;
+    int per = 1;                                       // rows of a CTA: a power of two up to 8
+    while (per < 8 && per * ctas < rows) per <<= 1;
+    const int share = 8 / per, r = cta * per + warp / share, part = warp % share;
     float M = -INFINITY, l = 0.0f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int k0 = c - 1 + warp; k0 <= last; k0 += 32) {    // four pieces' loads at a time
+    for (int k0 = head - 1 + part; k0 <= last && r < rows; k0 += 4 * share) {
         float2 ml[4];
         float4 x[4], y[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int k = k0 + 8 * i;
+            const int k = k0 + share * i;
             ml[i] = make_float2(-INFINITY, 0.0f);
             x[i] = y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
             const long long from = range_begin(st, k, a.ranges);
@@ -538,27 +545,29 @@ __global__ void __launch_bounds__(256) attn_paged_join_kernel(const PagedArgs a)
             o[6] = o[6] * f + y[i].z * g; o[7] = o[7] * f + y[i].w * g;
         }
     }
-    store8_out(&so[warp][8 * lane], o);
-    if (lane == 0) {
-        sml[warp][0] = M;
-        sml[warp][1] = l;
+    if (share > 1) {                                   // the same for the whole CTA
+        store8_out(&so[warp][8 * lane], o);
+        if (lane == 0) {
+            sml[warp][0] = M;
+            sml[warp][1] = l;
+        }
+        __syncthreads();
+        if (part != 0) return;
+        for (int k = warp; k < warp + share; ++k) M = fmaxf(M, sml[k][0]);
+        l = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = 0.0f;
+        for (int k = warp; k < warp + share; ++k) {
+            if (sml[k][1] == 0.0f) continue;
+            const float g = ex2(sml[k][0] - M);
+            l += g * sml[k][1];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] += g * so[k][8 * lane + i];
+        }
     }
-    __syncthreads();
-    if (warp != 0) return;
-    float Ma = sml[0][0];
-#pragma unroll
-    for (int k = 1; k < 8; ++k) Ma = fmaxf(Ma, sml[k][0]);
-    float la = 0.0f, e[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        if (sml[k][1] == 0.0f) continue;
-        const float g = ex2(sml[k][0] - Ma);
-        la += g * sml[k][1];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) e[i] += g * so[k][8 * lane + i];
-    }
-    finish8<TO>(a, t.row0 + (st.tile << a.tok_log2) + (r >> 3), KV_G * st.head + (r & 7), 8 * lane, e,
-                la != 0.0f ? 1.0f / la : 0.0f);
+    if (r < rows)
+        finish8<TO>(a, t.row0 + (st.tile << a.tok_log2) + (r >> 3), KV_G * st.head + (r & 7), 8 * lane, o,
+                    l != 0.0f ? 1.0f / l : 0.0f);
 }
 
 // ------------------------------------------------------------------ launcher
@@ -584,7 +593,7 @@ bool encode_tiled(CUtensorMap *map, CUtensorMapDataType dt, int rank, const void
 
 cudaError_t launch_paged_join(const PagedArgs &a, gdn_dtype out_dt, cudaStream_t s)
 {
-    const dim3 grid(a.ranges - 1, a.rows), block(256);
+    const dim3 grid(a.ranges - 1, a.rows / KV_G), block(256);
     return out_dt == GDN_F32 ? launch_pdl(attn_paged_join_kernel<float>, grid, block, 0, s, a)
                              : launch_pdl(attn_paged_join_kernel<bf16>, grid, block, 0, s, a);
 }
