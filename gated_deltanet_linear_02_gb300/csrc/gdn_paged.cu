@@ -39,21 +39,32 @@ namespace gdn {
 
 __device__ unsigned int g_paged_error;            // GDN_ERR_TIMEOUT if a bounded wait gave up
 
-constexpr int FA_THREADS = 384;
-constexpr int FA_STAGES = 4;
+constexpr int fa_threads(bool q4) { return q4 ? 512 : 384; }
 constexpr uint32_t FA_BOX = PG_TILE * 128;        // 128 rows x 64 dims of bf16: 16 KiB
 constexpr uint32_t FA_STAGE_BYTES = 2 * FA_BOX;   // 128 dims: 32 KiB
-constexpr uint32_t FA_Q = 0;                      // Q: 4 boxes of 64 dims
-constexpr uint32_t FA_RING = 4 * FA_BOX;
-constexpr uint32_t FA_EPI = FA_RING + FA_STAGES * FA_STAGE_BYTES;   // 4 KiB for each softmax warp
-constexpr uint32_t FA_SMALL = FA_EPI + 8 * 4096;
 constexpr uint32_t FA_S = 0, FA_O = 256;          // tensor memory columns: S buffers at 0 and 128, O at 256
 
+// Shared memory. 4-bit pages take one stage less and half of the epilogue's boxes
+// for two tiles of codes as they are stored: eight records' key or value parts.
+constexpr uint32_t FA_CODES = 2048, FA_TILE_BYTES = 8 * (2048 + 256);
+template <bool Q4> struct Fa {
+    static constexpr int STAGES = Q4 ? 3 : 4;
+    static constexpr int PART = Q4 ? 32 : 64;     // dims that an epilogue box holds
+    static constexpr uint32_t BOX = 32 * PART * 2;   // per softmax warp
+    static constexpr uint32_t Q = 0;              // Q: 4 boxes of 64 dims
+    static constexpr uint32_t RING = 4 * FA_BOX;
+    static constexpr uint32_t EPI = RING + STAGES * FA_STAGE_BYTES;
+    static constexpr uint32_t TILES = EPI + 8 * BOX;
+    static constexpr uint32_t SMALL = TILES + (Q4 ? 2 * FA_TILE_BYTES : 0);
+};
+
 struct FaSmall {
-    uint64_t full[FA_STAGES], empty[FA_STAGES];
+    uint64_t full[4], empty[4];
     uint64_t q_full, q_empty, s_full[2], p_full[2], pv_done[2], o_empty, done[2];
-    long long scan[FA_THREADS / 32 + 1];
-    uint32_t top[2][2][128];                        // by unit parity and group: a row's maximum
+    uint64_t t_full[2], t_empty[2];               // tiles of codes
+    int t_sees[2];                                // positions of the tile that the item sees; below 0: no more tiles
+    long long scan[fa_threads(true) / 32 + 1];
+    uint32_t top[2][2][128];                      // by unit parity and group: a row's maximum
     PagedStart start;
     uint32_t tmem;
     int abort;
@@ -61,11 +72,24 @@ struct FaSmall {
 // Slack to align the block to 1 KiB. Dynamic shared memory starts on such a boundary
 // as it is; the kernel checks that the slack is enough.
 constexpr uint32_t FA_SLACK = 512;
-constexpr size_t FA_SMEM = FA_SMALL + sizeof(FaSmall) + FA_SLACK;
-static_assert(FA_SMEM <= 232448, "shared memory of one CTA");
+template <bool Q4> constexpr size_t FA_SMEM = Fa<Q4>::SMALL + sizeof(FaSmall) + FA_SLACK;
+static_assert(FA_SMEM<false> <= 232448 && FA_SMEM<true> <= 232448, "shared memory of one CTA");
 
-template <typename TO>
-__global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_constant__ CUtensorMap qmap,
+// Two bf16 values of a word's codes t and t + 4: s c + z with one rounding (128 + c
+// by one logic operation, minus 128 exactly).
+__device__ __forceinline__ uint32_t value_pair(uint32_t w, int t, uint32_t s2, uint32_t z2)
+{
+    uint32_t c = ((w >> (4 * t)) & 0x000F000Fu) | 0x43004300u, v;
+    asm("sub.rn.bf16x2 %0, %0, %1;" : "+r"(c) : "r"(0x43004300u));
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(v) : "r"(c), "r"(s2), "r"(z2));
+    return v;
+}
+
+template <int N> __device__ __forceinline__ void set_registers_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void set_registers_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+template <typename TO, bool Q4>
+__global__ void __launch_bounds__(fa_threads(Q4), 1) attn_paged_kernel(const __grid_constant__ CUtensorMap qmap,
                                                                    const __grid_constant__ CUtensorMap kmap,
                                                                    const __grid_constant__ CUtensorMap vmap,
                                                                    const PagedArgs a)
@@ -77,15 +101,15 @@ __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_
         return;
     }
     unsigned char *blk = smem_raw + shift;
-    FaSmall &ss = *reinterpret_cast<FaSmall *>(blk + FA_SMALL);
+    FaSmall &ss = *reinterpret_cast<FaSmall *>(blk + Fa<Q4>::SMALL);
     const uint32_t sb = smem_u32(blk);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const PagedBatch &b = a.b;
     const int cap = b.max_pages << b.page_log2;
 
     if (tid == 0) {
-        for (int s = 0; s < FA_STAGES; ++s) {
-            mbar_init(smem_u32(&ss.full[s]), 1);
+        for (int s = 0; s < Fa<Q4>::STAGES; ++s) {
+            mbar_init(smem_u32(&ss.full[s]), Q4 ? 128 : 1);
             mbar_init(smem_u32(&ss.empty[s]), 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -93,6 +117,8 @@ __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_
             mbar_init(smem_u32(&ss.p_full[i]), 256);
             mbar_init(smem_u32(&ss.pv_done[i]), 1);
             mbar_init(smem_u32(&ss.done[i]), 1);
+            mbar_init(smem_u32(&ss.t_full[i]), 32);
+            mbar_init(smem_u32(&ss.t_empty[i]), 128);
         }
         mbar_init(smem_u32(&ss.q_full), 1);
         mbar_init(smem_u32(&ss.q_empty), 1);
@@ -106,7 +132,7 @@ __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_
     }
     grid_dep_wait();
     grid_dep_launch();
-    find_start<FA_THREADS>(a, blockIdx.x, ss.scan, &ss.start);   // ends in a CTA barrier
+    find_start<fa_threads(Q4)>(a, blockIdx.x, ss.scan, &ss.start);   // ends in a CTA barrier
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
@@ -115,14 +141,17 @@ __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_
     if (tid == 0) a.start[blockIdx.x] = st;
     const long long count = range_begin(st, blockIdx.x + 1, a.ranges) - range_begin(st, blockIdx.x, a.ranges);
     const volatile int &aborted = ss.abort;
-    auto stage = [&](uint32_t i) { return sb + FA_RING + (i % FA_STAGES) * FA_STAGE_BYTES; };
+    auto stage = [&](uint32_t i) { return sb + Fa<Q4>::RING + (i % Fa<Q4>::STAGES) * FA_STAGE_BYTES; };
     auto wait_full = [&](uint32_t i) {
-        return mbar_wait_bounded(smem_u32(&ss.full[i % FA_STAGES]), (i / FA_STAGES) & 1);
+        return mbar_wait_bounded(smem_u32(&ss.full[i % Fa<Q4>::STAGES]), (i / Fa<Q4>::STAGES) & 1);
     };
 
     PieceWalk first;
     if (count > 0) first.begin(a, st, count);
     if (count > 0 && first.len > 0) {
+        // registers with 4-bit pages: 72 + 2 x 168 + 104 of the 4 x 128 launched with
+        if (warp < 4) {
+        if (Q4) set_registers_down<72>();
         if (warp == 0) {
             // ---- TMA producer. Stage order: K(0), then K(u + 1), V(u) for each u.
             UnitWalk kw;
@@ -145,47 +174,115 @@ __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_
             };
             auto load = [&](const CUtensorMap *m, int row, int loaded) {
                 for (int half = 0; half < 2 && ok; ++half, ++i) {
-                    if (i >= FA_STAGES)
-                        ok = mbar_wait_bounded(smem_u32(&ss.empty[i % FA_STAGES]), (i / FA_STAGES - 1) & 1);
+                    if (i >= Fa<Q4>::STAGES)
+                        ok = mbar_wait_bounded(smem_u32(&ss.empty[i % Fa<Q4>::STAGES]), (i / Fa<Q4>::STAGES - 1) & 1);
                     ok = __all_sync(0xffffffffu, ok && !aborted);
                     if (!ok) break;
-                    const uint32_t bar = smem_u32(&ss.full[i % FA_STAGES]);
+                    const uint32_t bar = smem_u32(&ss.full[i % Fa<Q4>::STAGES]);
                     if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)loaded * b.page * 256);
                     __syncwarp();
                     if (seg < loaded) tma_load_2d(stage(i) + seg_dst, m, half * 128 + box * 64, row, bar);
                 }
             };
-            auto load_q = [&]() {
+            auto load_q = [&](int row0, int head) {
                 if (piece > 0) ok = mbar_wait_bounded(smem_u32(&ss.q_empty), (piece - 1) & 1);
                 ok = __all_sync(0xffffffffu, ok && !aborted);
                 if (ok && lane == 0) {
                     const uint32_t bar = smem_u32(&ss.q_full);
                     mbar_arrive_expect_tx(bar, 4 * FA_BOX);
                     for (int c = 0; c < 4; ++c)
-                        tma_load_3d(sb + FA_Q + c * FA_BOX, &qmap, 64 * c, KV_G * kw.w.head,
-                                    kw.w.t.row0 + PG_TOK * kw.w.tile, bar);
+                        tma_load_3d(sb + Fa<Q4>::Q + c * FA_BOX, &qmap, 64 * c, KV_G * head, row0, bar);
                 }
                 ++piece;
             };
-            int row, loaded;
-            segment(row, loaded);
-            load_q();
-            if (ok) load(&kmap, row, loaded);
-            while (ok) {
-                const int vrow = row, vloaded = loaded;
-                const bool more = !kw.last(a);
-                if (more) {
-                    kw.next(a);
-                    segment(row, loaded);
-                    if (kw.j == 0) load_q();
-                    if (ok) load(&kmap, row, loaded);
+            if (!Q4) {
+                int row, loaded;
+                segment(row, loaded);
+                load_q(kw.w.t.row0 + PG_TOK * kw.w.tile, kw.w.head);
+                if (ok) load(&kmap, row, loaded);
+                while (ok) {
+                    const int vrow = row, vloaded = loaded;
+                    const bool more = !kw.last(a);
+                    if (more) {
+                        kw.next(a);
+                        segment(row, loaded);
+                        if (kw.j == 0) load_q(kw.w.t.row0 + PG_TOK * kw.w.tile, kw.w.head);
+                        if (ok) load(&kmap, row, loaded);
+                    }
+                    if (ok) load(&vmap, vrow, vloaded);
+                    if (!more) break;
                 }
-                if (ok) load(&vmap, vrow, vloaded);
-                if (!more) break;
+            } else {
+                // tiles of codes in the same order: the keys of the next unit, unless those of two are
+                // ahead of their values (q0, q1), else the values of the oldest. Lane k: record k.
+                struct Unit {
+                    int rec, sees, row0, head;     // the lane's record (-1: zeros, -2: none), positions seen, the queries
+                    bool first;
+                };
+                Unit q0 = {}, q1 = {}, tile;
+                int ahead = 0, entry = 0;
+                bool have = true;
+                auto look_up = [&]() {             // page table entry of the lane's record of the unit kw is at
+                    const int p = (kw.w.unit + kw.j) * PG_TILE + 16 * lane;
+                    if (lane < 8 && p < tile_sees(a, kw.w.t, kw.w.tile))
+                        entry = __ldg(b.table + (size_t)kw.w.seq * b.max_pages + (p >> b.page_log2));
+                };
+                look_up();
+                for (uint32_t n = 0;; ++n) {
+                    const bool value = !(ahead < 2 && have);
+                    if (!value) {
+                        const int p = (kw.w.unit + kw.j) * PG_TILE, at = (kw.w.head << b.page_log2) + ((p + 16 * lane) & (b.page - 1));
+                        tile.sees = max(min(tile_sees(a, kw.w.t, kw.w.tile) - p, PG_TILE), 0);
+                        tile.rec = lane >= 8 || 16 * lane >= tile.sees ? -2
+                                   : (unsigned)entry < (unsigned)b.num_pages ? (((entry * KV_H) << b.page_log2) + at) >> 4 : -1;
+                        tile.row0 = kw.w.t.row0 + PG_TOK * kw.w.tile;
+                        tile.head = kw.w.head;
+                        tile.first = kw.j == 0;
+                        (ahead++ == 0 ? q0 : q1) = tile;
+                        have = !kw.last(a);
+                        if (have) {
+                            kw.next(a);
+                            look_up();
+                        }
+                        if (tile.first) load_q(tile.row0, tile.head);
+                    } else if (ahead > 0) {
+                        tile = q0;
+                        q0 = q1;
+                        --ahead;
+                    } else {
+                        tile.sees = -1;            // no more
+                        tile.rec = -2;
+                    }
+                    if (n >= 2) ok = ok && mbar_wait_bounded(smem_u32(&ss.t_empty[n & 1]), ((n >> 1) - 1) & 1);
+                    ok = __all_sync(0xffffffffu, ok && !aborted);
+                    if (!ok) break;
+                    const uint32_t bar = smem_u32(&ss.t_full[n & 1]);
+                    const uint32_t at = Fa<Q4>::TILES + (n & 1) * FA_TILE_BYTES;
+                    if (lane == 0) ss.t_sees[n & 1] = tile.sees;
+                    if (tile.rec >= 0) {
+                        const unsigned char *src = static_cast<const unsigned char *>(a.ck) + (size_t)tile.rec * REC_BYTES;
+                        mbar_arrive_expect_tx(bar, FA_CODES + 256);
+                        bulk_g2s(sb + at + lane * FA_CODES, src + (value ? REC_V : 0u), FA_CODES, bar);
+                        bulk_g2s(sb + at + 8 * FA_CODES + lane * 256, src + (value ? REC_VSZ : REC_KSZ), 256, bar);
+                    } else {
+                        if (tile.rec == -1) {      // a page id outside the cache: zeros
+                            const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+                            for (uint32_t k = 0; k < FA_CODES; k += 16) *reinterpret_cast<uint4 *>(blk + at + lane * FA_CODES + k) = zero;
+                            for (uint32_t k = 0; k < 256; k += 16) *reinterpret_cast<uint4 *>(blk + at + 8 * FA_CODES + lane * 256 + k) = zero;
+                            fence_proxy_async_smem();
+                        }
+                        mbar_arrive(bar);
+                    }
+                    if (tile.sees < 0) break;
+                    i = n + 1;                     // tiles loaded
+                }
             }
             if (!ok) {                             // copies in flight land before the CTA exits
                 if (lane == 0) ss.abort = 1;
-                for (uint32_t k = i > FA_STAGES ? i - FA_STAGES : 0; k < i; ++k) wait_full(k);
+                if (Q4)
+                    for (uint32_t k = i > 2 ? i - 2 : 0; k < i; ++k) mbar_wait_bounded(smem_u32(&ss.t_full[k & 1]), (k >> 1) & 1);
+                else
+                    for (uint32_t k = i > Fa<Q4>::STAGES ? i - Fa<Q4>::STAGES : 0; k < i; ++k) wait_full(k);
                 if (piece > 0) mbar_wait_bounded(smem_u32(&ss.q_full), (piece - 1) & 1);
             }
         } else if (warp == 1) {
@@ -208,10 +305,10 @@ __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk)
                             tc::mma_f16(tm + FA_S + (u & 1) * 128,
-                                        tc::sw128_desc(sb + FA_Q + (2 * half + (kk >> 2)) * FA_BOX + (kk & 3) * 32),
+                                        tc::sw128_desc(sb + Fa<Q4>::Q + (2 * half + (kk >> 2)) * FA_BOX + (kk & 3) * 32),
                                         tc::sw128_desc(stage(i) + (kk >> 2) * FA_BOX + (kk & 3) * 32), id,
                                         half + kk > 0 ? 1u : 0u);
-                        tc::mma_commit(smem_u32(&ss.empty[i % FA_STAGES]));
+                        tc::mma_commit(smem_u32(&ss.empty[i % Fa<Q4>::STAGES]));
                     }
                     if (!ok) break;
                     tc::mma_commit(smem_u32(&ss.s_full[u & 1]));
@@ -249,7 +346,7 @@ __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_
                             tc::mma_f16_tmem_a(tm + FA_O + half * 128, tm + FA_S + (u & 1) * 128 + kk * 8,
                                                tc::sw128_mn_desc(stage(i) + kk * 2048, FA_BOX), id,
                                                w.j + kk > 0 ? 1u : 0u);
-                        tc::mma_commit(smem_u32(&ss.empty[i % FA_STAGES]));
+                        tc::mma_commit(smem_u32(&ss.empty[i % Fa<Q4>::STAGES]));
                     }
                     if (!ok) break;
                     tc::mma_commit(smem_u32(&ss.pv_done[u & 1]));
@@ -260,7 +357,51 @@ __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_
                 tc::mma_commit(smem_u32(&ss.done[1]));
                 mbar_wait_bounded(smem_u32(&ss.done[1]), 0u);
             }
-        } else if (warp >= 4) {
+        }
+        } else if (Q4 && warp >= 12) {
+            set_registers_down<104>();
+            // ---- tiles of codes to bf16 stages: thread t has row t / 8 and dims 8 (t % 8) .. of each group
+            // of every record, two groups (a stage) at a time
+            const int t = tid - 384, rr = t >> 3, ch = t & 7;
+            bool ok = true;
+            uint32_t i = 0;
+            for (uint32_t n = 0;; ++n) {
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&ss.t_full[n & 1]), (n >> 1) & 1) && !aborted);
+                if (!ok) break;
+                const int sees = *const_cast<const volatile int *>(&ss.t_sees[n & 1]);
+                if (sees < 0) break;
+                const unsigned char *codes = blk + Fa<Q4>::TILES + (n & 1) * FA_TILE_BYTES + 16 * t;
+                const unsigned char *steps = blk + Fa<Q4>::TILES + (n & 1) * FA_TILE_BYTES + 8 * FA_CODES + 16 * rr;
+                for (int half = 0; half < 2; ++half, ++i) {
+                    if (i >= Fa<Q4>::STAGES)
+                        ok = mbar_wait_bounded(smem_u32(&ss.empty[i % Fa<Q4>::STAGES]), (i / Fa<Q4>::STAGES - 1) & 1);
+                    ok = __all_sync(0xffffffffu, ok && !aborted);
+                    if (!ok) break;
+                    unsigned char *dst = blk + (stage(i) - sb) + rr * 128 + ((ch ^ (rr & 7)) << 4);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const uint2 w = *reinterpret_cast<const uint2 *>(codes + k * FA_CODES + 8 * half);
+                        uint2 z = *reinterpret_cast<const uint2 *>(steps + k * 256 + 8 * half);
+                        if (16 * k + rr >= sees) z = make_uint2(0u, 0u);   // past the context: zeros, whatever is there
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            const uint32_t c = g == 0 ? w.x : w.y, sz = g == 0 ? z.x : z.y;
+                            const uint32_t s2 = __byte_perm(sz, sz, 0x1010), z2 = __byte_perm(sz, sz, 0x3232);
+                            const uint32_t v0 = value_pair(c, 0, s2, z2), v1 = value_pair(c, 1, s2, z2);
+                            const uint32_t v2 = value_pair(c, 2, s2, z2), v3 = value_pair(c, 3, s2, z2);
+                            *reinterpret_cast<uint4 *>(dst + g * FA_BOX + k * 2048) =
+                                make_uint4(__byte_perm(v0, v1, 0x5410), __byte_perm(v2, v3, 0x5410), __byte_perm(v0, v1, 0x7632), __byte_perm(v2, v3, 0x7632));
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    mbar_arrive(smem_u32(&ss.full[i % Fa<Q4>::STAGES]));
+                }
+                if (!ok) break;
+                mbar_arrive(smem_u32(&ss.t_empty[n & 1]));
+            }
+            if (!ok && lane == 0) ss.abort = 1;
+        } else {
+            if (Q4) set_registers_up<168>();
             // ---- softmax and epilogue: threads r of both groups share query row r of the item; group 0
             // has positions 0-63 of a tile and dims 0-127 of the output, group 1 the others
             const int r = tid & 127, q4 = warp & 3, grp = (warp >> 2) - 1;
@@ -353,7 +494,7 @@ __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_
                         tc::wait_st();
                     }
                     if (!ok) break;
-                    if (p0 + PG_TILE > sees) {
+                    if (!Q4 && p0 + PG_TILE > sees) {
                         // the tile's positions that no token of the item sees: their value rows become
                         // zeros, whatever the cache (or an earlier tile) left there (0 * NaN is NaN). The
                         // previous unit's products are waited for first: they free the stages' earlier use,
@@ -384,22 +525,26 @@ __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_
                 // unrolled it took 13,000 cycles per piece, most of them for that.
                 const bool mine = r < rows, whole = w.whole(), gated = whole && a.gate != nullptr;
                 const int row0 = w.t.row0 + PG_TOK * w.tile, h0 = KV_G * w.head;
-                const int er = lane >> 3, ec = lane & 7;       // copy i of a lane: row 4 i + er of the warp's 32, chunk ec
-                unsigned char *box = blk + FA_EPI + (warp - 4) * 4096;
-                // row 32 q4 + 4 i + er is token 4 q4 + i / 2, head 4 (i & 1) + er
-                uint4 gate[8];
-                const bf16 *gsrc = a.gate + (row0 + 4 * q4) * a.gate_row + (h0 + er) * a.gate_head + 128 * grp + 8 * ec;
+                // box rows of PART dims, the 16-byte chunk c of row k at place c ^ (k / (128 / row bytes)): no
+                // bank conflicts by rows nor by threads. Copy i of a lane: row RPC i + er, chunk ec.
+                constexpr int PART = Fa<Q4>::PART, CH = PART / 8, RPC = 32 / CH, COPIES = 32 / RPC;
+                const int er = lane / CH, ec = lane % CH;
+                auto place = [&](int k, int c) { return k * PART * 2 + ((c ^ ((k * CH >> 3) & (CH - 1))) << 4); };
+                unsigned char *box = blk + Fa<Q4>::EPI + (warp - 4) * Fa<Q4>::BOX;
+                // row 32 q4 + k is token 4 q4 + k / 8, head k % 8
+                uint4 gate[COPIES];
+                const bf16 *gsrc = a.gate + (row0 + 4 * q4) * a.gate_row + (h0 + (er & 7)) * a.gate_head + 128 * grp + 8 * ec;
                 auto load_gate = [&](int part) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        gate[i] = 4 * q4 + (i >> 1) < rows >> 3
-                                      ? __ldg(reinterpret_cast<const uint4 *>(gsrc + (i >> 1) * a.gate_row + 4 * (i & 1) * a.gate_head + 64 * part))
+                    for (int i = 0; i < COPIES; ++i)
+                        gate[i] = 4 * q4 + (RPC * i >> 3) < rows >> 3
+                                      ? __ldg(reinterpret_cast<const uint4 *>(gsrc + (RPC * i >> 3) * a.gate_row + (RPC * i & 7) * a.gate_head + PART * part))
                                       : make_uint4(0u, 0u, 0u, 0u);
                 };
                 if (gated && live) load_gate(0);
                 reinterpret_cast<float *>(box)[lane] = l;      // the row's sum over both groups
                 pair_bar();
-                const float l1 = reinterpret_cast<const float *>(blk + FA_EPI + ((warp - 4) ^ 4) * 4096)[lane];
+                const float l1 = reinterpret_cast<const float *>(blk + Fa<Q4>::EPI + ((warp - 4) ^ 4) * Fa<Q4>::BOX)[lane];
                 l = grp == 0 ? l + l1 : l1 + l;
                 pair_bar();
                 ok = __all_sync(0xffffffffu, wait_pv(u - 1) && !aborted);
@@ -410,23 +555,22 @@ __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_
                     const bool blank = __any_sync(0xffffffffu, l == 0.0f);   // a row that saw nothing gives zeros
                     TO *out = static_cast<TO *>(a.out);
 #pragma unroll 1
-                    for (int part = 0; part < 2; ++part) {
+                    for (int part = 0; part < 128 / PART; ++part) {
                         if (gated) {
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                *reinterpret_cast<uint4 *>(box + (4 * i + er) * 128 + ((ec ^ ((4 * i + er) & 7)) << 4)) = gate[i];
+                            for (int i = 0; i < COPIES; ++i) *reinterpret_cast<uint4 *>(box + place(RPC * i + er, ec)) = gate[i];
                             __syncwarp();
-                            if (part == 0) load_gate(1);
+                            if (part + 1 < 128 / PART) load_gate(part + 1);
                         }
 #pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {          // 16 dims
-                            const int d = 128 * grp + 64 * part + 16 * c;
+                        for (int c = 0; c < PART / 16; ++c) {  // 16 dims
+                            const int d = 128 * grp + PART * part + 16 * c;
                             float o[16];
                             tc::tmem_ld16(lbase + FA_O + d, o);
                             uint4 *at[2], g[2];
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
-                                at[i] = reinterpret_cast<uint4 *>(box + lane * 128 + (((2 * c + i) ^ (lane & 7)) << 4));
+                                at[i] = reinterpret_cast<uint4 *>(box + place(lane, 2 * c + i));
                                 g[i] = gated ? *at[i] : make_uint4(0u, 0u, 0u, 0u);
                             }
                             tc::wait_ld();
@@ -455,15 +599,14 @@ __global__ void __launch_bounds__(FA_THREADS, 1) attn_paged_kernel(const __grid_
                             __syncwarp();
                         }
                         if (whole && sizeof(TO) == 2) {
-                            uint4 v[8];
-                            TO *dst = out + ((size_t)(row0 + 4 * q4) * KV_HQ + h0 + er) * KV_D + 128 * grp + 64 * part + 8 * ec;
+                            uint4 v[COPIES];
+                            TO *dst = out + ((size_t)(row0 + 4 * q4) * KV_HQ + h0 + (er & 7)) * KV_D + 128 * grp + PART * part + 8 * ec;
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                v[i] = *reinterpret_cast<const uint4 *>(box + (4 * i + er) * 128 + ((ec ^ ((4 * i + er) & 7)) << 4));
+                            for (int i = 0; i < COPIES; ++i) v[i] = *reinterpret_cast<const uint4 *>(box + place(RPC * i + er, ec));
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                if (4 * q4 + (i >> 1) < rows >> 3)
-                                    *reinterpret_cast<uint4 *>(dst + ((i >> 1) * KV_HQ + 4 * (i & 1)) * KV_D) = v[i];
+                            for (int i = 0; i < COPIES; ++i)
+                                if (4 * q4 + (RPC * i >> 3) < rows >> 3)
+                                    *reinterpret_cast<uint4 *>(dst + ((RPC * i >> 3) * KV_HQ + (RPC * i & 7)) * KV_D) = v[i];
                             __syncwarp();
                         }
                     }
@@ -606,6 +749,8 @@ static bool encode_q_map(CUtensorMap *map, const void *q, int M)
     return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// New tokens of a sequence up to which a 4-bit cache is read token by token.
+constexpr int Q4_SINGLE = 1;
 constexpr int FA_RANGES = 152;                    // one CTA per SM
 constexpr size_t START_BYTES = (PG_MAX_CTAS * sizeof(PagedStart) + 255) / 256 * 256;
 
@@ -616,18 +761,17 @@ size_t paged_workspace_bytes(const gdn_paged_batch *b, const gdn_kv_cache *)
     return START_BYTES + (size_t)2 * FA_RANGES * piece_rows(b->max_q) * (KV_D + 2) * sizeof(float);
 }
 
-template <typename TO>
-static cudaError_t launch_bf16(const PagedArgs &a, cudaStream_t s)
+template <typename TO, bool Q4>
+static cudaError_t launch_tiles(const PagedArgs &a, cudaStream_t s)
 {
-    CUtensorMap qm, km, vm;
+    CUtensorMap qm, km = {}, vm = {};
     const long long rows = (long long)a.b.num_pages * KV_H * a.b.page;
-    if (!encode_q_map(&qm, a.q, a.b.M) || !make_bf16_sw128_map(&km, a.ck, rows, KV_D, a.b.page) ||
-        !make_bf16_sw128_map(&vm, a.cv, rows, KV_D, a.b.page))
+    if (!encode_q_map(&qm, a.q, a.b.M) ||
+        (!Q4 && (!make_bf16_sw128_map(&km, a.ck, rows, KV_D, a.b.page) || !make_bf16_sw128_map(&vm, a.cv, rows, KV_D, a.b.page))))
         return cudaErrorInvalidValue;
-    cudaError_t e = smem_attr_once<attn_paged_kernel<TO>>(FA_SMEM);
+    const cudaError_t e = smem_attr_once<attn_paged_kernel<TO, Q4>>(FA_SMEM<Q4>);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(attn_paged_kernel<TO>, dim3(a.ranges), dim3(FA_THREADS), FA_SMEM, s, qm, km, vm, a);
-    return e;
+    return launch_pdl(attn_paged_kernel<TO, Q4>, dim3(a.ranges), dim3(fa_threads(Q4)), FA_SMEM<Q4>, s, qm, km, vm, a);
 }
 
 cudaError_t launch_attn_paged(const gdn_paged_batch *b, const gdn_kv_cache *c, const void *q, const void *gate,
@@ -653,14 +797,16 @@ cudaError_t launch_attn_paged(const gdn_paged_batch *b, const gdn_kv_cache *c, c
     a.part_o = (float *)((char *)ws + START_BYTES);
     a.part_ml = a.part_o + (size_t)2 * a.ranges * a.rows * KV_D;
     cudaError_t e;
-    if (c->format == GDN_KV_Q4) {
+    if (c->format == GDN_KV_Q4 && b->max_q <= Q4_SINGLE) {
         a.tok = 1;
         a.tok_log2 = 0;
         a.rows = KV_G;
         a.lead = 2;
         e = launch_paged_q4(a, out_dt, s);
+    } else if (c->format == GDN_KV_Q4) {
+        e = out_dt == GDN_F32 ? launch_tiles<float, true>(a, s) : launch_tiles<bf16, true>(a, s);
     } else {
-        e = out_dt == GDN_F32 ? launch_bf16<float>(a, s) : launch_bf16<bf16>(a, s);
+        e = out_dt == GDN_F32 ? launch_tiles<float, false>(a, s) : launch_tiles<bf16, false>(a, s);
     }
     return e == cudaSuccess ? launch_paged_join(a, out_dt, s) : e;
 }
