@@ -79,7 +79,8 @@ static_assert(FA_SMEM<false> <= 232448 && FA_SMEM<true> <= 232448, "shared memor
 // by one logic operation, minus 128 exactly).
 __device__ __forceinline__ uint32_t value_pair(uint32_t w, int t, uint32_t s2, uint32_t z2)
 {
-    uint32_t c = ((w >> (4 * t)) & 0x000F000Fu) | 0x43004300u, v;
+    uint32_t c, v;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(c) : "r"(w >> (4 * t)), "r"(0x000F000Fu), "r"(0x43004300u));   // (w & b) | c
     asm("sub.rn.bf16x2 %0, %0, %1;" : "+r"(c) : "r"(0x43004300u));
     asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(v) : "r"(c), "r"(s2), "r"(z2));
     return v;
@@ -378,10 +379,16 @@ __global__ void __launch_bounds__(fa_threads(Q4), 1) attn_paged_kernel(const __g
                     ok = __all_sync(0xffffffffu, ok && !aborted);
                     if (!ok) break;
                     unsigned char *dst = blk + (stage(i) - sb) + rr * 128 + ((ch ^ (rr & 7)) << 4);
+                    uint2 code[8], step[8];        // all of them first: the compiler keeps loads behind stores
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        const uint2 w = *reinterpret_cast<const uint2 *>(codes + k * FA_CODES + 8 * half);
-                        uint2 z = *reinterpret_cast<const uint2 *>(steps + k * 256 + 8 * half);
+                        code[k] = *reinterpret_cast<const uint2 *>(codes + k * FA_CODES + 8 * half);
+                        step[k] = *reinterpret_cast<const uint2 *>(steps + k * 256 + 8 * half);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const uint2 w = code[k];
+                        uint2 z = step[k];
                         if (16 * k + rr >= sees) z = make_uint2(0u, 0u);   // past the context: zeros, whatever is there
 #pragma unroll
                         for (int g = 0; g < 2; ++g) {
