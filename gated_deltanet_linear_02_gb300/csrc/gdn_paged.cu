@@ -654,18 +654,28 @@ __global__ void __launch_bounds__(256) attn_paged_join_kernel(const PagedArgs a)
     const PagedStart st = a.start[c];
     // the item's first step, and the step of its first unit: a cut at or before that one cuts nothing
     const long long u = range_begin(st, c, a.ranges), begin = u - st.step, unit0 = begin + a.lead;
-    if (u >= range_begin(st, a.ranges, a.ranges) || u <= unit0) return;
-    const SeqTokens t = seq_tokens(a.b, st.seq);
+    const long long total = range_begin(st, a.ranges, a.ranges);
+    if (u >= total || u <= unit0) return;
+    const SeqTokens t = st.t;
     const long long end = unit0 + tile_units(a, t, st.tile);
-    int head = c - (int)((u - unit0 - 1) / (st.quot + 1));   // the item's first cut, at most
-    while (range_begin(st, head - 1, a.ranges) > unit0) --head;
-    int last = c + (int)((end - u - 1) / (st.quot + 1));     // its last range, at least
-    while (last + 1 < a.ranges && range_begin(st, last + 1, a.ranges) < end) ++last;
+    // range_begin(k) is floor(total k / ranges): the first cut above unit0, and the last below end
+    int head, last;
+    if (total < 0xFFFFFFFFll / PG_MAX_CTAS) {
+        head = (int)(((uint32_t)(unit0 + 1) * a.ranges + (uint32_t)total - 1) / (uint32_t)total);
+        last = (int)(((uint32_t)end * a.ranges - 1) / (uint32_t)total);
+    } else {
+        head = (int)(((unit0 + 1) * a.ranges + total - 1) / total);
+        last = (int)((end * a.ranges - 1) / total);
+    }
     const int rows = KV_G * min(a.tok, t.n - (st.tile << a.tok_log2));
     const int ctas = (last - head + 1) * gridDim.y, cta = (c - head) * gridDim.y + blockIdx.y;
     int per = 1;                                       // rows of a CTA: a power of two up to 8
     while (per < 8 && per * ctas < rows) per <<= 1;
     const int share = 8 / per, r = cta * per + warp / share, part = warp % share;
+    const int mrow = t.row0 + (st.tile << a.tok_log2) + (r >> 3), h = KV_G * st.head + (r & 7);
+    uint4 gate = make_uint4(0u, 0u, 0u, 0u);
+    const bool gated = a.gate != nullptr && r < rows && part == 0;
+    if (gated) gate = __ldg(reinterpret_cast<const uint4 *>(a.gate + mrow * a.gate_row + h * a.gate_head) + lane);
     float M = -INFINITY, l = 0.0f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     for (int k0 = head - 1 + part; k0 <= last && r < rows; k0 += 4 * share) {
         float2 ml[4];
@@ -715,9 +725,13 @@ __global__ void __launch_bounds__(256) attn_paged_join_kernel(const PagedArgs a)
             for (int i = 0; i < 8; ++i) o[i] += g * so[k][8 * lane + i];
         }
     }
-    if (r < rows)
-        finish8<TO>(a, t.row0 + (st.tile << a.tok_log2) + (r >> 3), KV_G * st.head + (r & 7), 8 * lane, o,
-                    l != 0.0f ? 1.0f / l : 0.0f);
+    if (r >= rows) return;
+    const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+    if (gated) gate8(gate, o, inv);
+    else
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] *= inv;
+    store8_out(static_cast<TO *>(a.out) + ((size_t)mrow * KV_HQ + h) * KV_D + 8 * lane, o);
 }
 
 // ------------------------------------------------------------------ launcher

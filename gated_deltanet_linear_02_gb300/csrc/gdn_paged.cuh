@@ -46,18 +46,19 @@ struct PagedArgs {
     int tok, tok_log2;                            // tokens per item: 16 or 1
 };
 
-// Where a range starts; the whole call has quot * ranges + rem steps.
-struct PagedStart {
-    long long quot;
-    int rem;
-    int seq, tile, head, step;
-};
-
 // One sequence's new tokens: packed rows [row0, row0 + n) at positions first,
 // first + 1, ...
 struct SeqTokens {
     int row0, n, first;
 };
+// Where a range starts; the whole call has quot * ranges + rem steps.
+struct PagedStart {
+    long long quot;
+    int rem;
+    int seq, tile, head, step;
+    SeqTokens t;                                  // of sequence seq
+};
+
 __device__ __forceinline__ SeqTokens seq_tokens(const PagedBatch &b, int s)
 {
     SeqTokens t;
@@ -151,8 +152,13 @@ __device__ __forceinline__ void find_start(const PagedArgs &a, int c, long long 
     __syncthreads();
     const long long total = scan[THREADS / 32 - 1], before = incl - mine + (warp > 0 ? scan[warp - 1] : 0);
     PagedStart cuts;
-    cuts.quot = total / a.ranges;
-    cuts.rem = (int)(total % a.ranges);
+    if (total < 0x7FFFFFFF) {                      // a 64-bit division takes four times as long
+        cuts.quot = (uint32_t)total / (uint32_t)a.ranges;
+        cuts.rem = (int)((uint32_t)total % (uint32_t)a.ranges);
+    } else {
+        cuts.quot = total / a.ranges;
+        cuts.rem = (int)(total % a.ranges);
+    }
     const long long u = range_begin(cuts, c, a.ranges);
     if (tid == 0) {
         out->quot = cuts.quot;
@@ -182,6 +188,7 @@ __device__ __forceinline__ void find_start(const PagedArgs &a, int c, long long 
         out->tile = lo;
         out->head = (int)(left / n);
         out->step = (int)(left % n);
+        out->t = t;
     }
     __syncthreads();
 }
@@ -209,7 +216,7 @@ struct PieceWalk {
         tile = s.tile;
         head = s.head;
         first = true;
-        t = seq_tokens(a.b, seq);
+        t = s.t;
         cut(a, s.step, count);                    // ends inside the leading steps: no piece, and left = 0
     }
     // Whether the range has a piece after this one: what is left reaches past the
@@ -304,20 +311,7 @@ __device__ __forceinline__ void gate8(const uint4 u, float (&o)[8], float inv)
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i] *= gate1(__uint_as_float((i & 1) ? (w[i >> 1] & 0xFFFF0000u) : (w[i >> 1] << 16)), inv);
 }
-// Normalised output times the gate, 8 dims from dim d of (packed row m, head h).
-template <typename TO>
-__device__ __forceinline__ void finish8(const PagedArgs &a, int m, int h, int d, float (&o)[8], float inv)
-{
-    if (a.gate != nullptr) {
-        gate8(__ldg(reinterpret_cast<const uint4 *>(a.gate + m * a.gate_row + h * a.gate_head + d)), o, inv);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] *= inv;
-    }
-    store8_out(static_cast<TO *>(a.out) + ((size_t)m * KV_HQ + h) * KV_D + d, o);
-}
-
-// The same for 4 dims.
+// Normalised output times the gate, 4 dims from dim d of (packed row m, head h).
 template <typename TO>
 __device__ __forceinline__ void finish4(const PagedArgs &a, int m, int h, int d, float4 o, float inv)
 {

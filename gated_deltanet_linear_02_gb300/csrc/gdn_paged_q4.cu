@@ -233,6 +233,12 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) attn_paged_q4_kernel(const __gr
         auto fetch = [&]() {
             Rec r = {more, false, 0, 0};
             if (!more) return r;
+            const int p = w.unit * PG_TILE + 16 * (base + lane), end = piece_end(w);
+            if (lane < DQ_WARPS && p < end) {
+                r.mine = true;
+                r.page = __ldg(b.table + (size_t)w.seq * b.max_pages + (p >> b.page_log2));
+                r.in_page = (w.head << b.page_log2) + (p & (b.page - 1));
+            }
             if (base == 0) {                       // a piece begins: its queries
                 const uint32_t qb = piece % DQ_QUERIES;
                 if (piece >= DQ_QUERIES)
@@ -248,12 +254,6 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) attn_paged_q4_kernel(const __gr
                 ++piece;
                 if (a.gate != nullptr && w.whole())    // and its gates, for the epilogue: 128 bytes per lane
                     asm volatile("prefetch.global.L2 [%0];" ::"l"(a.gate + m * a.gate_row + (KV_G * w.head + (lane >> 2)) * a.gate_head + 64 * (lane & 3)));
-            }
-            const int p = w.unit * PG_TILE + 16 * (base + lane), end = piece_end(w);
-            if (lane < DQ_WARPS && p < end) {
-                r.mine = true;
-                r.page = __ldg(b.table + (size_t)w.seq * b.max_pages + (p >> b.page_log2));
-                r.in_page = (w.head << b.page_log2) + (p & (b.page - 1));
             }
             base += DQ_WARPS;
             if (w.unit * PG_TILE + 16 * base >= end) {
