@@ -405,12 +405,20 @@ def _one_device(*tensors):
     return devs.pop() if devs else None
 
 
+_one_gpu = None          # cuda:0 where it is the only device, so that it is the current one
+
+
 def _on_current(device, where: str) -> torch.device:
     """The library launches on the current device: tensors of another one are refused."""
+    global _one_gpu
+    if device == _one_gpu:
+        return device
     if device.type != "cuda":
         raise ValueError(f"{where}: tensors must be on a CUDA device, not {device}")
     if device.index != torch.cuda.current_device():
         raise ValueError(f"{where}: tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+    if torch.cuda.device_count() == 1:
+        _one_gpu = device
     return device
 
 
@@ -469,17 +477,18 @@ def attn_qk_norm_rope(params: gdn_attn_params, q, positions, q_out, k=None, k_ou
         raise ValueError(f"the parameters are on {params._device}, expected {dev}")
     qp, qr, qh = _heads(q, "q", M, ATTN_HQ, dev)
     kp, kr, kh = _heads(k, "k", M, ATTN_HKV, dev, q.dtype)
-    st = lib().gdn_attn_qk_norm_rope(params._ref, qp, qr, qh, kp, kr, kh,
+    st = (_lib or lib()).gdn_attn_qk_norm_rope(params._ref, qp, qr, qh, kp, kr, kh,
                                      _dense(positions, "positions", (M,), dev, torch.int32), M,
                                      _dense(q_out, "q_out", (M, ATTN_HQ, ATTN_D), dev),
                                      _dense(k_out, "k_out", (M, ATTN_HKV, ATTN_D), dev, q_out.dtype), _act_dtype(q),
                                      _act_dtype(q_out), _raw_stream(stream, dev))
-    _check(st, "gdn_attn_qk_norm_rope")
+    if st:
+        _check(st, "gdn_attn_qk_norm_rope")
 
 
 def _on_batch(batch, cache, where: str, params=None):
     dev = _on_current(batch._device, where)
-    if cache._device != dev or (params is not None and params._device not in (None, dev)):
+    if cache._device != dev or (params is not None and params._device is not None and params._device != dev):
         raise ValueError(f"{where}: batch, cache and parameters are on different devices")
     return dev
 
@@ -495,11 +504,12 @@ def kv_append(params: gdn_attn_params, batch: gdn_paged_batch, cache: gdn_kv_cac
     kp, kr, kh = _heads(k, "k", M, ATTN_HKV, dev)
     vp, vr, vh = _heads(v, "v", M, ATTN_HKV, dev, k.dtype)
     qp, qr, qh = _heads(q, "q", M, ATTN_HQ, dev, k.dtype)
-    st = lib().gdn_kv_append(params._ref, batch._ref, cache._ref, kp, kr, kh, vp, vr, vh, qp, qr, qh,
+    st = (_lib or lib()).gdn_kv_append(params._ref, batch._ref, cache._ref, kp, kr, kh, vp, vr, vh, qp, qr, qh,
                              _dense(q_out, "q_out", (M, ATTN_HQ, ATTN_D), dev, torch.bfloat16),
                              _dense(positions, "positions", (M,), dev, torch.int32), _act_dtype(k),
                              _raw_stream(stream, dev))
-    _check(st, "gdn_kv_append")
+    if st:
+        _check(st, "gdn_kv_append")
 
 
 def kv_gather(batch: gdn_paged_batch, cache: gdn_kv_cache, k_out, v_out, stream=None):
@@ -509,10 +519,11 @@ def kv_gather(batch: gdn_paged_batch, cache: gdn_kv_cache, k_out, v_out, stream=
     some = k_out if k_out is not None else v_out
     if some is None:
         return
-    st = lib().gdn_kv_gather(batch._ref, cache._ref, _dense(k_out, "k_out", (M, ATTN_HKV, ATTN_D), dev, some.dtype),
+    st = (_lib or lib()).gdn_kv_gather(batch._ref, cache._ref, _dense(k_out, "k_out", (M, ATTN_HKV, ATTN_D), dev, some.dtype),
                              _dense(v_out, "v_out", (M, ATTN_HKV, ATTN_D), dev, some.dtype), _act_dtype(some),
                              _raw_stream(stream, dev))
-    _check(st, "gdn_kv_gather")
+    if st:
+        _check(st, "gdn_kv_gather")
 
 
 def attn_paged_workspace_size(batch: gdn_paged_batch, cache: gdn_kv_cache) -> int:
@@ -528,10 +539,11 @@ def attn_paged(batch: gdn_paged_batch, cache: gdn_kv_cache, q, out, gate=None, w
     gp, gr, gh = _heads(gate, "gate", M, ATTN_HQ, dev, torch.bfloat16)
     if workspace is None:
         workspace = torch.empty(max(attn_paged_workspace_size(batch, cache), 256), dtype=torch.uint8, device=dev)
-    st = lib().gdn_attn_paged(batch._ref, cache._ref, _dense(q, "q", (M, ATTN_HQ, ATTN_D), dev, torch.bfloat16), gp, gr, gh,
+    st = (_lib or lib()).gdn_attn_paged(batch._ref, cache._ref, _dense(q, "q", (M, ATTN_HQ, ATTN_D), dev, torch.bfloat16), gp, gr, gh,
                               _dense(out, "out", (M, ATTN_HQ, ATTN_D), dev), _dense(workspace, "workspace", workspace.shape, dev),
                               workspace.nbytes, _act_dtype(out), _raw_stream(stream, dev))
-    _check(st, "gdn_attn_paged")
+    if st:
+        _check(st, "gdn_attn_paged")
     return workspace
 
 
