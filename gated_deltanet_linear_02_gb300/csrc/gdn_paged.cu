@@ -13,7 +13,7 @@
 // 2^8, l and O lose nothing in fp32, and the rescale, a round trip of the whole
 // accumulator, happens a few times per context instead of at every tile.
 //
-// Roles in a CTA (one per SM, 384 threads):
+// Roles in a CTA (one per SM, 384 threads, 640 with 4-bit pages):
 //  - warp 0, TMA producer: 32 KiB stages of 128 positions x 128 dims (keys low,
 //    high, values low, high), one box per page and 64 dims, in a ring of four;
 //    the next tile's keys ahead of this tile's values, as the MMAs use them;
@@ -22,7 +22,12 @@
 //    tensor core idle for half of every unit: 2.6 us instead of 1.6);
 //  - warps 4-11, two threads per query row, each with half of a tile's positions
 //    and half of the output's dims: softmax, rescale, and the epilogue (normalise
-//    and gate, or store the piece's unnormalised output).
+//    and gate, or store the piece's unnormalised output);
+//  - warps 12-19, with 4-bit pages only: codes to bf16. The producer then copies
+//    the eight records' key or value codes of a tile (18 KiB, a quarter of the
+//    values) into one of two buffers, and these warps write the stages, a ring of
+//    three. Four warps instead of eight: 173 us instead of 162 for three sequences
+//    of 517 tokens over contexts of 6,001.
 // Tensor memory: two S buffers (P over their first half) and O, all 512 columns.
 //
 // Bound: for one token per sequence by HBM (1 KiB of keys and values per position
@@ -39,7 +44,8 @@ namespace gdn {
 
 __device__ unsigned int g_paged_error;            // GDN_ERR_TIMEOUT if a bounded wait gave up
 
-constexpr int fa_threads(bool q4) { return q4 ? 512 : 384; }
+constexpr int FA_DEQUANT = 256;                   // threads that turn codes to bf16
+constexpr int fa_threads(bool q4) { return 384 + (q4 ? FA_DEQUANT : 0); }
 constexpr uint32_t FA_BOX = PG_TILE * 128;        // 128 rows x 64 dims of bf16: 16 KiB
 constexpr uint32_t FA_STAGE_BYTES = 2 * FA_BOX;   // 128 dims: 32 KiB
 constexpr uint32_t FA_S = 0, FA_O = 256;          // tensor memory columns: S buffers at 0 and 128, O at 256
@@ -110,7 +116,7 @@ __global__ void __launch_bounds__(fa_threads(Q4), 1) attn_paged_kernel(const __g
 
     if (tid == 0) {
         for (int s = 0; s < Fa<Q4>::STAGES; ++s) {
-            mbar_init(smem_u32(&ss.full[s]), Q4 ? 128 : 1);
+            mbar_init(smem_u32(&ss.full[s]), Q4 ? FA_DEQUANT : 1);
             mbar_init(smem_u32(&ss.empty[s]), 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -119,7 +125,7 @@ __global__ void __launch_bounds__(fa_threads(Q4), 1) attn_paged_kernel(const __g
             mbar_init(smem_u32(&ss.pv_done[i]), 1);
             mbar_init(smem_u32(&ss.done[i]), 1);
             mbar_init(smem_u32(&ss.t_full[i]), 32);
-            mbar_init(smem_u32(&ss.t_empty[i]), 128);
+            mbar_init(smem_u32(&ss.t_empty[i]), FA_DEQUANT);
         }
         mbar_init(smem_u32(&ss.q_full), 1);
         mbar_init(smem_u32(&ss.q_empty), 1);
@@ -144,259 +150,260 @@ __global__ void __launch_bounds__(fa_threads(Q4), 1) attn_paged_kernel(const __g
     const volatile int &aborted = ss.abort;
     auto stage = [&](uint32_t i) { return sb + Fa<Q4>::RING + (i % Fa<Q4>::STAGES) * FA_STAGE_BYTES; };
     auto wait_full = [&](uint32_t i) {
-        return mbar_wait_bounded(smem_u32(&ss.full[i % Fa<Q4>::STAGES]), (i / Fa<Q4>::STAGES) & 1);
+        return mbar_wait_sleep(smem_u32(&ss.full[i % Fa<Q4>::STAGES]), (i / Fa<Q4>::STAGES) & 1);
     };
 
     PieceWalk first;
     if (count > 0) first.begin(a, st, count);
     if (count > 0 && first.len > 0) {
-        // registers with 4-bit pages: 72 + 2 x 168 + 104 of the 4 x 128 launched with
+        // registers with 4-bit pages: 64 + 2 x 152 + 2 x 56 of the 5 x 96 launched with
         if (warp < 4) {
-        if (Q4) set_registers_down<72>();
-        if (warp == 0) {
-            // ---- TMA producer. Stage order: K(0), then K(u + 1), V(u) for each u.
-            UnitWalk kw;
-            kw.begin(a, st, count);
-            const int seg = lane >> 1, box = lane & 1, nseg = PG_TILE >> b.page_log2;
-            const uint32_t seg_dst = (uint32_t)seg * ((uint32_t)b.page * 128) + box * FA_BOX;
-            uint32_t i = 0, piece = 0;
-            bool ok = true;
-            // row of the cache tensors where this lane's segment of the unit starts; segments past
-            // what the item sees are not loaded, bad page ids load past the end (zeros)
-            auto segment = [&](int &row, int &loaded) {
-                const int p = (kw.w.unit + kw.j) * PG_TILE;
-                const int sees = tile_sees(a, kw.w.t, kw.w.tile);
-                loaded = min(nseg, max(0, (sees - p + b.page - 1) >> b.page_log2));
-                row = 0;
-                if (seg < loaded) {
-                    const int page = cache_page(b, kw.w.seq, p + seg * b.page);
-                    row = page < 0 ? (b.num_pages * KV_H) << b.page_log2 : ((page * KV_H + kw.w.head) << b.page_log2);
-                }
-            };
-            auto load = [&](const CUtensorMap *m, int row, int loaded) {
-                for (int half = 0; half < 2 && ok; ++half, ++i) {
-                    if (i >= Fa<Q4>::STAGES)
-                        ok = mbar_wait_bounded(smem_u32(&ss.empty[i % Fa<Q4>::STAGES]), (i / Fa<Q4>::STAGES - 1) & 1);
-                    ok = __all_sync(0xffffffffu, ok && !aborted);
-                    if (!ok) break;
-                    const uint32_t bar = smem_u32(&ss.full[i % Fa<Q4>::STAGES]);
-                    if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)loaded * b.page * 256);
-                    __syncwarp();
-                    if (seg < loaded) tma_load_2d(stage(i) + seg_dst, m, half * 128 + box * 64, row, bar);
-                }
-            };
-            auto load_q = [&](int row0, int head) {
-                if (piece > 0) ok = mbar_wait_bounded(smem_u32(&ss.q_empty), (piece - 1) & 1);
-                ok = __all_sync(0xffffffffu, ok && !aborted);
-                if (ok && lane == 0) {
-                    const uint32_t bar = smem_u32(&ss.q_full);
-                    mbar_arrive_expect_tx(bar, 4 * FA_BOX);
-                    for (int c = 0; c < 4; ++c)
-                        tma_load_3d(sb + Fa<Q4>::Q + c * FA_BOX, &qmap, 64 * c, KV_G * head, row0, bar);
-                }
-                ++piece;
-            };
-            if (!Q4) {
-                int row, loaded;
-                segment(row, loaded);
-                load_q(kw.w.t.row0 + PG_TOK * kw.w.tile, kw.w.head);
-                if (ok) load(&kmap, row, loaded);
-                while (ok) {
-                    const int vrow = row, vloaded = loaded;
-                    const bool more = !kw.last(a);
-                    if (more) {
-                        kw.next(a);
-                        segment(row, loaded);
-                        if (kw.j == 0) load_q(kw.w.t.row0 + PG_TOK * kw.w.tile, kw.w.head);
-                        if (ok) load(&kmap, row, loaded);
-                    }
-                    if (ok) load(&vmap, vrow, vloaded);
-                    if (!more) break;
-                }
-            } else {
-                // tiles of codes in the same order: the keys of the next unit, unless those of two are
-                // ahead of their values (q0, q1), else the values of the oldest. Lane k: record k.
-                struct Unit {
-                    int rec, sees, row0, head;     // the lane's record (-1: zeros, -2: none), positions seen, the queries
-                    bool first;
-                };
-                Unit q0 = {}, q1 = {}, tile;
-                int ahead = 0, entry = 0;
-                bool have = true;
-                auto look_up = [&]() {             // page table entry of the lane's record of the unit kw is at
-                    const int p = (kw.w.unit + kw.j) * PG_TILE + 16 * lane;
-                    if (lane < 8 && p < tile_sees(a, kw.w.t, kw.w.tile))
-                        entry = __ldg(b.table + (size_t)kw.w.seq * b.max_pages + (p >> b.page_log2));
-                };
-                look_up();
-                for (uint32_t n = 0;; ++n) {
-                    const bool value = !(ahead < 2 && have);
-                    if (!value) {
-                        const int p = (kw.w.unit + kw.j) * PG_TILE, at = (kw.w.head << b.page_log2) + ((p + 16 * lane) & (b.page - 1));
-                        tile.sees = max(min(tile_sees(a, kw.w.t, kw.w.tile) - p, PG_TILE), 0);
-                        tile.rec = lane >= 8 || 16 * lane >= tile.sees ? -2
-                                   : (unsigned)entry < (unsigned)b.num_pages ? (((entry * KV_H) << b.page_log2) + at) >> 4 : -1;
-                        tile.row0 = kw.w.t.row0 + PG_TOK * kw.w.tile;
-                        tile.head = kw.w.head;
-                        tile.first = kw.j == 0;
-                        (ahead++ == 0 ? q0 : q1) = tile;
-                        have = !kw.last(a);
-                        if (have) {
-                            kw.next(a);
-                            look_up();
-                        }
-                        if (tile.first) load_q(tile.row0, tile.head);
-                    } else if (ahead > 0) {
-                        tile = q0;
-                        q0 = q1;
-                        --ahead;
-                    } else {
-                        tile.sees = -1;            // no more
-                        tile.rec = -2;
-                    }
-                    if (n >= 2) ok = ok && mbar_wait_bounded(smem_u32(&ss.t_empty[n & 1]), ((n >> 1) - 1) & 1);
-                    ok = __all_sync(0xffffffffu, ok && !aborted);
-                    if (!ok) break;
-                    const uint32_t bar = smem_u32(&ss.t_full[n & 1]);
-                    const uint32_t at = Fa<Q4>::TILES + (n & 1) * FA_TILE_BYTES;
-                    if (lane == 0) ss.t_sees[n & 1] = tile.sees;
-                    if (tile.rec >= 0) {
-                        const unsigned char *src = static_cast<const unsigned char *>(a.ck) + (size_t)tile.rec * REC_BYTES;
-                        mbar_arrive_expect_tx(bar, FA_CODES + 256);
-                        bulk_g2s(sb + at + lane * FA_CODES, src + (value ? REC_V : 0u), FA_CODES, bar);
-                        bulk_g2s(sb + at + 8 * FA_CODES + lane * 256, src + (value ? REC_VSZ : REC_KSZ), 256, bar);
-                    } else {
-                        if (tile.rec == -1) {      // a page id outside the cache: zeros
-                            const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-                            for (uint32_t k = 0; k < FA_CODES; k += 16) *reinterpret_cast<uint4 *>(blk + at + lane * FA_CODES + k) = zero;
-                            for (uint32_t k = 0; k < 256; k += 16) *reinterpret_cast<uint4 *>(blk + at + 8 * FA_CODES + lane * 256 + k) = zero;
-                            fence_proxy_async_smem();
-                        }
-                        mbar_arrive(bar);
-                    }
-                    if (tile.sees < 0) break;
-                    i = n + 1;                     // tiles loaded
-                }
-            }
-            if (!ok) {                             // copies in flight land before the CTA exits
-                if (lane == 0) ss.abort = 1;
-                if (Q4)
-                    for (uint32_t k = i > 2 ? i - 2 : 0; k < i; ++k) mbar_wait_bounded(smem_u32(&ss.t_full[k & 1]), (k >> 1) & 1);
-                else
-                    for (uint32_t k = i > Fa<Q4>::STAGES ? i - Fa<Q4>::STAGES : 0; k < i; ++k) wait_full(k);
-                if (piece > 0) mbar_wait_bounded(smem_u32(&ss.q_full), (piece - 1) & 1);
-            }
-        } else if (warp == 1) {
-            // ---- issuer of S(u) = Q K^T
-            if (lane == 0) {
-                const uint32_t id = tc::instr_desc(tc::FMT_BF16, 128, PG_TILE);
-                UnitWalk w;
-                w.begin(a, st, count);
+            if (Q4) set_registers_down<64>();
+            if (warp == 0) {
+                // ---- TMA producer. Stage order: K(0), then K(u + 1), V(u) for each u.
+                UnitWalk kw;
+                kw.begin(a, st, count);
+                const int seg = lane >> 1, box = lane & 1, nseg = PG_TILE >> b.page_log2;
+                const uint32_t seg_dst = (uint32_t)seg * ((uint32_t)b.page * 128) + box * FA_BOX;
                 uint32_t i = 0, piece = 0;
                 bool ok = true;
-                for (uint32_t u = 0; ok; ++u) {
-                    if (w.j == 0) ok = mbar_wait_bounded(smem_u32(&ss.q_full), piece++ & 1);
-                    // the buffer holds P of unit u - 2 until its product is complete
-                    if (u >= 2) ok = ok && mbar_wait_bounded(smem_u32(&ss.pv_done[u & 1]), ((u - 2) >> 1) & 1);
-                    if (u == 1) i = 2;
+                // row of the cache tensors where this lane's segment of the unit starts; segments past
+                // what the item sees are not loaded, bad page ids load past the end (zeros)
+                auto segment = [&](int &row, int &loaded) {
+                    const int p = (kw.w.unit + kw.j) * PG_TILE;
+                    const int sees = tile_sees(a, kw.w.t, kw.w.tile);
+                    loaded = min(nseg, max(0, (sees - p + b.page - 1) >> b.page_log2));
+                    row = 0;
+                    if (seg < loaded) {
+                        const int page = cache_page(b, kw.w.seq, p + seg * b.page);
+                        row = page < 0 ? (b.num_pages * KV_H) << b.page_log2 : ((page * KV_H + kw.w.head) << b.page_log2);
+                    }
+                };
+                auto load = [&](const CUtensorMap *m, int row, int loaded) {
                     for (int half = 0; half < 2 && ok; ++half, ++i) {
-                        ok = wait_full(i) && !aborted;
+                        if (i >= Fa<Q4>::STAGES)
+                            ok = mbar_wait_sleep(smem_u32(&ss.empty[i % Fa<Q4>::STAGES]), (i / Fa<Q4>::STAGES - 1) & 1);
+                        ok = __all_sync(0xffffffffu, ok && !aborted);
                         if (!ok) break;
-                        tc::fence_after_sync();
-#pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
-                            tc::mma_f16(tm + FA_S + (u & 1) * 128,
-                                        tc::sw128_desc(sb + Fa<Q4>::Q + (2 * half + (kk >> 2)) * FA_BOX + (kk & 3) * 32),
-                                        tc::sw128_desc(stage(i) + (kk >> 2) * FA_BOX + (kk & 3) * 32), id,
-                                        half + kk > 0 ? 1u : 0u);
-                        tc::mma_commit(smem_u32(&ss.empty[i % Fa<Q4>::STAGES]));
+                        const uint32_t bar = smem_u32(&ss.full[i % Fa<Q4>::STAGES]);
+                        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)loaded * b.page * 256);
+                        __syncwarp();
+                        if (seg < loaded) tma_load_2d(stage(i) + seg_dst, m, half * 128 + box * 64, row, bar);
                     }
-                    if (!ok) break;
-                    tc::mma_commit(smem_u32(&ss.s_full[u & 1]));
-                    if (w.j + 1 == w.w.len) tc::mma_commit(smem_u32(&ss.q_empty));
-                    if (w.last(a)) break;
-                    w.next(a);
-                    if (u > 0) i += 2;             // the values of unit u - 1 come between
-                }
-                if (!ok) ss.abort = 1;
-                tc::mma_commit(smem_u32(&ss.done[0]));   // every MMA completes before tensor memory is freed
-                mbar_wait_bounded(smem_u32(&ss.done[0]), 0u);
-            }
-        } else if (warp == 2) {
-            // ---- issuer of O += P(u) V
-            if (lane == 0) {
-                const uint32_t id = tc::instr_desc(tc::FMT_BF16, 128, 128) | tc::IDESC_B_MN;
-                UnitWalk w;
-                w.begin(a, st, count);
-                uint32_t piece = 0;
-                bool ok = true;
-                for (uint32_t u = 0; ok; ++u) {
-                    const bool last = w.last(a);
-                    uint32_t i = last ? 4 * u + 2 : 4 * u + 4;   // the keys of unit u + 1 come before
-                    if (w.j == 0) {                // O of the piece before has been read
-                        if (piece > 0) ok = mbar_wait_bounded(smem_u32(&ss.o_empty), (piece - 1) & 1);
-                        ++piece;
+                };
+                auto load_q = [&](int row0, int head) {
+                    if (piece > 0) ok = mbar_wait_sleep(smem_u32(&ss.q_empty), (piece - 1) & 1);
+                    ok = __all_sync(0xffffffffu, ok && !aborted);
+                    if (ok && lane == 0) {
+                        const uint32_t bar = smem_u32(&ss.q_full);
+                        mbar_arrive_expect_tx(bar, 4 * FA_BOX);
+                        for (int c = 0; c < 4; ++c)
+                            tma_load_3d(sb + Fa<Q4>::Q + c * FA_BOX, &qmap, 64 * c, KV_G * head, row0, bar);
                     }
-                    ok = ok && mbar_wait_bounded(smem_u32(&ss.p_full[u & 1]), (u >> 1) & 1);
-                    for (int half = 0; half < 2 && ok; ++half, ++i) {
-                        ok = wait_full(i) && !aborted;
+                    ++piece;
+                };
+                if (!Q4) {
+                    int row, loaded;
+                    segment(row, loaded);
+                    load_q(kw.w.t.row0 + PG_TOK * kw.w.tile, kw.w.head);
+                    if (ok) load(&kmap, row, loaded);
+                    while (ok) {
+                        const int vrow = row, vloaded = loaded;
+                        const bool more = !kw.last(a);
+                        if (more) {
+                            kw.next(a);
+                            segment(row, loaded);
+                            if (kw.j == 0) load_q(kw.w.t.row0 + PG_TOK * kw.w.tile, kw.w.head);
+                            if (ok) load(&kmap, row, loaded);
+                        }
+                        if (ok) load(&vmap, vrow, vloaded);
+                        if (!more) break;
+                    }
+                } else {
+                    // tiles of codes in the same order: the keys of the next unit, unless those of two are
+                    // ahead of their values (q0, q1), else the values of the oldest. Lane k: record k.
+                    struct Unit {
+                        int rec, sees, row0, head;     // the lane's record (-1: zeros, -2: none), positions seen, the queries
+                        bool first;
+                    };
+                    Unit q0 = {}, q1 = {}, tile;
+                    int ahead = 0, entry = 0;
+                    bool have = true;
+                    auto look_up = [&]() {             // page table entry of the lane's record of the unit kw is at
+                        const int p = (kw.w.unit + kw.j) * PG_TILE + 16 * lane;
+                        if (lane < 8 && p < tile_sees(a, kw.w.t, kw.w.tile))
+                            entry = __ldg(b.table + (size_t)kw.w.seq * b.max_pages + (p >> b.page_log2));
+                    };
+                    look_up();
+                    for (uint32_t n = 0;; ++n) {
+                        const bool value = !(ahead < 2 && have);
+                        if (!value) {
+                            const int p = (kw.w.unit + kw.j) * PG_TILE, at = (kw.w.head << b.page_log2) + ((p + 16 * lane) & (b.page - 1));
+                            tile.sees = max(min(tile_sees(a, kw.w.t, kw.w.tile) - p, PG_TILE), 0);
+                            tile.rec = lane >= 8 || 16 * lane >= tile.sees ? -2
+                                       : (unsigned)entry < (unsigned)b.num_pages ? (((entry * KV_H) << b.page_log2) + at) >> 4 : -1;
+                            tile.row0 = kw.w.t.row0 + PG_TOK * kw.w.tile;
+                            tile.head = kw.w.head;
+                            tile.first = kw.j == 0;
+                            (ahead++ == 0 ? q0 : q1) = tile;
+                            have = !kw.last(a);
+                            if (have) {
+                                kw.next(a);
+                                look_up();
+                            }
+                            if (tile.first) load_q(tile.row0, tile.head);
+                        } else if (ahead > 0) {
+                            tile = q0;
+                            q0 = q1;
+                            --ahead;
+                        } else {
+                            tile.sees = -1;            // no more
+                            tile.rec = -2;
+                        }
+                        if (n >= 2) ok = ok && mbar_wait_sleep(smem_u32(&ss.t_empty[n & 1]), ((n >> 1) - 1) & 1);
+                        ok = __all_sync(0xffffffffu, ok && !aborted);
                         if (!ok) break;
-                        tc::fence_after_sync();
-#pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
-                            tc::mma_f16_tmem_a(tm + FA_O + half * 128, tm + FA_S + (u & 1) * 128 + kk * 8,
-                                               tc::sw128_mn_desc(stage(i) + kk * 2048, FA_BOX), id,
-                                               w.j + kk > 0 ? 1u : 0u);
-                        tc::mma_commit(smem_u32(&ss.empty[i % Fa<Q4>::STAGES]));
+                        const uint32_t bar = smem_u32(&ss.t_full[n & 1]);
+                        const uint32_t at = Fa<Q4>::TILES + (n & 1) * FA_TILE_BYTES;
+                        if (lane == 0) ss.t_sees[n & 1] = tile.sees;
+                        if (tile.rec >= 0) {
+                            const unsigned char *src = static_cast<const unsigned char *>(a.ck) + (size_t)tile.rec * REC_BYTES;
+                            mbar_arrive_expect_tx(bar, FA_CODES + 256);
+                            bulk_g2s(sb + at + lane * FA_CODES, src + (value ? REC_V : 0u), FA_CODES, bar);
+                            bulk_g2s(sb + at + 8 * FA_CODES + lane * 256, src + (value ? REC_VSZ : REC_KSZ), 256, bar);
+                        } else {
+                            if (tile.rec == -1) {      // a page id outside the cache: zeros
+                                const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+                                for (uint32_t k = 0; k < FA_CODES; k += 16) *reinterpret_cast<uint4 *>(blk + at + lane * FA_CODES + k) = zero;
+                                for (uint32_t k = 0; k < 256; k += 16) *reinterpret_cast<uint4 *>(blk + at + 8 * FA_CODES + lane * 256 + k) = zero;
+                                fence_proxy_async_smem();
+                            }
+                            mbar_arrive(bar);
+                        }
+                        if (tile.sees < 0) break;
+                        i = n + 1;                     // tiles loaded
                     }
-                    if (!ok) break;
-                    tc::mma_commit(smem_u32(&ss.pv_done[u & 1]));
-                    if (last) break;
-                    w.next(a);
                 }
-                if (!ok) ss.abort = 1;
-                tc::mma_commit(smem_u32(&ss.done[1]));
-                mbar_wait_bounded(smem_u32(&ss.done[1]), 0u);
+                if (!ok) {                             // copies in flight land before the CTA exits
+                    if (lane == 0) ss.abort = 1;
+                    if (Q4)
+                        for (uint32_t k = i > 2 ? i - 2 : 0; k < i; ++k) mbar_wait_sleep(smem_u32(&ss.t_full[k & 1]), (k >> 1) & 1);
+                    else
+                        for (uint32_t k = i > Fa<Q4>::STAGES ? i - Fa<Q4>::STAGES : 0; k < i; ++k) wait_full(k);
+                    if (piece > 0) mbar_wait_sleep(smem_u32(&ss.q_full), (piece - 1) & 1);
+                }
+            } else if (warp == 1) {
+                // ---- issuer of S(u) = Q K^T
+                if (lane == 0) {
+                    const uint32_t id = tc::instr_desc(tc::FMT_BF16, 128, PG_TILE);
+                    UnitWalk w;
+                    w.begin(a, st, count);
+                    uint32_t i = 0, piece = 0;
+                    bool ok = true;
+                    for (uint32_t u = 0; ok; ++u) {
+                        if (w.j == 0) ok = mbar_wait_sleep(smem_u32(&ss.q_full), piece++ & 1);
+                        // the buffer holds P of unit u - 2 until its product is complete
+                        if (u >= 2) ok = ok && mbar_wait_sleep(smem_u32(&ss.pv_done[u & 1]), ((u - 2) >> 1) & 1);
+                        if (u == 1) i = 2;
+                        for (int half = 0; half < 2 && ok; ++half, ++i) {
+                            ok = wait_full(i) && !aborted;
+                            if (!ok) break;
+                            tc::fence_after_sync();
+#pragma unroll
+                            for (int kk = 0; kk < 8; ++kk)
+                                tc::mma_f16(tm + FA_S + (u & 1) * 128,
+                                            tc::sw128_desc(sb + Fa<Q4>::Q + (2 * half + (kk >> 2)) * FA_BOX + (kk & 3) * 32),
+                                            tc::sw128_desc(stage(i) + (kk >> 2) * FA_BOX + (kk & 3) * 32), id,
+                                            half + kk > 0 ? 1u : 0u);
+                            tc::mma_commit(smem_u32(&ss.empty[i % Fa<Q4>::STAGES]));
+                        }
+                        if (!ok) break;
+                        tc::mma_commit(smem_u32(&ss.s_full[u & 1]));
+                        if (w.j + 1 == w.w.len) tc::mma_commit(smem_u32(&ss.q_empty));
+                        if (w.last(a)) break;
+                        w.next(a);
+                        if (u > 0) i += 2;             // the values of unit u - 1 come between
+                    }
+                    if (!ok) ss.abort = 1;
+                    tc::mma_commit(smem_u32(&ss.done[0]));   // every MMA completes before tensor memory is freed
+                    mbar_wait_sleep(smem_u32(&ss.done[0]), 0u);
+                }
+            } else if (warp == 2) {
+                // ---- issuer of O += P(u) V
+                if (lane == 0) {
+                    const uint32_t id = tc::instr_desc(tc::FMT_BF16, 128, 128) | tc::IDESC_B_MN;
+                    UnitWalk w;
+                    w.begin(a, st, count);
+                    uint32_t piece = 0;
+                    bool ok = true;
+                    for (uint32_t u = 0; ok; ++u) {
+                        const bool last = w.last(a);
+                        uint32_t i = last ? 4 * u + 2 : 4 * u + 4;   // the keys of unit u + 1 come before
+                        if (w.j == 0) {                // O of the piece before has been read
+                            if (piece > 0) ok = mbar_wait_sleep(smem_u32(&ss.o_empty), (piece - 1) & 1);
+                            ++piece;
+                        }
+                        ok = ok && mbar_wait_sleep(smem_u32(&ss.p_full[u & 1]), (u >> 1) & 1);
+                        for (int half = 0; half < 2 && ok; ++half, ++i) {
+                            ok = wait_full(i) && !aborted;
+                            if (!ok) break;
+                            tc::fence_after_sync();
+#pragma unroll
+                            for (int kk = 0; kk < 8; ++kk)
+                                tc::mma_f16_tmem_a(tm + FA_O + half * 128, tm + FA_S + (u & 1) * 128 + kk * 8,
+                                                   tc::sw128_mn_desc(stage(i) + kk * 2048, FA_BOX), id,
+                                                   w.j + kk > 0 ? 1u : 0u);
+                            tc::mma_commit(smem_u32(&ss.empty[i % Fa<Q4>::STAGES]));
+                        }
+                        if (!ok) break;
+                        tc::mma_commit(smem_u32(&ss.pv_done[u & 1]));
+                        if (last) break;
+                        w.next(a);
+                    }
+                    if (!ok) ss.abort = 1;
+                    tc::mma_commit(smem_u32(&ss.done[1]));
+                    mbar_wait_sleep(smem_u32(&ss.done[1]), 0u);
+                }
             }
-        }
         } else if (Q4 && warp >= 12) {
-            set_registers_down<104>();
-            // ---- tiles of codes to bf16 stages: thread t has row t / 8 and dims 8 (t % 8) .. of each group
-            // of every record, two groups (a stage) at a time
-            const int t = tid - 384, rr = t >> 3, ch = t & 7;
+            set_registers_down<56>();
+            // ---- tiles of codes to bf16 stages: thread t of a warpgroup has row t / 8 and dims 8 (t % 8) ..
+            // of each group of every second record, two groups (a stage) at a time. Values and keys are
+            // rounded to bf16 here (one rounding), the type that the MMA takes.
+            const int t = tid & 127, odd = (warp >> 2) - 3, rr = t >> 3, ch = t & 7;
             bool ok = true;
             uint32_t i = 0;
             for (uint32_t n = 0;; ++n) {
-                ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&ss.t_full[n & 1]), (n >> 1) & 1) && !aborted);
+                ok = __all_sync(0xffffffffu, mbar_wait_sleep(smem_u32(&ss.t_full[n & 1]), (n >> 1) & 1) && !aborted);
                 if (!ok) break;
                 const int sees = *const_cast<const volatile int *>(&ss.t_sees[n & 1]);
                 if (sees < 0) break;
-                const unsigned char *codes = blk + Fa<Q4>::TILES + (n & 1) * FA_TILE_BYTES + 16 * t;
-                const unsigned char *steps = blk + Fa<Q4>::TILES + (n & 1) * FA_TILE_BYTES + 8 * FA_CODES + 16 * rr;
+                const unsigned char *codes = blk + Fa<Q4>::TILES + (n & 1) * FA_TILE_BYTES + odd * FA_CODES + 16 * t;
+                const unsigned char *steps = blk + Fa<Q4>::TILES + (n & 1) * FA_TILE_BYTES + 8 * FA_CODES + odd * 256 + 16 * rr;
                 for (int half = 0; half < 2; ++half, ++i) {
                     if (i >= Fa<Q4>::STAGES)
-                        ok = mbar_wait_bounded(smem_u32(&ss.empty[i % Fa<Q4>::STAGES]), (i / Fa<Q4>::STAGES - 1) & 1);
+                        ok = mbar_wait_sleep(smem_u32(&ss.empty[i % Fa<Q4>::STAGES]), (i / Fa<Q4>::STAGES - 1) & 1);
                     ok = __all_sync(0xffffffffu, ok && !aborted);
                     if (!ok) break;
-                    unsigned char *dst = blk + (stage(i) - sb) + rr * 128 + ((ch ^ (rr & 7)) << 4);
-                    uint2 code[8], step[8];        // all of them first: the compiler keeps loads behind stores
+                    unsigned char *dst = blk + (stage(i) - sb) + odd * 2048 + rr * 128 + ((ch ^ (rr & 7)) << 4);
+                    uint2 code[4], step[4];        // all of them first: the compiler keeps loads behind stores
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        code[k] = *reinterpret_cast<const uint2 *>(codes + k * FA_CODES + 8 * half);
-                        step[k] = *reinterpret_cast<const uint2 *>(steps + k * 256 + 8 * half);
+                    for (int k = 0; k < 4; ++k) {
+                        code[k] = *reinterpret_cast<const uint2 *>(codes + 2 * k * FA_CODES + 8 * half);
+                        step[k] = *reinterpret_cast<const uint2 *>(steps + 2 * k * 256 + 8 * half);
                     }
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
+                    for (int k = 0; k < 4; ++k) {
                         const uint2 w = code[k];
                         uint2 z = step[k];
-                        if (16 * k + rr >= sees) z = make_uint2(0u, 0u);   // past the context: zeros, whatever is there
+                        if (32 * k + 16 * odd + rr >= sees) z = make_uint2(0u, 0u);   // past the context: zeros, whatever is there
 #pragma unroll
                         for (int g = 0; g < 2; ++g) {
                             const uint32_t c = g == 0 ? w.x : w.y, sz = g == 0 ? z.x : z.y;
                             const uint32_t s2 = __byte_perm(sz, sz, 0x1010), z2 = __byte_perm(sz, sz, 0x3232);
                             const uint32_t v0 = value_pair(c, 0, s2, z2), v1 = value_pair(c, 1, s2, z2);
                             const uint32_t v2 = value_pair(c, 2, s2, z2), v3 = value_pair(c, 3, s2, z2);
-                            *reinterpret_cast<uint4 *>(dst + g * FA_BOX + k * 2048) =
+                            *reinterpret_cast<uint4 *>(dst + g * FA_BOX + k * 4096) =
                                 make_uint4(__byte_perm(v0, v1, 0x5410), __byte_perm(v2, v3, 0x5410), __byte_perm(v0, v1, 0x7632), __byte_perm(v2, v3, 0x7632));
                         }
                     }
@@ -408,7 +415,7 @@ __global__ void __launch_bounds__(fa_threads(Q4), 1) attn_paged_kernel(const __g
             }
             if (!ok && lane == 0) ss.abort = 1;
         } else {
-            if (Q4) set_registers_up<168>();
+            if (Q4) set_registers_up<152>();
             // ---- softmax and epilogue: threads r of both groups share query row r of the item; group 0
             // has positions 0-63 of a tile and dims 0-127 of the output, group 1 the others
             const int r = tid & 127, q4 = warp & 3, grp = (warp >> 2) - 1;
@@ -418,7 +425,7 @@ __global__ void __launch_bounds__(fa_threads(Q4), 1) attn_paged_kernel(const __g
             bool ok = true;
             // O += P V of unit v is complete. Two barriers in turn: S of unit u, which this thread has
             // seen, was issued after that of unit u - 2 completed, so each is one phase behind at most.
-            auto wait_pv = [&](uint32_t v) { return mbar_wait_bounded(smem_u32(&ss.pv_done[v & 1]), (v >> 1) & 1); };
+            auto wait_pv = [&](uint32_t v) { return mbar_wait_sleep(smem_u32(&ss.pv_done[v & 1]), (v >> 1) & 1); };
             // barrier of the two warps that share rows
             auto pair_bar = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + q4) : "memory"); };
             for (;;) {
@@ -428,7 +435,7 @@ __global__ void __launch_bounds__(fa_threads(Q4), 1) attn_paged_kernel(const __g
                 float m = -INFINITY, l = 0.0f;
                 for (int j = 0; j < w.len; ++j, ++u) {
                     const int p0 = (w.unit + j) * PG_TILE, c0 = p0 + 64 * grp;
-                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&ss.s_full[u & 1]), (u >> 1) & 1) && !aborted);
+                    ok = __all_sync(0xffffffffu, mbar_wait_sleep(smem_u32(&ss.s_full[u & 1]), (u >> 1) & 1) && !aborted);
                     tc::fence_after_sync();
                     if (live) {
                         const uint32_t sc = lbase + FA_S + (u & 1) * 128;
@@ -770,8 +777,8 @@ static bool encode_q_map(CUtensorMap *map, const void *q, int M)
     return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// New tokens of a sequence up to which a 4-bit cache is read token by token: two take 275 us against 364 for a tile
-// of all (76 contexts of 16,384), three 409 against 365.
+// New tokens of a sequence up to which a 4-bit cache is read token by token: two take 275 us against 352 for a tile
+// of all (76 contexts of 16,384), three 409 against 352.
 constexpr int Q4_SINGLE = 2;
 constexpr int FA_RANGES = 152;                    // one CTA per SM
 constexpr size_t START_BYTES = (PG_MAX_CTAS * sizeof(PagedStart) + 255) / 256 * 256;
