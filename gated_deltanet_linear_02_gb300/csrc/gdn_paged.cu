@@ -491,20 +491,22 @@ __global__ void __launch_bounds__(fa_threads(Q4), 1) attn_paged_kernel(const __g
                             m = move ? top : m;
                         }
                         const float off = m == -INFINITY ? 0.0f : m * SCORE_SCALE;
-                        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                        uint64_t sum[2] = {0ull, 0ull};
+                        const uint64_t scale2 = pair2(SCORE_SCALE, SCORE_SCALE), off2 = pair2(-off, -off);
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
                             uint32_t pk[16];
 #pragma unroll
                             for (int i = 0; i < 16; ++i) {
-                                const float e0 = ex2(fmaf(x[c][2 * i], SCORE_SCALE, -off));
-                                const float e1 = ex2(fmaf(x[c][2 * i + 1], SCORE_SCALE, -off));
-                                sum[2 * c + (i & 1)] += e0 + e1;
+                                const float2 y = unpair2(fma2(pair2(x[c][2 * i], x[c][2 * i + 1]), scale2, off2));
+                                const float e0 = ex2(y.x), e1 = ex2(y.y);
+                                sum[i & 1] = add2(sum[i & 1], pair2(e0, e1));
                                 pk[i] = pack_bf16(e0, e1);
                             }
                             tc::tmem_st16_u32(sc + 32 * grp + 16 * c, pk);
                         }
-                        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                        const float2 s2 = unpair2(add2(sum[0], sum[1]));
+                        l += s2.x + s2.y;
                         tc::wait_st();
                     }
                     if (!ok) break;
