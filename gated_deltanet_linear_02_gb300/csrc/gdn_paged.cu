@@ -28,6 +28,11 @@
 //    values) into one of two buffers, and these warps write the stages, a ring of
 //    three. Four warps instead of eight: 173 us instead of 162 for three sequences
 //    of 517 tokens over contexts of 6,001.
+// Values that are not finite: a weight of 0 times infinity or NaN is NaN, so a value
+// row may only enter the product as it is if all 16 tokens of the item see it. Rows
+// that none sees become zeros, and of those that some see (the item's own tokens, at
+// most 15) the infinities and NaN do; the epilogue then adds them to the rows that
+// see them. Looking at these rows is a few instructions per item.
 // Tensor memory: two S buffers (P over their first half) and O, all 512 columns.
 //
 // Bound: for one token per sequence by HBM (1 KiB of keys and values per position
@@ -68,12 +73,14 @@ struct FaSmall {
     uint64_t full[4], empty[4];
     uint64_t q_full, q_empty, s_full[2], p_full[2], pv_done[2], o_empty, done[2];
     uint64_t t_full[2], t_empty[2];               // tiles of codes
-    int t_sees[2];                                // positions of the tile that the item sees; below 0: no more tiles
+    int t_sees[2];                                // positions of the tile that the item sees, and << 8 of those that
+                                                  // all its tokens see (keys: the same); below 0: no more tiles
     long long scan[fa_threads(true) / 32 + 1];
     uint32_t top[2][2][128];                      // by unit parity and group: a row's maximum
     PagedStart start;
     uint32_t tmem;
     int abort;
+    int poison;                                   // values that are not finite have been set to zero
 };
 // Slack to align the block to 1 KiB. Dynamic shared memory starts on such a boundary
 // as it is; the kernel checks that the slack is enough.
@@ -90,6 +97,30 @@ __device__ __forceinline__ uint32_t value_pair(uint32_t w, int t, uint32_t s2, u
     asm("sub.rn.bf16x2 %0, %0, %1;" : "+r"(c) : "r"(0x43004300u));
     asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(v) : "r"(c), "r"(s2), "r"(z2));
     return v;
+}
+
+// Marks (bits 15 and 31) of the two bf16 of a word that are infinite or NaN.
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
+
+// Which of the 16 values from dim d of position p's value row are +infinity (bits 0-15) or -infinity (16-31); both:
+// NaN.
+template <bool Q4> __device__ __forceinline__ uint32_t poison_of(const PagedArgs &a, int seq, int head, int p, int d)
+{
+    const int page = cache_page(a.b, seq, p), off = p & (a.b.page - 1);
+    if (page < 0) return 0u;
+    if (Q4) {
+        const unsigned char *rec = static_cast<const unsigned char *>(a.ck) + record_of(a.b, page, head, off);
+        const uint32_t sz = __ldg(reinterpret_cast<const uint32_t *>(rec + REC_VSZ + (off % REC_ROWS) * 16) + d / 64);
+        return not_finite(sz) != 0u ? 0xFFFFFFFFu : 0u;
+    }
+    const uint16_t *row = static_cast<const uint16_t *>(a.cv) + row_bf16(a.b, page, head, off) + d;
+    uint32_t m = 0u;
+#pragma unroll 1
+    for (int k = 0; k < 16; ++k) {
+        const uint32_t x = __ldg(row + k);
+        if ((x & 0x7F80u) == 0x7F80u) m |= (x & 0x7Fu) != 0u ? 0x10001u << k : 1u << (k + 16 * (x >> 15));
+    }
+    return m;
 }
 
 template <int N> __device__ __forceinline__ void set_registers_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -130,7 +161,7 @@ __global__ void __launch_bounds__(fa_threads(Q4), 1) attn_paged_kernel(const __g
         mbar_init(smem_u32(&ss.q_full), 1);
         mbar_init(smem_u32(&ss.q_empty), 1);
         mbar_init(smem_u32(&ss.o_empty), 256);
-        ss.abort = 0;
+        ss.abort = ss.poison = 0;
         fence_mbar_init();
     }
     if (warp == 3) {
@@ -223,7 +254,7 @@ __global__ void __launch_bounds__(fa_threads(Q4), 1) attn_paged_kernel(const __g
                     // tiles of codes in the same order: the keys of the next unit, unless those of two are
                     // ahead of their values (q0, q1), else the values of the oldest. Lane k: record k.
                     struct Unit {
-                        int rec, sees, row0, head;     // the lane's record (-1: zeros, -2: none), positions seen, the queries
+                        int rec, sees, all, row0, head;   // the lane's record (-1: zeros, -2: none), positions seen (by all), the queries
                         bool first;
                     };
                     Unit q0 = {}, q1 = {}, tile;
@@ -242,7 +273,8 @@ __global__ void __launch_bounds__(fa_threads(Q4), 1) attn_paged_kernel(const __g
                             tile.sees = max(min(tile_sees(a, kw.w.t, kw.w.tile) - p, PG_TILE), 0);
                             tile.rec = lane >= 8 || 16 * lane >= tile.sees ? -2
                                        : (unsigned)entry < (unsigned)b.num_pages ? (((entry * KV_H) << b.page_log2) + at) >> 4 : -1;
-                            tile.row0 = kw.w.t.row0 + PG_TOK * kw.w.tile;
+                            tile.all = min(max(kw.w.t.first + PG_TOK * kw.w.tile + 1 - p, 0), tile.sees);
+                        tile.row0 = kw.w.t.row0 + PG_TOK * kw.w.tile;
                             tile.head = kw.w.head;
                             tile.first = kw.j == 0;
                             (ahead++ == 0 ? q0 : q1) = tile;
@@ -265,7 +297,7 @@ __global__ void __launch_bounds__(fa_threads(Q4), 1) attn_paged_kernel(const __g
                         if (!ok) break;
                         const uint32_t bar = smem_u32(&ss.t_full[n & 1]);
                         const uint32_t at = Fa<Q4>::TILES + (n & 1) * FA_TILE_BYTES;
-                        if (lane == 0) ss.t_sees[n & 1] = tile.sees;
+                        if (lane == 0) ss.t_sees[n & 1] = tile.sees < 0 ? -1 : tile.sees | (value ? tile.all : tile.sees) << 8;
                         if (tile.rec >= 0) {
                             const unsigned char *src = static_cast<const unsigned char *>(a.ck) + (size_t)tile.rec * REC_BYTES;
                             mbar_arrive_expect_tx(bar, FA_CODES + 256);
@@ -376,8 +408,8 @@ __global__ void __launch_bounds__(fa_threads(Q4), 1) attn_paged_kernel(const __g
             for (uint32_t n = 0;; ++n) {
                 ok = __all_sync(0xffffffffu, mbar_wait_sleep(smem_u32(&ss.t_full[n & 1]), (n >> 1) & 1) && !aborted);
                 if (!ok) break;
-                const int sees = *const_cast<const volatile int *>(&ss.t_sees[n & 1]);
-                if (sees < 0) break;
+                const int mark = *const_cast<const volatile int *>(&ss.t_sees[n & 1]), sees = mark & 255, all = mark >> 8;
+                if (mark < 0) break;
                 const unsigned char *codes = blk + Fa<Q4>::TILES + (n & 1) * FA_TILE_BYTES + odd * FA_CODES + 16 * t;
                 const unsigned char *steps = blk + Fa<Q4>::TILES + (n & 1) * FA_TILE_BYTES + 8 * FA_CODES + odd * 256 + 16 * rr;
                 for (int half = 0; half < 2; ++half, ++i) {
@@ -396,7 +428,15 @@ __global__ void __launch_bounds__(fa_threads(Q4), 1) attn_paged_kernel(const __g
                     for (int k = 0; k < 4; ++k) {
                         const uint2 w = code[k];
                         uint2 z = step[k];
-                        if (32 * k + 16 * odd + rr >= sees) z = make_uint2(0u, 0u);   // past the context: zeros, whatever is there
+                        if (32 * k + 16 * odd + rr >= all) {
+                            if (32 * k + 16 * odd + rr >= sees) {
+                                z = make_uint2(0u, 0u);    // past the context: zeros, whatever is there
+                            } else {                       // not finite, see above
+                                if ((not_finite(z.x) | not_finite(z.y)) != 0u) ss.poison = 1;
+                                if (not_finite(z.x) != 0u) z.x = 0u;
+                                if (not_finite(z.y) != 0u) z.y = 0u;
+                            }
+                        }
 #pragma unroll
                         for (int g = 0; g < 2; ++g) {
                             const uint32_t c = g == 0 ? w.x : w.y, sz = g == 0 ? z.x : z.y;
@@ -431,6 +471,7 @@ __global__ void __launch_bounds__(fa_threads(Q4), 1) attn_paged_kernel(const __g
             for (;;) {
                 const int rows = KV_G * w.tokens(a), sees = tile_sees(a, w.t, w.tile);
                 const int limit = min(w.t.first + PG_TOK * w.tile + (r >> 3) + 1, cap);   // positions this row sees
+                const int all = min(w.t.first + PG_TOK * w.tile + 1, sees);               // ... and all rows
                 const bool live = 32 * q4 < rows;      // the warp has rows of the item
                 float m = -INFINITY, l = 0.0f;
                 for (int j = 0; j < w.len; ++j, ++u) {
@@ -510,11 +551,11 @@ __global__ void __launch_bounds__(fa_threads(Q4), 1) attn_paged_kernel(const __g
                         tc::wait_st();
                     }
                     if (!ok) break;
-                    if (!Q4 && p0 + PG_TILE > sees) {
-                        // the tile's positions that no token of the item sees: their value rows become
-                        // zeros, whatever the cache (or an earlier tile) left there (0 * NaN is NaN). The
-                        // previous unit's products are waited for first: they free the stages' earlier use,
-                        // without which the phase of `full` would be ambiguous.
+                    if (!Q4 && p0 + PG_TILE > all) {
+                        // Value rows that not every token of the item sees, see above: zeros past the context,
+                        // whatever the cache (or an earlier tile) left there, and for values that are not
+                        // finite. The previous unit's products are waited for first: they free the stages'
+                        // earlier use, without which the phase of `full` would be ambiguous.
                         const uint32_t vi = (j + 1 == w.len && !w.more(a) ? 4 * u + 2 : 4 * u + 4) + grp;
                         ok = u == 0 || wait_pv(u - 1);
                         ok = __all_sync(0xffffffffu, ok && wait_full(vi) && !aborted);
@@ -526,6 +567,22 @@ __global__ void __launch_bounds__(fa_threads(Q4), 1) attn_paged_kernel(const __g
                                 uint4 *row = reinterpret_cast<uint4 *>(blk + (stage(vi) - sb) + k * FA_BOX + r * 128);
 #pragma unroll
                                 for (int c = 0; c < 8; ++c) row[c] = zero;
+                            }
+                        }
+                        const int own = max(all, p0) + (r >> 3);       // eight threads for each of at most 15 rows
+                        if (own < min(sees, p0 + PG_TILE)) {
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                uint4 *at = reinterpret_cast<uint4 *>(blk + (stage(vi) - sb) + k * FA_BOX + (own - p0) * 128) + (r & 7);
+                                uint4 v = *at;
+                                if ((not_finite(v.x) | not_finite(v.y) | not_finite(v.z) | not_finite(v.w)) != 0u) {
+                                    ss.poison = 1;
+                                    v.x &= ~((not_finite(v.x) >> 15) * 0xFFFFu);
+                                    v.y &= ~((not_finite(v.y) >> 15) * 0xFFFFu);
+                                    v.z &= ~((not_finite(v.z) >> 15) * 0xFFFFu);
+                                    v.w &= ~((not_finite(v.w) >> 15) * 0xFFFFu);
+                                    *at = v;
+                                }
                             }
                         }
                         fence_proxy_async_smem();
@@ -569,6 +626,25 @@ __global__ void __launch_bounds__(fa_threads(Q4), 1) attn_paged_kernel(const __g
                     const size_t slot = ((size_t)2 * blockIdx.x + (w.first ? 0 : 1)) * a.rows + r;
                     const float inv = l == 0.0f ? 0.0f : (whole ? 1.0f / l : 1.0f);
                     const bool blank = __any_sync(0xffffffffu, l == 0.0f);   // a row that saw nothing gives zeros
+                    if (__any_sync(0xffffffffu, *const_cast<const volatile int *>(&ss.poison) != 0)) {
+                        // what the piece's value rows that not all see have left out
+                        const int begin = max(max(all, 0), w.unit * PG_TILE), end = min(limit, (w.unit + w.len) * PG_TILE);
+#pragma unroll 1
+                        for (int d = 128 * grp; d < 128 * grp + 128; d += 16) {
+                            uint32_t m = 0u, x[16];
+#pragma unroll 1
+                            for (int p = begin; p < end; ++p) m |= poison_of<Q4>(a, w.seq, w.head, p, d);
+                            float o[16];
+                            tc::tmem_ld16(lbase + FA_O + d, o);
+                            tc::wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 16; ++k)
+                                x[k] = __float_as_uint(o[k] + ((m >> k & 1u) != 0u ? INFINITY : 0.0f) - ((m >> (16 + k) & 1u) != 0u ? INFINITY : 0.0f));
+                            __syncwarp();
+                            tc::tmem_st16_u32(lbase + FA_O + d, x);
+                        }
+                        tc::wait_st();
+                    }
                     TO *out = static_cast<TO *>(a.out);
 #pragma unroll 1
                     for (int part = 0; part < 128 / PART; ++part) {

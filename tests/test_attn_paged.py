@@ -235,6 +235,53 @@ def test_deterministic_shared_pages_streams_and_graphs(ops, fmt, new):
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "q4"])
+@pytest.mark.parametrize("page", [16, 128])
+@pytest.mark.parametrize("new,ctx", [([2, 16], [300, 16]), ([3, 20], [1000, 131]), ([16, 5, 130], [135, 260, 700])])
+def test_values_that_are_not_finite_stay_with_the_tokens_that_see_them(ops, fmt, page, new, ctx):
+    """Infinities and NaN in the value row of a new token, and NaN in the key row
+    of the last one: tokens before it give what they give without, the others
+    infinities and NaN in those dims alone (all dims for the key)."""
+    b = P.make_batch(700 + page, fmt, new, ctx, page, pad_rows=1)
+    ref = P.reference(b)
+    at, dims = {}, {}
+    for i, n in enumerate(new):
+        j = n // 2
+        pos = ctx[i] - n + j
+        pg, off = int(b.table[i, pos // page]), pos % page
+        if fmt == "bf16":
+            b.v[pg, 1, off, 5], b.v[pg, 1, off, 77], b.v[pg, 1, off, 255] = float("inf"), -float("inf"), float("nan")
+            dims[i] = [5, 77, 255]
+        else:
+            rec = b.k[pg, 1, off // 16].numpy()
+            rec[4352 + 16 * (off % 16) + 4:4352 + 16 * (off % 16) + 8] = 0xFF     # group 1's step and zero: NaN
+            dims[i] = list(range(64, 128))
+        at[i] = j
+        last = ctx[i] - 1
+        pg, off = int(b.table[i, last // page]), last % page
+        if fmt == "bf16":
+            b.k[pg, 0, off, 9] = float("nan")
+        else:
+            b.k[pg, 0, off // 16].numpy()[4096 + 16 * (off % 16):4096 + 16 * (off % 16) + 4] = 0xFF
+    for dtype in (torch.float32, torch.bfloat16):
+        got = run(ops, b, dtype).cpu().double().numpy()
+        for i, n in enumerate(new):
+            x, (r, tol) = got[int(b.cu[i]):int(b.cu[i]) + n], ref[i]
+            if dtype == torch.bfloat16:
+                tol = tol + P.EPS * (np.abs(r) + tol)
+            clean = np.ones_like(x, dtype=bool)
+            clean[n - 1, :8] = False                       # the last token sees the NaN key
+            assert np.isnan(x[n - 1, :8]).all()
+            hit = np.ix_(range(at[i], n), range(8, 16), dims[i])
+            clean[hit] = False
+            if fmt == "bf16":
+                assert (x[at[i]:, 8:, 5] == np.inf).all() and (x[at[i]:, 8:, 77] == -np.inf).all()
+                assert np.isnan(x[at[i]:, 8:, 255]).all()
+            else:
+                assert np.isnan(x[hit]).all()
+            assert np.isfinite(x[clean]).all() and (np.abs(x - r)[clean] <= tol[clean]).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "q4"])
 def test_a_conversation(ops, fmt):
     """The operators together as a layer uses them: a prompt appended and
     attended, a second chunk on top, then single tokens and a few draft tokens;
