@@ -11,7 +11,6 @@ constexpr int KV_HQ = GDN_ATTN_Q_HEADS;           // 16 query heads
 constexpr int KV_H = GDN_ATTN_KV_HEADS;           // 2 KV heads
 constexpr int KV_D = GDN_ATTN_HEAD_DIM;           // 256
 constexpr int KV_G = KV_HQ / KV_H;                // 8 query heads per KV head
-constexpr int KV_NG = 4;                          // 4-bit groups per row, 64 dims each
 constexpr int REC_ROWS = GDN_KV_RECORD_ROWS;      // 16 rows per 4-bit record
 constexpr uint32_t REC_BYTES = GDN_KV_RECORD_BYTES;
 constexpr uint32_t REC_V = REC_ROWS * 128;        // value codes of a record

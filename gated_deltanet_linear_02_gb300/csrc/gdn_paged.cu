@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(fa_threads(Q4), 1) attn_paged_kernel(const __g
     const uint32_t tm = ss.tmem;
     const PagedStart st = ss.start;
     if (tid == 0) a.start[blockIdx.x] = st;
-    const long long count = range_begin(st, blockIdx.x + 1, a.ranges) - range_begin(st, blockIdx.x, a.ranges);
+    const long long count = range_begin(st, blockIdx.x + 1) - range_begin(st, blockIdx.x);
     const volatile int &aborted = ss.abort;
     auto stage = [&](uint32_t i) { return sb + Fa<Q4>::RING + (i % Fa<Q4>::STAGES) * FA_STAGE_BYTES; };
     auto wait_full = [&](uint32_t i) {
@@ -738,19 +738,19 @@ __global__ void __launch_bounds__(256) attn_paged_join_kernel(const PagedArgs a)
     grid_dep_launch();
     const PagedStart st = a.start[c];
     // the item's first step, and the step of its first unit: a cut at or before that one cuts nothing
-    const long long u = range_begin(st, c, a.ranges), begin = u - st.step, unit0 = begin + a.lead;
-    const long long total = range_begin(st, a.ranges, a.ranges);
+    const long long u = range_begin(st, c), begin = u - st.step, unit0 = begin + a.lead;
+    const long long total = range_begin(st, PG_RANGES);
     if (u >= total || u <= unit0) return;
     const SeqTokens t = st.t;
     const long long end = unit0 + tile_units(a, t, st.tile);
     // range_begin(k) is floor(total k / ranges): the first cut above unit0, and the last below end
     int head, last;
-    if (total < 0xFFFFFFFFll / PG_MAX_CTAS) {
-        head = (int)(((uint32_t)(unit0 + 1) * a.ranges + (uint32_t)total - 1) / (uint32_t)total);
-        last = (int)(((uint32_t)end * a.ranges - 1) / (uint32_t)total);
+    if (total < 0xFFFFFFFFll / PG_RANGES) {
+        head = (int)(((uint32_t)(unit0 + 1) * PG_RANGES + (uint32_t)total - 1) / (uint32_t)total);
+        last = (int)(((uint32_t)end * PG_RANGES - 1) / (uint32_t)total);
     } else {
-        head = (int)(((unit0 + 1) * a.ranges + total - 1) / total);
-        last = (int)((end * a.ranges - 1) / total);
+        head = (int)(((unit0 + 1) * PG_RANGES + total - 1) / total);
+        last = (int)((end * PG_RANGES - 1) / total);
     }
     const int rows = KV_G * min(a.tok, t.n - (st.tile << a.tok_log2));
     const int ctas = (last - head + 1) * gridDim.y, cta = (c - head) * gridDim.y + blockIdx.y;
@@ -770,8 +770,8 @@ __global__ void __launch_bounds__(256) attn_paged_join_kernel(const PagedArgs a)
             const int k = k0 + share * i;
             ml[i] = make_float2(-INFINITY, 0.0f);
             x[i] = y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            const long long from = range_begin(st, k, a.ranges);
-            if (k > last || range_begin(st, k + 1, a.ranges) == from) continue;   // past the item, or an empty range
+            const long long from = range_begin(st, k);
+            if (k > last || range_begin(st, k + 1) == from) continue;   // past the item, or an empty range
             const size_t slot = ((size_t)2 * k + (from >= begin ? 0 : 1)) * a.rows + r;
             ml[i] = *reinterpret_cast<const float2 *>(a.part_ml + slot * 2);
             const float4 *src = reinterpret_cast<const float4 *>(a.part_o + slot * KV_D) + 2 * lane;
@@ -842,7 +842,7 @@ bool encode_tiled(CUtensorMap *map, CUtensorMapDataType dt, int rank, const void
 
 cudaError_t launch_paged_join(const PagedArgs &a, gdn_dtype out_dt, cudaStream_t s)
 {
-    const dim3 grid(a.ranges - 1, a.rows / KV_G), block(256);
+    const dim3 grid(PG_RANGES - 1, a.rows / KV_G), block(256);
     return out_dt == GDN_F32 ? launch_pdl(attn_paged_join_kernel<float>, grid, block, 0, s, a)
                              : launch_pdl(attn_paged_join_kernel<bf16>, grid, block, 0, s, a);
 }
@@ -858,14 +858,13 @@ static bool encode_q_map(CUtensorMap *map, const void *q, int M)
 // New tokens of a sequence up to which a 4-bit cache is read token by token: two take 275 us against 352 for a tile
 // of all (76 contexts of 16,384), three 409 against 352.
 constexpr int Q4_SINGLE = 2;
-constexpr int FA_RANGES = 152;                    // one CTA per SM
-constexpr size_t START_BYTES = (PG_MAX_CTAS * sizeof(PagedStart) + 255) / 256 * 256;
+constexpr size_t START_BYTES = (PG_RANGES * sizeof(PagedStart) + 255) / 256 * 256;
 
 static int piece_rows(int max_q) { return KV_G * (max_q < PG_TOK ? max_q : PG_TOK); }
 
 size_t paged_workspace_bytes(const gdn_paged_batch *b, const gdn_kv_cache *)
 {
-    return START_BYTES + (size_t)2 * FA_RANGES * piece_rows(b->max_q) * (KV_D + 2) * sizeof(float);
+    return START_BYTES + (size_t)2 * PG_RANGES * piece_rows(b->max_q) * (KV_D + 2) * sizeof(float);
 }
 
 template <typename TO, bool Q4>
@@ -878,7 +877,7 @@ static cudaError_t launch_tiles(const PagedArgs &a, cudaStream_t s)
         return cudaErrorInvalidValue;
     const cudaError_t e = smem_attr_once<attn_paged_kernel<TO, Q4>>(FA_SMEM<Q4>);
     if (e != cudaSuccess) return e;
-    return launch_pdl(attn_paged_kernel<TO, Q4>, dim3(a.ranges), dim3(fa_threads(Q4)), FA_SMEM<Q4>, s, qm, km, vm, a);
+    return launch_pdl(attn_paged_kernel<TO, Q4>, dim3(PG_RANGES), dim3(fa_threads(Q4)), FA_SMEM<Q4>, s, qm, km, vm, a);
 }
 
 cudaError_t launch_attn_paged(const gdn_paged_batch *b, const gdn_kv_cache *c, const void *q, const void *gate,
@@ -895,14 +894,13 @@ cudaError_t launch_attn_paged(const gdn_paged_batch *b, const gdn_kv_cache *c, c
     a.gate_head = gate_head;
     a.out = out;
     a.rows = piece_rows(b->max_q);
-    a.ranges = FA_RANGES;
     // measured with 16 and 8 query rows: about 9 and 4 us per item against 2.5 and 2.9 per unit
     a.tok = PG_TOK;
     a.tok_log2 = 4;
     a.lead = b->max_q >= PG_TOK ? 4 : b->max_q > 1 ? 3 : 2;
     a.start = (PagedStart *)ws;
     a.part_o = (float *)((char *)ws + START_BYTES);
-    a.part_ml = a.part_o + (size_t)2 * a.ranges * a.rows * KV_D;
+    a.part_ml = a.part_o + (size_t)2 * PG_RANGES * a.rows * KV_D;
     cudaError_t e;
     if (c->format == GDN_KV_Q4 && b->max_q <= Q4_SINGLE) {
         a.tok = 1;

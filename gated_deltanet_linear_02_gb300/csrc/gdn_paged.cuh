@@ -25,8 +25,7 @@ namespace gdn {
 
 constexpr int PG_TOK = 16;                        // tokens per item, at most
 constexpr int PG_TILE = 128;                      // positions per unit
-constexpr int PG_ROWS = PG_TOK * KV_G;            // 128 query rows
-constexpr int PG_MAX_CTAS = 304;                  // ranges, at most (two per SM of 152)
+constexpr int PG_RANGES = 152;                    // one CTA per SM
 
 constexpr float SCORE_SCALE = 1.4426950408889634f / 16.0f;   // log2 e / sqrt(256)
 constexpr float RESCALE_AT = 8.0f;                // powers of two a maximum may pass the reference by
@@ -37,11 +36,10 @@ struct PagedArgs {
     const bf16 *q, *gate;
     long long gate_row, gate_head;
     void *out;
-    struct PagedStart *start;                     // [ranges]
-    float *part_o;                                // [2 * ranges][rows][256]
-    float *part_ml;                               // [2 * ranges][rows][2]
+    struct PagedStart *start;                     // [PG_RANGES]
+    float *part_o;                                // [2 * PG_RANGES][rows][256]
+    float *part_ml;                               // [2 * PG_RANGES][rows][2]
     int rows;                                     // rows per piece in the workspace: 8 min(max_q, 16)
-    int ranges;
     int lead;                                     // leading steps of an item
     int tok, tok_log2;                            // tokens per item: 16 or 1
 };
@@ -51,7 +49,7 @@ struct PagedArgs {
 struct SeqTokens {
     int row0, n, first;
 };
-// Where a range starts; the whole call has quot * ranges + rem steps.
+// Where a range starts; the whole call has quot * PG_RANGES + rem steps.
 struct PagedStart {
     long long quot;
     int rem;
@@ -113,9 +111,9 @@ __device__ __forceinline__ long long steps_before(const PagedArgs &a, const SeqT
     return KV_H * (units_before(a, t, i) + (long long)a.lead * i);
 }
 
-__device__ __forceinline__ long long range_begin(const PagedStart &s, int c, int ranges)
+__device__ __forceinline__ long long range_begin(const PagedStart &s, int c)
 {
-    return s.quot * c + s.rem * c / ranges;
+    return s.quot * c + s.rem * c / PG_RANGES;
 }
 
 // The start of range c, by all THREADS threads of the CTA: per-thread sums over
@@ -153,13 +151,13 @@ __device__ __forceinline__ void find_start(const PagedArgs &a, int c, long long 
     const long long total = scan[THREADS / 32 - 1], before = incl - mine + (warp > 0 ? scan[warp - 1] : 0);
     PagedStart cuts;
     if (total < 0x7FFFFFFF) {                      // a 64-bit division takes four times as long
-        cuts.quot = (uint32_t)total / (uint32_t)a.ranges;
-        cuts.rem = (int)((uint32_t)total % (uint32_t)a.ranges);
+        cuts.quot = (uint32_t)total / PG_RANGES;
+        cuts.rem = (int)((uint32_t)total % PG_RANGES);
     } else {
-        cuts.quot = total / a.ranges;
-        cuts.rem = (int)(total % a.ranges);
+        cuts.quot = total / PG_RANGES;
+        cuts.rem = (int)(total % PG_RANGES);
     }
-    const long long u = range_begin(cuts, c, a.ranges);
+    const long long u = range_begin(cuts, c);
     if (tid == 0) {
         out->quot = cuts.quot;
         out->rem = cuts.rem;

@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) attn_paged_q4_kernel(const __gr
     find_start<DQ_THREADS>(a, blockIdx.x, ss.scan, &ss.start);   // ends in a CTA barrier
     const PagedStart st = ss.start;
     if (tid == 0) a.start[blockIdx.x] = st;
-    const long long count = range_begin(st, blockIdx.x + 1, a.ranges) - range_begin(st, blockIdx.x, a.ranges);
+    const long long count = range_begin(st, blockIdx.x + 1) - range_begin(st, blockIdx.x);
     PieceWalk w;
     if (count > 0) w.begin(a, st, count);
     if (count == 0 || w.len == 0) return;
@@ -515,7 +515,7 @@ static cudaError_t launch_typed(const CUtensorMap &cm, const CUtensorMap &sm, co
 {
     const cudaError_t e = smem_attr_once<attn_paged_q4_kernel<TO>>(DQ_SMEM);
     if (e != cudaSuccess) return e;
-    return launch_pdl(attn_paged_q4_kernel<TO>, dim3(a.ranges), dim3(DQ_THREADS), DQ_SMEM, s, cm, sm, a);
+    return launch_pdl(attn_paged_q4_kernel<TO>, dim3(PG_RANGES), dim3(DQ_THREADS), DQ_SMEM, s, cm, sm, a);
 }
 
 cudaError_t launch_paged_q4(const PagedArgs &a, gdn_dtype out_dt, cudaStream_t s)
