@@ -13,7 +13,10 @@
 // head 512 bytes in, 512 (bf16) or 144 (4 bits) out, and the rotation table's 256
 // bytes per token. With many tokens a warp takes four rows of one token, whose
 // loads all start before the token's place in the cache is looked up (a chain of
-// dependent reads); with few, one row, so that more SMs share them.
+// dependent reads); with few, one row, so that more SMs share them. Measured: norms and
+// rotation of 4,096 tokens 16.6 us (4.6 TB/s; a copy of as many bytes at full rate takes
+// 11.3), bf16 append with queries 17.4 us (4.6 TB/s), 4-bit append 13.9 us: there the
+// exact codes are bound by instructions, some 500 per row and warp.
 #include "gdn_async.cuh"
 #include "gdn_kv.cuh"
 
@@ -617,15 +620,20 @@ __global__ void __launch_bounds__(KV_WARPS * 32, input_ctas(NQ, Q4)) attn_input_
     else if (NKV > 0) walk_tokens<TI, TO, NKV, Q4, false, NKV == 4 ? 4 : 2>(a, 0, m0, m1, lane);
 }
 
-// Rows from which the walking kernel is used: two waves of one-row warps, 48 on each
-// of 152 SMs.
-constexpr long long FEW_ROWS = 2 * 152 * 48;
+// Rows up to which one warp takes one row, two waves of 48 warps on each of 152 SMs,
+// and above which warps walk. Both sides, us: norms of 512 tokens (9,216 rows) 4.2
+// against 5.2, of 4,096 18.4 against 16.6; bf16 append with queries 512 5.4 against
+// 5.6, 4,096 24.4 against 17.4; 4-bit append 2,048 (8,192 rows) 9.7 against 12.1,
+// 4,096 14.4 against 13.9. Keys and values into bf16 pages are copies but for the
+// norm, and gain from the walk's loads ahead sooner: 512 tokens 3.3 on both sides,
+// 2,048 5.5 against 3.7.
+constexpr long long few_rows(int nq, int nkv, bool q4) { return nq == 0 && nkv == 4 && !q4 ? 2048 : 2 * 152 * 48; }
 
 template <typename TI, typename TO, int NQ, int NKV, bool Q4>
 static cudaError_t launch_input(const InputArgs &a, cudaStream_t s)
 {
     const long long rows = (long long)a.M * (NQ + NKV);
-    if (rows <= FEW_ROWS)
+    if (rows <= few_rows(NQ, NKV, Q4))
         return launch_pdl(attn_input_few_kernel<TI, TO, NQ, NKV, Q4>, dim3((unsigned)((rows + KV_WARPS - 1) / KV_WARPS)),
                           dim3(KV_WARPS * 32), 0, s, a);
     return launch_pdl(attn_input_kernel<TI, TO, NQ, NKV, Q4>, dim3(input_ctas(NQ, Q4) * 152), dim3(KV_WARPS * 32),
@@ -664,14 +672,14 @@ cudaError_t launch_kv_append(const gdn_attn_params *p, const gdn_paged_batch *b,
 }
 
 // Reads rows back: the same warp layout, values z + s c in fp32 (s c is exact:
-// 8 x 4 bits), one rounding to the output type. R rows of k0, k1, v0, v1 per warp.
-template <typename TO, bool Q4, int R>
+// 8 x 4 bits), one rounding to the output type. A warp takes a token's k0, k1, v0, v1:
+// 4,096 tokens in bf16 out of 4-bit pages 3.1 us (one row per warp: 4.1).
+template <typename TO, bool Q4>
 __global__ void __launch_bounds__(KV_WARPS * 32) kv_gather_kernel(const PagedBatch b, const void *ck, const void *cv,
                                                                   TO *k_out, TO *v_out)
 {
     const int lane = threadIdx.x & 31;
-    const long long item = (long long)blockIdx.x * KV_WARPS + (threadIdx.x >> 5);
-    const int m = (int)(item / (4 / R)), row0 = (int)(item % (4 / R)) * R;
+    const int m = blockIdx.x * KV_WARPS + (threadIdx.x >> 5);
     grid_dep_wait();
     grid_dep_launch();
     if (m >= b.M) return;
@@ -679,12 +687,12 @@ __global__ void __launch_bounds__(KV_WARPS * 32) kv_gather_kernel(const PagedBat
     if (at.seq < 0) return;
     const int page = cache_page(b, at.seq, at.pos), off = at.pos & (b.page - 1);
     const int r = off & (REC_ROWS - 1), g = lane >> 3, c = lane & 7;
-    uint4 raw[R];
-    uint32_t sz[R];
+    uint4 raw[4];
+    uint32_t sz[4];
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-        const bool isv = row0 + i >= KV_H;
-        const int h = (row0 + i) & 1;
+    for (int i = 0; i < 4; ++i) {
+        const bool isv = i >= KV_H;
+        const int h = i & 1;
         raw[i] = make_uint4(0u, 0u, 0u, 0u);
         sz[i] = 0;
         if (page < 0 || (isv ? v_out : k_out) == nullptr) continue;
@@ -697,8 +705,8 @@ __global__ void __launch_bounds__(KV_WARPS * 32) kv_gather_kernel(const PagedBat
         }
     }
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-        TO *out = row0 + i >= KV_H ? v_out : k_out;
+    for (int i = 0; i < 4; ++i) {
+        TO *out = i >= KV_H ? v_out : k_out;
         if (out == nullptr) continue;
         const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
         const float s = __uint_as_float(sz[i] << 16), z = __uint_as_float(sz[i] & 0xFFFF0000u);
@@ -707,19 +715,15 @@ __global__ void __launch_bounds__(KV_WARPS * 32) kv_gather_kernel(const PagedBat
         for (int k = 0; k < 8; ++k)
             x[k] = Q4 ? fmaf(s, (float)((w[0] >> (4 * k)) & 15u), z)
                       : __uint_as_float((k & 1) ? (w[k >> 1] & 0xFFFF0000u) : (w[k >> 1] << 16));
-        store8(out + ((size_t)m * KV_H + ((row0 + i) & 1)) * KV_D + 8 * lane, x);
+        store8(out + ((size_t)m * KV_H + (i & 1)) * KV_D + 8 * lane, x);
     }
 }
 
 template <typename TO, bool Q4>
 static cudaError_t launch_gather(const PagedBatch &b, const gdn_kv_cache *c, void *k_out, void *v_out, cudaStream_t s)
 {
-    const bool few = (long long)b.M * 2 * KV_H <= FEW_ROWS;
-    const long long items = (long long)b.M * (few ? 2 * KV_H : 1);
-    const dim3 grid((unsigned)((items + KV_WARPS - 1) / KV_WARPS)), block(KV_WARPS * 32);
-    const void *ck = c->k, *cv = c->v;
-    return few ? launch_pdl(kv_gather_kernel<TO, Q4, 1>, grid, block, 0, s, b, ck, cv, (TO *)k_out, (TO *)v_out)
-               : launch_pdl(kv_gather_kernel<TO, Q4, 4>, grid, block, 0, s, b, ck, cv, (TO *)k_out, (TO *)v_out);
+    const dim3 grid((unsigned)((b.M + KV_WARPS - 1) / KV_WARPS));
+    return launch_pdl(kv_gather_kernel<TO, Q4>, grid, dim3(KV_WARPS * 32), 0, s, b, c->k, c->v, (TO *)k_out, (TO *)v_out);
 }
 
 cudaError_t launch_kv_gather(const gdn_paged_batch *b, const gdn_kv_cache *c, void *k_out, void *v_out,

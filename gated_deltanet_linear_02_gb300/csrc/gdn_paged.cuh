@@ -40,7 +40,7 @@ struct PagedArgs {
     float *part_o;                                // [2 * PG_RANGES][rows][256]
     float *part_ml;                               // [2 * PG_RANGES][rows][2]
     int rows;                                     // rows per piece in the workspace: 8 min(max_q, 16)
-    int lead;                                     // leading steps of an item
+    int lead;                                     // leading steps of an item: its epilogue and start, counted in units
     int tok, tok_log2;                            // tokens per item: 16 or 1
 };
 

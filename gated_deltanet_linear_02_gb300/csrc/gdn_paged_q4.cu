@@ -1,6 +1,8 @@
 // gdn_paged_q4.cu -- attention of single tokens over the 4-bit paged cache.
 //
-// Bound by HBM: 288 bytes per cached position and KV head. At the measured copy
+// 288 bytes per cached position and KV head: 256 contexts of up to 4,096 take 117 us
+// (3.9 TB/s, 58% of a copy's rate), bound by the instructions per record (about 580)
+// and their latency rather than by HBM. At the measured copy
 // rate an SM receives a 16-position record (4608 bytes) every 190 cycles, so
 // what the codes cost on chip decides: expanding them to bf16 in shared memory
 // for the 5th-generation tensor cores would write and read back 16 KiB per
