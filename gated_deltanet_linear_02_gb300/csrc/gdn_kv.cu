@@ -76,11 +76,12 @@ __device__ __forceinline__ void store8(bf16 *p, const float (&x)[8])
     *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// RMSNorm and rotation of a row in fp32. `big` returns the largest magnitude
-// that went into any value of this lane's 4-bit group (before or after the
-// rotation), which scales the error of the result.
+// RMSNorm and rotation of a row in fp32. `tol` returns a bound of each value's error,
+// in units of 2^-24 of what went into it: the mean of squares 9 (a tree of 8 additions
+// on rounded squares, and eps), halved by the root, the refined root 1.5, two products
+// 2: 8 of |x|; a rotated one three roundings more, 11 of |x c| + |y s|.
 __device__ __forceinline__ void norm_rotate(float (&x)[8], const float *__restrict__ w, const float *__restrict__ rope,
-                                            float eps, int lane, float &big, bool &tame)
+                                            float eps, int lane, float (&tol)[8], bool &tame)
 {
     tame = true;
     if (w != nullptr) {
@@ -95,9 +96,8 @@ __device__ __forceinline__ void norm_rotate(float (&x)[8], const float *__restri
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = x[i] * r * wv[i];
     }
-    big = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(x[i]));
+    for (int i = 0; i < 8; ++i) tol[i] = 4.9e-7f * fabsf(x[i]);
     if (rope != nullptr) {
         float y[8];
 #pragma unroll
@@ -109,9 +109,9 @@ __device__ __forceinline__ void norm_rotate(float (&x)[8], const float *__restri
             const float sg = lane < 4 ? -1.0f : 1.0f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                big = fmaxf(big, fabsf(y[i]));
-                x[i] = fmaf(x[i], c[i], sg * y[i] * s[i]);
-                big = fmaxf(big, fabsf(x[i]));
+                const float t = sg * y[i] * s[i];
+                tol[i] = 6.7e-7f * (fabsf(x[i] * c[i]) + fabsf(t));
+                x[i] = fmaf(x[i], c[i], t);
             }
         }
     }
@@ -197,9 +197,14 @@ __device__ __forceinline__ void norm_rotate_pair(const float (&in)[8], Pair (&x)
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = Pair{in[i], 0.0f};
     if (w != nullptr) {
-        Pair ss = {0.0f, 0.0f};
+        Pair sq[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = add(ss, mul(x[i], in[i]));
+        for (int i = 0; i < 8; ++i) sq[i] = mul(x[i], in[i]);
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < o; ++i) sq[i] = add(sq[i], sq[i + o]);
+        Pair ss = sq[0];
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) ss = add(ss, shfl_xor(ss, o));
         const Pair v = add(mul(ss, 1.0f / KV_D), Pair{eps, 0.0f});
@@ -236,15 +241,15 @@ struct Quant {
     float s, z;
 };
 
-// A lane's 8 codes and its group's step and zero, in fp32. `err` bounds the
-// distance of every x of the group from the real value it stands for. Returns
-// whether neither that nor the arithmetic's own error can change anything: the
-// zero and the step round to the same bf16 at both ends of their error intervals,
-// (`range`) and every x is further from a border between two codes than all errors
-// together (those of x - z and its product with 1 / s: 3 roundings of at most 16 s).
-// Rounding to an integer is adding 1.5 2^23; four codes are joined in fp32, whose
-// 24 bits hold them exactly.
-__device__ __forceinline__ bool quantise_f32(const float (&x)[8], float err, Quant &q, bool &range)
+// A lane's 8 codes and its group's step and zero, in fp32. `tol` bounds the distance
+// of each x from the real value it stands for, `err` those of the whole group. Returns
+// whether neither that nor the arithmetic's own error can change anything: the zero
+// and the step round to the same bf16 at both ends of their error intervals (`range`),
+// and every x lies inside its code's interval by more than its error and the rounding
+// of x - z. (That the product with 1 / s rounds to a neighbour's code shows as x
+// outside the interval.) Rounding to an integer is adding 1.5 2^23; four codes are
+// joined in fp32, whose 24 bits hold them exactly.
+__device__ __forceinline__ bool quantise_f32(const float (&x)[8], const float (&tol)[8], float err, Quant &q, bool &range)
 {
     float lo = fminf(fminf(fminf(x[0], x[1]), fminf(x[2], x[3])), fminf(fminf(x[4], x[5]), fminf(x[6], x[7])));
     float hi = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
@@ -262,19 +267,20 @@ __device__ __forceinline__ bool quantise_f32(const float (&x)[8], float err, Qua
         return range = true;
     }
     const float inv = __fdividef(1.0f, q.s), half = 0.5f * q.s, magic = 12582912.0f;
-    float nearest = q.s, n[8];
+    float inside = q.s, n[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const float d = x[i] - q.z;
-        n[i] = fminf(fmaxf(fmaf(d, inv, magic), magic), magic + 15.0f) - magic;
-        nearest = fminf(nearest, fabsf(fabsf(fmaf(-q.s, n[i], d)) - half));
+        n[i] = fmaf(d, inv, magic) - magic;
+        inside = fminf(inside, half - fabsf(fmaf(-q.s, n[i], d)) - fmaf(1.2e-7f, fabsf(d), tol[i]));
+        n[i] = fminf(fmaxf(n[i], 0.0f), 15.0f);
     }
     const float a = fmaf(4096.0f, n[3], fmaf(256.0f, n[2], fmaf(16.0f, n[1], n[0])));
     const float b = fmaf(4096.0f, n[7], fmaf(256.0f, n[6], fmaf(16.0f, n[5], n[4])));
     q.codes = __byte_perm(__float_as_uint(a + 8388608.0f), __float_as_uint(b + 8388608.0f), 0x5410);   // low 16 bits of each
     range = to_f(__float2bfloat16_rn(lo - err)) == to_f(__float2bfloat16_rn(lo + err)) &&
             to_f(__float2bfloat16_rn(t - et)) == to_f(__float2bfloat16_rn(t + et)) && q.s > 1e-30f && q.s < 1e30f;
-    return range && nearest > fmaf(q.s, 4e-6f, err);
+    return range && inside > 0.0f;
 }
 
 // Exact x (err = 0) next to a border: the same with every comparison exact in fp32,
@@ -372,29 +378,27 @@ __device__ __noinline__ void quantise_f64(const double (&x)[8], Quant &q)
 __device__ __forceinline__ void store_row_q4(const InputArgs &a, const float (&in)[8], bool isv, const float *rope, int page,
                                              int head, int off, int lane)
 {
-    float x[8], err = 0.0f, big = 0.0f;
+    float x[8], tol[8] = {}, err = 0.0f;
     bool tame = true;
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = in[i];
     if (!isv && (a.k_w != nullptr || rope != nullptr)) {
-        // Error of a normed and rotated value, in units of 2^-24 relative: the mean of squares 9 (a
-        // tree of 8 additions on rounded squares, and eps), halved by the root, the refined root 1.5,
-        // two products 2: 8; in the rotated group three roundings more, of a sum of two terms that is
-        // at most sqrt 2 times the larger: 16 of `big`, 1e-6.
-        norm_rotate(x, a.k_w, rope, a.eps, lane, big, tame);
+        norm_rotate(x, a.k_w, rope, a.eps, lane, tol, tame);
 #pragma unroll
-        for (int o = 4; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-        err = 1e-6f * big;
+        for (int i = 0; i < 8; ++i) err = fmaxf(err, tol[i]);
+        tame = tame && ((tol[0] + tol[1]) + (tol[2] + tol[3])) + ((tol[4] + tol[5]) + (tol[6] + tol[7])) < 1e30f;   // no NaN
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) err = fmaxf(err, __shfl_xor_sync(0xffffffffu, err, o));
     }
     float all = 0.0f;                              // of the row as it came; infinities and NaN are the 64-bit form's
 #pragma unroll
     for (int i = 0; i < 8; ++i) all += fabsf(in[i]);
     Quant q;
-    bool range, sure = quantise_f32(x, err, q, range) && tame && all < 1e30f;
+    bool range, sure = quantise_f32(x, tol, err, q, range) && tame && all < 1e30f;
     // Exact values that are next to a border are mostly ties, which fp32 can settle.
     if (err == 0.0f && !__all_sync(0xffffffffu, sure)) sure = sure || (range && all < 1e30f && quantise_exact(x, q));
     if (!__all_sync(0xffffffffu, sure)) {
-        const bool mid = all < 1e12f && (all > 1e-10f || all == 0.0f) && big < 1e12f && (big > 1e-10f || big == 0.0f) &&
+        const bool mid = tame && all < 1e12f && (all > 1e-10f || all == 0.0f) && err < 5e5f && (err > 5e-17f || err == 0.0f) &&
                          q.s < 1e12f && (q.s > 1e-12f || q.s == 0.0f);
         if (__all_sync(0xffffffffu, mid)) {
             Pair xp[8];
@@ -449,15 +453,15 @@ __global__ void __launch_bounds__(KV_WARPS * 32) attn_input_few_kernel(const Inp
             store_row_q4(a, x, isv, rope, page, h, off, lane);
             return;
         }
-        float big;
+        float tol[8];
         bool tame;
-        if (!isv) norm_rotate(x, a.k_w, rope, a.eps, lane, big, tame);
+        if (!isv) norm_rotate(x, a.k_w, rope, a.eps, lane, tol, tame);
         store8(static_cast<bf16 *>(isv ? a.cache_v : a.cache_k) + row_bf16(a.b, page, h, off) + 8 * lane, x);
         return;
     }
-    float big;
+    float tol[8];
     bool tame;
-    norm_rotate(x, isq ? a.q_w : a.k_w, rope, a.eps, lane, big, tame);
+    norm_rotate(x, isq ? a.q_w : a.k_w, rope, a.eps, lane, tol, tame);
     store8(isq ? static_cast<TO *>(a.q_out) + ((size_t)m * KV_HQ + h) * KV_D + 8 * lane
                : static_cast<TO *>(a.k_out) + ((size_t)m * KV_H + h) * KV_D + 8 * lane, x);
 }

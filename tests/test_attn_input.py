@@ -169,6 +169,54 @@ def test_append_q4_is_the_definition_bit_for_bit(ops, page, new, ctx, act, norm,
     assert not len(bad), f"{len(bad)} bytes differ, first at {bad[:3].tolist()}"
 
 
+@pytest.mark.parametrize("act", [torch.bfloat16, torch.float32])
+def test_append_q4_scaled_rotation_and_offset_rows(ops, act):
+    """Rotation tables with factors above 1, and rows whose offset is far larger than
+    their range: the definition bit for bit, over rows enough to meet borders between
+    codes, steps and zeros."""
+    M = 1500
+    b, k, v, kw, table, _ = setup(ops, 50, "q4", [M], [M], 32, act)
+    table = table * 3.0
+    v[::3] = (v[::3].float() * 0.01 + 37.0).to(act)
+    k[::5] = (k[::5].float() * 0.003 - 1.0).to(act)
+    plan, cache = P.handles(ops, b)
+    ops.kv_append(ops.make_attn_params(None, kw.to(DEV), table.to(DEV)), plan, cache, k.to(DEV), v.to(DEV))
+    kk = oracle.norm_rope(k.double(), kw, table[:M])
+    kr, vr = (torch.empty(M, 2, 256, device=DEV) for _ in range(2))
+    ops.kv_gather(plan, cache, kr, vr)
+    got = cache._keep_alive[0].cpu().numpy()
+    pos = np.arange(M)
+    rec = got[b.table.numpy()[0][pos // 32], :, pos % 32 // 16]               # [M][2][4608]
+    for at, sz, x in ((0, 4096, kk), (2048, 4352, v.double().numpy())):
+        c, st, z, _ = oracle.kv4(x)
+        rows = rec.reshape(M, 2, -1)
+        codes = np.stack([rows[m, :, at + m % 16 * 128:at + m % 16 * 128 + 128] for m in pos])
+        steps = np.stack([rows[m, :, sz + m % 16 * 16:sz + m % 16 * 16 + 16] for m in pos])
+        np.testing.assert_array_equal(steps, P.bf16_bytes(np.stack([st, z], -1)).reshape(M, 2, 16))
+        np.testing.assert_array_equal(codes, P.row_bytes(c))
+
+
+@pytest.mark.parametrize("where", ["weight", "rotation", "huge"])
+def test_append_q4_parameters_that_are_not_finite(ops, where):
+    """NaN in a weight or in the rotation of one position, or a weight that
+    overflows: the groups that hold it read NaN, the others as ever."""
+    M = 40
+    b, k, v, kw, table, _ = setup(ops, 60, "q4", [M], [M], 16)
+    kw, table = kw.clone(), table.clone()
+    if where == "weight":
+        kw[70] = float("nan")
+    elif where == "huge":
+        kw[70] = float("inf")
+    else:
+        table[7, 3] = float("nan")
+    plan, cache = P.handles(ops, b)
+    ops.kv_append(ops.make_attn_params(None, kw.to(DEV), table.to(DEV)), plan, cache, k.to(DEV), v.to(DEV))
+    kr, vr = (torch.empty(M, 2, 256, device=DEV) for _ in range(2))
+    ops.kv_gather(plan, cache, kr, vr)
+    for got, x in ((kr, oracle.norm_rope(k.double(), kw, table[:M])), (vr, v.double())):
+        np.testing.assert_array_equal(got.cpu().numpy(), oracle.kv4(x)[3].astype(np.float32))
+
+
 def test_append_q4_corner_rows(ops):
     """Constant groups, zeros, exact ties, infinities and NaN, subnormals, huge
     ranges: bit for bit, except that groups that hold a non-finite value read NaN."""
