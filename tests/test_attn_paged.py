@@ -281,6 +281,25 @@ def test_values_that_are_not_finite_stay_with_the_tokens_that_see_them(ops, fmt,
             assert np.isfinite(x[clean]).all() and (np.abs(x - r)[clean] <= tol[clean]).all()
 
 
+@pytest.mark.parametrize("scales", [(1e-7,), (1e-3,), (3e4, 1e5), (1e20,), (1.0, 1e6, 1e-4), (0.0, 1.0)])
+@pytest.mark.parametrize("new,ctx", [([3, 17], [130, 700]), ([70], [1300])])
+def test_values_of_any_magnitude(ops, scales, new, ctx):
+    """4-bit values beyond fp16's range, far below it, and both in one context, by
+    turns of 150 positions: within the bound wherever they lie."""
+    b = P.make_batch(800, "q4", new, ctx, 32, pad_rows=1)
+    for i, c in enumerate(ctx):
+        k, v = b.kv[i]
+        at = np.array(scales)[np.arange(c) // 150 % len(scales)]
+        codes, steps, zeros, v = oracle.kv4((v * at[:, None]).astype(np.float32))
+        for p in range(c):
+            rec = b.k[int(b.table[i, p // 32]), :, p % 32 // 16].numpy()
+            r = p % 16
+            rec[:, 2048 + 128 * r:2176 + 128 * r] = P.row_bytes(codes[:, p])
+            rec[:, 4352 + 16 * r:4368 + 16 * r] = P.bf16_bytes(np.stack([steps[:, p], zeros[:, p]], -1)).reshape(2, 16)
+        b.kv[i] = (k, v)
+    P.compare(b, run(ops, b, torch.float32), P.reference(b), f"scales {scales} new {new}")
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "q4"])
 def test_a_conversation(ops, fmt):
     """The operators together as a layer uses them: a prompt appended and
