@@ -1,7 +1,7 @@
 // gdn_paged_q4.cu -- attention of single tokens over the 4-bit paged cache.
 //
-// 288 bytes per cached position and KV head: 256 contexts of up to 4,096 take 117 us
-// (3.9 TB/s, 58% of a copy's rate), bound by the instructions per record (about 580)
+// 288 bytes per cached position and KV head: 256 contexts of up to 4,096 take 110 us
+// (4.2 TB/s, 62% of a copy's rate), bound by the instructions per record (about 580)
 // and their latency rather than by HBM. At the measured copy
 // rate an SM receives a 16-position record (4608 bytes) every 190 cycles, so
 // what the codes cost on chip decides: expanding them to bf16 in shared memory
@@ -227,37 +227,22 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) attn_paged_q4_kernel(const __gr
         int base = 0;                              // first record of the round, from the piece's first position
         bool more = true;
         // A round's record of this lane: whether it has one, its page table entry (a load that is two
-        // rounds old when its value is first needed) and its place in the page.
+        // rounds old when its value is first needed) and its place in the page; in a piece's first round
+        // also the piece's token and head, else below 0.
         struct Rec {
-            bool round, mine;
-            int page, in_page;
+            bool round, mine, whole;
+            int page, in_page, token, head;
         };
         uint32_t piece = 0;
         bool ok = true;
         auto fetch = [&]() {
-            Rec r = {more, false, 0, 0};
+            Rec r = {more, false, w.whole(), 0, 0, base == 0 ? w.t.row0 + w.tile : -1, w.head};
             if (!more) return r;
             const int p = w.unit * PG_TILE + 16 * (base + lane), end = piece_end(w);
             if (lane < DQ_WARPS && p < end) {
                 r.mine = true;
                 r.page = __ldg(b.table + (size_t)w.seq * b.max_pages + (p >> b.page_log2));
                 r.in_page = (w.head << b.page_log2) + (p & (b.page - 1));
-            }
-            if (base == 0) {                       // a piece begins: its queries
-                const uint32_t qb = piece % DQ_QUERIES;
-                if (piece >= DQ_QUERIES)
-                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&ss.q_empty[qb]), (piece / DQ_QUERIES - 1) & 1));
-                if (!ok) {
-                    r.round = false;
-                    return r;
-                }
-                const int m = w.t.row0 + w.tile;
-                make_query(reinterpret_cast<const uint4 *>(a.q + ((size_t)m * KV_HQ + KV_G * w.head + (lane >> 2)) * KV_D) + 2 * (lane & 3),
-                           ss.query[qb], lane);
-                mbar_arrive(smem_u32(&ss.q_full[qb]));
-                ++piece;
-                if (a.gate != nullptr && w.whole())    // and its gates, for the epilogue: 128 bytes per lane
-                    asm volatile("prefetch.global.L2 [%0];" ::"l"(a.gate + m * a.gate_row + (KV_G * w.head + (lane >> 2)) * a.gate_head + 64 * (lane & 3)));
             }
             base += DQ_WARPS;
             if (w.unit * PG_TILE + 16 * base >= end) {
@@ -286,6 +271,19 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) attn_paged_q4_kernel(const __gr
                 }
             }
             ok = __all_sync(0xffffffffu, ok && !aborted);
+            if (ok && r0.token >= 0) {             // the piece's queries, while its first records come (before them: 117 us)
+                const uint32_t qb = piece % DQ_QUERIES;
+                if (piece >= DQ_QUERIES)
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&ss.q_empty[qb]), (piece / DQ_QUERIES - 1) & 1));
+                if (ok) {
+                    make_query(reinterpret_cast<const uint4 *>(a.q + ((size_t)r0.token * KV_HQ + KV_G * r0.head + (lane >> 2)) * KV_D) + 2 * (lane & 3),
+                               ss.query[qb], lane);
+                    mbar_arrive(smem_u32(&ss.q_full[qb]));
+                    ++piece;
+                    if (a.gate != nullptr && r0.whole) // and its gates, for the epilogue: 128 bytes per lane
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.gate + r0.token * a.gate_row + (KV_G * r0.head + (lane >> 2)) * a.gate_head + 64 * (lane & 3)));
+                }
+            }
             if (!ok) break;
             r0 = r1;
             r1 = r2;
