@@ -334,17 +334,16 @@ __device__ __forceinline__ void gate8(const uint4 u, float (&o)[8], float inv)
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i] *= gate1(__uint_as_float((i & 1) ? (w[i >> 1] & 0xFFFF0000u) : (w[i >> 1] << 16)), inv);
 }
-// Normalised output times the gate, 4 dims from dim d of (packed row m, head h).
+// Normalised output times the gate (if there is one), 4 dims from dim d of (packed row m, head h).
 template <typename TO>
-__device__ __forceinline__ void finish4(const PagedArgs &a, int m, int h, int d, float4 o, float inv)
+__device__ __forceinline__ void finish4(const PagedArgs &a, uint2 gate, int m, int h, int d, float4 o, float inv)
 {
     float s[4] = {inv, inv, inv, inv};
     if (a.gate != nullptr) {
-        const float4 g = load4(a.gate + m * a.gate_row + h * a.gate_head + d);
-        s[0] = gate1(g.x, inv);
-        s[1] = gate1(g.y, inv);
-        s[2] = gate1(g.z, inv);
-        s[3] = gate1(g.w, inv);
+        s[0] = gate1(__uint_as_float(gate.x << 16), inv);
+        s[1] = gate1(__uint_as_float(gate.x & 0xFFFF0000u), inv);
+        s[2] = gate1(__uint_as_float(gate.y << 16), inv);
+        s[3] = gate1(__uint_as_float(gate.y & 0xFFFF0000u), inv);
     }
     store4(static_cast<TO *>(a.out) + ((size_t)m * KV_HQ + h) * KV_D + d,
            make_float4(o.x * s[0], o.y * s[1], o.z * s[2], o.w * s[3]));

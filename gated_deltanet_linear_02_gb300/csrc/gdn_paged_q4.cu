@@ -1,6 +1,6 @@
 // gdn_paged_q4.cu -- attention of single tokens over the 4-bit paged cache.
 //
-// 288 bytes per cached position and KV head: 256 contexts of up to 4,096 take 110 us
+// 288 bytes per cached position and KV head: 256 contexts of up to 4,096 take 109 us
 // (4.2 TB/s, 62% of a copy's rate), bound by the instructions per record (about 580)
 // and their latency rather than by HBM. At the measured copy
 // rate an SM receives a 16-position record (4608 bytes) every 190 cycles, so
@@ -218,6 +218,12 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) attn_paged_q4_kernel(const __gr
     auto codes_at = [&](int wp, uint32_t i) { return sb + DQ_RING + (wp * DQ_STAGES + i) * DQ_CODES; };
     auto sz_at = [&](int wp, uint32_t i) { return sb + DQ_RING_SZ + (wp * DQ_STAGES + i) * DQ_SZ; };
 
+    // a piece's queries into one of the buffers; a whole warp
+    auto query = [&](uint32_t qb, int token, int head) {
+        make_query(reinterpret_cast<const uint4 *>(a.q + ((size_t)token * KV_HQ + KV_G * head + (lane >> 2)) * KV_D) + 2 * (lane & 3),
+                   ss.query[qb], lane);
+        mbar_arrive(smem_u32(&ss.q_full[qb]));
+    };
     // where the positions of a piece end
     auto piece_end = [&](const PieceWalk &p) { return min(tile_sees(a, p.t, p.tile), (p.unit + p.len) * PG_TILE); };
 
@@ -276,9 +282,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) attn_paged_q4_kernel(const __gr
                 if (piece >= DQ_QUERIES)
                     ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&ss.q_empty[qb]), (piece / DQ_QUERIES - 1) & 1));
                 if (ok) {
-                    make_query(reinterpret_cast<const uint4 *>(a.q + ((size_t)r0.token * KV_HQ + KV_G * r0.head + (lane >> 2)) * KV_D) + 2 * (lane & 3),
-                               ss.query[qb], lane);
-                    mbar_arrive(smem_u32(&ss.q_full[qb]));
+                    if (piece > 0) query(qb, r0.token, r0.head);   // warp 0 makes the first
                     ++piece;
                     if (a.gate != nullptr && r0.whole) // and its gates, for the epilogue: 128 bytes per lane
                         asm volatile("prefetch.global.L2 [%0];" ::"l"(a.gate + r0.token * a.gate_row + (KV_G * r0.head + (lane >> 2)) * a.gate_head + 64 * (lane & 3)));
@@ -302,6 +306,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) attn_paged_q4_kernel(const __gr
         asm volatile("mov.u32 %0, 0x000F000F;\n\tmov.u32 %1, 0x43004300;" : "=r"(mask), "=r"(magic));
         asm volatile("mov.u32 %0, 0x00F000F0;\n\tmov.u32 %1, 0x64006400;" : "=r"(mask16), "=r"(one));
         bool ok = true;
+        if (warp == 0) query(0, w.t.row0 + w.tile, w.head);
         for (;;) {
             const int sees = tile_sees(a, w.t, w.tile);
             const int mrow = w.t.row0 + w.tile;
@@ -463,6 +468,11 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) attn_paged_q4_kernel(const __gr
                 }
             if (!ok) ss.abort = ss.stop = 1;
             float *const all = reinterpret_cast<float *>(blk + DQ_OUT);
+            uint2 gates[2] = {};                   // of the warp's outputs in either half, before the warps wait for each other
+            if (a.gate != nullptr && w.whole() && warp < 8)
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+                    gates[half] = __ldg(reinterpret_cast<const uint2 *>(a.gate + mrow * a.gate_row + (KV_G * w.head + 4 * half + (warp >> 1)) * a.gate_head) + 32 * (warp & 1) + lane);
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {
                 if (j4 >> 1 == half) {
@@ -492,7 +502,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) attn_paged_q4_kernel(const __gr
                         e.x = fmaf(f, x.x, e.x); e.y = fmaf(f, x.y, e.y); e.z = fmaf(f, x.z, e.z); e.w = fmaf(f, x.w, e.w);
                     }
                     if (w.whole()) {
-                        finish4<TO>(a, mrow, KV_G * w.head + h, d, e, L != 0.0f ? 1.0f / L : 0.0f);
+                        finish4<TO>(a, half == 0 ? gates[0] : gates[1], mrow, KV_G * w.head + h, d, e, L != 0.0f ? 1.0f / L : 0.0f);
                     } else {
                         const size_t at = ((size_t)2 * blockIdx.x + (w.first ? 0 : 1)) * a.rows + h;
                         *reinterpret_cast<float4 *>(a.part_o + at * KV_D + d) = e;
