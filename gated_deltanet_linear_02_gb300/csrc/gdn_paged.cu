@@ -628,9 +628,6 @@ __global__ void __launch_bounds__(fa_threads(Q4), 1) attn_paged_kernel(const __g
                 ok = __all_sync(0xffffffffu, wait_pv(u - 1) && !aborted);
                 tc::fence_after_sync();
                 if (live && ok) {
-                    const size_t slot = ((size_t)2 * blockIdx.x + (w.first ? 0 : 1)) * a.rows + r;
-                    const float inv = l == 0.0f ? 0.0f : (whole ? 1.0f / l : 1.0f);
-                    const bool blank = __any_sync(0xffffffffu, l == 0.0f);   // a row that saw nothing gives zeros
                     if (__any_sync(0xffffffffu, *const_cast<const volatile int *>(&ss.poison) != 0)) {
                         // what the piece's value rows that not all see have left out
                         const int begin = max(max(all, 0), w.unit * PG_TILE), end = min(limit, (w.unit + w.len) * PG_TILE);
@@ -650,6 +647,23 @@ __global__ void __launch_bounds__(fa_threads(Q4), 1) attn_paged_kernel(const __g
                         }
                         tc::wait_st();
                     }
+                }
+                if (live && ok && !whole) {            // a piece: as it is, in fp32 (a row that saw nothing is left out by the join)
+                    const size_t slot = ((size_t)2 * blockIdx.x + (w.first ? 0 : 1)) * a.rows + r;
+#pragma unroll 1
+                    for (int c = 128 * grp; c < 128 * grp + 128; c += 32) {
+                        float o[32];
+                        tc::tmem_ld32(lbase + FA_O + c, o);
+                        tc::wait_ld();
+                        if (mine)
+#pragma unroll
+                            for (int k = 0; k < 32; k += 4)
+                                *reinterpret_cast<float4 *>(a.part_o + slot * KV_D + c + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                    }
+                    if (mine && grp == 0) *reinterpret_cast<float2 *>(a.part_ml + slot * 2) = make_float2(m * SCORE_SCALE, l);
+                } else if (live && ok) {
+                    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                    const bool blank = __any_sync(0xffffffffu, l == 0.0f);   // a row that saw nothing gives zeros
                     TO *out = static_cast<TO *>(a.out);
 #pragma unroll 1
                     for (int part = 0; part < 128 / PART; ++part) {
@@ -685,9 +699,7 @@ __global__ void __launch_bounds__(fa_threads(Q4), 1) attn_paged_kernel(const __g
 #pragma unroll
                                     for (int k = 0; k < 8; ++k) e[k] *= inv;
                                 }
-                                if (!whole) {
-                                    if (mine) store8_out(a.part_o + slot * KV_D + d + 8 * i, e);
-                                } else if (sizeof(TO) == 4) {
+                                if (sizeof(TO) == 4) {
                                     if (mine) store8_out(out + ((size_t)(row0 + (r >> 3)) * KV_HQ + h0 + (r & 7)) * KV_D + d + 8 * i, e);
                                 } else {
                                     store8_out(reinterpret_cast<bf16 *>(at[i]), e);
@@ -695,7 +707,7 @@ __global__ void __launch_bounds__(fa_threads(Q4), 1) attn_paged_kernel(const __g
                             }
                             __syncwarp();
                         }
-                        if (whole && sizeof(TO) == 2) {
+                        if (sizeof(TO) == 2) {
                             uint4 v[COPIES];
                             TO *dst = out + ((size_t)(row0 + 4 * q4) * KV_HQ + h0 + (er & 7)) * KV_D + 128 * grp + PART * part + 8 * ec;
 #pragma unroll
@@ -707,7 +719,6 @@ __global__ void __launch_bounds__(fa_threads(Q4), 1) attn_paged_kernel(const __g
                             __syncwarp();
                         }
                     }
-                    if (mine && !whole && grp == 0) *reinterpret_cast<float2 *>(a.part_ml + slot * 2) = make_float2(m * SCORE_SCALE, l);
                 }
                 tc::fence_before_sync();
                 mbar_arrive(smem_u32(&ss.o_empty));
