@@ -26,8 +26,8 @@
 //  - warps 12-19, with 4-bit pages only: codes to bf16. The producer then copies
 //    the eight records' key or value codes of a tile (18 KiB, a quarter of the
 //    values) into one of two buffers, and these warps write the stages, a ring of
-//    three. Four warps instead of eight: 173 us instead of 162 for three sequences
-//    of 517 tokens over contexts of 6,001.
+//    three. With four warps 173 us where eight take 162, for three sequences
+//    of up to 517 tokens over contexts of up to 6,001.
 // Values that are not finite: a weight of 0 times infinity or NaN is NaN, so a value
 // row may only enter the product as it is if all 16 tokens of the item see it. Rows
 // that none sees become zeros, and of those that some see (the item's own tokens, at
@@ -37,12 +37,12 @@
 //
 // Bound: for one token per sequence by HBM (1 KiB of keys and values per position
 // and KV head; the 120 unused rows cost tensor time that hides behind it): 256
-// contexts of up to 4,096 take 247 us, 6.5 TB/s. For prompts by the shared-memory
+// contexts of up to 4,096 take 244 us, 6.6 TB/s. For prompts by the shared-memory
 // port, which carries Q, K, V and the TMA writes of a tile in about 2,500 cycles
-// against 2,048 of tensor work: 1.63 us per tile over contexts of 16,384 (1,560
-// TFLOP/s), and about 10 us per item for its epilogue, its tile on the diagonal and
+// against 2,048 of tensor work: 1.60 us per tile over contexts of 16,384 (1,590
+// TFLOP/s), and about 9 us per item for its epilogue, its tile on the diagonal and
 // the start of the next, during which the products wait: a prompt of 4,096 tokens
-// takes 145 us. With 4-bit pages the port also carries the codes, and the logic
+// takes 139 us. With 4-bit pages the port also carries the codes, and the logic
 // pipe their expansion: 2.7 us per tile.
 #include <cuda.h>
 
@@ -910,8 +910,8 @@ cudaError_t launch_attn_paged(const gdn_paged_batch *b, const gdn_kv_cache *c, c
     a.gate_head = gate_head;
     a.out = out;
     a.rows = piece_rows(b->max_q);
-    // an item's own cost in units of tiles. One prompt of 4,096: 187 us with 2, 157 with 3, 145 with 4 to 6, 149
-    // with 8; items of fewer rows have a shorter epilogue and longer tiles
+    // an item's own cost in units of tiles. One prompt of 4,096: 174 us with 2, 150 with 3, 139 with 4, 140 with
+    // 6, 144 with 8; items of fewer rows have a shorter epilogue and longer tiles
     a.tok = PG_TOK;
     a.tok_log2 = 4;
     a.lead = b->max_q >= PG_TOK ? 4 : b->max_q > 1 ? 3 : 2;
