@@ -534,11 +534,19 @@ def attn_paged(batch: gdn_paged_batch, cache: gdn_kv_cache, q, out, gate=None, w
     """gdn_attn_paged: causal attention of the batch's new tokens over the paged
     cache. q [M][16][256] dense bf16 (normed and rotated), out dense fp32 or
     bf16, gate [M][16][256] bf16 (strided views allowed; None: no output gate).
-    Allocates the workspace through torch when none is given and returns it."""
+    Allocates the workspace through torch, for the stream the call runs on, when
+    none is given, and returns it."""
     M, dev = batch.M, _on_batch(batch, cache, "attn_paged")
     gp, gr, gh = _heads(gate, "gate", M, ATTN_HQ, dev, torch.bfloat16)
     if workspace is None:
-        workspace = torch.empty(max(attn_paged_workspace_size(batch, cache), 256), dtype=torch.uint8, device=dev)
+        need = max(attn_paged_workspace_size(batch, cache), 256)
+        if stream is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        else:                                      # from that stream's memory: the current one may still use its own
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(stream), device=dev)
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     st = (_lib or lib()).gdn_attn_paged(batch._ref, cache._ref, _dense(q, "q", (M, ATTN_HQ, ATTN_D), dev, torch.bfloat16), gp, gr, gh,
                               _dense(out, "out", (M, ATTN_HQ, ATTN_D), dev), _dense(workspace, "workspace", workspace.shape, dev),
                               workspace.nbytes, _act_dtype(out), _raw_stream(stream, dev))

@@ -300,6 +300,24 @@ def test_values_of_any_magnitude(ops, scales, new, ctx):
     P.compare(b, run(ops, b, torch.float32), P.reference(b), f"scales {scales} new {new}")
 
 
+@pytest.mark.parametrize("raw", [False, True])
+def test_another_stream_allocates_its_own_workspace(ops, raw):
+    """Without a workspace the call takes one from its own stream's memory: the
+    current stream's blocks may still be in use there."""
+    b = P.make_batch(900, "bf16", [20], [300], 16)
+    ref = run(ops, b)
+    side = torch.cuda.Stream()
+    plan, cache = P.handles(ops, b)
+    q, gate, out = b.q.to(DEV), b.gate.to(DEV), torch.empty(20, 16, 256, dtype=torch.bfloat16, device=DEV)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        busy = torch.full((1 << 22,), 1.0, device=DEV).mul_(2.0)   # its block is free for the current stream alone
+        del busy
+        ops.attn_paged(plan, cache, q, out, gate, stream=side.cuda_stream if raw else side)
+    torch.cuda.synchronize()
+    assert ops.device_error() == ops.GDN_OK and torch.equal(out, ref)
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "q4"])
 def test_a_conversation(ops, fmt):
     """The operators together as a layer uses them: a prompt appended and
