@@ -510,8 +510,10 @@ gdn_status gdn_kv_gather(const gdn_paged_batch *batch, const gdn_kv_cache *cache
  *               gdn_attn_paged_workspace_size(batch, cache) bytes; contents need
  *               no initialisation. Calls that share one must be ordered on a
  *               stream
- * Rows of the cache at or past ctx_len are never used, whatever they hold. The
- * softmax weights enter the value product rounded to bf16 (fp32 sums).
+ * Rows of the cache at or past ctx_len are never used, whatever they hold, nor are
+ * a later token's rows by an earlier one. The softmax weights enter the value
+ * product rounded to bf16 (fp32 sums); with 4-bit pages and max_q > 2 the keys and
+ * values that the pages stand for are rounded to bf16 as well.
  * Errors: GDN_ERR_INVALID_ARG, GDN_ERR_WORKSPACE, GDN_ERR_CUDA (also when the
  * driver's tensor-map encoder is unavailable). A bounded device wait that gives
  * up is reported afterwards by gdn_device_error.
