@@ -132,7 +132,7 @@ __device__ __noinline__ void make_query(const uint4 *q, DqQuery &out, int lane)
         float sum = 0.0f;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            const uint4 v = __ldg(q + 8 * g + c);
+            const uint4 v = q[8 * g + c];          // not __ldg: the kernel before may have written them while this one started
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 qf[g][c][k] = word_of(v, k);
