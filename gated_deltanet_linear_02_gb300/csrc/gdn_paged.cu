@@ -42,7 +42,7 @@
 // against 2,048 of tensor work: 1.60 us per tile over contexts of 16,384 (1,590
 // TFLOP/s), and about 9 us per item for its epilogue, its tile on the diagonal and
 // the start of the next, during which the products wait: a prompt of 4,096 tokens
-// takes 139 us. With 4-bit pages the port also carries the codes, and the logic
+// takes 138 us. With 4-bit pages the port also carries the codes, and the logic
 // pipe their expansion: 2.7 us per tile.
 #include <cuda.h>
 
@@ -128,6 +128,9 @@ template <bool Q4> __device__ __forceinline__ uint32_t poison_of(const PagedArgs
     return m;
 }
 
+// Brings a tensor map near before its first use.
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *m) { asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory"); }
+
 template <int N> __device__ __forceinline__ void set_registers_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void set_registers_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
@@ -168,6 +171,11 @@ __global__ void __launch_bounds__(fa_threads(Q4), 1) attn_paged_kernel(const __g
         mbar_init(smem_u32(&ss.o_empty), 256);
         ss.abort = ss.poison = 0;
         fence_mbar_init();
+    }
+    if (!Q4 && tid == 32) {                        // 1% of a prompt; none with 4-bit pages, whose first copies are of codes
+        prefetch_map(&qmap);
+        prefetch_map(&kmap);
+        prefetch_map(&vmap);
     }
     if (warp == 3) {
         tc::tmem_alloc(smem_u32(&ss.tmem), 512);
@@ -239,9 +247,9 @@ __global__ void __launch_bounds__(fa_threads(Q4), 1) attn_paged_kernel(const __g
                     ++piece;
                 };
                 if (!Q4) {
+                    load_q(kw.w.t.row0 + PG_TOK * kw.w.tile, kw.w.head);
                     int row, loaded;
                     segment(row, loaded);
-                    load_q(kw.w.t.row0 + PG_TOK * kw.w.tile, kw.w.head);
                     if (ok) load(&kmap, row, loaded);
                     while (ok) {
                         const int vrow = row, vloaded = loaded;
