@@ -42,7 +42,7 @@
 // against 2,048 of tensor work: 1.60 us per tile over contexts of 16,384 (1,590
 // TFLOP/s), and about 9 us per item for its epilogue, its tile on the diagonal and
 // the start of the next, during which the products wait: a prompt of 4,096 tokens
-// takes 138 us. With 4-bit pages the port also carries the codes, and the logic
+// takes 137 us. With 4-bit pages the port also carries the codes, and the logic
 // pipe their expansion: 2.7 us per tile.
 #include <cuda.h>
 
