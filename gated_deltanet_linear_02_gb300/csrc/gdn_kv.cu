@@ -395,12 +395,15 @@ __device__ __forceinline__ void store_row_q4(const InputArgs &a, const float (&i
     for (int i = 0; i < 8; ++i) all += fabsf(in[i]);
     Quant q;
     bool range, sure = quantise_f32(x, tol, err, q, range) && tame && all < 1e30f;
-    // Exact values that are next to a border are mostly ties, which fp32 can settle.
-    if (err == 0.0f && !__all_sync(0xffffffffu, sure)) sure = sure || (range && all < 1e30f && quantise_exact(x, q));
+    // `err` is a group's own, so groups of one row may differ in it: the votes are taken by the whole warp, and
+    // only what has no exchange between lanes depends on it.
     if (!__all_sync(0xffffffffu, sure)) {
+        // Exact values that are next to a border are mostly ties, which fp32 can settle.
+        if (!sure && err == 0.0f && tame && range && all < 1e30f) sure = quantise_exact(x, q);
         const bool mid = tame && all < 1e12f && (all > 1e-10f || all == 0.0f) && err < 5e5f && (err > 5e-17f || err == 0.0f) &&
                          q.s < 1e12f && (q.s > 1e-12f || q.s == 0.0f);
-        if (__all_sync(0xffffffffu, mid)) {
+        if (__all_sync(0xffffffffu, sure)) {
+        } else if (__all_sync(0xffffffffu, mid)) {
             Pair xp[8];
             norm_rotate_pair(in, xp, isv ? nullptr : a.k_w, isv ? nullptr : rope, a.eps, lane);
             quantise_pair(xp, q);
