@@ -479,12 +479,18 @@ __global__ void __launch_bounds__(fa_threads(Q4), 1) attn_paged_kernel(const __g
             // O += P V of unit v is complete. Two barriers in turn: S of unit u, which this thread has
             // seen, was issued after that of unit u - 2 completed, so each is one phase behind at most.
             auto wait_pv = [&](uint32_t v) { return mbar_wait_sleep(smem_u32(&ss.pv_done[v & 1]), (v >> 1) & 1); };
-            // barrier of the two warps that share rows
+            // Barriers of the two warps that share rows; the second is the epilogue's, right behind a first one.
+            // They have no limit of their own, so a warp that gives up (ok = false; perhaps alone, where one of
+            // its waits ran out or it was the first to see the stop) marks its maxima, sets the stop and arrives
+            // at both without waiting, see the end. Its partner's next barriers then open, and behind them it
+            // finds the mark or the stop and leaves in the same way.
             auto pair_bar = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + q4) : "memory"); };
+            auto pair_bar2 = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(5 + q4) : "memory"); };
             for (;;) {
                 const int rows = KV_G * w.tokens(a), sees = tile_sees(a, w.t, w.tile);
-                const int limit = min(w.t.first + PG_TOK * w.tile + (r >> 3) + 1, cap);   // positions this row sees
-                const int all = min(w.t.first + PG_TOK * w.tile + 1, sees);               // ... and all rows
+                // positions this row sees, and those that all rows see; formed at each use, as registers are short
+                auto limit_of = [&]() { return min(w.t.first + PG_TOK * w.tile + (r >> 3) + 1, cap); };
+                auto all_see = [&]() { return min(w.t.first + PG_TOK * w.tile + 1, sees); };
                 const bool live = 32 * q4 < rows;      // the warp has rows of the item
                 float m = -INFINITY, l = 0.0f;
                 for (int j = 0; j < w.len; ++j, ++u) {
@@ -499,6 +505,7 @@ __global__ void __launch_bounds__(fa_threads(Q4), 1) attn_paged_kernel(const __g
                             tc::tmem_ld32(sc + 64 * grp + 32, x[1]);
                             tc::wait_ld();
                         }
+                        const int limit = limit_of();
                         if (__any_sync(0xffffffffu, c0 + 64 > limit)) {
 #pragma unroll
                             for (int c = 0; c < 2; ++c)
@@ -564,7 +571,7 @@ __global__ void __launch_bounds__(fa_threads(Q4), 1) attn_paged_kernel(const __g
                         tc::wait_st();
                     }
                     if (!ok) break;
-                    if (!Q4 && p0 + PG_TILE > all) {
+                    if (!Q4 && p0 + PG_TILE > all_see()) {
                         // Value rows that not every token of the item sees, see above: zeros past the context,
                         // whatever the cache (or an earlier tile) left there, and for values that are not
                         // finite. The previous unit's products are waited for first: they free the stages'
@@ -582,7 +589,7 @@ __global__ void __launch_bounds__(fa_threads(Q4), 1) attn_paged_kernel(const __g
                                 for (int c = 0; c < 8; ++c) row[c] = zero;
                             }
                         }
-                        const int own = max(all, p0) + (r >> 3);       // eight threads for each of at most 15 rows
+                        const int own = max(all_see(), p0) + (r >> 3);   // eight threads for each of at most 15 rows
                         if (own < min(sees, p0 + PG_TILE)) {
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
@@ -632,13 +639,13 @@ __global__ void __launch_bounds__(fa_threads(Q4), 1) attn_paged_kernel(const __g
                 pair_bar();
                 const float l1 = reinterpret_cast<const float *>(blk + Fa<Q4>::EPI + ((warp - 4) ^ 4) * Fa<Q4>::BOX)[lane];
                 l = grp == 0 ? l + l1 : l1 + l;
-                pair_bar();
+                pair_bar2();
                 ok = __all_sync(0xffffffffu, wait_pv(u - 1) && !aborted);
                 tc::fence_after_sync();
                 if (live && ok) {
                     if (__any_sync(0xffffffffu, *const_cast<const volatile int *>(&ss.poison) != 0)) {
                         // what the piece's value rows that not all see have left out
-                        const int begin = max(max(all, 0), w.unit * PG_TILE), end = min(limit, (w.unit + w.len) * PG_TILE);
+                        const int begin = max(max(all_see(), 0), w.unit * PG_TILE), end = min(limit_of(), (w.unit + w.len) * PG_TILE);
 #pragma unroll 1
                         for (int d = 128 * grp; d < 128 * grp + 128; d += 16) {
                             uint32_t m = 0u, x[16];
@@ -733,7 +740,13 @@ __global__ void __launch_bounds__(fa_threads(Q4), 1) attn_paged_kernel(const __g
                 if (!ok || !w.more(a)) break;
                 w.next(a);
             }
-            if (!ok && lane == 0) ss.abort = 1;
+            if (!ok) {
+                ss.top[0][grp][r] = ss.top[1][grp][r] = 0xFFFFFFFFu;
+                ss.abort = 1;
+                __threadfence_block();
+                __syncwarp();
+                asm volatile("bar.arrive %0, 64;\n\tbar.arrive %1, 64;" ::"r"(1 + q4), "r"(5 + q4) : "memory");
+            }
         }
     }
     tc::fence_before_sync();
