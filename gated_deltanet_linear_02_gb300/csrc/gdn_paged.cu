@@ -108,21 +108,21 @@ __device__ __forceinline__ uint32_t value_pair(uint32_t w, int t, uint32_t s2, u
 __device__ __forceinline__ uint32_t not_finite(uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
 
 // Which of the 16 values from dim d of position p's value row are +infinity (bits 0-15) or -infinity (16-31); both:
-// NaN.
+// NaN. Plain loads: the append before this kernel may write the row while this one has started.
 template <bool Q4> __device__ __forceinline__ uint32_t poison_of(const PagedArgs &a, int seq, int head, int p, int d)
 {
     const int page = cache_page(a.b, seq, p), off = p & (a.b.page - 1);
     if (page < 0) return 0u;
     if (Q4) {
         const unsigned char *rec = static_cast<const unsigned char *>(a.ck) + record_of(a.b, page, head, off);
-        const uint32_t sz = __ldg(reinterpret_cast<const uint32_t *>(rec + REC_VSZ + (off % REC_ROWS) * 16) + d / 64);
+        const uint32_t sz = *(reinterpret_cast<const uint32_t *>(rec + REC_VSZ + (off % REC_ROWS) * 16) + d / 64);
         return not_finite(sz) != 0u ? 0xFFFFFFFFu : 0u;
     }
     const uint16_t *row = static_cast<const uint16_t *>(a.cv) + row_bf16(a.b, page, head, off) + d;
     uint32_t m = 0u;
 #pragma unroll 1
     for (int k = 0; k < 16; ++k) {
-        const uint32_t x = __ldg(row + k);
+        const uint32_t x = row[k];
         if ((x & 0x7F80u) == 0x7F80u) m |= (x & 0x7Fu) != 0u ? 0x10001u << k : 1u << (k + 16 * (x >> 15));
     }
     return m;
@@ -613,7 +613,8 @@ __global__ void __launch_bounds__(fa_threads(Q4), 1) attn_paged_kernel(const __g
                 if (!ok) break;
                 // Epilogue: this group's 128 dims, 64 at a time. A thread's row lies 512 bytes from its
                 // neighbour's, so gates come in and outputs leave through 4 KiB of shared memory per warp,
-                // in whole 128-byte lines. The gates are read while the last product runs. The loops stay
+                // in whole 128-byte lines. The gates are read (plainly, as all data that the
+                // kernel before may have written) while the last product runs. The loops stay
                 // rolled: this runs once per piece, so its instructions are fetched anew each time, and
                 // unrolled it took 13,000 cycles per piece, most of them for that.
                 const bool mine = r < rows, whole = w.whole(), gated = whole && a.gate != nullptr;
@@ -631,7 +632,7 @@ __global__ void __launch_bounds__(fa_threads(Q4), 1) attn_paged_kernel(const __g
 #pragma unroll
                     for (int i = 0; i < COPIES; ++i)
                         gate[i] = 4 * q4 + (RPC * i >> 3) < rows >> 3
-                                      ? __ldg(reinterpret_cast<const uint4 *>(gsrc + (RPC * i >> 3) * a.gate_row + (RPC * i & 7) * a.gate_head + PART * part))
+                                      ? load_global(reinterpret_cast<const uint4 *>(gsrc + (RPC * i >> 3) * a.gate_row + (RPC * i & 7) * a.gate_head + PART * part))
                                       : make_uint4(0u, 0u, 0u, 0u);
                 };
                 if (gated && live) load_gate(0);
@@ -651,6 +652,7 @@ __global__ void __launch_bounds__(fa_threads(Q4), 1) attn_paged_kernel(const __g
                             uint32_t m = 0u, x[16];
 #pragma unroll 1
                             for (int p = begin; p < end; ++p) m |= poison_of<Q4>(a, w.seq, w.head, p, d);
+                            __syncwarp();              // the rows' ends differ
                             float o[16];
                             tc::tmem_ld16(lbase + FA_O + d, o);
                             tc::wait_ld();
@@ -797,7 +799,7 @@ __global__ void __launch_bounds__(256) attn_paged_join_kernel(const PagedArgs a)
     const int mrow = t.row0 + (st.tile << a.tok_log2) + (r >> 3), h = KV_G * st.head + (r & 7);
     uint4 gate = make_uint4(0u, 0u, 0u, 0u);
     const bool gated = a.gate != nullptr && r < rows && part == 0;
-    if (gated) gate = __ldg(reinterpret_cast<const uint4 *>(a.gate + mrow * a.gate_row + h * a.gate_head) + lane);
+    if (gated) gate = *(reinterpret_cast<const uint4 *>(a.gate + mrow * a.gate_row + h * a.gate_head) + lane);
     float M = -INFINITY, l = 0.0f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     for (int k0 = head - 1 + part; k0 <= last && r < rows; k0 += 4 * share) {
         float2 ml[4];

@@ -319,6 +319,14 @@ __device__ __forceinline__ void store8_out(bf16 *p, const float (&x)[8])
     *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
                                                pack_bf16(x[6], x[7]));
 }
+// A load of global memory that the kernel before may have written (not through the read-only path), free to move
+// past stores to shared memory.
+__device__ __forceinline__ uint4 load_global(const uint4 *p)
+{
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
 // inv * sigmoid(g) in four instructions, two of them special functions (a few 2^-23
 // relative). Epilogues wait for these: with expf and a division in full an item's
 // 32,768 outputs took three times as long, with a Newton reciprocal twice.

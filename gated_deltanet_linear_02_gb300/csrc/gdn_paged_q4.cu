@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) attn_paged_q4_kernel(const __gr
             if (a.gate != nullptr && w.whole() && warp < 8)
 #pragma unroll
                 for (int half = 0; half < 2; ++half)
-                    gates[half] = __ldg(reinterpret_cast<const uint2 *>(a.gate + mrow * a.gate_row + (KV_G * w.head + 4 * half + (warp >> 1)) * a.gate_head) + 32 * (warp & 1) + lane);
+                    gates[half] = *(reinterpret_cast<const uint2 *>(a.gate + mrow * a.gate_row + (KV_G * w.head + 4 * half + (warp >> 1)) * a.gate_head) + 32 * (warp & 1) + lane);
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {
                 if (j4 >> 1 == half) {
