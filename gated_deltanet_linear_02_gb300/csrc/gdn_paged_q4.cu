@@ -12,19 +12,30 @@
 // operation per two codes and few shifts:
 //  - keys in fp16: nibble c in bits 0-3 of 0x6400 is 1024 + c, in bits 4-7 1024 +
 //    16 c, so a word of eight codes needs one shift; q enters in fp16, scaled by a
-//    power of two per head (exact down to 2^-22 of the head's largest element) and
+//    power of two per head (exact down to 2^-20 of the head's largest element) and
 //    by 1/16 where the code has its 16;
 //  - values in bf16: the sum runs over positions, so words of two positions are
-//    interleaved by halves, and nibble c in the low bits of 0x4300 is 128 + c.
+//    interleaved by halves, and nibble c in the low bits of 0x4300 is 128 + c, and
+//    inverted in those of 0xC300 c - 143: the positions of a record take these in
+//    turn, odd ones first in its second half.
 // (fp8 instructions would take the nibbles as they are, 0..15 being c 2^-9 in e4m3,
 // but they are carried out as conversions to fp16 here: measured 10% slower.)
 // Steps and zeros stay out of the products: with sums per group g of 64 dims,
 //   q . k = sum_g s_g (sum_{d in g} q_d (1024 + c_d) - 1024 sum q_d) + z_g sum_{d in g} q_d,
-//   o_d   = sum_p w'_p (128 + c_d) + sum_p (w_p (z_p + 8 s_p) - 136 w'_p),  w'_p = bf16(w_p s_p).
-// The roundings to fewer bits are w' and q's elements below 2^-22 of the largest.
-// The 1024s and 128s are taken out with the rounded numbers they went in with; the
-// 8 puts the rounding of w' on c - 8, half as large as c (error of a decode batch
-// 2.3e-3 instead of 4.5e-3, 1.7e-3 of it the output's own rounding).
+//   o_d   = sum_p w'_p (128 + c_d, or c_d - 143) + sum_p (w_p (z_p + 8 s_p) - 136 w'_p, or + 135 w'_p),
+//   w'_p  = bf16(w_p s_p).
+// The roundings to fewer bits are w' and q's elements below 2^-20 of the largest.
+// The offsets are taken out with the rounded numbers they went in with; the 8 puts
+// the rounding of w' on c - 8, half as large as c.
+// The warp instructions' sums are truncated, so a sum that an offset makes large
+// moves by a part of that offset, always in one direction. So positions next to
+// each other, and the halves, carry offsets of opposite sign, and every DQ_FOLD records a warp takes
+// what they have left out of its sums. Error against 64 bits (norm of the difference
+// over that of the result, values about zero, fp32 outputs): 1.6e-3 to 1.8e-3 from
+// 1,024 to 262,144 positions in one piece, the rounding of w' alone; with 128 + c throughout and
+// one correction at the end 1.8e-3 at 4,096, 8e-3 at 16,384, 0.13 at 65,536. The
+// keys' 1,024 q are gone after each 64 dims of a record: below 1e-4 of the spread of
+// a score.
 //
 // Work: gdn_paged.cuh with one token per item. The records of a piece go round the
 // 11 warps, each with its own online softmax, and the warps meet once per piece.
@@ -46,6 +57,10 @@ constexpr int DQ_WARPS = 11;                      // with the producer three war
 constexpr int DQ_THREADS = 32 * (DQ_WARPS + 1);
 constexpr int DQ_STAGES = 3;
 constexpr uint32_t DQ_CODES = 4096, DQ_SZ = 512;  // bytes of a record's codes; of its steps and zeros
+// Records of a warp after which the offsets leave its sums. A decode batch takes 109.0 us with 32, 109.8 with 16,
+// 110.5 with 8 (108.5 when they leave at the end only); where one of every 16 positions has all the weight, so that
+// offsets do not cancel, 262,144 positions in a piece give an error of 2.1e-3, 1.8e-3, 1.7e-3.
+constexpr int DQ_FOLD = 32;
 constexpr int DQ_OSTRIDE = KV_D + 8;              // floats per head of a warp's output in shared memory
 constexpr uint32_t DQ_RING = 0;
 constexpr uint32_t DQ_RING_SZ = DQ_WARPS * DQ_STAGES * DQ_CODES;
@@ -105,6 +120,13 @@ __device__ __forceinline__ uint32_t mask_or(uint32_t w, uint32_t mask, uint32_t 
 {
     uint32_t r;
     asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(magic));
+    return r;
+}
+// (w & mask) ^ magic: halves of 0x4300 give 128 + c, halves of 0xC30F the negative of 128 + (15 - c), c - 143.
+__device__ __forceinline__ uint32_t mask_xor(uint32_t w, uint32_t mask, uint32_t magic)
+{
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(r) : "r"(w), "r"(mask), "r"(magic));
     return r;
 }
 __device__ __forceinline__ float sz_step(uint32_t w) { return __uint_as_float(w << 16); }
@@ -302,9 +324,11 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) attn_paged_q4_kernel(const __gr
         // ---- consumers. Fragment coordinates: i = lane / 4, j = lane % 4.
         const int i4 = lane >> 2, j4 = lane & 3;
         uint32_t slot = 0, phase = 0, piece = 0;   // of the warp's ring; pieces begun
-        uint32_t mask, magic, mask16, one;         // not constants to the compiler, so that they stay in registers
-        asm volatile("mov.u32 %0, 0x000F000F;\n\tmov.u32 %1, 0x43004300;" : "=r"(mask), "=r"(magic));
+        uint32_t mask, plus_minus, minus_plus, mask16, one;   // not constants to the compiler, so that they stay in registers
+        asm volatile("mov.u32 %0, 0x000F000F;\n\tmov.u32 %1, 0xC30F4300;\n\tmov.u32 %2, 0x4300C30F;" : "=r"(mask), "=r"(plus_minus), "=r"(minus_plus));
         asm volatile("mov.u32 %0, 0x00F000F0;\n\tmov.u32 %1, 0x64006400;" : "=r"(mask16), "=r"(one));
+        // what takes the offset out, for positions i and 8 + i of a record
+        const float back0 = i4 & 1 ? 135.0f : -136.0f, back1 = i4 & 1 ? -136.0f : 135.0f;
         bool ok = true;
         if (warp == 0) query(0, w.t.row0 + w.tile, w.head);
         for (;;) {
@@ -323,6 +347,15 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) attn_paged_q4_kernel(const __gr
                     for (int k = 0; k < 4; ++k) o[g][t][k] = 0.0f;
             }
             const int end = piece_end(w);
+            int folds = DQ_FOLD;                   // records until the biases next go into the outputs
+            auto sum_bias = [&]() {                // over the lanes that share a head
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1)
+#pragma unroll
+                    for (int g = 0; g < 4; ++g)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) bias[g][k] += __shfl_xor_sync(0xffffffffu, bias[g][k], d);
+            };
             for (int p0 = w.unit * PG_TILE + 16 * warp; p0 < end && ok; p0 += 16 * DQ_WARPS) {
                 ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&ss.full[warp][slot]), phase));
                 if (!ok) break;
@@ -427,16 +460,16 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) attn_paged_q4_kernel(const __gr
                         const float s0 = sz_step(word_of(z0, g)), s1 = sz_step(word_of(z1, g));
                         const uint32_t w0 = pack_bf16(p[0] * s0, p[1] * s0), w1 = pack_bf16(p[2] * s1, p[3] * s1);
                         const float e0 = fmaf(8.0f, s0, sz_zero(word_of(z0, g))), e1 = fmaf(8.0f, s1, sz_zero(word_of(z1, g)));
-                        bias[g][0] += fmaf(p[0], e0, p[2] * e1) - 136.0f * (sz_step(w0) + sz_step(w1));
-                        bias[g][1] += fmaf(p[1], e0, p[3] * e1) - 136.0f * (sz_zero(w0) + sz_zero(w1));
+                        bias[g][0] += fmaf(p[0], e0, p[2] * e1) + fmaf(back0, sz_step(w0), back1 * sz_step(w1));
+                        bias[g][1] += fmaf(p[1], e0, p[3] * e1) + fmaf(back0, sz_zero(w0), back1 * sz_zero(w1));
                         const uint32_t b0 = transpose8(w0), b1 = transpose8(w1);
                         const uint32_t lo = __byte_perm(word_of(v0, g), word_of(v1, g), 0x5410), hi = __byte_perm(word_of(v0, g), word_of(v1, g), 0x7632);
                         const uint32_t lo2 = __byte_perm(word_of(v2, g), word_of(v3, g), 0x5410), hi2 = __byte_perm(word_of(v2, g), word_of(v3, g), 0x7632);
                         // product t: rows 0-7 are dims 8 i + 2 t of the group, rows 8-15 dims 8 i + 2 t + 1
-                        mma_m16n8k16(o[g][0], mask_or(lo, mask, magic), mask_or(lo >> 4, mask, magic), mask_or(lo2, mask, magic), mask_or(lo2 >> 4, mask, magic), b0, b1);
-                        mma_m16n8k16(o[g][1], mask_or(lo >> 8, mask, magic), mask_or(lo >> 12, mask, magic), mask_or(lo2 >> 8, mask, magic), mask_or(lo2 >> 12, mask, magic), b0, b1);
-                        mma_m16n8k16(o[g][2], mask_or(hi, mask, magic), mask_or(hi >> 4, mask, magic), mask_or(hi2, mask, magic), mask_or(hi2 >> 4, mask, magic), b0, b1);
-                        mma_m16n8k16(o[g][3], mask_or(hi >> 8, mask, magic), mask_or(hi >> 12, mask, magic), mask_or(hi2 >> 8, mask, magic), mask_or(hi2 >> 12, mask, magic), b0, b1);
+                        mma_m16n8k16(o[g][0], mask_xor(lo, mask, plus_minus), mask_xor(lo >> 4, mask, plus_minus), mask_xor(lo2, mask, minus_plus), mask_xor(lo2 >> 4, mask, minus_plus), b0, b1);
+                        mma_m16n8k16(o[g][1], mask_xor(lo >> 8, mask, plus_minus), mask_xor(lo >> 12, mask, plus_minus), mask_xor(lo2 >> 8, mask, minus_plus), mask_xor(lo2 >> 12, mask, minus_plus), b0, b1);
+                        mma_m16n8k16(o[g][2], mask_xor(hi, mask, plus_minus), mask_xor(hi >> 4, mask, plus_minus), mask_xor(hi2, mask, minus_plus), mask_xor(hi2 >> 4, mask, minus_plus), b0, b1);
+                        mma_m16n8k16(o[g][3], mask_xor(hi >> 8, mask, plus_minus), mask_xor(hi >> 12, mask, plus_minus), mask_xor(hi2 >> 8, mask, minus_plus), mask_xor(hi2 >> 12, mask, minus_plus), b0, b1);
                     }
                 }
                 };
@@ -447,19 +480,27 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) attn_paged_q4_kernel(const __gr
                     slot = 0;
                     phase ^= 1;
                 }
+                if (--folds == 0) {                // the offsets out of the sums
+                    folds = DQ_FOLD;
+                    sum_bias();
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+#pragma unroll
+                        for (int t = 0; t < 4; ++t)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) o[g][t][k] += bias[g][k & 1];
+                        bias[g][0] = bias[g][1] = 0.0f;
+                    }
+                }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&ss.q_empty[qb]));
             // the warps' outputs, maxima and sums meet in shared memory, four heads at a time
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) {
+            for (int d = 4; d < 32; d <<= 1)
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    l[k] += __shfl_xor_sync(0xffffffffu, l[k], d);
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) bias[g][k] += __shfl_xor_sync(0xffffffffu, bias[g][k], d);
-                }
-            }
+                for (int k = 0; k < 2; ++k) l[k] += __shfl_xor_sync(0xffffffffu, l[k], d);
+            sum_bias();
             if (i4 == 0)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
