@@ -665,7 +665,7 @@ __global__ void __launch_bounds__(fa_threads(Q4), 1) attn_paged_kernel(const __g
                         tc::wait_st();
                     }
                 }
-                if (live && ok && !whole) {            // a piece: as it is, in fp32 (a row that saw nothing is left out by the join)
+                if (live && ok && !whole) {            // a piece: as it is, in fp32 (a row that saw nothing in it is left out by the join)
                     const size_t slot = ((size_t)2 * blockIdx.x + (w.first ? 0 : 1)) * a.rows + r;
 #pragma unroll 1
                     for (int c = 128 * grp; c < 128 * grp + 128; c += 32) {
@@ -679,8 +679,9 @@ __global__ void __launch_bounds__(fa_threads(Q4), 1) attn_paged_kernel(const __g
                     }
                     if (mine && grp == 0) *reinterpret_cast<float2 *>(a.part_ml + slot * 2) = make_float2(m * SCORE_SCALE, l);
                 } else if (live && ok) {
-                    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-                    const bool blank = __any_sync(0xffffffffu, l == 0.0f);   // a row that saw nothing gives zeros
+                    // a row that sees nothing gives zeros; one whose scores are all -infinity NaN, as the formula does
+                    const bool blind = limit_of() <= 0, blank = __any_sync(0xffffffffu, blind);
+                    const float inv = blind ? 0.0f : 1.0f / l;
                     TO *out = static_cast<TO *>(a.out);
 #pragma unroll 1
                     for (int part = 0; part < 128 / PART; ++part) {
@@ -704,7 +705,7 @@ __global__ void __launch_bounds__(fa_threads(Q4), 1) attn_paged_kernel(const __g
                             tc::wait_ld();
                             if (blank)
 #pragma unroll
-                                for (int k = 0; k < 16; ++k) o[k] = l == 0.0f ? 0.0f : o[k];
+                                for (int k = 0; k < 16; ++k) o[k] = blind ? 0.0f : o[k];
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
                                 float e[8];
@@ -850,7 +851,9 @@ __global__ void __launch_bounds__(256) attn_paged_join_kernel(const PagedArgs a)
         }
     }
     if (r >= rows) return;
-    const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+    // l is 0 where the row sees nothing (zeros), and where all its scores are -infinity (NaN, as the formula)
+    const bool blind = t.first + (st.tile << a.tok_log2) + (r >> 3) < 0;
+    const float inv = blind ? 0.0f : 1.0f / l;
     if (gated) gate8(gate, o, inv);
     else
 #pragma unroll

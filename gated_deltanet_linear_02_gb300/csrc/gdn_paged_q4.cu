@@ -29,13 +29,13 @@
 // the rounding of w' on c - 8, half as large as c.
 // The warp instructions' sums are truncated, so a sum that an offset makes large
 // moves by a part of that offset, always in one direction. So positions next to
-// each other, and the halves, carry offsets of opposite sign, and every DQ_FOLD records a warp takes
-// what they have left out of its sums. Error against 64 bits (norm of the difference
-// over that of the result, values about zero, fp32 outputs): 1.6e-3 to 1.8e-3 from
-// 1,024 to 262,144 positions in one piece, the rounding of w' alone; with 128 + c throughout and
-// one correction at the end 1.8e-3 at 4,096, 8e-3 at 16,384, 0.13 at 65,536. The
-// keys' 1,024 q are gone after each 64 dims of a record: below 1e-4 of the spread of
-// a score.
+// each other, and the halves, carry offsets of opposite sign, and every DQ_FOLD
+// records a warp takes what they have left out of its sums. Error against 64 bits
+// (norm of the difference over that of the result, values about zero, fp32 outputs):
+// 1.6e-3 to 1.8e-3 from 1,024 to 262,144 positions in one piece, the rounding of w'
+// alone; with 128 + c throughout and one correction at the end 1.8e-3 at 4,096, 8e-3
+// at 16,384, 0.13 at 65,536. The keys' 1,024 q are gone after each 64 dims of a
+// record: below 1e-4 of the spread of a score.
 //
 // Work: gdn_paged.cuh with one token per item. The records of a piece go round the
 // 11 warps, each with its own online softmax, and the warps meet once per piece.
@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) attn_paged_q4_kernel(const __gr
                         e.x = fmaf(f, x.x, e.x); e.y = fmaf(f, x.y, e.y); e.z = fmaf(f, x.z, e.z); e.w = fmaf(f, x.w, e.w);
                     }
                     if (w.whole()) {
-                        finish4<TO>(a, half == 0 ? gates[0] : gates[1], mrow, KV_G * w.head + h, d, e, L != 0.0f ? 1.0f / L : 0.0f);
+                        finish4<TO>(a, half == 0 ? gates[0] : gates[1], mrow, KV_G * w.head + h, d, e, sees > 0 ? 1.0f / L : 0.0f);   // nothing seen: zeros
                     } else {
                         const size_t at = ((size_t)2 * blockIdx.x + (w.first ? 0 : 1)) * a.rows + h;
                         *reinterpret_cast<float4 *>(a.part_o + at * KV_D + d) = e;

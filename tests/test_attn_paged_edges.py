@@ -62,3 +62,56 @@ def test_attention_reads_what_the_append_before_it_wrote(ops, fmt, new, ctx):
             assert not torch.isfinite(out[spoilt]).any() and torch.isfinite(out[~spoilt]).all()
             if fmt == "bf16":                                  # finite rows enter as they are: the same bits
                 assert torch.equal(out[~spoilt], outs[0][~spoilt])
+
+
+def one_context(ops, fmt, L, new, k, v, q, page=64, repeat=1):
+    """`new` last tokens of `repeat` sequences over one context of L rows k, v [L][2][256]: outputs [repeat * new][16][256]."""
+    rows = A.Rows(fmt, [L], [L], page)
+    plan, cache = rows.handles(ops)
+    ops.kv_append(ops.make_attn_params(), plan, cache, k.to(DEV), v.to(DEV))
+    table = plan._keep_alive[0].repeat(repeat, 1)
+    batch = ops.make_paged_batch(table, torch.full((repeat,), L, dtype=torch.int32, device=DEV), new * repeat,
+                                 torch.arange(0, new * repeat + 1, new, dtype=torch.int32, device=DEV), new)
+    out = torch.full((new * repeat, 16, 256), 7.0, device=DEV)
+    ops.attn_paged(batch, cache, q.to(DEV), out)
+    torch.cuda.synchronize()
+    assert ops.device_error() == ops.GDN_OK
+    return out.cpu().double().numpy()
+
+
+@pytest.mark.parametrize("L,new", [(40, 1), (40, 40), (300, 3), (300, 20), (20000, 1), (20000, 17)])
+def test_scores_of_minus_infinity(ops, L, new):
+    """Keys whose scores are all -infinity give NaN, as their softmax does (0 / 0), not
+    the zeros of a token that sees nothing; beside finite scores they have no weight."""
+    k, v, q = A.draw(11, L, 2, 256), A.draw(12, L, 2, 256), A.draw(13, new, 16, 256)
+    q[..., 3] = q[..., 3].abs() + 0.5
+    low = k.clone()
+    low[:, 1, 3] = -float("inf")
+    x = one_context(ops, "bf16", L, new, low, v, q)
+    assert np.isnan(x[:, 8:]).all() and np.isfinite(x[:, :8]).all()
+    some = k.clone()
+    first = L - new + 1                                        # what the first token sees
+    some[:first // 2, 1, 3] = -float("inf")
+    some[first // 2 + 1::3, 1, 3] = -float("inf")
+    x = one_context(ops, "bf16", L, new, some, v, q)
+    kd, vd, qd = some.double().numpy(), v.double().numpy(), q.double().numpy()
+    ref = np.zeros_like(x)
+    for t in range(new):
+        see = first + t
+        for h in range(16):
+            with np.errstate(invalid="ignore"):
+                s = np.where(np.isinf(kd[:see, h // 8, 3]), -np.inf, np.nan_to_num(kd[:see, h // 8], neginf=0.0) @ qd[t, h] / 16)
+            w = np.exp(s - s.max())
+            ref[t, h] = (w / w.sum()) @ vd[:see, h // 8]
+    # weights rounded to bf16: half a step of the spread and the mean, see paged_testlib
+    assert (np.abs(x - ref) <= P.EPS / (1 - P.EPS) * 2 * np.abs(vd).max() + 1e-4 * np.abs(vd).max()).all()
+
+
+@pytest.mark.parametrize("L,new", [(40, 1), (40, 3), (3000, 1), (3000, 3), (40000, 2)])
+def test_scores_that_overflow_to_minus_infinity_over_4_bits(ops, L, new):
+    """The same over 4-bit pages, whose keys are finite: scores past fp32 on the negative
+    side are no zeros either."""
+    k, v, q = A.draw(21, L, 2, 256), A.draw(22, L, 2, 256), A.draw(23, new, 16, 256).abs() + 0.5
+    k[:, 1] = -3e38
+    x = one_context(ops, "q4", L, new, k, v, q)
+    assert np.isnan(x[:, 8:]).all() and np.isfinite(x[:, :8]).all()
