@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(fa_threads(Q4), 1) attn_paged_kernel(const __g
                                     tc::tmem_ld32(lbase + FA_O + 128 * grp + 32 * c, o);
                                     tc::wait_ld();
 #pragma unroll
-                                    for (int i = 0; i < 32; ++i) o[i] = f > 0.0f ? o[i] * f : 0.0f;
+                                    for (int i = 0; i < 32; ++i) o[i] *= f;   // infinities and NaN stay, also where f is 0
                                     tc::tmem_st32(lbase + FA_O + 128 * grp + 32 * c, o);
                                 }
                                 tc::wait_st();

@@ -115,3 +115,25 @@ def test_scores_that_overflow_to_minus_infinity_over_4_bits(ops, L, new):
     k[:, 1] = -3e38
     x = one_context(ops, "q4", L, new, k, v, q)
     assert np.isnan(x[:, 8:]).all() and np.isfinite(x[:, :8]).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "q4"])
+@pytest.mark.parametrize("L,new", [(700, 1), (700, 3), (700, 20), (30000, 1), (30000, 4)])
+def test_a_value_that_is_not_finite_stays_when_its_weight_underflows(ops, fmt, L, new):
+    """A value row with an infinity and a NaN early in the context, and a key far later
+    whose score takes every other weight below fp32: the dims of the row (in 4 bits its
+    groups) are not finite, the others are the late row's."""
+    k, v, q = A.draw(31, L, 2, 256, scale=0.1), A.draw(32, L, 2, 256), A.draw(33, new, 16, 256)
+    q[:] = q[:1, :1]
+    v[5, 1, 70], v[5, 1, 200] = float("inf"), float("nan")
+    late = L - new - 2
+    k[late, 1] = 20 * q[0, 0]                                  # a score of about 300, the others near 0
+    repeat = 152 if L == 700 else 8                            # whole contexts in a CTA; cut into pieces
+    x = one_context(ops, fmt, L, new, k, v, q.repeat(repeat, 1, 1), repeat=repeat)
+    dims = [70, 200] if fmt == "bf16" else list(range(64, 128)) + list(range(192, 256))
+    clean = np.setdiff1d(np.arange(256), dims)
+    assert not np.isfinite(x[:, 8:, dims]).any()
+    assert np.isfinite(x[:, 8:, clean]).all() and np.isfinite(x[:, :8]).all()
+    want = v[late, 1].double().numpy()
+    step = 0.0 if fmt == "bf16" else (want.max() - want.min()) / 15
+    assert (np.abs(x[:, 8:, clean] - want[clean]) <= P.EPS * np.abs(want).max() + step).all()
