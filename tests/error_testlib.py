@@ -36,3 +36,8 @@ def bound(four_bits: bool, max_q: int, out_dtype) -> float:
 def relative(got, ref) -> float:
     got = got.detach().cpu().double().numpy() if isinstance(got, torch.Tensor) else np.asarray(got)
     return float(np.linalg.norm(got - ref) / np.linalg.norm(ref))
+
+
+# new tokens and contexts of the batches that are compared by norm
+BATCHES = [([257], [1300]), ([513, 64], [513, 900]), ([130, 1], [200, 700]), ([3, 20, 0, 17], [1000, 131, 50, 333]),
+           ([70], [1300]), ([1, 1, 1], [1025, 129, 513]), ([2, 1, 2], [900, 700, 130]), ([8, 5], [300, 2600])]
