@@ -547,7 +547,7 @@ constexpr int QR = 4;                             // queries per warp and token
 template <typename TI, typename TO, int NKV, bool Q4, bool ISQ, int N>
 __device__ __forceinline__ void walk_tokens(const InputArgs &a, int first, int m0, int m1, int lane)
 {
-    const bool rot = a.rope != nullptr && !(NKV == 4 && !ISQ && N == 1 && first >= KV_H && !Q4);
+    const bool rot = a.rope != nullptr;
     const float *wp = ISQ ? a.q_w : a.k_w;
     float w[8] = {}, c[8] = {}, s[8] = {};
     if (wp != nullptr) load8(wp + 8 * lane, w);

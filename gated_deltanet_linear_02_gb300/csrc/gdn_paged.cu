@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(fa_threads(Q4), 1) attn_paged_kernel(const __g
                             tile.rec = lane >= 8 || 16 * lane >= tile.sees ? -2
                                        : (unsigned)entry < (unsigned)b.num_pages ? (((entry * KV_H) << b.page_log2) + at) >> 4 : -1;
                             tile.all = min(max(kw.w.t.first + PG_TOK * kw.w.tile + 1 - p, 0), tile.sees);
-                        tile.row0 = kw.w.t.row0 + PG_TOK * kw.w.tile;
+                            tile.row0 = kw.w.t.row0 + PG_TOK * kw.w.tile;
                             tile.head = kw.w.head;
                             tile.first = kw.j == 0;
                             (ahead++ == 0 ? q0 : q1) = tile;

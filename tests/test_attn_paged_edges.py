@@ -137,3 +137,32 @@ def test_a_value_that_is_not_finite_stays_when_its_weight_underflows(ops, fmt, L
     want = v[late, 1].double().numpy()
     step = 0.0 if fmt == "bf16" else (want.max() - want.min()) / 15
     assert (np.abs(x[:, 8:, clean] - want[clean]) <= P.EPS * np.abs(want).max() + step).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "q4"])
+@pytest.mark.parametrize("n", [1, 20])
+def test_sequences_without_new_tokens_between(ops, fmt, n):
+    """65,535 sequences, of which the first, one in the middle and the last have new tokens."""
+    B, L, page = 65535, 200, 64
+    per = -(-L // page)
+    some = [0, 40000, B - 1]
+    small = P.make_batch(70, fmt, [n] * 3, [L, 150, 64], page)
+    table = torch.full((B, per), -1, dtype=torch.int32)
+    ctx, new = torch.full((B,), 77, dtype=torch.int32), torch.zeros(B, dtype=torch.int32)
+    for i, s in enumerate(some):
+        table[s, :small.table.shape[1]] = small.table[i]
+        ctx[s], new[s] = small.ctx[i], n
+    cu = torch.zeros(B + 1, dtype=torch.int32)
+    cu[1:] = torch.cumsum(new, 0)
+    cache = ops.make_kv_cache(small.k.to(DEV), None if small.v is None else small.v.to(DEV))
+    plan = ops.make_paged_batch(table.to(DEV), ctx.to(DEV), 3 * n, cu.to(DEV), n)
+    out = torch.full((3 * n, 16, 256), 7.0, device=DEV)
+    ops.attn_paged(plan, cache, small.q.to(DEV), out, small.gate.to(DEV))
+    torch.cuda.synchronize()
+    assert ops.device_error() == ops.GDN_OK
+    P.compare(small, out, P.reference(small), f"{fmt} n {n}")
+    kr, vr = (torch.empty(3 * n, 2, 256, device=DEV) for _ in range(2))
+    ops.kv_gather(plan, cache, kr, vr)
+    for i in range(3):
+        k, v = (t[:, -n:].transpose(1, 0, 2) for t in small.kv[i])
+        assert np.array_equal(kr[i * n:i * n + n].cpu().numpy(), k.astype(np.float32)) and np.array_equal(vr[i * n:i * n + n].cpu().numpy(), v.astype(np.float32))
