@@ -103,9 +103,10 @@ __device__ __forceinline__ float mean_square_far(float (&x)[8], float eps)
 // RMSNorm and rotation of a row in fp32. `tol` returns a bound of each value's error,
 // in units of 2^-24 of what went into it: the mean of squares 10 (a rounded square, a
 // tree of 8 additions, and eps), halved by the root, the refined root 1.5, two products
-// 2: 8.5 of |x|; a rotated one three roundings more, 11.5 of |x c| + |y s|. (bf16 rows,
-// whose squares are exact, stay 0.5 below.) `tame`: the mean of squares is such that
+// 2: 8.5 of |x|; a rotated one three roundings more, 11.5 of |x c| + |y s|. In bf16 rows
+// (TI) the squares are exact, which is 0.5 less. `tame`: the mean of squares is such that
 // this holds.
+template <typename TI>
 __device__ __forceinline__ void norm_rotate(float (&x)[8], const float *__restrict__ w, const float *__restrict__ rope,
                                             float eps, int lane, float (&tol)[8], bool &tame)
 {
@@ -123,7 +124,7 @@ __device__ __forceinline__ void norm_rotate(float (&x)[8], const float *__restri
         for (int i = 0; i < 8; ++i) x[i] = x[i] * r * wv[i];
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) tol[i] = 5.1e-7f * fabsf(x[i]);
+    for (int i = 0; i < 8; ++i) tol[i] = (sizeof(TI) == 2 ? 4.8e-7f : 5.1e-7f) * fabsf(x[i]);
     if (rope != nullptr) {
         float y[8];
 #pragma unroll
@@ -136,7 +137,7 @@ __device__ __forceinline__ void norm_rotate(float (&x)[8], const float *__restri
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float t = sg * y[i] * s[i];
-                tol[i] = 6.9e-7f * (fabsf(x[i] * c[i]) + fabsf(t));
+                tol[i] = (sizeof(TI) == 2 ? 6.6e-7f : 6.9e-7f) * (fabsf(x[i] * c[i]) + fabsf(t));
                 x[i] = fmaf(x[i], c[i], t);
             }
         }
@@ -401,6 +402,7 @@ __device__ __noinline__ void quantise_f64(const double (&x)[8], Quant &q)
 
 // One K or V row in registers to its 4-bit place: fp32 where its error can change
 // nothing, else in pairs, or in 64 bits where pairs leave their range.
+template <typename TI>
 __device__ __forceinline__ void store_row_q4(const InputArgs &a, const float (&in)[8], bool isv, const float *rope, int page,
                                              int head, int off, int lane)
 {
@@ -409,7 +411,7 @@ __device__ __forceinline__ void store_row_q4(const InputArgs &a, const float (&i
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = in[i];
     if (!isv && (a.k_w != nullptr || rope != nullptr)) {
-        norm_rotate(x, a.k_w, rope, a.eps, lane, tol, tame);
+        norm_rotate<TI>(x, a.k_w, rope, a.eps, lane, tol, tame);
 #pragma unroll
         for (int i = 0; i < 8; ++i) err = fmaxf(err, tol[i]);
         tame = tame && ((tol[0] + tol[1]) + (tol[2] + tol[3])) + ((tol[4] + tol[5]) + (tol[6] + tol[7])) < 1e30f;   // no NaN
@@ -479,18 +481,18 @@ __global__ void __launch_bounds__(KV_WARPS * 32) attn_input_few_kernel(const Inp
         const int page = cache_page(a.b, at.seq, at.pos), off = at.pos & (a.b.page - 1);
         if (page < 0) return;
         if (Q4) {
-            store_row_q4(a, x, isv, rope, page, h, off, lane);
+            store_row_q4<TI>(a, x, isv, rope, page, h, off, lane);
             return;
         }
         float tol[8];
         bool tame;
-        if (!isv) norm_rotate(x, a.k_w, rope, a.eps, lane, tol, tame);
+        if (!isv) norm_rotate<TI>(x, a.k_w, rope, a.eps, lane, tol, tame);
         store8(static_cast<bf16 *>(isv ? a.cache_v : a.cache_k) + row_bf16(a.b, page, h, off) + 8 * lane, x);
         return;
     }
     float tol[8];
     bool tame;
-    norm_rotate(x, isq ? a.q_w : a.k_w, rope, a.eps, lane, tol, tame);
+    norm_rotate<TI>(x, isq ? a.q_w : a.k_w, rope, a.eps, lane, tol, tame);
     store8(isq ? static_cast<TO *>(a.q_out) + ((size_t)m * KV_HQ + h) * KV_D + 8 * lane
                : static_cast<TO *>(a.k_out) + ((size_t)m * KV_H + h) * KV_D + 8 * lane, x);
 }
@@ -641,7 +643,7 @@ __device__ __forceinline__ void walk_tokens(const InputArgs &a, int first, int m
                 cur[i].get(x);
                 if (Q4 && !ISQ) {
                     const int row = first + i;
-                    store_row_q4(a, x, row >= KV_H, a.rope != nullptr ? a.rope + (size_t)r * GDN_ATTN_ROT_DIM : nullptr, pg,
+                    store_row_q4<TI>(a, x, row >= KV_H, a.rope != nullptr ? a.rope + (size_t)r * GDN_ATTN_ROT_DIM : nullptr, pg,
                                  row < KV_H ? row : row - KV_H, off, lane);
                     continue;
                 }
