@@ -9,14 +9,15 @@
 // group of 64 dims is 8 lanes, whose 8 codes each pack into one 32-bit word; a
 // row's 32 words are one 128-byte line of the record.
 //
-// The kernels are bound by HBM (or, for a few tokens, by latency): per token and
-// head 512 bytes in, 512 (bf16) or 144 (4 bits) out, and the rotation table's 256
-// bytes per token. With many tokens a warp takes four rows of one token, whose
+// Per token and head 512 bytes go in, 512 (bf16) or 144 (4 bits) out, and the rotation
+// table's 256 bytes per token. With many tokens a warp takes four rows of one token, whose
 // loads all start before the token's place in the cache is looked up (a chain of
-// dependent reads); with few, one row, so that more SMs share them. Measured: norms and
-// rotation of 4,096 tokens 16.6 us (4.6 TB/s; a copy of as many bytes at full rate takes
-// 11.3), bf16 append with queries 17.4 us (4.6 TB/s), 4-bit append 13.9 us: there the
-// exact codes are bound by instructions, some 500 per row and warp.
+// dependent reads); with few, one row, so that more SMs share them. Few tokens are bound
+// by latency, many by bytes and instructions together (two thirds of the issue slots
+// while an SM is active). Measured, buffers in turn beyond L2: norms and rotation of
+// 4,096 tokens 16.9 us (4.5 TB/s; a copy of as many bytes at full rate takes 11.3; 15.8
+// in L2), bf16 append with queries 17.8 us (4.7 TB/s), 4-bit append 14.4 us: there the
+// exact codes are bound by instructions, 489 per row and warp.
 #include "gdn_async.cuh"
 #include "gdn_kv.cuh"
 
@@ -694,12 +695,12 @@ __global__ void __launch_bounds__(KV_WARPS * 32, input_ctas(NQ, Q4)) attn_input_
 }
 
 // Rows up to which one warp takes one row, two waves of 48 warps on each of 152 SMs,
-// and above which warps walk. Both sides, us: norms of 512 tokens (9,216 rows) 4.2
-// against 5.2, of 4,096 18.4 against 16.6; bf16 append with queries 512 5.4 against
-// 5.6, 4,096 24.4 against 17.4; 4-bit append 2,048 (8,192 rows) 9.7 against 12.1,
-// 4,096 14.4 against 13.9. Keys and values into bf16 pages are copies but for the
-// norm, and gain from the walk's loads ahead sooner: 512 tokens 3.3 on both sides,
-// 2,048 5.5 against 3.7.
+// and above which warps walk. Both sides, us, in L2: norms of 512 tokens (9,216 rows) 4.1
+// against 4.9, 811 (14,598 rows) 5.1 both, 4,096 18.0 against 15.8; bf16 append with
+// queries 512 5.4 both, 811 6.8 against 5.5, 4,096 24.6 against 16.9; 4-bit append 1,024
+// (4,096 rows) 6.9 against 8.6, 2,048 9.7 against 10.3, 4,096 14.6 against 14.0. Keys and
+// values into bf16 pages are copies but for the norm, and gain from the walk's loads
+// ahead sooner: 512 tokens 3.3 both, 2,048 5.5 against 3.9.
 constexpr long long few_rows(int nq, int nkv, bool q4) { return nq == 0 && nkv == 4 && !q4 ? 2048 : 2 * 152 * 48; }
 
 template <typename TI, typename TO, int NQ, int NKV, bool Q4>
@@ -746,7 +747,8 @@ cudaError_t launch_kv_append(const gdn_attn_params *p, const gdn_paged_batch *b,
 
 // Reads rows back: the same warp layout, values z + s c in fp32 (s c is exact:
 // 8 x 4 bits), one rounding to the output type. A warp takes a token's k0, k1, v0, v1:
-// 4,096 tokens in bf16 out of 4-bit pages 3.1 us (one row per warp: 4.1).
+// 4,096 tokens in bf16 out of 4-bit pages 4.2 us, 3.5 in L2 (one row per warp a third
+// more), out of bf16 pages 4.2; 2^20 tokens 414 us (6.6 TB/s) and 617 us (7.0 TB/s).
 template <typename TO, bool Q4>
 __global__ void __launch_bounds__(KV_WARPS * 32) kv_gather_kernel(const PagedBatch b, const void *ck, const void *cv,
                                                                   TO *k_out, TO *v_out)

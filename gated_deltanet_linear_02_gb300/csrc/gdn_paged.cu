@@ -37,9 +37,9 @@
 //
 // Bound: for one token per sequence by HBM (1 KiB of keys and values per position
 // and KV head; the 120 unused rows cost tensor time that hides behind it): 256
-// contexts of up to 4,096 take 244 us, 6.6 TB/s. For prompts by the shared-memory
+// contexts of up to 4,096 take 245 us, 6.6 TB/s. For prompts by the shared-memory
 // port, which carries Q, K, V and the TMA writes of a tile in about 2,500 cycles
-// against 2,048 of tensor work: 1.60 us per tile over contexts of 16,384 (1,590
+// against 2,048 of tensor work: 1.59 us per tile over contexts of 16,384 (1,600
 // TFLOP/s), and about 9 us per item for its epilogue, its tile on the diagonal and
 // the start of the next, during which the products wait: a prompt of 4,096 tokens
 // takes 137 us. With 4-bit pages the port also carries the codes, and the logic
@@ -897,8 +897,8 @@ static bool encode_q_map(CUtensorMap *map, const void *q, int M)
     return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// New tokens of a sequence up to which a 4-bit cache is read token by token: two take 275 us against 352 for a tile
-// of all (76 contexts of 16,384), three 409 against 352.
+// New tokens of a sequence up to which a 4-bit cache is read token by token: two take 271 us against 377 for a tile
+// of all (76 contexts of 16,384), three 404 against 369; 64 contexts of 1,024: 31 against 36, 41 against 36.
 constexpr int Q4_SINGLE = 2;
 constexpr size_t START_BYTES = (PG_RANGES * sizeof(PagedStart) + 255) / 256 * 256;
 
@@ -937,7 +937,9 @@ cudaError_t launch_attn_paged(const gdn_paged_batch *b, const gdn_kv_cache *c, c
     a.out = out;
     a.rows = piece_rows(b->max_q);
     // an item's own cost in units of tiles. One prompt of 4,096: 174 us with 2, 150 with 3, 139 with 4, 140 with
-    // 6, 144 with 8; items of fewer rows have a shorter epilogue and longer tiles
+    // 6, 144 with 8. Items of fewer rows have a shorter epilogue and tiles bound by HBM, and it matters little:
+    // with 1, 2, 3 and 4, four tokens on 64 contexts of 2,048 take 54, 57, 57 and 56 us, eight on 20 of 4,096 44, 43,
+    // 44 and 43, one token on 256 of 2,048 166, 165, 166 and 166; over 4-bit pages 78, 78, 77 and 78
     a.tok = PG_TOK;
     a.tok_log2 = 4;
     a.lead = b->max_q >= PG_TOK ? 4 : b->max_q > 1 ? 3 : 2;

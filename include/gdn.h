@@ -417,10 +417,12 @@ typedef struct {
  *   cu_q        device int32 [B+1], 0 = cu[0] <= ... <= cu[B] <= M; NULL: one
  *               new token per sequence, row b
  *   M           packed rows; rows at or past cu_q[B] (B without cu_q) are
- *               padding, neither read nor written
+ *               padding: never written, and not used (they may be loaded, so
+ *               the inputs have to have all M rows)
  *   max_q       at least the largest n_b (1 without cu_q). It chooses kernels
  *               and workspace; rows of a sequence with more tokens than this
  *               are unspecified
+ * The three tensors must not change while a call that reads them runs.
  * B <= 65535, M <= 2^24, max_pages * page_size <= 2^30. */
 typedef struct {
     const int32_t *page_table, *ctx_len, *cu_q;
@@ -441,7 +443,9 @@ typedef struct {
 /*
  * gdn_attn_qk_norm_rope -- steps 2-4 for M tokens in one pass:
  *   out = rotate(x * (mean(x^2) + norm_eps)^-1/2 * w, rope[positions[m]])
- * per head of 256 dims, fp32 arithmetic, one rounding at the end.
+ * per head of 256 dims, fp32 arithmetic, one rounding at the end. Rows may have any
+ * finite magnitude (squares that leave fp32 are scaled); with norm_eps 0 a row of
+ * zeros gives NaN, as 0 / 0 does.
  *   q           [M][16][256] act with element strides q_row_stride and
  *               q_head_stride (the last dim dense; e.g. 8192 and 512 for the
  *               joint query+gate projection)
@@ -473,8 +477,9 @@ gdn_status gdn_attn_qk_norm_rope(const gdn_attn_params *p, const void *q, long l
  *               in its context. A token whose row is outside [0, n_pos) is
  *               neither stored nor written to q_out (not read without rope)
  * Keys are rounded once, from fp32 to bf16 or, in the 4-bit format, as the
- * format defines it from the unrounded keys: codes, steps and zeros that fp32
- * cannot decide are settled in 64 bits. Two tokens that name the same cache row
+ * format defines it from the unrounded keys: codes, steps and zeros that fp32's
+ * error could change are settled in pairs of fp32 numbers (48 bits), or in 64 bits
+ * where those leave their range. Two tokens that name the same cache row
  * (a page listed for two sequences) leave that row unspecified.
  * Errors: GDN_ERR_INVALID_ARG, GDN_ERR_CUDA.
  */
@@ -505,15 +510,19 @@ gdn_status gdn_kv_gather(const gdn_paged_batch *batch, const gdn_kv_cache *cache
  *   gate        [M][16][256] bf16 with element strides (multiples of 8), or NULL:
  *               no gate
  *   out         dense [M][16][256] out_dt; a token that sees no position gives
- *               zeros. Must not overlap the inputs
+ *               zeros, one whose scores are all -infinity NaN. Must not overlap
+ *               the inputs
  *   workspace   device scratch, 16-byte aligned, of
  *               gdn_attn_paged_workspace_size(batch, cache) bytes; contents need
  *               no initialisation. Calls that share one must be ordered on a
  *               stream
  * Rows of the cache at or past ctx_len are never used, whatever they hold, nor are
  * a later token's rows by an earlier one. The softmax weights enter the value
- * product rounded to bf16 (fp32 sums); with 4-bit pages and max_q > 2 the keys and
- * values that the pages stand for are rounded to bf16 as well.
+ * product rounded to bf16 (fp32 sums; over 4-bit pages with max_q <= 2 times each
+ * group's step); with 4-bit pages and max_q > 2 the keys and values that the pages
+ * stand for are rounded to bf16 as well. max_q chooses for the whole call: single
+ * tokens over 4-bit pages are both faster and more accurate in a call of their own
+ * than beside a prompt.
  * Errors: GDN_ERR_INVALID_ARG, GDN_ERR_WORKSPACE, GDN_ERR_CUDA (also when the
  * driver's tensor-map encoder is unavailable). A bounded device wait that gives
  * up is reported afterwards by gdn_device_error.
