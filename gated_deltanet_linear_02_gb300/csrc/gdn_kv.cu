@@ -290,7 +290,7 @@ __device__ __forceinline__ bool quantise_f32(const float (&x)[8], const float (&
     const float t = (hi - lo) * (1.0f / 15.0f), et = err * (2.0f / 15.0f) + t * 3e-7f;
     q.s = to_f(__float2bfloat16_rn(t));
     q.codes = 0;
-    if (hi == lo && err == 0.0f) {                 // a constant group: s = 0
+    if (hi == lo && err == 0.0f && (lo == 0.0f || fabsf(lo) > 1e-30f)) {   // a constant group: s = 0 (not where `tol` underflows)
         q.s = 0.0f;
         return range = true;
     }

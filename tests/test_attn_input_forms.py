@@ -215,3 +215,18 @@ def test_append_q4_of_many_tokens(ops, M, queries, act):
         live = (rows.seq >= 0) & (rows.pos >= 0)
         close(qo[live], oracle.norm_rope(q.double(), kw * 2, turn)[live], "queries")
         assert torch.equal(qo[~live].cpu(), q[~live].to(torch.bfloat16) if act == torch.bfloat16 else torch.zeros_like(qo[~live].cpu()))
+
+
+@pytest.mark.parametrize("M", [8, WALK_Q4])
+def test_append_q4_rotated_keys_below_the_normal_numbers(ops, M):
+    """A rotated group that is constant in fp32 and whose least value lies half a bf16 step
+    and a little from 0: the little decides its zero."""
+    rows = A.Rows("q4", [M], [M], 32)
+    k, v = torch.zeros(M, 2, 256), A.draw(91, M, 2, 256, dtype=torch.float32)
+    k[..., :64] = -2.0 ** -134
+    k[1::2, :, :64] = 2.0 ** -134
+    k[2::3, :, 64:128] = 2.0 ** -134                # not rotated: exact
+    table = torch.cat([torch.ones(M, 32), torch.full((M, 32), 2.0 ** -17)], 1)
+    plan, cache = rows.handles(ops)
+    ops.kv_append(ops.make_attn_params(None, None, table.to(DEV)), plan, cache, k.to(DEV), v.to(DEV))
+    A.check_q4(rows, cache._keep_alive[0], oracle.norm_rope(k.double(), None, table), v.double().numpy())
