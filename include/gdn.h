@@ -523,6 +523,8 @@ gdn_status gdn_kv_gather(const gdn_paged_batch *batch, const gdn_kv_cache *cache
  * stand for are rounded to bf16 as well. max_q chooses for the whole call: single
  * tokens over 4-bit pages are both faster and more accurate in a call of their own
  * than beside a prompt.
+ * Weights times values are summed in fp32 before they are normalised: cached
+ * values up to 2^85 in magnitude stay finite at any length.
  * Errors: GDN_ERR_INVALID_ARG, GDN_ERR_WORKSPACE, GDN_ERR_CUDA (also when the
  * driver's tensor-map encoder is unavailable). A bounded device wait that gives
  * up is reported afterwards by gdn_device_error.
