@@ -57,6 +57,17 @@ size_t paged_workspace_bytes(const gdn_paged_batch *b, const gdn_kv_cache *c);
 cudaError_t launch_attn_paged(const gdn_paged_batch *b, const gdn_kv_cache *c, const void *q, const void *gate,
                               long long gate_row, long long gate_head, void *out, void *ws, gdn_dtype out_dt,
                               cudaStream_t s);
+cudaError_t launch_add_norm(const gdn_norm_params *, const void *, long long, const void *, long long, const void *,
+                            long long, void *, long long, void *, long long, int, gdn_dtype, gdn_dtype, cudaStream_t);
+cudaError_t launch_linear(const void *, long long, const void *, const float *, const void *, long long, void *,
+                          long long, int, int, int, gdn_activation, gdn_dtype, cudaStream_t);
+void *linear_error_word();
+cudaError_t launch_route(const gdn_moe_params *, const void *, long long, int, int32_t *, float *, cudaStream_t);
+void *route_error_word();
+size_t moe_workspace_bytes(const gdn_moe_params *, int);
+cudaError_t launch_moe(const gdn_moe_params *, const void *, long long, const void *, void *, int, const int32_t *,
+                       const float *, void *, gdn_dtype, cudaStream_t);
+void *moe_error_word();
 cudaError_t launch_wait_timeout(cudaStream_t s);
 void *selftest_error_word();
 }  // namespace gdn
@@ -177,6 +188,45 @@ gdn_status check_batch(const gdn_paged_batch *b, const gdn_kv_cache *c)
     return GDN_OK;
 }
 
+size_t elem_size(gdn_dtype d) { return d == GDN_F32 ? 4 : 2; }
+
+// Rows of `width` elements, `row` elements apart: how far they reach, and whether
+// the stride keeps them 16-byte aligned and apart (0, one row for all, where `once`).
+struct Rows {
+    const void *p;
+    long long row;
+    int width;
+    gdn_dtype dt;
+    size_t bytes(int M) const { return ((size_t)(M - 1) * (size_t)row + (size_t)width) * elem_size(dt); }
+    bool ok(bool once = false) const
+    {
+        return ok_ptr(p) && row % (long long)(16 / elem_size(dt)) == 0 && row <= (1ll << 32) &&
+               (row >= width || (once && row == 0));
+    }
+};
+bool overlap(const Rows &a, const Rows &b, int M) { return a.p && b.p && overlap(a.p, a.bytes(M), b.p, b.bytes(M)); }
+bool same_rows(const Rows &a, const Rows &b) { return a.p == b.p && a.row == b.row && a.dt == b.dt; }
+
+gdn_status check_moe_route(const gdn_moe_params *p)
+{
+    if (p == nullptr) return fail(GDN_ERR_INVALID_ARG, "moe params is NULL");
+    if (p->num_experts < 1 || p->num_experts > GDN_MOE_MAX_EXPERTS)
+        return fail(GDN_ERR_INVALID_ARG, "num_experts out of range [1, 256]");
+    if (p->top_k < 1 || p->top_k > GDN_MOE_MAX_TOPK || p->top_k > p->num_experts)
+        return fail(GDN_ERR_INVALID_ARG, "top_k out of range [1, min(num_experts, 16)]");
+    return GDN_OK;
+}
+
+gdn_status check_moe_sizes(const gdn_moe_params *p, int M)
+{
+    const gdn_status st = check_moe_route(p);
+    if (st != GDN_OK) return st;
+    if (p->ffn_dim < 128 || p->ffn_dim > 8192 || p->ffn_dim % 128)
+        return fail(GDN_ERR_INVALID_ARG, "ffn_dim must be a multiple of 128 in [128, 8192]");
+    if (M < 0 || M > MAX_T) return fail(GDN_ERR_INVALID_ARG, "M out of range [0, 2^24]");
+    return GDN_OK;
+}
+
 // chunk_size 0 = library choice: the exact scan for fp32 activations, the
 // chunked tensor-core form for bf16 activations.
 int resolve_chunk(int chunk_size, gdn_dtype act)
@@ -193,7 +243,7 @@ namespace gdn {
 // clears all of them with one small kernel (an atomic exchange each, so a word
 // set while the call runs is either reported now or kept for the next call)
 // and one copy of the OR back to the host.
-constexpr int N_ERROR_WORDS = 10;
+constexpr int N_ERROR_WORDS = 13;
 struct ErrorWords {
     unsigned int *p[N_ERROR_WORDS];
 };
@@ -224,7 +274,8 @@ static bool error_words(ErrorWords *out)
         void *(*const fns[N_ERROR_WORDS])() = {decode_error_word, chunk_error_word,    multi_error_word,
                                                gemm_error_word,   attn_error_word,     selftest_error_word,
                                                gproj_error_word,  inconv_error_word,   paged_error_word,
-                                               paged_q4_error_word};
+                                               paged_q4_error_word, linear_error_word, route_error_word,
+                                               moe_error_word};
         for (int i = 0; i < N_ERROR_WORDS; ++i) {
             cache[dev].p[i] = static_cast<unsigned int *>(fns[i]());
             if (cache[dev].p[i] == nullptr) return false;
@@ -597,6 +648,121 @@ gdn_status gdn_prefill_xhat(const gdn_params *p, const void *xhat, const void *z
                                            ssm_state_in, ssm_state_out, out, out_dt, body, ws_bytes - WS_HEADER,
                                            (cudaStream_t)stream, xhat);
     return e == cudaSuccess ? GDN_OK : cuda_fail(e, "gdn_prefill_xhat");
+}
+
+gdn_status gdn_add_norm(const gdn_norm_params *p, const void *x, long long x_row_stride, const void *delta,
+                        long long delta_row_stride, const void *gate, long long gate_row_stride, void *x_out,
+                        long long x_out_row_stride, void *h, long long h_row_stride, int M, gdn_dtype stream_dt,
+                        gdn_dtype act, void *stream)
+{
+    if (!ok_dtype(stream_dt) || !ok_dtype(act)) return fail(GDN_ERR_INVALID_ARG, "unknown dtype");
+    if (p == nullptr) return fail(GDN_ERR_INVALID_ARG, "norm params is NULL");
+    if (M < 0 || M > MAX_T) return fail(GDN_ERR_INVALID_ARG, "M out of range [0, 2^24]");
+    if (!ok_opt_ptr(p->norm_w) || !ok_opt_ptr(p->post_w) || (h != nullptr && p->norm_w == nullptr))
+        return fail(GDN_ERR_INVALID_ARG, "a norm weight is not 16-byte aligned, or norm_w is NULL with an output h");
+    if (!(p->norm_eps >= 0.0f)) return fail(GDN_ERR_INVALID_ARG, "norm_eps must be >= 0");
+    if (M == 0) return GDN_OK;
+    if (delta == nullptr && gate != nullptr) return fail(GDN_ERR_INVALID_ARG, "gate without delta");
+    if (x_out == nullptr && h == nullptr) return fail(GDN_ERR_INVALID_ARG, "no output");
+    const Rows rx = {x, x_row_stride, GDN_HIDDEN, stream_dt}, rd = {delta, delta_row_stride, GDN_HIDDEN, act},
+               rg = {gate, gate_row_stride, GDN_HIDDEN, act}, ro = {x_out, x_out_row_stride, GDN_HIDDEN, stream_dt},
+               rh = {h, h_row_stride, GDN_HIDDEN, act};
+    if (!rx.ok() || (delta && !rd.ok()) || (gate && !rg.ok(true)) || (x_out && !ro.ok()) || (h && !rh.ok()))
+        return fail(GDN_ERR_INVALID_ARG,
+                    "a tensor is NULL or not 16-byte aligned, or a row stride is below 2048 or not a multiple of 16 bytes");
+    if ((overlap(ro, rx, M) && !same_rows(ro, rx)) || overlap(ro, rd, M) || overlap(ro, rg, M) || overlap(ro, rh, M) ||
+        (overlap(rh, rd, M) && !same_rows(rh, rd)) || overlap(rh, rx, M) || overlap(rh, rg, M))
+        return fail(GDN_ERR_INVALID_ARG, "an output overlaps another tensor");
+    cudaError_t e = launch_add_norm(p, x, x_row_stride, delta, delta_row_stride, gate, gate_row_stride, x_out,
+                                    x_out_row_stride, h, h_row_stride, M, stream_dt, act, (cudaStream_t)stream);
+    return e == cudaSuccess ? GDN_OK : cuda_fail(e, "gdn_add_norm");
+}
+
+gdn_status gdn_linear(const void *x, long long x_row_stride, const void *w, const float *bias, const void *residual,
+                      long long residual_row_stride, void *y, long long y_row_stride, int M, int N, int K,
+                      gdn_activation activation, gdn_dtype out_dt, void *stream)
+{
+    if (!ok_dtype(out_dt)) return fail(GDN_ERR_INVALID_ARG, "unknown output dtype");
+    if (activation != GDN_ACT_NONE && activation != GDN_ACT_SILU && activation != GDN_ACT_GELU &&
+        activation != GDN_ACT_SIGMOID)
+        return fail(GDN_ERR_INVALID_ARG, "unknown activation");
+    if (M < 0 || M > MAX_T) return fail(GDN_ERR_INVALID_ARG, "M out of range [0, 2^24]");
+    if (N < 8 || N > (1 << 20) || N % 8 || K < 8 || K > (1 << 20) || K % 8)
+        return fail(GDN_ERR_INVALID_ARG, "N and K must be multiples of 8 in [8, 2^20]");
+    if (M == 0) return GDN_OK;
+    const Rows rx = {x, x_row_stride, K, GDN_BF16}, rw = {w, K, K, GDN_BF16},
+               rr = {residual, residual_row_stride, N, out_dt}, ry = {y, y_row_stride, N, out_dt};
+    if (!rx.ok() || !rw.ok() || !ok_opt_ptr(bias) || (residual && !rr.ok()) || !ry.ok())
+        return fail(GDN_ERR_INVALID_ARG,
+                    "a tensor is NULL or not 16-byte aligned, or a row stride is below the row or not a multiple of 16 bytes");
+    if (overlap(ry, rx, M) || overlap(y, ry.bytes(M), w, rw.bytes(N)) || (overlap(ry, rr, M) && !same_rows(ry, rr)) ||
+        (bias && overlap(y, ry.bytes(M), bias, (size_t)N * 4)))
+        return fail(GDN_ERR_INVALID_ARG, "y overlaps an input");
+    cudaError_t e = launch_linear(x, x_row_stride, w, bias, residual, residual_row_stride, y, y_row_stride, M, N, K,
+                                  activation, out_dt, (cudaStream_t)stream);
+    return e == cudaSuccess ? GDN_OK : cuda_fail(e, "gdn_linear");
+}
+
+gdn_status gdn_moe_route(const gdn_moe_params *p, const void *x, long long x_row_stride, int M, int32_t *ids,
+                         float *weights, void *stream)
+{
+    gdn_status st = check_moe_route(p);
+    if (st != GDN_OK) return st;
+    if (M < 0 || M > MAX_T) return fail(GDN_ERR_INVALID_ARG, "M out of range [0, 2^24]");
+    if (M == 0) return GDN_OK;
+    const Rows rx = {x, x_row_stride, GDN_HIDDEN, GDN_BF16};
+    if (!rx.ok() || !ok_ptr(p->router) || !ok_ptr(ids) || !ok_ptr(weights))
+        return fail(GDN_ERR_INVALID_ARG, "a tensor is NULL or not 16-byte aligned, or the row stride is below 2048 or not a multiple of 8");
+    const size_t n = (size_t)M * p->top_k * 4, nr = (size_t)p->num_experts * GDN_HIDDEN * 2;
+    if (overlap(ids, n, weights, n) || overlap(ids, n, x, rx.bytes(M)) || overlap(weights, n, x, rx.bytes(M)) ||
+        overlap(ids, n, p->router, nr) || overlap(weights, n, p->router, nr))
+        return fail(GDN_ERR_INVALID_ARG, "an output overlaps another tensor");
+    cudaError_t e = launch_route(p, x, x_row_stride, M, ids, weights, (cudaStream_t)stream);
+    return e == cudaSuccess ? GDN_OK : cuda_fail(e, "gdn_moe_route");
+}
+
+size_t gdn_moe_workspace_size(const gdn_moe_params *p, int M)
+{
+    if (check_moe_sizes(p, M) != GDN_OK) return 0;
+    return moe_workspace_bytes(p, M);
+}
+
+gdn_status gdn_moe(const gdn_moe_params *p, const void *x, long long x_row_stride, const void *residual, void *out,
+                   int M, const int32_t *ids, const float *weights, void *workspace, size_t workspace_bytes,
+                   gdn_dtype out_dt, void *stream)
+{
+    if (!ok_dtype(out_dt)) return fail(GDN_ERR_INVALID_ARG, "unknown output dtype");
+    gdn_status st = check_moe_sizes(p, M);
+    if (st != GDN_OK || M == 0) return st;
+    if ((ids == nullptr) != (weights == nullptr)) return fail(GDN_ERR_INVALID_ARG, "ids and weights go together");
+    if ((p->sh_gate == nullptr) != (p->sh_up == nullptr) || (p->sh_gate == nullptr) != (p->sh_down == nullptr) ||
+        (p->sh_gate == nullptr && p->sh_router != nullptr))
+        return fail(GDN_ERR_INVALID_ARG, "the shared expert's tensors go together");
+    const Rows rx = {x, x_row_stride, GDN_HIDDEN, GDN_BF16};
+    if (!rx.ok() || !ok_opt_ptr(residual) || !ok_ptr(out) || !ok_ptr(p->gate) || !ok_ptr(p->up) || !ok_ptr(p->down) ||
+        !ok_opt_ptr(p->sh_gate) || !ok_opt_ptr(p->sh_up) || !ok_opt_ptr(p->sh_down) || !ok_opt_ptr(p->sh_router) ||
+        !ok_opt_ptr(ids) || !ok_opt_ptr(weights) || (ids == nullptr && !ok_ptr(p->router)) || !ok_opt_ptr(p->router))
+        return fail(GDN_ERR_INVALID_ARG, "a tensor is NULL or not 16-byte aligned, or the row stride is below 2048 or not a multiple of 8");
+    const size_t no = (size_t)M * GDN_HIDDEN * elem_size(out_dt), nx = rx.bytes(M), np = (size_t)M * p->top_k * 4;
+    const size_t nf = (size_t)p->ffn_dim * GDN_HIDDEN * 2, ne = (size_t)p->num_experts * nf;
+    const size_t need = moe_workspace_bytes(p, M);
+    struct { const void *q; size_t n; } in[] = {
+        {x, nx}, {p->gate, ne}, {p->up, ne}, {p->down, ne}, {p->sh_gate, p->sh_gate ? nf : 0}, {p->sh_up, p->sh_up ? nf : 0},
+        {p->sh_down, p->sh_down ? nf : 0}, {p->sh_router, p->sh_router ? GDN_HIDDEN * 2 : 0},
+        {p->router, p->router ? (size_t)p->num_experts * GDN_HIDDEN * 2 : 0}, {ids, ids ? np : 0}, {weights, ids ? np : 0},
+        {residual, residual && residual != out ? no : 0}};
+    for (const auto &t : in)
+        if (overlap(out, no, t.q, t.n)) return fail(GDN_ERR_INVALID_ARG, "out overlaps an input");
+    if (workspace == nullptr || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u)) {
+        snprintf(g_last_error, sizeof(g_last_error),
+                 "workspace missing, misaligned (256 B) or too small: %zu bytes given, %zu needed", workspace_bytes, need);
+        return GDN_ERR_WORKSPACE;
+    }
+    for (const auto &t : in)
+        if (overlap(workspace, need, t.q, t.n)) return fail(GDN_ERR_INVALID_ARG, "the workspace overlaps an input");
+    if (overlap(workspace, need, out, no)) return fail(GDN_ERR_INVALID_ARG, "the workspace overlaps out");
+    cudaError_t e = launch_moe(p, x, x_row_stride, residual, out, M, ids, weights, workspace, out_dt, (cudaStream_t)stream);
+    return e == cudaSuccess ? GDN_OK : cuda_fail(e, "gdn_moe");
 }
 
 gdn_status gdn_device_error(void *stream)

@@ -1,0 +1,497 @@
+// gdn_moe.cu -- the mixture-of-experts feed-forward ("qwen35moe -- Forward-Pass
+// Design (Pantheon port)", the MoE section): with the chosen experts e and weights
+// w of each token x (gdn_route.cu),
+//   out = residual + sum_e w_e down_e (silu(gate_e x) * (up_e x))
+//         + sigmoid(x . sh_router) sh_down (silu(sh_gate x) * (sh_up x)).
+//
+// Bound by the weights: even a long prompt has only a hundred tokens per expert. So the
+// weights are the tensor core's A operand (128 rows of a weight per product) and an
+// expert's tokens its N (16 to 128), each weight tile passing through shared
+// memory once per 128 tokens.
+//  - moe_place: the pairs (token, expert) sorted by expert.
+//  - moe_experts: one persistent kernel for both halves. Units of work are handed out
+//    in order by a counter: first (expert, 128 rows of gate and of up, token
+//    tile), whose epilogue writes h = silu(g) * u; then (expert, 256 rows of down,
+//    token tile), which wait until their tile's h is complete. A unit waits only for units
+//    that were handed out before it, so it never waits for a CTA that is not running.
+//    Both kinds are the same pipeline: two A tiles and one B tile per stage of
+//    64 along K, two accumulators, double-buffered against the epilogue. Token rows
+//    come by TMA gathers of four rows.
+//  - moe_combine: residual, the pairs' outputs in slot order, the shared expert with its gate.
+#include <mutex>
+
+#include "gdn_moe.cuh"
+#include "gdn_tc.cuh"
+#include "gdn_tma.cuh"
+
+namespace gdn {
+
+__device__ unsigned int g_moe_error;      // GDN_ERR_TIMEOUT if a bounded wait gave up
+
+// ------------------------------------------------------------------ places
+
+constexpr int PL_THREADS = 1024;
+
+__global__ void __launch_bounds__(PL_THREADS) moe_place_kernel(const int32_t *ids, int pairs, int k, int E, int tiles, MoeWs ws)
+{
+    __shared__ int count[GDN_MOE_MAX_EXPERTS], first[GDN_MOE_MAX_EXPERTS];
+    const int tid = threadIdx.x;
+    if (tid < GDN_MOE_MAX_EXPERTS) count[tid] = 0;
+    __syncthreads();
+    grid_dep_wait();
+    grid_dep_launch();
+    for (int i = tid; i < tiles; i += PL_THREADS) ws.ready[i] = 0;
+    if (tid == 0) *ws.ticket = 0;
+    for (int p = tid; p < pairs; p += PL_THREADS) {
+        const int e = ids[p];
+        ws.place[p] = (unsigned)e < (unsigned)E ? atomicAdd(&count[e], 1) : -1;
+    }
+    __syncthreads();
+    if (tid < 32) {                                    // exclusive prefix of the counts, 8 a lane
+        int c[GDN_MOE_MAX_EXPERTS / 32], sum = 0;
+#pragma unroll
+        for (int j = 0; j < GDN_MOE_MAX_EXPERTS / 32; ++j) {
+            c[j] = sum;
+            sum += count[tid * (GDN_MOE_MAX_EXPERTS / 32) + j];
+        }
+        int before = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int n = __shfl_up_sync(0xffffffffu, before, o);
+            if (tid >= o) before += n;
+        }
+        before -= sum;
+#pragma unroll
+        for (int j = 0; j < GDN_MOE_MAX_EXPERTS / 32; ++j) first[tid * (GDN_MOE_MAX_EXPERTS / 32) + j] = before + c[j];
+    }
+    __syncthreads();
+    if (tid < E) {
+        ws.count[tid] = count[tid];
+        ws.offset[tid] = first[tid];
+    }
+    for (int p = tid; p < pairs; p += PL_THREADS) {
+        const int r = ws.place[p];
+        if (r < 0) continue;
+        const int at = first[ids[p]] + r;
+        ws.place[p] = at;
+        ws.token[at] = p / k;
+    }
+}
+
+// ------------------------------------------------------------------ experts
+
+constexpr int EX_BK = 64, EX_THREADS = 192, EX_INFO = 4;
+constexpr uint32_t EX_A_BYTES = 128 * EX_BK * 2;
+constexpr int EX_DOWN_UNITS = LD / 256;
+
+struct ExpertMaps {
+    CUtensorMap gate, up, down, sh_gate, sh_up, sh_down, x, h;
+};
+
+struct Unit {
+    int kind;                             // 0: gate and up, 1: down, -1: no more
+    int tile, rows_at, row0, n;           // token tile, weight-row tile, first sorted pair, tokens
+};
+
+template <int NT>
+struct ExpertSmem {
+    static constexpr uint32_t STAGE_BYTES = 2 * EX_A_BYTES + NT * EX_BK * 2;
+    static constexpr int STAGES = NT <= 32 ? 5 : 4;
+    alignas(1024) unsigned char stage[STAGES][STAGE_BYTES];
+    alignas(8) uint64_t full[STAGES], empty[STAGES], acc_full[2], acc_empty[2], info_full[EX_INFO], info_empty[EX_INFO];
+    Unit info[EX_INFO];
+    int last_it[STAGES];
+    int tile0[GDN_MOE_MAX_EXPERTS + 2];   // tiles before each expert (the shared one is the last), and their number
+    int count[GDN_MOE_MAX_EXPERTS + 1], offset[GDN_MOE_MAX_EXPERTS + 1];
+    uint32_t tmem;
+    int abort;
+};
+
+__device__ __forceinline__ int load_acquire(const int *p)
+{
+    int v;
+    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+template <int NT>
+__global__ void __launch_bounds__(EX_THREADS, 1)
+    moe_experts_kernel(const __grid_constant__ ExpertMaps maps, int M, int E, int F, int k, int shared, MoeWs ws)
+{
+    using Smem = ExpertSmem<NT>;
+    constexpr int STAGES = Smem::STAGES;
+    extern __shared__ unsigned char smem_raw[];
+    Smem &sm = *reinterpret_cast<Smem *>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const volatile int &aborted = sm.abort;
+    const int NE = E + (shared ? 1 : 0), FU = F / 128;   // experts with the shared one; gate/up units per token tile
+
+    if (warp == 1) {
+        tc::tmem_alloc(smem_u32(&sm.tmem), 4 * NT);
+        tc::tmem_relinquish();
+    }
+    if (tid == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(smem_u32(&sm.full[s]), 1);
+            mbar_init(smem_u32(&sm.empty[s]), 1);
+            sm.last_it[s] = -1;
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&sm.acc_full[b]), 1);
+            mbar_init(smem_u32(&sm.acc_empty[b]), 4);
+        }
+        for (int i = 0; i < EX_INFO; ++i) {
+            mbar_init(smem_u32(&sm.info_full[i]), 1);
+            mbar_init(smem_u32(&sm.info_empty[i]), 5);
+        }
+        sm.abort = 0;
+        fence_mbar_init();
+    }
+    grid_dep_wait();
+    for (int e = tid; e < NE; e += EX_THREADS) {
+        sm.count[e] = e < E ? ws.count[e] : M;
+        sm.offset[e] = e < E ? ws.offset[e] : M * k;
+    }
+    __syncthreads();
+    if (warp == 0) {                                   // tiles before each expert
+        int sum = 0;
+        for (int e0 = 0; e0 < NE; e0 += 32) {
+            const int t = e0 + lane < NE ? (sm.count[e0 + lane] + NT - 1) / NT : 0;
+            int inc = t;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int n = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += n;
+            }
+            if (e0 + lane < NE) sm.tile0[e0 + lane] = sum + inc - t;
+            sum += __shfl_sync(0xffffffffu, inc, 31);
+        }
+        if (lane == 0) sm.tile0[NE] = sum;
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tm = sm.tmem;
+    grid_dep_launch();
+
+    if (warp == 0) {
+        // ---- units and copies
+        const int tiles = sm.tile0[NE], units1 = tiles * FU, units = units1 + tiles * EX_DOWN_UNITS;
+        int it = 0, next = 0;
+        if (lane == 0) next = atomicAdd(ws.ticket, 1);
+        for (int ui = 0;; ++ui) {
+            const int u = __shfl_sync(0xffffffffu, next, 0);
+            const int slot = ui % EX_INFO;
+            if (ui >= EX_INFO && !mbar_wait_bounded(smem_u32(&sm.info_empty[slot]), (uint32_t)((ui / EX_INFO - 1) & 1)))
+                sm.abort = 1;
+            Unit un = {-1, 0, 0, 0, 0};
+            int e = 0, t0 = 0;
+            if (u < units && !aborted) {
+                un.kind = u >= units1;
+                const int per = un.kind ? EX_DOWN_UNITS : FU, v = un.kind ? u - units1 : u;
+                int lo = 0, hi = NE;                   // the expert: tile0[lo] <= v / per < tile0[hi]
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (sm.tile0[mid] <= v / per) lo = mid;
+                    else hi = mid;
+                }
+                e = lo;
+                const int nt = sm.tile0[e + 1] - sm.tile0[e], r = v - per * sm.tile0[e];
+                un.rows_at = r / nt;
+                t0 = (r % nt) * NT;
+                un.tile = sm.tile0[e] + r % nt;
+                un.row0 = sm.offset[e] + t0;
+                un.n = min(NT, sm.count[e] - t0);
+            }
+            if (lane == 0) {
+                sm.info[slot] = un;
+                mbar_arrive(smem_u32(&sm.info_full[slot]));
+            }
+            if (un.kind < 0) break;
+            if (lane == 0) next = atomicAdd(ws.ticket, 1);
+            const bool sh = e == E;
+            const int n16 = (un.n + 15) & ~15;
+            const uint32_t bytes = 2 * EX_A_BYTES + (uint32_t)n16 * EX_BK * 2;
+            const CUtensorMap *ma, *mb;
+            int ya, yb, slices;
+            int4 rows = make_int4(0, 0, 0, 0);
+            if (un.kind == 0) {
+                ma = sh ? &maps.sh_gate : &maps.gate;
+                mb = sh ? &maps.sh_up : &maps.up;
+                ya = yb = (sh ? 0 : e * F) + un.rows_at * 128;
+                slices = LD / EX_BK;
+                if (4 * lane < n16) {                  // rows past the last token repeat it
+                    int r[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int t = min(4 * lane + i, un.n - 1);
+                        r[i] = sh ? t0 + t : ws.token[un.row0 + t];
+                    }
+                    rows = make_int4(r[0], r[1], r[2], r[3]);
+                }
+            } else {
+                ma = mb = sh ? &maps.sh_down : &maps.down;
+                ya = (sh ? 0 : e * LD) + un.rows_at * 256;
+                yb = ya + 128;
+                slices = F / EX_BK;
+                if (lane == 0) {                       // the tile's h: four warps of each gate/up unit report it
+                    const uint64_t since = global_timer_ns();
+                    while (load_acquire(ws.ready + un.tile) < 4 * FU) {
+                        __nanosleep(100);
+                        if (global_timer_ns() - since > WAIT_LIMIT_NS) {
+                            sm.abort = 1;
+                            break;
+                        }
+                    }
+                }
+                __syncwarp();
+                fence_proxy_async_all();
+            }
+            for (int kb = 0; kb < slices; ++kb, ++it) {
+                const int s = it % STAGES;
+                if (it >= STAGES && !mbar_wait_bounded(smem_u32(&sm.empty[s]), (uint32_t)((it / STAGES - 1) & 1)))
+                    sm.abort = 1;
+                __syncwarp();
+                if (aborted) break;
+                const uint32_t dst = smem_u32(sm.stage[s]), bar = smem_u32(&sm.full[s]), b0 = dst + 2 * EX_A_BYTES;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar, bytes);
+                    tma_load_2d(dst, ma, kb * EX_BK, ya, bar);
+                    tma_load_2d(dst + EX_A_BYTES, mb, kb * EX_BK, yb, bar);
+                    sm.last_it[s] = it;
+                }
+                __syncwarp();
+                if (un.kind == 0) {
+                    if (4 * lane < n16) tma_gather4(b0 + 512u * lane, &maps.x, kb * EX_BK, rows, bar);
+                } else if (16 * lane < n16) {
+                    tma_load_2d(b0 + 2048u * lane, &maps.h, kb * EX_BK, un.row0 + 16 * lane, bar);
+                }
+            }
+        }
+        if (lane == 0 && aborted)                      // copies in flight land before the CTA exits
+            for (int s = 0; s < STAGES; ++s)
+                if (sm.last_it[s] >= 0) mbar_wait_bounded(smem_u32(&sm.full[s]), (uint32_t)((sm.last_it[s] / STAGES) & 1));
+    } else if (warp == 1) {
+        // ---- products
+        if (lane == 0) {
+            int it = 0;
+            for (int ui = 0; !aborted; ++ui) {
+                const int slot = ui % EX_INFO, ab = ui & 1;
+                if (!mbar_wait_bounded(smem_u32(&sm.info_full[slot]), (uint32_t)((ui / EX_INFO) & 1))) sm.abort = 1;
+                if (aborted) break;
+                const Unit un = sm.info[slot];
+                mbar_arrive(smem_u32(&sm.info_empty[slot]));
+                if (un.kind < 0) break;
+                if (ui >= 2 && !mbar_wait_bounded(smem_u32(&sm.acc_empty[ab]), (uint32_t)(((ui >> 1) - 1) & 1)))
+                    sm.abort = 1;
+                tc::fence_after_sync();
+                const uint32_t idesc = tc::instr_desc(tc::FMT_BF16, 128, (un.n + 15) & ~15);
+                const uint32_t d0 = tm + (uint32_t)(2 * NT * ab), d1 = d0 + NT;
+                const int slices = (un.kind ? F : LD) / EX_BK;
+                for (int kb = 0; kb < slices; ++kb, ++it) {
+                    const int s = it % STAGES;
+                    if (!mbar_wait_bounded(smem_u32(&sm.full[s]), (uint32_t)((it / STAGES) & 1))) sm.abort = 1;
+                    if (aborted) break;
+                    tc::fence_after_sync();
+                    const uint32_t a0 = smem_u32(sm.stage[s]);
+                    const uint64_t ad = tc::sw128_desc(a0), ud = tc::sw128_desc(a0 + EX_A_BYTES);
+                    const uint64_t bd = tc::sw128_desc(a0 + 2 * EX_A_BYTES);
+#pragma unroll
+                    for (int kk = 0; kk < EX_BK / 16; ++kk) {
+                        tc::mma_f16(d0, ad + 2u * kk, bd + 2u * kk, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+                        tc::mma_f16(d1, ud + 2u * kk, bd + 2u * kk, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+                    }
+                    tc::mma_commit(smem_u32(&sm.empty[s]));
+                }
+                if (aborted) break;
+                tc::mma_commit(smem_u32(&sm.acc_full[ab]));
+            }
+        }
+    } else {
+        // ---- epilogue: thread = weight row (tensor-memory lane), columns = tokens
+        const int q = warp & 3, row = 32 * q + lane;
+        for (int ui = 0; !aborted; ++ui) {
+            const int slot = ui % EX_INFO, ab = ui & 1;
+            if (!mbar_wait_sleep(smem_u32(&sm.info_full[slot]), (uint32_t)((ui / EX_INFO) & 1))) sm.abort = 1;
+            if (aborted) break;
+            const Unit un = sm.info[slot];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm.info_empty[slot]));
+            if (un.kind < 0) break;
+            if (!mbar_wait_sleep(smem_u32(&sm.acc_full[ab]), (uint32_t)((ui >> 1) & 1))) sm.abort = 1;
+            if (aborted) break;
+            __syncwarp();
+            tc::fence_after_sync();
+            const uint32_t d0 = tc::tmem_addr(tm, 32 * q, 2 * NT * ab);
+            for (int c = 0; c < un.n; c += 16) {
+                float a[16], b[16];
+                tc::tmem_ld16(d0 + (uint32_t)c, a);
+                tc::tmem_ld16(d0 + (uint32_t)(NT + c), b);
+                tc::wait_ld();
+                if (un.kind == 0) {
+                    bf16 *p = ws.h + (size_t)(un.row0 + c) * F + un.rows_at * 128 + row;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (c + i < un.n) p[(size_t)i * F] = from_f<bf16>(silu_fast(a[i]) * b[i]);
+                } else {
+                    float *p = ws.y + (size_t)(un.row0 + c) * LD + un.rows_at * 256 + row;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (c + i < un.n) {
+                            p[(size_t)i * LD] = a[i];
+                            p[(size_t)i * LD + 128] = b[i];
+                        }
+                }
+            }
+            tc::fence_before_sync();
+            if (un.kind == 0) fence_proxy_async_all();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(smem_u32(&sm.acc_empty[ab]));
+                if (un.kind == 0) {
+                    __threadfence();
+                    asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(ws.ready + un.tile) : "memory");
+                }
+            }
+        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 1) tc::tmem_dealloc(tm, 4 * NT);
+    if (tid == 0 && sm.abort) atomicExch(&g_moe_error, (unsigned int)GDN_ERR_TIMEOUT);
+}
+
+// ------------------------------------------------------------------ combine
+
+constexpr int CB_THREADS = LD / 8;
+
+template <typename TO>
+__global__ void __launch_bounds__(CB_THREADS)
+    moe_combine_kernel(const bf16 *x, long long x_row, const bf16 *sh_router, const float *weights, const void *residual,
+                       void *out, int M, int k, int shared, MoeWs ws)
+{
+    __shared__ float part[CB_THREADS / 32];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = tid * 8;
+    const size_t m = blockIdx.x;
+    grid_dep_wait();
+    grid_dep_launch();
+    float acc[8] = {};
+    if (residual) ld8(static_cast<const TO *>(residual) + m * LD + c, acc);
+    float gate = 1.0f;
+    if (sh_router) {                                   // the shared expert's gate
+        float a[8], b[8], s = 0.0f;
+        ld8(x + m * x_row + c, a);
+        ld8(sh_router + c, b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s = fmaf(a[i], b[i], s);
+        s = warp_sum(s);
+        if (lane == 0) part[warp] = s;
+        __syncthreads();
+        s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < CB_THREADS / 32; ++i) s += part[i];
+        gate = 1.0f / (1.0f + expf(-s));
+    }
+    float sum[8] = {};
+    for (int j = 0; j < k; ++j) {
+        const int at = ws.place[m * k + j];
+        if (at < 0) continue;
+        const float w = weights[m * k + j];
+        float y[8];
+        ld8(ws.y + (size_t)at * LD + c, y);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] = fmaf(w, y[i], sum[i]);
+    }
+    if (shared) {
+        float y[8];
+        ld8(ws.y + ((size_t)M * k + m) * LD + c, y);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] = fmaf(gate, y[i], sum[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] += sum[i];
+    st8(static_cast<TO *>(out) + m * LD + c, acc);
+}
+
+// ------------------------------------------------------------------ launcher
+
+static bool moe_setup()
+{
+    static bool ready[64] = {};
+    static std::mutex mu;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!ready[dev]) {
+        if (cudaFuncSetAttribute(moe_experts_kernel<32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)sizeof(ExpertSmem<32>) + 1024) != cudaSuccess ||
+            cudaFuncSetAttribute(moe_experts_kernel<MOE_TILE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)sizeof(ExpertSmem<MOE_TILE>) + 1024) != cudaSuccess)
+            return false;
+        ready[dev] = true;
+    }
+    return true;
+}
+
+size_t moe_workspace_bytes(const gdn_moe_params *p, int M) { return moe_workspace(p, M, nullptr).bytes; }
+
+cudaError_t launch_moe(const gdn_moe_params *p, const void *x, long long x_row, const void *residual, void *out, int M,
+                       const int32_t *ids, const float *weights, void *workspace, gdn_dtype out_dt, cudaStream_t s)
+{
+    const int n_sm = sm_count();
+    if (n_sm <= 0 || !moe_setup()) return cudaErrorInvalidDevice;
+    const int E = p->num_experts, F = p->ffn_dim, k = p->top_k;
+    const bool shared = p->sh_gate != nullptr;
+    const size_t out_row = (size_t)LD * (out_dt == GDN_F32 ? 4 : 2);
+    MoeWs ws = moe_workspace(p, M, workspace);
+    ExpertMaps maps;
+    if (!make_bf16_strided_map(&maps.gate, p->gate, (long long)E * F, LD, LD, 128) ||
+        !make_bf16_strided_map(&maps.up, p->up, (long long)E * F, LD, LD, 128) ||
+        !make_bf16_strided_map(&maps.down, p->down, (long long)E * LD, F, F, 128))
+        return cudaErrorInvalidValue;
+    if (shared && (!make_bf16_strided_map(&maps.sh_gate, p->sh_gate, F, LD, LD, 128) ||
+                   !make_bf16_strided_map(&maps.sh_up, p->sh_up, F, LD, LD, 128) ||
+                   !make_bf16_strided_map(&maps.sh_down, p->sh_down, LD, F, F, 128)))
+        return cudaErrorInvalidValue;
+    if (!shared) maps.sh_gate = maps.sh_up = maps.sh_down = maps.gate;    // not read
+    for (int m0 = 0; m0 < M; m0 += MOE_WINDOW) {
+        const int W = M - m0 < MOE_WINDOW ? M - m0 : MOE_WINDOW;
+        const bf16 *xw = static_cast<const bf16 *>(x) + (size_t)m0 * x_row;
+        const int32_t *idw = ids ? ids + (size_t)m0 * k : ws.ids;
+        const float *ww = ids ? weights + (size_t)m0 * k : ws.weights;
+        const size_t rows = (size_t)W * (k + (shared ? 1 : 0));
+        if (!make_bf16_strided_map(&maps.x, xw, W, LD, x_row, 1) || !make_bf16_strided_map(&maps.h, ws.h, rows, F, F, 16))
+            return cudaErrorInvalidValue;
+        cudaError_t e = cudaSuccess;
+        if (!ids) e = launch_route(p, xw, x_row, W, ws.ids, ws.weights, s);
+        if (e != cudaSuccess) return e;
+        e = launch_pdl(moe_place_kernel, dim3(1), dim3(PL_THREADS), 0, s, idw, W * k, k, E, moe_max_tiles(p, W), ws);
+        if (e != cudaSuccess) return e;
+        if (W <= 512)
+            e = launch_pdl(moe_experts_kernel<32>, dim3(n_sm), dim3(EX_THREADS), sizeof(ExpertSmem<32>) + 1024, s, maps,
+                           W, E, F, k, (int)shared, ws);
+        else
+            e = launch_pdl(moe_experts_kernel<MOE_TILE>, dim3(n_sm), dim3(EX_THREADS), sizeof(ExpertSmem<MOE_TILE>) + 1024,
+                           s, maps, W, E, F, k, (int)shared, ws);
+        if (e != cudaSuccess) return e;
+        const void *rw = residual ? static_cast<const char *>(residual) + m0 * out_row : nullptr;
+        void *ow = static_cast<char *>(out) + m0 * out_row;
+        const bf16 *shr = static_cast<const bf16 *>(p->sh_router);
+        e = out_dt == GDN_F32 ? launch_pdl(moe_combine_kernel<float>, dim3(W), dim3(CB_THREADS), 0, s, xw, x_row, shr, ww,
+                                           rw, ow, W, k, (int)shared, ws)
+                              : launch_pdl(moe_combine_kernel<bf16>, dim3(W), dim3(CB_THREADS), 0, s, xw, x_row, shr, ww,
+                                           rw, ow, W, k, (int)shared, ws);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+// Device address of this file's error word, for gdn_device_error (NULL if the lookup fails).
+void *moe_error_word()
+{
+    void *p = nullptr;
+    return cudaGetSymbolAddress(&p, g_moe_error) == cudaSuccess ? p : nullptr;
+}
+
+}  // namespace gdn

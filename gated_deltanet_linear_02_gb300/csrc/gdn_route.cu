@@ -1,0 +1,354 @@
+// gdn_route.cu -- the router of the mixture-of-experts feed-forward ("qwen35moe --
+// Forward-Pass Design (Pantheon port)", the MoE section): logits x . router^T of E
+// experts, the top_k of them per token, and softmax weights.
+//
+// A cluster of S CTAs takes 128 tokens, CTA r the r-th part of K = 2048: all E logits
+// of a token come from one tcgen05 product (M = 128 tokens, N = E), with K split so
+// that few tokens still spread over SMs. Every 256 of K have an accumulator of
+// their own; those partial sums are added in fp32 rounded to nearest (the tensor
+// core truncates its sums, so short ones keep the logits' error near 1e-7 of their
+// terms). They meet in distributed shared memory, where each CTA has 128 / S
+// tokens: a warp per token holds 8 logits a lane and takes the largest k times.
+//
+// The choice is exact: where two of the first k + 1 logits are closer than 2^-13 of
+// the largest magnitude (the error bound is far below), the warp sums the logits
+// of all candidates again in pairs of fp32 (48 bits; products of bf16 are exact).
+// Ties go to the lowest index. NaN ranks below everything.
+#include <mutex>
+
+#include "gdn_layer.cuh"
+#include "gdn_moe.cuh"
+#include "gdn_tc.cuh"
+#include "gdn_tma.cuh"
+
+namespace gdn {
+
+__device__ unsigned int g_route_error;    // GDN_ERR_TIMEOUT if a bounded wait gave up
+
+constexpr int RT_BM = 128, RT_BK = 64, RT_THREADS = 256, RT_STAGES = 4;
+constexpr uint32_t RT_A_BYTES = RT_BM * RT_BK * 2;
+constexpr int RT_ACC_K = 256;             // K of one accumulator
+constexpr int RT_MAX_E = GDN_MOE_MAX_EXPERTS;
+constexpr int RT_SLOTS = RT_MAX_E / 32;   // logits per lane
+
+struct RouteSmem {
+    alignas(1024) unsigned char stage[RT_STAGES][RT_A_BYTES + RT_MAX_E * RT_BK * 2];
+    alignas(8) uint64_t full[RT_STAGES], empty[RT_STAGES], done;
+    int last_it[RT_STAGES];
+    uint32_t tmem;
+    int abort;
+};
+static_assert(RT_BM * (RT_MAX_E + 4) * 4 <= sizeof(RouteSmem::stage), "partial logits fit the stages");
+
+// Order-preserving keys of floats; NaN is the smallest, -0 is +0.
+__device__ __forceinline__ uint32_t sort_key(float x)
+{
+    if (!(x == x)) return 0u;
+    const uint32_t u = __float_as_uint(x + 0.0f);
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+// a + b as (sum, error), both exact.
+__device__ __forceinline__ float2 two_sum(float a, float b)
+{
+    const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+    return make_float2(s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t)));
+}
+__device__ __forceinline__ float2 pair_add(float2 a, float2 b)
+{
+    const float2 s = two_sum(a.x, b.x);
+    const float e = __fadd_rn(s.y, __fadd_rn(a.y, b.y)), h = __fadd_rn(s.x, e);
+    return make_float2(h, __fsub_rn(e, __fsub_rn(h, s.x)));
+}
+
+// The logit of one expert as a pair of fp32, the same in every lane.
+__device__ __noinline__ float2 pair_dot(const bf16 *x, const bf16 *w, int lane)
+{
+    float2 acc = make_float2(0.0f, 0.0f);
+    for (int c = 0; c < LD / 256; ++c) {
+        float a[8], b[8];
+        ld8(x + c * 256 + lane * 8, a);
+        ld8(w + c * 256 + lane * 8, b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc = pair_add(acc, make_float2(__fmul_rn(a[i], b[i]), 0.0f));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        acc = pair_add(acc, make_float2(__shfl_xor_sync(0xffffffffu, acc.x, o), __shfl_xor_sync(0xffffffffu, acc.y, o)));
+    return acc;
+}
+
+// The k largest of the warp's logits v[j] (expert lane + 32 j, -inf past E with
+// valid == false): lane i < k gets the i-th expert and its weight.
+__device__ void choose(float (&v)[RT_SLOTS], int E, int k, bool renorm, const bf16 *x, const bf16 *router, int lane,
+                       int &id, float &weight)
+{
+    uint32_t key[RT_SLOTS];
+    float big = 0.0f;
+#pragma unroll
+    for (int j = 0; j < RT_SLOTS; ++j) {
+        const bool there = lane + 32 * j < E;
+        key[j] = there ? sort_key(v[j]) : 0u;
+        if (there && fabsf(v[j]) < INFINITY) big = fmaxf(big, fabsf(v[j]));
+    }
+    big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
+    float lo[RT_SLOTS];
+#pragma unroll
+    for (int j = 0; j < RT_SLOTS; ++j) lo[j] = 0.0f;
+    float best = 0.0f;                                 // lane i: the i-th logit
+    id = 0;
+    bool settled = false;
+    for (;;) {
+        uint32_t taken = 0;                            // this lane's slots that are out
+        float prev = 0.0f, kth = 0.0f;
+        bool close = false;
+        const int rounds = settled || k >= E ? k : k + 1;
+        for (int i = 0; i < rounds; ++i) {
+            uint32_t mk = 0;
+#pragma unroll
+            for (int j = 0; j < RT_SLOTS; ++j)
+                if (!(taken >> j & 1u) && lane + 32 * j < E) mk = max(mk, key[j]);
+            const uint32_t top = __reduce_max_sync(0xffffffffu, mk);
+            uint32_t ml = 0;                           // settled: the larger low part among equal high ones
+            if (settled) {
+#pragma unroll
+                for (int j = 0; j < RT_SLOTS; ++j)
+                    if (!(taken >> j & 1u) && lane + 32 * j < E && key[j] == top) ml = max(ml, sort_key(lo[j]));
+                ml = __reduce_max_sync(0xffffffffu, ml);
+            }
+            uint32_t at = 0xffffffffu;
+#pragma unroll
+            for (int j = RT_SLOTS - 1; j >= 0; --j)
+                if (!(taken >> j & 1u) && lane + 32 * j < E && key[j] == top && (!settled || sort_key(lo[j]) == ml))
+                    at = (uint32_t)(lane + 32 * j);
+            at = __reduce_min_sync(0xffffffffu, at);
+            float val = 0.0f;
+#pragma unroll
+            for (int j = 0; j < RT_SLOTS; ++j)
+                if ((int)at == lane + 32 * j) {
+                    val = v[j];
+                    taken |= 1u << j;
+                }
+            val = __shfl_sync(0xffffffffu, val, (int)(at & 31u));
+            if (i > 0 && prev - val <= 0x1p-13f * big) close = true;
+            prev = val;
+            if (i < k) {
+                kth = val;
+                if (lane == i) {
+                    best = val;
+                    id = (int)at;
+                }
+            }
+        }
+        if (settled || !close || !(big > 0.0f)) break;
+        // every expert that may belong to the first k, in 48 bits
+        settled = true;
+        const float floor_v = kth - 0x1p-13f * big;
+        for (int e = 0; e < E; ++e) {
+            float ve = 0.0f;
+#pragma unroll
+            for (int j = 0; j < RT_SLOTS; ++j)
+                if (e >> 5 == j) ve = v[j];
+            ve = __shfl_sync(0xffffffffu, ve, e & 31);
+            if (!(ve >= floor_v) || !(fabsf(ve) < INFINITY)) continue;
+            const float2 p = pair_dot(x, router + (size_t)e * LD, lane);
+#pragma unroll
+            for (int j = 0; j < RT_SLOTS; ++j)
+                if (e == lane + 32 * j) {
+                    v[j] = p.x;
+                    key[j] = sort_key(p.x);
+                    lo[j] = p.y;
+                }
+        }
+    }
+    const float top = __shfl_sync(0xffffffffu, best, 0);
+    const float ex = lane < k ? expf(best - top) : 0.0f;
+    float sum = ex;
+    if (!renorm) {
+        sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < RT_SLOTS; ++j)
+            if (lane + 32 * j < E) sum += expf(v[j] - top);
+    }
+    weight = ex / warp_sum(sum);
+}
+
+__global__ void __launch_bounds__(RT_THREADS, 1)
+    route_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mr, const bf16 *x,
+                 long long x_row, const bf16 *router, int M, int E, int N, int k, int renorm, int splits,
+                 int32_t *ids, float *weights)
+{
+    extern __shared__ unsigned char smem_raw[];
+    RouteSmem &sm = *reinterpret_cast<RouteSmem *>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tile = (int)blockIdx.x / splits, part = (int)blockIdx.x % splits;
+    const int kbn = LD / RT_BK / splits, kb0 = part * kbn;                 // 4 to 16 K slices
+    const int naccs = (kbn * RT_BK + RT_ACC_K - 1) / RT_ACC_K;             // 1 or 2 (splits >= 4)
+    const int PLD = N + 4;
+    const uint32_t cols = naccs > 1 ? 512u : 256u;
+    const volatile int &aborted = sm.abort;
+
+    if (warp == 1) {
+        tc::tmem_alloc(smem_u32(&sm.tmem), cols);
+        tc::tmem_relinquish();
+    }
+    if (tid == 0) {
+        for (int s = 0; s < RT_STAGES; ++s) {
+            mbar_init(smem_u32(&sm.full[s]), 1);
+            mbar_init(smem_u32(&sm.empty[s]), 1);
+            sm.last_it[s] = -1;
+        }
+        mbar_init(smem_u32(&sm.done), 1);
+        sm.abort = 0;
+        fence_mbar_init();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tm = sm.tmem;
+    grid_dep_wait();
+    grid_dep_launch();
+
+    if (warp == 0) {
+        if (lane == 0) {
+            for (int it = 0; it < kbn; ++it) {
+                const int s = it % RT_STAGES;
+                if (it >= RT_STAGES && !mbar_wait_bounded(smem_u32(&sm.empty[s]), (uint32_t)((it / RT_STAGES - 1) & 1)))
+                    sm.abort = 1;
+                if (aborted) break;
+                const uint32_t dst = smem_u32(sm.stage[s]), bar = smem_u32(&sm.full[s]);
+                mbar_arrive_expect_tx(bar, RT_A_BYTES + (uint32_t)N * RT_BK * 2);
+                tma_load_2d(dst, &mx, (kb0 + it) * RT_BK, tile * RT_BM, bar);
+                tma_load_2d(dst + RT_A_BYTES, &mr, (kb0 + it) * RT_BK, 0, bar);
+                sm.last_it[s] = it;
+            }
+            if (aborted)
+                for (int s = 0; s < RT_STAGES; ++s)
+                    if (sm.last_it[s] >= 0)
+                        mbar_wait_bounded(smem_u32(&sm.full[s]), (uint32_t)((sm.last_it[s] / RT_STAGES) & 1));
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t idesc = tc::instr_desc(tc::FMT_BF16, RT_BM, N);
+            for (int it = 0; it < kbn; ++it) {
+                const int s = it % RT_STAGES;
+                if (!mbar_wait_bounded(smem_u32(&sm.full[s]), (uint32_t)((it / RT_STAGES) & 1))) sm.abort = 1;
+                if (aborted) break;
+                tc::fence_after_sync();
+                const uint64_t ad = tc::sw128_desc(smem_u32(sm.stage[s]));
+                const uint64_t bd = tc::sw128_desc(smem_u32(sm.stage[s]) + RT_A_BYTES);
+                const int in = it % (RT_ACC_K / RT_BK);
+                const uint32_t d = tm + 256u * (uint32_t)(it / (RT_ACC_K / RT_BK));
+#pragma unroll
+                for (int kk = 0; kk < RT_BK / 16; ++kk)
+                    tc::mma_f16(d, ad + 2u * kk, bd + 2u * kk, idesc, (in > 0 || kk > 0) ? 1u : 0u);
+                tc::mma_commit(smem_u32(&sm.empty[s]));
+            }
+            if (!aborted) tc::mma_commit(smem_u32(&sm.done));
+        }
+    } else if (warp >= 4) {
+        if (!mbar_wait_bounded(smem_u32(&sm.done), 0)) sm.abort = 1;
+        tc::fence_after_sync();
+        const int q = warp & 3, row = 32 * q + lane;
+        float *p = reinterpret_cast<float *>(sm.stage[0]) + row * PLD;
+        if (!aborted)
+            for (int c = 0; c < N; c += 16) {
+                float v[16];
+                tc::tmem_ld16(tc::tmem_addr(tm, 32 * q, c), v);
+                if (naccs > 1) {
+                    float u[16];
+                    tc::tmem_ld16(tc::tmem_addr(tm, 32 * q, 256 + c), u);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] += u[i];
+                } else {
+                    tc::wait_ld();
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    reinterpret_cast<float4 *>(p + c)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            }
+    }
+    cluster_sync_all();
+    {
+        const int rows = RT_BM / splits;
+        const uint32_t base = smem_u32(sm.stage[0]);
+        for (int t = part * rows + warp; t < (part + 1) * rows; t += RT_THREADS / 32) {
+            const int m = tile * RT_BM + t;
+            if (m >= M || aborted) break;
+            float v[RT_SLOTS];
+#pragma unroll
+            for (int j = 0; j < RT_SLOTS; ++j) v[j] = 0.0f;
+            for (int r = 0; r < splits; ++r) {
+                const uint32_t at = mapa_shared(base + (uint32_t)(t * PLD + lane) * 4u, (uint32_t)r);
+#pragma unroll
+                for (int j = 0; j < RT_SLOTS; ++j)
+                    if (lane + 32 * j < E) v[j] += ld_cluster_f32(at + 128u * j);
+            }
+            int id;
+            float w;
+            choose(v, E, k, renorm != 0, x + (size_t)m * x_row, router, lane, id, w);
+            if (lane < k) {
+                ids[(size_t)m * k + lane] = id;
+                weights[(size_t)m * k + lane] = w;
+            }
+        }
+    }
+    cluster_sync_all();                                // no CTA leaves while others read its partial logits
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 1) tc::tmem_dealloc(tm, cols);
+    if (tid == 0 && sm.abort) atomicExch(&g_route_error, (unsigned int)GDN_ERR_TIMEOUT);
+}
+
+static bool route_setup()
+{
+    static bool ready[64] = {};
+    static std::mutex mu;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!ready[dev]) {
+        if (cudaFuncSetAttribute(route_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)sizeof(RouteSmem) + 1024) != cudaSuccess)
+            return false;
+        ready[dev] = true;
+    }
+    return true;
+}
+
+cudaError_t launch_route(const gdn_moe_params *p, const void *x, long long x_row, int M, int32_t *ids, float *weights,
+                         cudaStream_t s)
+{
+    if (!route_setup()) return cudaErrorInvalidDevice;
+    const int E = p->num_experts, N = (E + 15) & ~15;
+    CUtensorMap mx, mr;
+    if (!make_bf16_strided_map(&mx, x, M, LD, x_row, RT_BM) || !make_bf16_strided_map(&mr, p->router, E, LD, LD, N))
+        return cudaErrorInvalidValue;
+    const int tiles = (M + RT_BM - 1) / RT_BM, splits = tiles <= 16 ? 8 : 4;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(tiles * splits);
+    cfg.blockDim = dim3(RT_THREADS);
+    cfg.dynamicSmemBytes = sizeof(RouteSmem) + 1024;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)splits;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, route_kernel, mx, mr, (const bf16 *)x, x_row, (const bf16 *)p->router, M, E, N,
+                              p->top_k, p->norm_topk, splits, ids, weights);
+}
+
+// Device address of this file's error word, for gdn_device_error (NULL if the lookup fails).
+void *route_error_word()
+{
+    void *p = nullptr;
+    return cudaGetSymbolAddress(&p, g_route_error) == cudaSuccess ? p : nullptr;
+}
+
+}  // namespace gdn

@@ -42,6 +42,16 @@ class gdn_attn_params(ctypes.Structure):
                 ("n_pos", ctypes.c_int), ("norm_eps", ctypes.c_float)]
 
 
+class gdn_norm_params(ctypes.Structure):
+    _fields_ = [("norm_w", ctypes.c_void_p), ("post_w", ctypes.c_void_p), ("res_scale", ctypes.c_float),
+                ("norm_eps", ctypes.c_float)]
+
+
+class gdn_moe_params(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("router", "gate", "up", "down", "sh_gate", "sh_up", "sh_down", "sh_router")] + \
+        [(n, ctypes.c_int) for n in ("num_experts", "top_k", "ffn_dim", "norm_topk")]
+
+
 class gdn_kv_cache(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("num_pages", ctypes.c_int),
                 ("page_size", ctypes.c_int), ("format", ctypes.c_int)]
@@ -103,6 +113,16 @@ def lib() -> ctypes.CDLL:
         L.gdn_attn_paged.argtypes = [_vp, _vp, _vp, _vp, _ll, _ll, _vp, _vp, _sz, _int, _vp]
         L.gdn_attn_paged_workspace_size.restype = _sz
         L.gdn_attn_paged_workspace_size.argtypes = [_vp, _vp]
+        L.gdn_add_norm.restype = _int
+        L.gdn_add_norm.argtypes = [_vp] + [_vp, _ll] * 5 + [_int, _int, _int, _vp]
+        L.gdn_linear.restype = _int
+        L.gdn_linear.argtypes = [_vp, _ll, _vp, _vp, _vp, _ll, _vp, _ll] + [_int] * 5 + [_vp]
+        L.gdn_moe_route.restype = _int
+        L.gdn_moe_route.argtypes = [_vp, _vp, _ll, _int, _vp, _vp, _vp]
+        L.gdn_moe.restype = _int
+        L.gdn_moe.argtypes = [_vp, _vp, _ll, _vp, _vp, _int, _vp, _vp, _vp, _sz, _int, _vp]
+        L.gdn_moe_workspace_size.restype = _sz
+        L.gdn_moe_workspace_size.argtypes = [_vp, _int]
         L.gdn_prefill_workspace_size.restype = _sz
         L.gdn_prefill_workspace_size.argtypes = [_int, _int, _int, _int]
         L.gdn_selftest_wait_timeout.restype = _int
@@ -552,6 +572,143 @@ def attn_paged(batch: gdn_paged_batch, cache: gdn_kv_cache, q, out, gate=None, w
                               workspace.nbytes, _act_dtype(out), _raw_stream(stream, dev))
     if st:
         _check(st, "gdn_attn_paged")
+    return workspace
+
+
+# ---- around the mixers: residual and norms, dense products, mixture of experts
+
+ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2, "sigmoid": 3}      # gdn_activation
+MOE_MAX_EXPERTS, MOE_MAX_TOPK = 256, 16
+
+
+def _rows(t, name: str, M: int, width: int, device, dtype=None):
+    """(pointer, row stride) of a [M][width] tensor whose rows are dense."""
+    if t is None:
+        return None, 0
+    if t.shape == (M, width) and t.device == device and (dtype is None or t.dtype is dtype):
+        row, last = t.stride()
+        if last == 1:
+            return t.data_ptr(), row if M > 1 or row == 0 else width
+    _refuse(t, name, (M, width), device, dtype)
+    raise ValueError(f"{name} must be dense in its last dimension")
+
+
+def make_norm_params(norm_w=None, post_w=None, res_scale: float = 1.0, norm_eps: float = 1e-6) -> gdn_norm_params:
+    """gdn_norm_params from fp32 CUDA tensors [2048]: the weight of the sum's norm
+    (None: no normed output) and of the norm of the block's output (None: none).
+    The struct keeps the tensors alive."""
+    p = gdn_norm_params(_ptr(norm_w, "norm_w", (N_EMBD,), torch.float32), _ptr(post_w, "post_w", (N_EMBD,), torch.float32),
+                        float(res_scale), float(norm_eps))
+    p._keep_alive = (norm_w, post_w)
+    p._device = _one_device(norm_w, post_w)
+    p._ref = ctypes.addressof(p)
+    return p
+
+
+def add_norm(params: gdn_norm_params, x, delta, x_out, h, gate=None, stream=None):
+    """gdn_add_norm: x_out = x + res_scale * gate * norm(delta) and its norm h, rows
+    of 2048. x and x_out share one dtype (fp32 or bf16), delta, gate and h another;
+    rows may be strided. delta, gate, x_out and h may be None; x_out may be x, and
+    h may be delta. A gate of one row for all tokens: gate.expand(M, 2048)."""
+    M, dev = x.shape[0], _on_current(x.device, "add_norm")
+    if params._device is not None and params._device != dev:
+        raise ValueError(f"the parameters are on {params._device}, expected {dev}")
+    act = h if h is not None else delta if delta is not None else x
+    xp, xr = _rows(x, "x", M, N_EMBD, dev)
+    dp, dr = _rows(delta, "delta", M, N_EMBD, dev, act.dtype)
+    gp, gr = _rows(gate, "gate", M, N_EMBD, dev, act.dtype)
+    op, orow = _rows(x_out, "x_out", M, N_EMBD, dev, x.dtype)
+    hp, hr = _rows(h, "h", M, N_EMBD, dev)
+    st = (_lib or lib()).gdn_add_norm(params._ref, xp, xr, dp, dr, gp, gr, op, orow, hp, hr, M, _act_dtype(x),
+                                      _act_dtype(act), _raw_stream(stream, dev))
+    if st:
+        _check(st, "gdn_add_norm")
+
+
+def linear(x, w, y, bias=None, residual=None, activation: str = "none", stream=None):
+    """gdn_linear: y = residual + activation(x w^T + bias). x [M][K] and w [N][K]
+    bf16, y [M][N] and residual fp32 or bf16, bias [N] fp32; rows of x, residual
+    and y may be strided, residual may be y. activation: one of ACTIVATIONS."""
+    (M, K), N, dev = x.shape, w.shape[0], _on_current(x.device, "linear")
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation {activation!r}: expected one of {sorted(ACTIVATIONS)}")
+    xp, xr = _rows(x, "x", M, K, dev, torch.bfloat16)
+    yp, yr = _rows(y, "y", M, N, dev)
+    rp, rr = _rows(residual, "residual", M, N, dev, y.dtype)
+    st = (_lib or lib()).gdn_linear(xp, xr, _dense(w, "w", (N, K), dev, torch.bfloat16),
+                                    _dense(bias, "bias", (N,), dev, torch.float32), rp, rr, yp, yr, M, N, K,
+                                    ACTIVATIONS[activation], _act_dtype(y), _raw_stream(stream, dev))
+    if st:
+        _check(st, "gdn_linear")
+
+
+def make_moe_params(router, gate=None, up=None, down=None, sh_gate=None, sh_up=None, sh_down=None, sh_router=None,
+                    top_k: int = 8, norm_topk: bool = True) -> gdn_moe_params:
+    """gdn_moe_params from bf16 CUDA tensors: router [E][2048] (None: the routing is
+    always given), gate and up [E][F][2048], down [E][2048][F] (None: for
+    moe_route alone), the shared expert's gate and up [F][2048], down [2048][F]
+    and sigmoid gate [2048] (None: none). The struct keeps the tensors alive."""
+    bf = torch.bfloat16
+    E = router.shape[0] if router is not None else gate.shape[0]
+    F = gate.shape[1] if gate is not None and gate.dim() == 3 else 0
+    ts = (router, gate, up, down, sh_gate, sh_up, sh_down, sh_router)
+    shapes = ((E, N_EMBD), (E, F, N_EMBD), (E, F, N_EMBD), (E, N_EMBD, F), (F, N_EMBD), (F, N_EMBD), (N_EMBD, F), (N_EMBD,))
+    names = [n for n, _ in gdn_moe_params._fields_]
+    p = gdn_moe_params(*(_ptr(t, n, s, bf) for t, n, s in zip(ts, names, shapes)), E, int(top_k), F, int(bool(norm_topk)))
+    p._keep_alive = ts
+    p._device = _one_device(*ts)
+    p._ref = ctypes.addressof(p)
+    return p
+
+
+def moe_route(params: gdn_moe_params, x, ids, weights, stream=None):
+    """gdn_moe_route: the top_k experts of each row of x [M][2048] bf16 (rows may be
+    strided), best first, into ids [M][top_k] int32 and weights [M][top_k] fp32."""
+    M, dev = x.shape[0], _on_current(x.device, "moe_route")
+    if params._device != dev:
+        raise ValueError(f"the parameters are on {params._device}, expected {dev}")
+    xp, xr = _rows(x, "x", M, N_EMBD, dev, torch.bfloat16)
+    st = (_lib or lib()).gdn_moe_route(params._ref, xp, xr, M, _dense(ids, "ids", (M, params.top_k), dev, torch.int32),
+                                       _dense(weights, "weights", (M, params.top_k), dev, torch.float32),
+                                       _raw_stream(stream, dev))
+    if st:
+        _check(st, "gdn_moe_route")
+
+
+def moe_workspace_size(params: gdn_moe_params, M: int) -> int:
+    return int(lib().gdn_moe_workspace_size(params._ref, int(M)))
+
+
+def _workspace(need: int, device, stream):
+    """Scratch through torch, from the memory of the stream that the call runs on."""
+    if stream is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(need, dtype=torch.uint8, device=device)
+
+
+def moe(params: gdn_moe_params, x, out, residual=None, ids=None, weights=None, workspace=None, stream=None):
+    """gdn_moe: the whole mixture-of-experts feed-forward of x [M][2048] bf16 (rows
+    may be strided) into out [M][2048] (fp32 or bf16), plus residual (same dtype;
+    may be out). ids and weights [M][top_k]: the routing, if it is given.
+    Allocates the workspace through torch, for the stream the call runs on, when
+    none is given, and returns it."""
+    M, dev = x.shape[0], _on_current(x.device, "moe")
+    if params._device != dev:
+        raise ValueError(f"the parameters are on {params._device}, expected {dev}")
+    if workspace is None:
+        workspace = _workspace(max(moe_workspace_size(params, M), 256), dev, stream)
+    xp, xr = _rows(x, "x", M, N_EMBD, dev, torch.bfloat16)
+    st = (_lib or lib()).gdn_moe(params._ref, xp, xr, _dense(residual, "residual", (M, N_EMBD), dev, out.dtype),
+                                 _dense(out, "out", (M, N_EMBD), dev), M,
+                                 _dense(ids, "ids", (M, params.top_k), dev, torch.int32),
+                                 _dense(weights, "weights", (M, params.top_k), dev, torch.float32),
+                                 _dense(workspace, "workspace", workspace.shape, dev), workspace.nbytes, _act_dtype(out),
+                                 _raw_stream(stream, dev))
+    if st:
+        _check(st, "gdn_moe")
     return workspace
 
 

@@ -538,6 +538,125 @@ gdn_status gdn_attn_paged(const gdn_paged_batch *batch, const gdn_kv_cache *cach
  * arithmetic. */
 size_t gdn_attn_paged_workspace_size(const gdn_paged_batch *batch, const gdn_kv_cache *cache);
 
+/* ---------------------------------------------------------------------------
+ * Around the mixers: the residual stream and its norms, the dense products that
+ * have no entry point of their own, and the mixture-of-experts feed-forward.
+ * The residual stream is GDN_HIDDEN (2048) wide.
+ * ------------------------------------------------------------------------- */
+
+/* Parameters of gdn_add_norm: device fp32 weights, applied as w. */
+typedef struct {
+    const float *norm_w;   /* [2048] norm of the sum, the next block's input     */
+    const float *post_w;   /* [2048] norm of the block's output, or NULL: none   */
+    float res_scale;       /* factor of the block's output                       */
+    float norm_eps;
+} gdn_norm_params;
+
+/*
+ * gdn_add_norm -- between two blocks: adds a block's output to the residual
+ * stream and norms the sum for the next block, in one pass:
+ *   x_out = x + res_scale * gate * n(delta),  n(d) = d, or with post_w
+ *           d * (mean(d^2) + norm_eps)^-1/2 * post_w
+ *   h     = x_out * (mean(x_out^2) + norm_eps)^-1/2 * norm_w
+ * in fp32, each output rounded once (h comes from the unrounded sum). Rows may
+ * have any finite magnitude (squares that leave fp32 are scaled); a row of zeros
+ * with norm_eps 0 gives NaN, as 0 / 0 does.
+ *   x       [M][2048] stream_dt       x_out [M][2048] stream_dt, or NULL
+ *   delta   [M][2048] act, or NULL (then x_out = x; gate has to be NULL too)
+ *   gate    [M][2048] act, a factor per element (row stride 0: one row for all
+ *           tokens), or NULL
+ *   h       [M][2048] act, or NULL (norm_w may be NULL then)
+ * Rows are dense; row strides are in elements, multiples of 16 bytes and (but for
+ * gate) at least 2048. x_out may be x (same stride), and h may be delta (same
+ * stride); outputs must not overlap anything otherwise.
+ * 0 <= M <= 2^24. Errors: GDN_ERR_INVALID_ARG, GDN_ERR_CUDA.
+ */
+gdn_status gdn_add_norm(const gdn_norm_params *p, const void *x, long long x_row_stride, const void *delta,
+                        long long delta_row_stride, const void *gate, long long gate_row_stride, void *x_out,
+                        long long x_out_row_stride, void *h, long long h_row_stride, int M, gdn_dtype stream_dt,
+                        gdn_dtype act, void *stream);
+
+/* GELU is the exact one, v / 2 * (1 + erf(v / sqrt(2))). */
+typedef enum { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1, GDN_ACT_GELU = 2, GDN_ACT_SIGMOID = 3 } gdn_activation;
+
+/*
+ * gdn_linear -- a dense product with its epilogue,
+ *   y[m][n] = residual[m][n] + activation(sum_k x[m][k] w[n][k] + bias[n]),
+ * bf16 operands, fp32 accumulation and epilogue, one rounding at the end. With it:
+ * the joint query, gate, key and value projection of a full-attention layer (step
+ * 1 of section "Full-attention block") and attn_output with the residual (step 7).
+ *   x         [M][K] bf16             w [N][K] bf16, dense
+ *   bias      [N] fp32, or NULL
+ *   residual  [M][N] out_dt, or NULL; may be y itself (same stride)
+ *   y         [M][N] out_dt; must not overlap an input otherwise
+ * N and K are multiples of 8, at most 2^20; row strides are in elements, multiples of
+ * 16 bytes, at least the row. All pointers 16-byte aligned. 0 <= M <= 2^24. Errors:
+ * GDN_ERR_INVALID_ARG, GDN_ERR_CUDA (also when the driver's tensor-map encoder
+ * is unavailable). A bounded device wait that gives up is reported afterwards by
+ * gdn_device_error.
+ */
+gdn_status gdn_linear(const void *x, long long x_row_stride, const void *w, const float *bias, const void *residual,
+                      long long residual_row_stride, void *y, long long y_row_stride, int M, int N, int K,
+                      gdn_activation activation, gdn_dtype out_dt, void *stream);
+
+/* The mixture-of-experts feed-forward of a layer. All weights bf16, dense,
+ * 16-byte aligned, one row per output feature. Page tensor names in brackets. */
+#define GDN_MOE_MAX_EXPERTS 256
+#define GDN_MOE_MAX_TOPK 16
+typedef struct {
+    const void *router;            /* [E][2048] (ffn_gate_inp)                        */
+    const void *gate, *up;         /* [E][F][2048] (ffn_gate_exps, ffn_up_exps)       */
+    const void *down;              /* [E][2048][F] (ffn_down_exps)                    */
+    const void *sh_gate, *sh_up;   /* [F][2048] the shared expert, or all three NULL  */
+    const void *sh_down;           /* [2048][F]                                       */
+    const void *sh_router;         /* [2048] its sigmoid gate, or NULL: factor 1      */
+    int num_experts, top_k;        /* 1 <= E <= 256, 1 <= top_k <= min(E, 16)         */
+    int ffn_dim;                   /* F, a multiple of 128, at most 8192              */
+    int norm_topk;                 /* weights of the chosen experts sum to 1; else
+                                      they are their share of the softmax over all E  */
+} gdn_moe_params;
+
+/*
+ * gdn_moe_route -- the router alone: of the logits l[e] = x . router[e] the top_k
+ * largest, in falling order (ties: the lowest index; a NaN ranks below every
+ * number), and their weights softmax(l) (with norm_topk over the chosen ones).
+ *   x        [M][2048] bf16 with its row stride
+ *   ids      [M][top_k] int32          weights [M][top_k] fp32
+ * The order is that of the exact logits: neighbours closer than 2^-13 of the
+ * token's largest logit are settled in 48 bits. Only router, num_experts, top_k and
+ * norm_topk of the parameters are used. 0 <= M <= 2^24. Errors:
+ * GDN_ERR_INVALID_ARG, GDN_ERR_CUDA.
+ */
+gdn_status gdn_moe_route(const gdn_moe_params *p, const void *x, long long x_row_stride, int M, int32_t *ids,
+                         float *weights, void *stream);
+
+/*
+ * gdn_moe -- the whole feed-forward of M tokens, from one token to prompts:
+ *   out = residual + sum_i weights_i * f(ids_i, x) + sigmoid(x . sh_router) * f(shared, x),
+ *   f(e, x) = down[e] (silu(gate[e] x) * (up[e] x))
+ *   x         [M][2048] bf16 with its row stride
+ *   residual  [M][2048] out_dt dense, or NULL; may be out itself
+ *   ids, weights  the routing, as gdn_moe_route gives it, or both NULL: routed here.
+ *             An id outside [0, E) contributes nothing; the same id twice counts twice
+ *   out       [M][2048] out_dt dense; must not overlap an input otherwise
+ *   workspace device scratch, 256-byte aligned, of gdn_moe_workspace_size(p, M)
+ *             bytes; contents need no initialisation. Calls that share one must be
+ *             ordered on a stream
+ * fp32 sums and epilogues; rounded to bf16 once, by at most half a step, are the
+ * hidden activations silu(.) * (.), which enter a bf16 product. A row of x affects
+ * its own output alone, whatever it holds. 0 <= M <= 2^24. Errors:
+ * GDN_ERR_INVALID_ARG, GDN_ERR_WORKSPACE, GDN_ERR_CUDA (also when the driver's
+ * tensor-map encoder is unavailable). A bounded device wait that gives up is
+ * reported afterwards by gdn_device_error.
+ */
+gdn_status gdn_moe(const gdn_moe_params *p, const void *x, long long x_row_stride, const void *residual, void *out,
+                   int M, const int32_t *ids, const float *weights, void *workspace, size_t workspace_bytes,
+                   gdn_dtype out_dt, void *stream);
+
+/* Bytes of workspace gdn_moe needs; 0 if the sizes are out of range. It stops
+ * growing at 8,192 tokens. Pure host arithmetic. */
+size_t gdn_moe_workspace_size(const gdn_moe_params *p, int M);
+
 /* Bytes of workspace gdn_prefill needs for these sizes (0 if the arguments are
  * invalid; never 0 for valid ones). Pure host arithmetic. */
 size_t gdn_prefill_workspace_size(int N, int T_total, gdn_dtype act, int chunk_size);
