@@ -62,7 +62,7 @@ cudaError_t launch_add_norm(const gdn_norm_params *, const void *, long long, co
 cudaError_t launch_linear(const void *, long long, const void *, const float *, const void *, long long, void *,
                           long long, int, int, int, gdn_activation, gdn_dtype, cudaStream_t);
 void *linear_error_word();
-cudaError_t launch_route(const gdn_moe_params *, const void *, long long, int, int32_t *, float *, cudaStream_t);
+cudaError_t launch_route_only(const gdn_moe_params *, const void *, long long, int, int32_t *, float *, cudaStream_t);
 void *route_error_word();
 size_t moe_workspace_bytes(const gdn_moe_params *, int);
 cudaError_t launch_moe(const gdn_moe_params *, const void *, long long, const void *, void *, int, const int32_t *,
@@ -717,7 +717,7 @@ gdn_status gdn_moe_route(const gdn_moe_params *p, const void *x, long long x_row
     if (overlap(ids, n, weights, n) || overlap(ids, n, x, rx.bytes(M)) || overlap(weights, n, x, rx.bytes(M)) ||
         overlap(ids, n, p->router, nr) || overlap(weights, n, p->router, nr))
         return fail(GDN_ERR_INVALID_ARG, "an output overlaps another tensor");
-    cudaError_t e = launch_route(p, x, x_row_stride, M, ids, weights, (cudaStream_t)stream);
+    cudaError_t e = launch_route_only(p, x, x_row_stride, M, ids, weights, (cudaStream_t)stream);
     return e == cudaSuccess ? GDN_OK : cuda_fail(e, "gdn_moe_route");
 }
 

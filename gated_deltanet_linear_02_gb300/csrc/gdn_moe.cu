@@ -8,7 +8,8 @@
 // weights are the tensor core's A operand (128 rows of a weight per product) and an
 // expert's tokens its N (16 to 128), each weight tile passing through shared
 // memory once per 128 tokens.
-//  - moe_place: the pairs (token, expert) sorted by expert.
+//  - The pairs (token, expert) enter their expert's list as they are routed (or by
+//    moe_place, for a given routing).
 //  - moe_experts: one persistent kernel for both halves. Units of work are handed out
 //    in order by a counter: first (expert, 128 rows of gate and of up, token
 //    tile), whose epilogue writes h = silu(g) * u; then (expert, 256 rows of down,
@@ -30,57 +31,28 @@ __device__ unsigned int g_moe_error;      // GDN_ERR_TIMEOUT if a bounded wait g
 
 // ------------------------------------------------------------------ places
 
-constexpr int PL_THREADS = 1024;
-
-__global__ void __launch_bounds__(PL_THREADS) moe_place_kernel(const int32_t *ids, int pairs, int k, int E, int tiles, MoeWs ws)
+__global__ void __launch_bounds__(256) moe_zero_kernel(int *state, int n)
 {
-    __shared__ int count[GDN_MOE_MAX_EXPERTS], first[GDN_MOE_MAX_EXPERTS];
-    const int tid = threadIdx.x;
-    if (tid < GDN_MOE_MAX_EXPERTS) count[tid] = 0;
-    __syncthreads();
     grid_dep_wait();
     grid_dep_launch();
-    for (int i = tid; i < tiles; i += PL_THREADS) ws.ready[i] = 0;
-    if (tid == 0) *ws.ticket = 0;
-    for (int p = tid; p < pairs; p += PL_THREADS) {
-        const int e = ids[p];
-        ws.place[p] = (unsigned)e < (unsigned)E ? atomicAdd(&count[e], 1) : -1;
-    }
-    __syncthreads();
-    if (tid < 32) {                                    // exclusive prefix of the counts, 8 a lane
-        int c[GDN_MOE_MAX_EXPERTS / 32], sum = 0;
-#pragma unroll
-        for (int j = 0; j < GDN_MOE_MAX_EXPERTS / 32; ++j) {
-            c[j] = sum;
-            sum += count[tid * (GDN_MOE_MAX_EXPERTS / 32) + j];
-        }
-        int before = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int n = __shfl_up_sync(0xffffffffu, before, o);
-            if (tid >= o) before += n;
-        }
-        before -= sum;
-#pragma unroll
-        for (int j = 0; j < GDN_MOE_MAX_EXPERTS / 32; ++j) first[tid * (GDN_MOE_MAX_EXPERTS / 32) + j] = before + c[j];
-    }
-    __syncthreads();
-    if (tid < E) {
-        ws.count[tid] = count[tid];
-        ws.offset[tid] = first[tid];
-    }
-    for (int p = tid; p < pairs; p += PL_THREADS) {
-        const int r = ws.place[p];
-        if (r < 0) continue;
-        const int at = first[ids[p]] + r;
-        ws.place[p] = at;
-        ws.token[at] = p / k;
-    }
+    for (int i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) state[i] = 0;
+}
+
+// Places of a given routing.
+__global__ void __launch_bounds__(256) moe_place_kernel(const int32_t *ids, int pairs, int k, int E, MoePlaces places)
+{
+    grid_dep_wait();
+    grid_dep_launch();
+    const int p = blockIdx.x * 256 + threadIdx.x;
+    if (p >= pairs) return;
+    const int e = ids[p];
+    if ((unsigned)e < (unsigned)E) place_pair(places, p / k, p % k, e, k);
+    else places.rank[p] = -1;
 }
 
 // ------------------------------------------------------------------ experts
 
-constexpr int EX_BK = 64, EX_THREADS = 192, EX_INFO = 4;
+constexpr int EX_BK = 64, EX_INFO = 4;
 constexpr uint32_t EX_A_BYTES = 128 * EX_BK * 2;
 constexpr int EX_DOWN_UNITS = LD / 256;
 
@@ -90,13 +62,20 @@ struct ExpertMaps {
 
 struct Unit {
     int kind;                             // 0: gate and up, 1: down, -1: no more
-    int tile, rows_at, row0, n;           // token tile, weight-row tile, first sorted pair, tokens
+    int tile, rows_at, row0, n;           // token tile, weight-row tile, first row of h and y, tokens
+    int expert, t0;                       // the tile's place in the expert's list
 };
 
 template <int NT>
 struct ExpertSmem {
     static constexpr uint32_t STAGE_BYTES = 2 * EX_A_BYTES + NT * EX_BK * 2;
     static constexpr int STAGES = NT <= 32 ? 5 : 4;
+    // Token rows: up to eight gathers a stage by TMA, above that by four warps with
+    // 16-byte asynchronous copies. (A gather of four rows holds the TMA unit as long as a
+    // whole weight tile: 32 of them a stage took 4,096 tokens 504 us.)
+    static constexpr bool LOADERS = NT > 32;
+    static constexpr int THREADS = LOADERS ? 320 : 192;
+    static constexpr int H_BOX = NT <= 32 ? 16 : 64;      // rows of h per copy
     alignas(1024) unsigned char stage[STAGES][STAGE_BYTES];
     alignas(8) uint64_t full[STAGES], empty[STAGES], acc_full[2], acc_empty[2], info_full[EX_INFO], info_empty[EX_INFO];
     Unit info[EX_INFO];
@@ -113,11 +92,20 @@ __device__ __forceinline__ int load_acquire(const int *p)
     asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
     return v;
 }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 __device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
 template <int NT>
-__global__ void __launch_bounds__(EX_THREADS, 1)
-    moe_experts_kernel(const __grid_constant__ ExpertMaps maps, int M, int E, int F, int k, int shared, MoeWs ws)
+__global__ void __launch_bounds__(ExpertSmem<NT>::THREADS, 1)
+    moe_experts_kernel(const __grid_constant__ ExpertMaps maps, const bf16 *x, long long x_row, int M, int E, int F, int k, int shared, MoeWs ws)
 {
     using Smem = ExpertSmem<NT>;
     constexpr int STAGES = Smem::STAGES;
@@ -133,7 +121,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
     }
     if (tid == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(smem_u32(&sm.full[s]), 1);
+            mbar_init(smem_u32(&sm.full[s]), Smem::LOADERS ? 5 : 1);
             mbar_init(smem_u32(&sm.empty[s]), 1);
             sm.last_it[s] = -1;
         }
@@ -143,31 +131,38 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
         }
         for (int i = 0; i < EX_INFO; ++i) {
             mbar_init(smem_u32(&sm.info_full[i]), 1);
-            mbar_init(smem_u32(&sm.info_empty[i]), 5);
+            mbar_init(smem_u32(&sm.info_empty[i]), Smem::LOADERS ? 9 : 5);
         }
         sm.abort = 0;
         fence_mbar_init();
     }
     grid_dep_wait();
-    for (int e = tid; e < NE; e += EX_THREADS) {
-        sm.count[e] = e < E ? ws.count[e] : M;
-        sm.offset[e] = e < E ? ws.offset[e] : M * k;
+    for (int e = tid; e < NE; e += Smem::THREADS) {
+        sm.count[e] = e < E ? ws.places.count[e] : M;
     }
     __syncthreads();
-    if (warp == 0) {                                   // tiles before each expert
-        int sum = 0;
+    if (warp == 0) {                                   // tiles and rows before each expert
+        int tiles = 0, rows = 0;
         for (int e0 = 0; e0 < NE; e0 += 32) {
-            const int t = e0 + lane < NE ? (sm.count[e0 + lane] + NT - 1) / NT : 0;
-            int inc = t;
+            const int e = e0 + lane, c = e < NE ? sm.count[e] : 0, t = (c + NT - 1) / NT;
+            int ti = t, ci = c;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int n = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += n;
+                const int a = __shfl_up_sync(0xffffffffu, ti, o), b = __shfl_up_sync(0xffffffffu, ci, o);
+                if (lane >= o) {
+                    ti += a;
+                    ci += b;
+                }
             }
-            if (e0 + lane < NE) sm.tile0[e0 + lane] = sum + inc - t;
-            sum += __shfl_sync(0xffffffffu, inc, 31);
+            if (e < NE) {
+                sm.tile0[e] = tiles + ti - t;
+                sm.offset[e] = e < E ? rows + ci - c : M * k;
+                if (blockIdx.x == 0 && e < E) ws.offset[e] = rows + ci - c;
+            }
+            tiles += __shfl_sync(0xffffffffu, ti, 31);
+            rows += __shfl_sync(0xffffffffu, ci, 31);
         }
-        if (lane == 0) sm.tile0[NE] = sum;
+        if (lane == 0) sm.tile0[NE] = tiles;
     }
     tc::fence_before_sync();
     __syncthreads();
@@ -185,8 +180,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
             const int slot = ui % EX_INFO;
             if (ui >= EX_INFO && !mbar_wait_bounded(smem_u32(&sm.info_empty[slot]), (uint32_t)((ui / EX_INFO - 1) & 1)))
                 sm.abort = 1;
-            Unit un = {-1, 0, 0, 0, 0};
-            int e = 0, t0 = 0;
+            Unit un = {-1, 0, 0, 0, 0, 0, 0};
             if (u < units && !aborted) {
                 un.kind = u >= units1;
                 const int per = un.kind ? EX_DOWN_UNITS : FU, v = un.kind ? u - units1 : u;
@@ -196,13 +190,13 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
                     if (sm.tile0[mid] <= v / per) lo = mid;
                     else hi = mid;
                 }
-                e = lo;
+                const int e = un.expert = lo;
                 const int nt = sm.tile0[e + 1] - sm.tile0[e], r = v - per * sm.tile0[e];
                 un.rows_at = r / nt;
-                t0 = (r % nt) * NT;
+                un.t0 = (r % nt) * NT;
                 un.tile = sm.tile0[e] + r % nt;
-                un.row0 = sm.offset[e] + t0;
-                un.n = min(NT, sm.count[e] - t0);
+                un.row0 = sm.offset[e] + un.t0;
+                un.n = min(NT, sm.count[e] - un.t0);
             }
             if (lane == 0) {
                 sm.info[slot] = un;
@@ -210,9 +204,10 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
             }
             if (un.kind < 0) break;
             if (lane == 0) next = atomicAdd(ws.ticket, 1);
+            const int e = un.expert;
             const bool sh = e == E;
-            const int n16 = (un.n + 15) & ~15;
-            const uint32_t bytes = 2 * EX_A_BYTES + (uint32_t)n16 * EX_BK * 2;
+            const int n16 = (un.n + 15) & ~15, boxes = (un.n + Smem::H_BOX - 1) / Smem::H_BOX;
+            const uint32_t bytes = 2 * EX_A_BYTES + (un.kind ? (uint32_t)(boxes * Smem::H_BOX) : Smem::LOADERS ? 0u : (uint32_t)n16) * EX_BK * 2;
             const CUtensorMap *ma, *mb;
             int ya, yb, slices;
             int4 rows = make_int4(0, 0, 0, 0);
@@ -221,12 +216,12 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
                 mb = sh ? &maps.sh_up : &maps.up;
                 ya = yb = (sh ? 0 : e * F) + un.rows_at * 128;
                 slices = LD / EX_BK;
-                if (4 * lane < n16) {                  // rows past the last token repeat it
+                if (!Smem::LOADERS && 4 * lane < n16) {   // rows past the last token repeat it
                     int r[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int t = min(4 * lane + i, un.n - 1);
-                        r[i] = sh ? t0 + t : ws.token[un.row0 + t];
+                        r[i] = sh ? un.t0 + t : ws.places.token[(size_t)e * ws.places.stride + un.t0 + t];
                     }
                     rows = make_int4(r[0], r[1], r[2], r[3]);
                 }
@@ -263,9 +258,9 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
                 }
                 __syncwarp();
                 if (un.kind == 0) {
-                    if (4 * lane < n16) tma_gather4(b0 + 512u * lane, &maps.x, kb * EX_BK, rows, bar);
-                } else if (16 * lane < n16) {
-                    tma_load_2d(b0 + 2048u * lane, &maps.h, kb * EX_BK, un.row0 + 16 * lane, bar);
+                    if (!Smem::LOADERS && 4 * lane < n16) tma_gather4(b0 + 512u * lane, &maps.x, kb * EX_BK, rows, bar);
+                } else if (lane < boxes) {
+                    tma_load_2d(b0 + 128u * Smem::H_BOX * lane, &maps.h, kb * EX_BK, un.row0 + Smem::H_BOX * lane, bar);
                 }
             }
         }
@@ -308,6 +303,55 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
                 tc::mma_commit(smem_u32(&sm.acc_full[ab]));
             }
         }
+    } else if (warp >= 6) {
+        // ---- token rows (LOADERS): 8 lanes bring the 128 bytes of a row, four rows at a time. A
+        //      stage is reported two slices later, when its copies have landed.
+        constexpr int LAG = 2;
+        const int w = warp - 6, sub = lane >> 3, chunk = lane & 7;
+        int it = 0;
+        auto report = [&](int i) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm.full[i % STAGES]));
+        };
+        for (int ui = 0; !aborted; ++ui) {
+            const int slot = ui % EX_INFO;
+            if (!mbar_wait_sleep(smem_u32(&sm.info_full[slot]), (uint32_t)((ui / EX_INFO) & 1))) sm.abort = 1;
+            if (aborted) break;
+            const Unit un = sm.info[slot];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm.info_empty[slot]));
+            if (un.kind < 0) break;
+            const int n16 = un.kind ? 0 : (un.n + 15) & ~15;
+            const unsigned char *src[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = 32 * w + 4 * i + sub, t = min(r, un.n - 1);
+                int tok = 0;
+                if (r < n16) tok = un.expert == E ? un.t0 + t : ws.places.token[(size_t)un.expert * ws.places.stride + un.t0 + t];
+                src[i] = reinterpret_cast<const unsigned char *>(x + (size_t)tok * x_row) + 16 * chunk;
+            }
+            const int slices = (un.kind ? F : LD) / EX_BK;
+            for (int kb = 0; kb < slices; ++kb, ++it) {
+                const int s = it % STAGES;
+                if (it >= STAGES && !mbar_wait_bounded(smem_u32(&sm.empty[s]), (uint32_t)((it / STAGES - 1) & 1)))
+                    sm.abort = 1;
+                if (aborted) break;
+                const uint32_t b0 = smem_u32(sm.stage[s]) + 2 * EX_A_BYTES;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int r = 32 * w + 4 * i + sub;
+                    if (r < n16) cp_async16(b0 + 128u * r + ((uint32_t)(chunk ^ (r & 7)) << 4), src[i] + 128 * kb);
+                }
+                cp_async_commit();
+                if (it >= LAG) {
+                    cp_async_wait<LAG>();
+                    report(it - LAG);
+                }
+            }
+        }
+        cp_async_wait<0>();
+        for (int i = max(0, it - LAG); i < it && !aborted; ++i) report(i);
     } else {
         // ---- epilogue: thread = weight row (tensor-memory lane), columns = tokens
         const int q = warp & 3, row = 32 * q + lane;
@@ -368,46 +412,58 @@ constexpr int CB_THREADS = LD / 8;
 
 template <typename TO>
 __global__ void __launch_bounds__(CB_THREADS)
-    moe_combine_kernel(const bf16 *x, long long x_row, const bf16 *sh_router, const float *weights, const void *residual,
-                       void *out, int M, int k, int shared, MoeWs ws)
+    moe_combine_kernel(const bf16 *x, long long x_row, const bf16 *sh_router, const int32_t *ids, const float *weights,
+                       const void *residual, void *out, int M, int k, int shared, MoeWs ws)
 {
-    __shared__ float part[CB_THREADS / 32];
+    __shared__ float part[CB_THREADS / 32], weight[GDN_MOE_MAX_TOPK];
+    __shared__ int row[GDN_MOE_MAX_TOPK];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = tid * 8;
     const size_t m = blockIdx.x;
     grid_dep_wait();
     grid_dep_launch();
-    float acc[8] = {};
+    if (tid < k) {
+        const int r = ws.places.rank[m * k + tid];
+        row[tid] = r < 0 ? -1 : ws.offset[ids[m * k + tid]] + r;
+        weight[tid] = weights[m * k + tid];
+    }
+    float acc[8] = {}, ys[8];
     if (residual) ld8(static_cast<const TO *>(residual) + m * LD + c, acc);
-    float gate = 1.0f;
+    if (shared) ld8(ws.y + ((size_t)M * k + m) * LD + c, ys);
+    float s = 0.0f;
     if (sh_router) {                                   // the shared expert's gate
-        float a[8], b[8], s = 0.0f;
+        float a[8], b[8];
         ld8(x + m * x_row + c, a);
         ld8(sh_router + c, b);
 #pragma unroll
         for (int i = 0; i < 8; ++i) s = fmaf(a[i], b[i], s);
         s = warp_sum(s);
         if (lane == 0) part[warp] = s;
-        __syncthreads();
-        s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < CB_THREADS / 32; ++i) s += part[i];
-        gate = 1.0f / (1.0f + expf(-s));
     }
+    __syncthreads();
     float sum[8] = {};
-    for (int j = 0; j < k; ++j) {
-        const int at = ws.place[m * k + j];
-        if (at < 0) continue;
-        const float w = weights[m * k + j];
-        float y[8];
-        ld8(ws.y + (size_t)at * LD + c, y);
+    for (int j = 0; j < k; j += 4) {                   // four rows in flight, added in slot order
+        float y[4][8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum[i] = fmaf(w, y[i], sum[i]);
+        for (int i = 0; i < 4; ++i)
+            if (j + i < k && row[j + i] >= 0) ld8(ws.y + (size_t)row[j + i] * LD + c, y[i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (j + i < k && row[j + i] >= 0) {
+                const float w = weight[j + i];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum[e] = fmaf(w, y[i][e], sum[e]);
+            }
     }
     if (shared) {
-        float y[8];
-        ld8(ws.y + ((size_t)M * k + m) * LD + c, y);
+        float gate = 1.0f;
+        if (sh_router) {
+            s = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum[i] = fmaf(gate, y[i], sum[i]);
+            for (int i = 0; i < CB_THREADS / 32; ++i) s += part[i];
+            gate = 1.0f / (1.0f + expf(-s));
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] = fmaf(gate, ys[i], sum[i]);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] += sum[i];
@@ -415,6 +471,8 @@ __global__ void __launch_bounds__(CB_THREADS)
 }
 
 // ------------------------------------------------------------------ launcher
+
+constexpr int MOE_FEW = 512;              // tokens up to which tiles hold 32 of them
 
 static bool moe_setup()
 {
@@ -461,27 +519,26 @@ cudaError_t launch_moe(const gdn_moe_params *p, const void *x, long long x_row, 
         const int32_t *idw = ids ? ids + (size_t)m0 * k : ws.ids;
         const float *ww = ids ? weights + (size_t)m0 * k : ws.weights;
         const size_t rows = (size_t)W * (k + (shared ? 1 : 0));
-        if (!make_bf16_strided_map(&maps.x, xw, W, LD, x_row, 1) || !make_bf16_strided_map(&maps.h, ws.h, rows, F, F, 16))
+        if (!make_bf16_strided_map(&maps.x, xw, W, LD, x_row, 1) || !make_bf16_strided_map(&maps.h, ws.h, rows, F, F, W <= MOE_FEW ? ExpertSmem<32>::H_BOX : ExpertSmem<MOE_TILE>::H_BOX))
             return cudaErrorInvalidValue;
-        cudaError_t e = cudaSuccess;
-        if (!ids) e = launch_route(p, xw, x_row, W, ws.ids, ws.weights, s);
+        const int n_state = (int)ws.state_ints;
+        cudaError_t e = launch_pdl(moe_zero_kernel, dim3((n_state + 1023) / 1024), dim3(256), 0, s, ws.state, n_state);
         if (e != cudaSuccess) return e;
-        e = launch_pdl(moe_place_kernel, dim3(1), dim3(PL_THREADS), 0, s, idw, W * k, k, E, moe_max_tiles(p, W), ws);
+        e = ids ? launch_pdl(moe_place_kernel, dim3((W * k + 255) / 256), dim3(256), 0, s, idw, W * k, k, E, ws.places)
+                : launch_route(p, xw, x_row, W, ws.ids, ws.weights, ws.places, s);
         if (e != cudaSuccess) return e;
-        if (W <= 512)
-            e = launch_pdl(moe_experts_kernel<32>, dim3(n_sm), dim3(EX_THREADS), sizeof(ExpertSmem<32>) + 1024, s, maps,
-                           W, E, F, k, (int)shared, ws);
-        else
-            e = launch_pdl(moe_experts_kernel<MOE_TILE>, dim3(n_sm), dim3(EX_THREADS), sizeof(ExpertSmem<MOE_TILE>) + 1024,
-                           s, maps, W, E, F, k, (int)shared, ws);
+        e = W <= MOE_FEW ? launch_pdl(moe_experts_kernel<32>, dim3(n_sm), dim3(ExpertSmem<32>::THREADS),
+                                      sizeof(ExpertSmem<32>) + 1024, s, maps, xw, x_row, W, E, F, k, (int)shared, ws)
+                         : launch_pdl(moe_experts_kernel<MOE_TILE>, dim3(n_sm), dim3(ExpertSmem<MOE_TILE>::THREADS),
+                                      sizeof(ExpertSmem<MOE_TILE>) + 1024, s, maps, xw, x_row, W, E, F, k, (int)shared, ws);
         if (e != cudaSuccess) return e;
         const void *rw = residual ? static_cast<const char *>(residual) + m0 * out_row : nullptr;
         void *ow = static_cast<char *>(out) + m0 * out_row;
         const bf16 *shr = static_cast<const bf16 *>(p->sh_router);
-        e = out_dt == GDN_F32 ? launch_pdl(moe_combine_kernel<float>, dim3(W), dim3(CB_THREADS), 0, s, xw, x_row, shr, ww,
-                                           rw, ow, W, k, (int)shared, ws)
-                              : launch_pdl(moe_combine_kernel<bf16>, dim3(W), dim3(CB_THREADS), 0, s, xw, x_row, shr, ww,
-                                           rw, ow, W, k, (int)shared, ws);
+        e = out_dt == GDN_F32 ? launch_pdl(moe_combine_kernel<float>, dim3(W), dim3(CB_THREADS), 0, s, xw, x_row, shr, idw,
+                                           ww, rw, ow, W, k, (int)shared, ws)
+                              : launch_pdl(moe_combine_kernel<bf16>, dim3(W), dim3(CB_THREADS), 0, s, xw, x_row, shr, idw,
+                                           ww, rw, ow, W, k, (int)shared, ws);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

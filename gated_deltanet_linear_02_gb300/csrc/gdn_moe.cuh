@@ -26,14 +26,31 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *map
                    "r"(bar) : "memory");
 }
 
-// Workspace of a window of at most W tokens: routing, the pairs (token, expert)
-// sorted by expert, their activations h and their outputs y. The shared expert's
-// rows follow the W * top_k routed ones, in token order.
+// Where the pairs (token, expert) go: each expert's list of tokens, in any order (a token's result does not depend on its place), filled through counters.
+struct MoePlaces {
+    int *count;                           // [E], zero before the first pair; NULL: no places wanted
+    int *token;                           // [E][stride]
+    int *rank;                            // [tokens][k]: the pair's place in its expert's list, or -1
+    int stride;                           // tokens * k: a given routing may name an expert several times a token
+};
+
+__device__ __forceinline__ void place_pair(const MoePlaces &p, int m, int slot, int e, int k)
+{
+    const int r = atomicAdd(p.count + e, 1);
+    p.token[(size_t)e * p.stride + r] = m;
+    p.rank[(size_t)m * k + slot] = r;
+}
+
+// Workspace of a window of at most W tokens. Rows of h and y: each expert's pairs in
+// the order of its list, one expert after the other, then the shared expert's, in
+// token order, from row W * top_k on.
 struct MoeWs {
+    int *state;                           // what a call starts from zero: ticket, count, ready
+    size_t state_ints;
     int *ticket;                          // next unit of work
-    int *count, *offset;                  // [E] pairs of each expert, and where they begin
     int *ready;                           // [tiles] finished parts of each tile's h
-    int *token, *place;                   // sorted pair -> token; (token, slot) -> sorted pair, or -1
+    int *offset;                          // [E] first row of each expert
+    MoePlaces places;
     int *ids;
     float *weights;
     bf16 *h;                              // [rows][F]
@@ -59,13 +76,17 @@ inline MoeWs moe_workspace(const gdn_moe_params *p, int M, void *base)
         at += (n + 255) & ~(size_t)255;
         return static_cast<char *>(base) + here;
     };
+    const int tiles = moe_max_tiles(p, W);
     MoeWs w;
-    w.ticket = (int *)take(4);
-    w.count = (int *)take(GDN_MOE_MAX_EXPERTS * 4);
+    w.state_ints = 1 + GDN_MOE_MAX_EXPERTS + (size_t)tiles;
+    w.state = (int *)take(w.state_ints * 4);
+    w.ticket = w.state;
+    w.places.count = w.state + 1;
+    w.ready = w.state + 1 + GDN_MOE_MAX_EXPERTS;
     w.offset = (int *)take(GDN_MOE_MAX_EXPERTS * 4);
-    w.ready = (int *)take((size_t)moe_max_tiles(p, W) * 4);
-    w.token = (int *)take(pairs * 4);
-    w.place = (int *)take(pairs * 4);
+    w.places.token = (int *)take((size_t)p->num_experts * pairs * 4);
+    w.places.rank = (int *)take(pairs * 4);
+    w.places.stride = (int)pairs;
     w.ids = (int *)take(pairs * 4);
     w.weights = (float *)take(pairs * 4);
     w.h = (bf16 *)take(rows * p->ffn_dim * 2);
@@ -75,6 +96,6 @@ inline MoeWs moe_workspace(const gdn_moe_params *p, int M, void *base)
 }
 
 cudaError_t launch_route(const gdn_moe_params *p, const void *x, long long x_row, int M, int32_t *ids, float *weights,
-                         cudaStream_t s);
+                         const MoePlaces &places, cudaStream_t s);
 
 }  // namespace gdn

@@ -11,8 +11,8 @@
 // tokens: a warp per token holds 8 logits a lane and takes the largest k times.
 //
 // The choice is exact: where two of the first k + 1 logits are closer than 2^-13 of
-// the largest magnitude (the error bound is far below), the warp sums the logits
-// of all candidates again in pairs of fp32 (48 bits; products of bf16 are exact).
+// the largest magnitude (the error bound is far below), the warp sums theirs again
+// in pairs of fp32 (48 bits; products of bf16 are exact).
 // Ties go to the lowest index. NaN ranks below everything.
 #include <mutex>
 
@@ -25,7 +25,7 @@ namespace gdn {
 
 __device__ unsigned int g_route_error;    // GDN_ERR_TIMEOUT if a bounded wait gave up
 
-constexpr int RT_BM = 128, RT_BK = 64, RT_THREADS = 256, RT_STAGES = 4;
+constexpr int RT_BM = 128, RT_BK = 64, RT_THREADS = 512, RT_STAGES = 4;
 constexpr uint32_t RT_A_BYTES = RT_BM * RT_BK * 2;
 constexpr int RT_ACC_K = 256;             // K of one accumulator
 constexpr int RT_MAX_E = GDN_MOE_MAX_EXPERTS;
@@ -61,21 +61,28 @@ __device__ __forceinline__ float2 pair_add(float2 a, float2 b)
     return make_float2(h, __fsub_rn(e, __fsub_rn(h, s.x)));
 }
 
-// The logit of one expert as a pair of fp32, the same in every lane.
+// The logit of one expert as a pair of fp32, the same in every lane. Four running
+// sums, each with the sum of its rounding errors beside it: one addition per product
+// on the critical path.
 __device__ __noinline__ float2 pair_dot(const bf16 *x, const bf16 *w, int lane)
 {
-    float2 acc = make_float2(0.0f, 0.0f);
+    float2 acc[4] = {};
+#pragma unroll 4
     for (int c = 0; c < LD / 256; ++c) {
         float a[8], b[8];
         ld8(x + c * 256 + lane * 8, a);
         ld8(w + c * 256 + lane * 8, b);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc = pair_add(acc, make_float2(__fmul_rn(a[i], b[i]), 0.0f));
+        for (int i = 0; i < 8; ++i) {
+            const float2 s = two_sum(acc[i & 3].x, __fmul_rn(a[i], b[i]));
+            acc[i & 3] = make_float2(s.x, __fadd_rn(acc[i & 3].y, s.y));
+        }
     }
+    float2 sum = pair_add(pair_add(acc[0], acc[1]), pair_add(acc[2], acc[3]));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
-        acc = pair_add(acc, make_float2(__shfl_xor_sync(0xffffffffu, acc.x, o), __shfl_xor_sync(0xffffffffu, acc.y, o)));
-    return acc;
+        sum = pair_add(sum, make_float2(__shfl_xor_sync(0xffffffffu, sum.x, o), __shfl_xor_sync(0xffffffffu, sum.y, o)));
+    return sum;
 }
 
 // The k largest of the warp's logits v[j] (expert lane + 32 j, -inf past E with
@@ -100,8 +107,10 @@ __device__ void choose(float (&v)[RT_SLOTS], int E, int k, bool renorm, const bf
     bool settled = false;
     for (;;) {
         uint32_t taken = 0;                            // this lane's slots that are out
+        uint32_t near = 0;                             // this lane's slots that are close to a neighbour
         float prev = 0.0f, kth = 0.0f;
-        bool close = false;
+        int prev_at = 0;
+        bool close = false, border = false;
         const int rounds = settled || k >= E ? k : k + 1;
         for (int i = 0; i < rounds; ++i) {
             uint32_t mk = 0;
@@ -130,8 +139,14 @@ __device__ void choose(float (&v)[RT_SLOTS], int E, int k, bool renorm, const bf
                     taken |= 1u << j;
                 }
             val = __shfl_sync(0xffffffffu, val, (int)(at & 31u));
-            if (i > 0 && prev - val <= 0x1p-13f * big) close = true;
+            if (i > 0 && prev - val <= 0x1p-13f * big) {
+                close = true;
+                border |= i == k;
+                if ((prev_at & 31) == lane) near |= 1u << (prev_at >> 5);
+                if ((int)(at & 31u) == lane) near |= 1u << (at >> 5);
+            }
             prev = val;
+            prev_at = (int)at;
             if (i < k) {
                 kth = val;
                 if (lane == i) {
@@ -141,24 +156,27 @@ __device__ void choose(float (&v)[RT_SLOTS], int E, int k, bool renorm, const bf
             }
         }
         if (settled || !close || !(big > 0.0f)) break;
-        // every expert that may belong to the first k, in 48 bits
+        // in 48 bits: the neighbours among the first k, and where the last of them is
+        // close to the next, every expert that may be in its place
         settled = true;
-        const float floor_v = kth - 0x1p-13f * big;
-        for (int e = 0; e < E; ++e) {
-            float ve = 0.0f;
+        if (border) {
 #pragma unroll
             for (int j = 0; j < RT_SLOTS; ++j)
-                if (e >> 5 == j) ve = v[j];
-            ve = __shfl_sync(0xffffffffu, ve, e & 31);
-            if (!(ve >= floor_v) || !(fabsf(ve) < INFINITY)) continue;
-            const float2 p = pair_dot(x, router + (size_t)e * LD, lane);
+                if (lane + 32 * j < E && !(v[j] < kth - 0x1p-13f * big) && v[j] <= kth) near |= 1u << j;
+        }
 #pragma unroll
-            for (int j = 0; j < RT_SLOTS; ++j)
-                if (e == lane + 32 * j) {
+        for (int j = 0; j < RT_SLOTS; ++j) {
+            uint32_t who = __ballot_sync(0xffffffffu, (near >> j & 1u) && fabsf(v[j]) < INFINITY);
+            while (who) {
+                const int from = __ffs(who) - 1;
+                who &= who - 1;
+                const float2 p = pair_dot(x, router + (size_t)(from + 32 * j) * LD, lane);
+                if (lane == from) {
                     v[j] = p.x;
                     key[j] = sort_key(p.x);
                     lo[j] = p.y;
                 }
+            }
         }
     }
     const float top = __shfl_sync(0xffffffffu, best, 0);
@@ -176,7 +194,7 @@ __device__ void choose(float (&v)[RT_SLOTS], int E, int k, bool renorm, const bf
 __global__ void __launch_bounds__(RT_THREADS, 1)
     route_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mr, const bf16 *x,
                  long long x_row, const bf16 *router, int M, int E, int N, int k, int renorm, int splits,
-                 int32_t *ids, float *weights)
+                 int32_t *ids, float *weights, MoePlaces places)
 {
     extern __shared__ unsigned char smem_raw[];
     RouteSmem &sm = *reinterpret_cast<RouteSmem *>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
@@ -246,7 +264,7 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
             }
             if (!aborted) tc::mma_commit(smem_u32(&sm.done));
         }
-    } else if (warp >= 4) {
+    } else if (warp >= 4 && warp < 8) {
         if (!mbar_wait_bounded(smem_u32(&sm.done), 0)) sm.abort = 1;
         tc::fence_after_sync();
         const int q = warp & 3, row = 32 * q + lane;
@@ -291,6 +309,7 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
             if (lane < k) {
                 ids[(size_t)m * k + lane] = id;
                 weights[(size_t)m * k + lane] = w;
+                if (places.count) place_pair(places, m, lane, id, k);
             }
         }
     }
@@ -318,7 +337,7 @@ static bool route_setup()
 }
 
 cudaError_t launch_route(const gdn_moe_params *p, const void *x, long long x_row, int M, int32_t *ids, float *weights,
-                         cudaStream_t s)
+                         const MoePlaces &places, cudaStream_t s)
 {
     if (!route_setup()) return cudaErrorInvalidDevice;
     const int E = p->num_experts, N = (E + 15) & ~15;
@@ -341,7 +360,13 @@ cudaError_t launch_route(const gdn_moe_params *p, const void *x, long long x_row
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, route_kernel, mx, mr, (const bf16 *)x, x_row, (const bf16 *)p->router, M, E, N,
-                              p->top_k, p->norm_topk, splits, ids, weights);
+                              p->top_k, p->norm_topk, splits, ids, weights, places);
+}
+
+cudaError_t launch_route_only(const gdn_moe_params *p, const void *x, long long x_row, int M, int32_t *ids,
+                              float *weights, cudaStream_t s)
+{
+    return launch_route(p, x, x_row, M, ids, weights, MoePlaces{}, s);
 }
 
 // Device address of this file's error word, for gdn_device_error (NULL if the lookup fails).
