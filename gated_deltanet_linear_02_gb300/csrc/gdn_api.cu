@@ -68,6 +68,7 @@ size_t moe_workspace_bytes(const gdn_moe_params *, int);
 cudaError_t launch_moe(const gdn_moe_params *, const void *, long long, const void *, void *, int, const int32_t *,
                        const float *, void *, gdn_dtype, cudaStream_t);
 void *moe_error_word();
+void *few_error_word();
 cudaError_t launch_wait_timeout(cudaStream_t s);
 void *selftest_error_word();
 }  // namespace gdn
@@ -243,7 +244,7 @@ namespace gdn {
 // clears all of them with one small kernel (an atomic exchange each, so a word
 // set while the call runs is either reported now or kept for the next call)
 // and one copy of the OR back to the host.
-constexpr int N_ERROR_WORDS = 13;
+constexpr int N_ERROR_WORDS = 14;
 struct ErrorWords {
     unsigned int *p[N_ERROR_WORDS];
 };
@@ -275,7 +276,7 @@ static bool error_words(ErrorWords *out)
                                                gemm_error_word,   attn_error_word,     selftest_error_word,
                                                gproj_error_word,  inconv_error_word,   paged_error_word,
                                                paged_q4_error_word, linear_error_word, route_error_word,
-                                               moe_error_word};
+                                               moe_error_word,    few_error_word};
         for (int i = 0; i < N_ERROR_WORDS; ++i) {
             cache[dev].p[i] = static_cast<unsigned int *>(fns[i]());
             if (cache[dev].p[i] == nullptr) return false;

@@ -503,6 +503,7 @@ cudaError_t launch_moe(const gdn_moe_params *p, const void *x, long long x_row, 
     const bool shared = p->sh_gate != nullptr;
     const size_t out_row = (size_t)LD * (out_dt == GDN_F32 ? 4 : 2);
     MoeWs ws = moe_workspace(p, M, workspace);
+    if (M <= MOE_FEW_TOKENS) return launch_moe_few(p, x, x_row, residual, out, M, ids, weights, ws, out_dt, s);
     ExpertMaps maps;
     if (!make_bf16_strided_map(&maps.gate, p->gate, (long long)E * F, LD, LD, 128) ||
         !make_bf16_strided_map(&maps.up, p->up, (long long)E * F, LD, LD, 128) ||

@@ -8,11 +8,12 @@ namespace gdn {
 
 constexpr int MOE_WINDOW = 8192;          // tokens that one pass over the experts takes, at most
 constexpr int MOE_TILE = 128;             // tokens of one product, at most
+constexpr int MOE_FEW_TOKENS = 4;         // tokens up to which the weights pass through the CUDA cores
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr)
 {
     float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr));
     return v;
 }
 
@@ -26,7 +27,8 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *map
                    "r"(bar) : "memory");
 }
 
-// Where the pairs (token, expert) go: each expert's list of tokens, in any order (a token's result does not depend on its place), filled through counters.
+// Where the pairs (token, expert) go: each expert's list of tokens, in any order (a
+// token's result does not depend on its place), filled through counters.
 struct MoePlaces {
     int *count;                           // [E], zero before the first pair; NULL: no places wanted
     int *token;                           // [E][stride]
@@ -54,7 +56,8 @@ struct MoeWs {
     int *ids;
     float *weights;
     bf16 *h;                              // [rows][F]
-    float *y;                             // [rows][2048]
+    float *y;                             // [rows][2048]; few tokens: h in fp32, [rows][F]
+    float *logits;                        // few tokens: [M][E + 1]
     size_t bytes;
 };
 
@@ -78,7 +81,7 @@ inline MoeWs moe_workspace(const gdn_moe_params *p, int M, void *base)
     };
     const int tiles = moe_max_tiles(p, W);
     MoeWs w;
-    w.state_ints = 1 + GDN_MOE_MAX_EXPERTS + (size_t)tiles;
+    w.state_ints = 1 + GDN_MOE_MAX_EXPERTS + (size_t)tiles;   // few tokens: two counters
     w.state = (int *)take(w.state_ints * 4);
     w.ticket = w.state;
     w.places.count = w.state + 1;
@@ -90,12 +93,16 @@ inline MoeWs moe_workspace(const gdn_moe_params *p, int M, void *base)
     w.ids = (int *)take(pairs * 4);
     w.weights = (float *)take(pairs * 4);
     w.h = (bf16 *)take(rows * p->ffn_dim * 2);
-    w.y = (float *)take(rows * LD * 4);
+    w.y = (float *)take(rows * (W <= MOE_FEW_TOKENS && p->ffn_dim > LD ? p->ffn_dim : LD) * 4);
+    w.logits = (float *)take(W <= MOE_FEW_TOKENS ? (size_t)W * (p->num_experts + 1) * 4 : 0);
     w.bytes = at;
     return w;
 }
 
 cudaError_t launch_route(const gdn_moe_params *p, const void *x, long long x_row, int M, int32_t *ids, float *weights,
                          const MoePlaces &places, cudaStream_t s);
+
+cudaError_t launch_moe_few(const gdn_moe_params *p, const void *x, long long x_row, const void *residual, void *out, int M,
+                           const int32_t *ids, const float *weights, const MoeWs &ws, gdn_dtype out_dt, cudaStream_t s);
 
 }  // namespace gdn

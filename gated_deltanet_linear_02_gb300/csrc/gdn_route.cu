@@ -18,6 +18,7 @@
 
 #include "gdn_layer.cuh"
 #include "gdn_moe.cuh"
+#include "gdn_route.cuh"
 #include "gdn_tc.cuh"
 #include "gdn_tma.cuh"
 
@@ -28,8 +29,6 @@ __device__ unsigned int g_route_error;    // GDN_ERR_TIMEOUT if a bounded wait g
 constexpr int RT_BM = 128, RT_BK = 64, RT_THREADS = 512, RT_STAGES = 4;
 constexpr uint32_t RT_A_BYTES = RT_BM * RT_BK * 2;
 constexpr int RT_ACC_K = 256;             // K of one accumulator
-constexpr int RT_MAX_E = GDN_MOE_MAX_EXPERTS;
-constexpr int RT_SLOTS = RT_MAX_E / 32;   // logits per lane
 
 struct RouteSmem {
     alignas(1024) unsigned char stage[RT_STAGES][RT_A_BYTES + RT_MAX_E * RT_BK * 2];
@@ -39,157 +38,6 @@ struct RouteSmem {
     int abort;
 };
 static_assert(RT_BM * (RT_MAX_E + 4) * 4 <= sizeof(RouteSmem::stage), "partial logits fit the stages");
-
-// Order-preserving keys of floats; NaN is the smallest, -0 is +0.
-__device__ __forceinline__ uint32_t sort_key(float x)
-{
-    if (!(x == x)) return 0u;
-    const uint32_t u = __float_as_uint(x + 0.0f);
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-
-// a + b as (sum, error), both exact.
-__device__ __forceinline__ float2 two_sum(float a, float b)
-{
-    const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
-    return make_float2(s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t)));
-}
-__device__ __forceinline__ float2 pair_add(float2 a, float2 b)
-{
-    const float2 s = two_sum(a.x, b.x);
-    const float e = __fadd_rn(s.y, __fadd_rn(a.y, b.y)), h = __fadd_rn(s.x, e);
-    return make_float2(h, __fsub_rn(e, __fsub_rn(h, s.x)));
-}
-
-// The logit of one expert as a pair of fp32, the same in every lane. Four running
-// sums, each with the sum of its rounding errors beside it: one addition per product
-// on the critical path.
-__device__ __noinline__ float2 pair_dot(const bf16 *x, const bf16 *w, int lane)
-{
-    float2 acc[4] = {};
-#pragma unroll 4
-    for (int c = 0; c < LD / 256; ++c) {
-        float a[8], b[8];
-        ld8(x + c * 256 + lane * 8, a);
-        ld8(w + c * 256 + lane * 8, b);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float2 s = two_sum(acc[i & 3].x, __fmul_rn(a[i], b[i]));
-            acc[i & 3] = make_float2(s.x, __fadd_rn(acc[i & 3].y, s.y));
-        }
-    }
-    float2 sum = pair_add(pair_add(acc[0], acc[1]), pair_add(acc[2], acc[3]));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        sum = pair_add(sum, make_float2(__shfl_xor_sync(0xffffffffu, sum.x, o), __shfl_xor_sync(0xffffffffu, sum.y, o)));
-    return sum;
-}
-
-// The k largest of the warp's logits v[j] (expert lane + 32 j, -inf past E with
-// valid == false): lane i < k gets the i-th expert and its weight.
-__device__ void choose(float (&v)[RT_SLOTS], int E, int k, bool renorm, const bf16 *x, const bf16 *router, int lane,
-                       int &id, float &weight)
-{
-    uint32_t key[RT_SLOTS];
-    float big = 0.0f;
-#pragma unroll
-    for (int j = 0; j < RT_SLOTS; ++j) {
-        const bool there = lane + 32 * j < E;
-        key[j] = there ? sort_key(v[j]) : 0u;
-        if (there && fabsf(v[j]) < INFINITY) big = fmaxf(big, fabsf(v[j]));
-    }
-    big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
-    float lo[RT_SLOTS];
-#pragma unroll
-    for (int j = 0; j < RT_SLOTS; ++j) lo[j] = 0.0f;
-    float best = 0.0f;                                 // lane i: the i-th logit
-    id = 0;
-    bool settled = false;
-    for (;;) {
-        uint32_t taken = 0;                            // this lane's slots that are out
-        uint32_t near = 0;                             // this lane's slots that are close to a neighbour
-        float prev = 0.0f, kth = 0.0f;
-        int prev_at = 0;
-        bool close = false, border = false;
-        const int rounds = settled || k >= E ? k : k + 1;
-        for (int i = 0; i < rounds; ++i) {
-            uint32_t mk = 0;
-#pragma unroll
-            for (int j = 0; j < RT_SLOTS; ++j)
-                if (!(taken >> j & 1u) && lane + 32 * j < E) mk = max(mk, key[j]);
-            const uint32_t top = __reduce_max_sync(0xffffffffu, mk);
-            uint32_t ml = 0;                           // settled: the larger low part among equal high ones
-            if (settled) {
-#pragma unroll
-                for (int j = 0; j < RT_SLOTS; ++j)
-                    if (!(taken >> j & 1u) && lane + 32 * j < E && key[j] == top) ml = max(ml, sort_key(lo[j]));
-                ml = __reduce_max_sync(0xffffffffu, ml);
-            }
-            uint32_t at = 0xffffffffu;
-#pragma unroll
-            for (int j = RT_SLOTS - 1; j >= 0; --j)
-                if (!(taken >> j & 1u) && lane + 32 * j < E && key[j] == top && (!settled || sort_key(lo[j]) == ml))
-                    at = (uint32_t)(lane + 32 * j);
-            at = __reduce_min_sync(0xffffffffu, at);
-            float val = 0.0f;
-#pragma unroll
-            for (int j = 0; j < RT_SLOTS; ++j)
-                if ((int)at == lane + 32 * j) {
-                    val = v[j];
-                    taken |= 1u << j;
-                }
-            val = __shfl_sync(0xffffffffu, val, (int)(at & 31u));
-            if (i > 0 && prev - val <= 0x1p-13f * big) {
-                close = true;
-                border |= i == k;
-                if ((prev_at & 31) == lane) near |= 1u << (prev_at >> 5);
-                if ((int)(at & 31u) == lane) near |= 1u << (at >> 5);
-            }
-            prev = val;
-            prev_at = (int)at;
-            if (i < k) {
-                kth = val;
-                if (lane == i) {
-                    best = val;
-                    id = (int)at;
-                }
-            }
-        }
-        if (settled || !close || !(big > 0.0f)) break;
-        // in 48 bits: the neighbours among the first k, and where the last of them is
-        // close to the next, every expert that may be in its place
-        settled = true;
-        if (border) {
-#pragma unroll
-            for (int j = 0; j < RT_SLOTS; ++j)
-                if (lane + 32 * j < E && !(v[j] < kth - 0x1p-13f * big) && v[j] <= kth) near |= 1u << j;
-        }
-#pragma unroll
-        for (int j = 0; j < RT_SLOTS; ++j) {
-            uint32_t who = __ballot_sync(0xffffffffu, (near >> j & 1u) && fabsf(v[j]) < INFINITY);
-            while (who) {
-                const int from = __ffs(who) - 1;
-                who &= who - 1;
-                const float2 p = pair_dot(x, router + (size_t)(from + 32 * j) * LD, lane);
-                if (lane == from) {
-                    v[j] = p.x;
-                    key[j] = sort_key(p.x);
-                    lo[j] = p.y;
-                }
-            }
-        }
-    }
-    const float top = __shfl_sync(0xffffffffu, best, 0);
-    const float ex = lane < k ? expf(best - top) : 0.0f;
-    float sum = ex;
-    if (!renorm) {
-        sum = 0.0f;
-#pragma unroll
-        for (int j = 0; j < RT_SLOTS; ++j)
-            if (lane + 32 * j < E) sum += expf(v[j] - top);
-    }
-    weight = ex / warp_sum(sum);
-}
 
 __global__ void __launch_bounds__(RT_THREADS, 1)
     route_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mr, const bf16 *x,
@@ -297,11 +145,18 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
             float v[RT_SLOTS];
 #pragma unroll
             for (int j = 0; j < RT_SLOTS; ++j) v[j] = 0.0f;
-            for (int r = 0; r < splits; ++r) {
-                const uint32_t at = mapa_shared(base + (uint32_t)(t * PLD + lane) * 4u, (uint32_t)r);
+            for (int r0 = 0; r0 < splits; r0 += 4) {   // 32 loads in flight
+                float u[4][RT_SLOTS];
 #pragma unroll
-                for (int j = 0; j < RT_SLOTS; ++j)
-                    if (lane + 32 * j < E) v[j] += ld_cluster_f32(at + 128u * j);
+                for (int r = 0; r < 4; ++r) {
+                    const uint32_t at = mapa_shared(base + (uint32_t)(t * PLD + lane) * 4u, (uint32_t)(r0 + r));
+#pragma unroll
+                    for (int j = 0; j < RT_SLOTS; ++j) u[r][j] = lane + 32 * j < E ? ld_cluster_f32(at + 128u * j) : 0.0f;
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int j = 0; j < RT_SLOTS; ++j) v[j] += u[r][j];
             }
             int id;
             float w;

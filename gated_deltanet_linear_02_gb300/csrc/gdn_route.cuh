@@ -1,0 +1,228 @@
+// gdn_route.cuh -- a warp's choice of the top_k experts of one token, from logits
+// that it holds 8 a lane (gdn_route.cu for many tokens, gdn_moe_few.cu for few).
+#pragma once
+
+#include "gdn_layer.cuh"
+
+namespace gdn {
+
+constexpr int RT_MAX_E = GDN_MOE_MAX_EXPERTS;
+constexpr int RT_SLOTS = RT_MAX_E / 32;   // logits per lane
+
+// Order-preserving keys of floats; NaN is the smallest, -0 is +0.
+__device__ __forceinline__ uint32_t sort_key(float x)
+{
+    if (!(x == x)) return 0u;
+    const uint32_t u = __float_as_uint(x + 0.0f);
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+// a + b as (sum, error), both exact.
+__device__ __forceinline__ float2 two_sum(float a, float b)
+{
+    const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+    return make_float2(s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t)));
+}
+__device__ __forceinline__ float2 pair_add(float2 a, float2 b)
+{
+    const float2 s = two_sum(a.x, b.x);
+    const float e = __fadd_rn(s.y, __fadd_rn(a.y, b.y)), h = __fadd_rn(s.x, e);
+    return make_float2(h, __fsub_rn(e, __fsub_rn(h, s.x)));
+}
+
+// The logit of one expert as a pair of fp32, the same in every lane. Four running
+// sums, each with the sum of its rounding errors beside it: one addition per product
+// on the critical path.
+static __device__ __noinline__ float2 pair_dot(const bf16 *x, const bf16 *w, int lane)
+{
+    float2 acc[4] = {};
+    uint4 xs[LD / 256], ws[LD / 256];                  // all loads in flight together
+#pragma unroll
+    for (int c = 0; c < LD / 256; ++c) {
+        ws[c] = *reinterpret_cast<const uint4 *>(w + c * 256 + lane * 8);
+        xs[c] = *reinterpret_cast<const uint4 *>(x + c * 256 + lane * 8);
+    }
+#pragma unroll
+    for (int c = 0; c < LD / 256; ++c) {
+        float a[8], b[8];
+        unpack8(xs[c], a);
+        unpack8(ws[c], b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float2 s = two_sum(acc[i & 3].x, __fmul_rn(a[i], b[i]));
+            acc[i & 3] = make_float2(s.x, __fadd_rn(acc[i & 3].y, s.y));
+        }
+    }
+    float2 sum = pair_add(pair_add(acc[0], acc[1]), pair_add(acc[2], acc[3]));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        sum = pair_add(sum, make_float2(__shfl_xor_sync(0xffffffffu, sum.x, o), __shfl_xor_sync(0xffffffffu, sum.y, o)));
+    return sum;
+}
+
+// The same choice as below for tokens with near ties: neighbours are settled.
+static __device__ __noinline__ void choose_settled(const float *logits, int E, int k, bool renorm, const bf16 *x, const bf16 *router, int lane,
+                       int &id, float &weight)
+{
+    uint32_t key[RT_SLOTS];
+    float v[RT_SLOTS], big = 0.0f;
+#pragma unroll
+    for (int j = 0; j < RT_SLOTS; ++j) v[j] = logits[j];
+#pragma unroll
+    for (int j = 0; j < RT_SLOTS; ++j) {
+        const bool there = lane + 32 * j < E;
+        key[j] = there ? sort_key(v[j]) : 0u;
+        if (there && fabsf(v[j]) < INFINITY) big = fmaxf(big, fabsf(v[j]));
+    }
+    big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
+    float lo[RT_SLOTS];
+#pragma unroll
+    for (int j = 0; j < RT_SLOTS; ++j) lo[j] = 0.0f;
+    float best = 0.0f;                                 // lane i: the i-th logit
+    id = 0;
+    bool settled = false;
+    for (;;) {
+        uint32_t taken = 0;                            // this lane's slots that are out
+        uint32_t near = 0;                             // this lane's slots that are close to a neighbour
+        float prev = 0.0f, kth = 0.0f;
+        int prev_at = 0;
+        bool close = false, border = false;
+        const int rounds = settled || k >= E ? k : k + 1;
+        for (int i = 0; i < rounds; ++i) {
+            uint32_t mk = 0;
+#pragma unroll
+            for (int j = 0; j < RT_SLOTS; ++j)
+                if (!(taken >> j & 1u) && lane + 32 * j < E) mk = max(mk, key[j]);
+            const uint32_t top = __reduce_max_sync(0xffffffffu, mk);
+            uint32_t ml = 0;                           // settled: the larger low part among equal high ones
+            if (settled) {
+#pragma unroll
+                for (int j = 0; j < RT_SLOTS; ++j)
+                    if (!(taken >> j & 1u) && lane + 32 * j < E && key[j] == top) ml = max(ml, sort_key(lo[j]));
+                ml = __reduce_max_sync(0xffffffffu, ml);
+            }
+            uint32_t at = 0xffffffffu;
+#pragma unroll
+            for (int j = RT_SLOTS - 1; j >= 0; --j)
+                if (!(taken >> j & 1u) && lane + 32 * j < E && key[j] == top && (!settled || sort_key(lo[j]) == ml))
+                    at = (uint32_t)(lane + 32 * j);
+            at = __reduce_min_sync(0xffffffffu, at);
+            float val = 0.0f;
+#pragma unroll
+            for (int j = 0; j < RT_SLOTS; ++j)
+                if ((int)at == lane + 32 * j) {
+                    val = v[j];
+                    taken |= 1u << j;
+                }
+            val = __shfl_sync(0xffffffffu, val, (int)(at & 31u));
+            if (i > 0 && prev - val <= 0x1p-13f * big) {
+                close = true;
+                border |= i == k;
+                if ((prev_at & 31) == lane) near |= 1u << (prev_at >> 5);
+                if ((int)(at & 31u) == lane) near |= 1u << (at >> 5);
+            }
+            prev = val;
+            prev_at = (int)at;
+            if (i < k) {
+                kth = val;
+                if (lane == i) {
+                    best = val;
+                    id = (int)at;
+                }
+            }
+        }
+        if (settled || !close || !(big > 0.0f)) break;
+        // in 48 bits: the neighbours among the first k, and where the last of them is
+        // close to the next, every expert that may be in its place
+        settled = true;
+        if (border) {
+#pragma unroll
+            for (int j = 0; j < RT_SLOTS; ++j)
+                if (lane + 32 * j < E && !(v[j] < kth - 0x1p-13f * big) && v[j] <= kth) near |= 1u << j;
+        }
+#pragma unroll
+        for (int j = 0; j < RT_SLOTS; ++j) {
+            uint32_t who = __ballot_sync(0xffffffffu, (near >> j & 1u) && fabsf(v[j]) < INFINITY);
+            while (who) {
+                const int from = __ffs(who) - 1;
+                who &= who - 1;
+                const float2 p = pair_dot(x, router + (size_t)(from + 32 * j) * LD, lane);
+                if (lane == from) {
+                    v[j] = p.x;
+                    key[j] = sort_key(p.x);
+                    lo[j] = p.y;
+                }
+            }
+        }
+    }
+    const float top = __shfl_sync(0xffffffffu, best, 0);
+    const float ex = lane < k ? expf(best - top) : 0.0f;
+    float sum = ex;
+    if (!renorm) {
+        sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < RT_SLOTS; ++j)
+            if (lane + 32 * j < E) sum += expf(v[j] - top);
+    }
+    weight = ex / warp_sum(sum);
+}
+
+// The k largest of the warp's logits v[j] (expert lane + 32 j; whatever past E):
+// lane i < k gets the i-th expert and its weight.
+__device__ __forceinline__ void choose(const float (&v)[RT_SLOTS], int E, int k, bool renorm, const bf16 *x,
+                                       const bf16 *router, int lane, int &id, float &weight)
+{
+    uint32_t key[RT_SLOTS];
+    float big = 0.0f;
+#pragma unroll
+    for (int j = 0; j < RT_SLOTS; ++j) {
+        const bool there = lane + 32 * j < E;
+        key[j] = there ? sort_key(v[j]) : 0u;
+        if (there && fabsf(v[j]) < INFINITY) big = fmaxf(big, fabsf(v[j]));
+    }
+    big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
+    // the largest k and the one behind them; a lane offers the best that it has left
+    float best = 0.0f, prev = 0.0f;
+    bool close = false;
+    id = 0;
+    uint32_t left = 0;                                 // this lane's slots below E
+#pragma unroll
+    for (int j = 0; j < RT_SLOTS; ++j) left |= (uint32_t)(lane + 32 * j < E) << j;
+    const int rounds = k < E ? k + 1 : k;
+#pragma unroll 1
+    for (int i = 0; i < rounds; ++i) {
+        uint32_t mk = 0, mj = 0;
+#pragma unroll
+        for (int j = RT_SLOTS - 1; j >= 0; --j)
+            if ((left >> j & 1u) && key[j] >= mk) {
+                mk = key[j];
+                mj = (uint32_t)j;
+            }
+        const uint32_t top = __reduce_max_sync(0xffffffffu, mk);
+        const uint32_t at = __reduce_min_sync(0xffffffffu, left != 0u && mk == top ? (uint32_t)lane + 32u * mj : 0xffffffffu);
+        if ((at & 31u) == (uint32_t)lane) left &= ~(1u << (at >> 5));
+        const float val = top == 0u ? __uint_as_float(0x7fffffffu) : __uint_as_float((top & 0x80000000u) ? top ^ 0x80000000u : ~top);
+        close |= i > 0 && prev - val <= 0x1p-13f * big;
+        prev = val;
+        if (lane == i && i < k) {
+            best = val;
+            id = (int)at;
+        }
+    }
+    if (close && big > 0.0f) {
+        choose_settled(v, E, k, renorm, x, router, lane, id, weight);
+        return;
+    }
+    const float top = __shfl_sync(0xffffffffu, best, 0);
+    const float ex = lane < k ? expf(best - top) : 0.0f;
+    float sum = ex;
+    if (!renorm) {
+        sum = 0.0f;
+#pragma unroll 1
+        for (int j = 0; j < RT_SLOTS; ++j)
+            if (lane + 32 * j < E) sum += expf(v[j] - top);
+    }
+    weight = ex / warp_sum(sum);
+}
+
+}  // namespace gdn
