@@ -5,11 +5,16 @@
 // entry point of their own: steps 1 and 7 of section "Full-attention block"
 // (joint query and gate, key and value projection; attn_output with the residual).
 //
-// Tiles of 128 rows x BN columns (BN = 256, or 128 where the 256-wide tiles fill
-// at most half of the SMs) over a persistent grid: a TMA warp, an MMA warp, four epilogue
-// warps with the accumulators double-buffered in tensor memory. Where the tiles are
-// too few for the GPU, each tile's K range is split over the CTAs of a cluster,
-// whose partial tiles meet in distributed shared memory (always in the same order).
+// Two forms:
+//  - pair_kernel, for many rows: pairs of CTAs (cta_group::2) take 256 x BN tiles (BN = 256,
+//    or 128 where those are too few), each CTA 128 rows of x and half of the
+//    columns' weights, so that an operand byte in shared memory serves twice the products of
+//    a lone CTA (whose 128 x 256 tiles run into the shared-memory port at 1.45
+//    PFLOP/s). A TMA warp in each CTA, one issuing thread in the leader, eight epilogue
+//    warps in each, two accumulators in tensor memory.
+//  - linear_kernel, for few rows: tiles of 128 rows x 128 columns, each tile's K range
+//    split over the CTAs of a cluster, whose partial tiles meet in distributed
+//    shared memory (always in the same order).
 #include <mutex>
 
 #include "gdn_layer.cuh"
@@ -28,43 +33,215 @@ struct LinearOut {
     const void *residual;
     void *y;
     long long r_row, y_row;
-    int act;
 };
 
-__device__ __forceinline__ float apply_act(float v, int act)
+// exp and the division by special functions: a few 2^-23 of the result. Beyond fp32's
+// exponents the limits come out (silu and sigmoid of -100: 0).
+template <int ACT>
+__device__ __forceinline__ float apply_act(float v)
 {
-    if (act == GDN_ACT_SILU) return v / (1.0f + __expf(-v));
-    if (act == GDN_ACT_GELU) return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
-    if (act == GDN_ACT_SIGMOID) return 1.0f / (1.0f + __expf(-v));
+    if (ACT == GDN_ACT_SILU) return __fdividef(v, 1.0f + __expf(-v));
+    if (ACT == GDN_ACT_GELU) return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+    if (ACT == GDN_ACT_SIGMOID) return __fdividef(1.0f, 1.0f + __expf(-v));
     return v;
 }
 
-// Epilogue of 8 neighbouring columns of row m.
-template <typename TO>
-__device__ __forceinline__ void finish8(const LinearOut &o, int m, int n, float (&v)[8])
+// Epilogue of NC (8 or 32) neighbouring columns of row m, those below N; loads first.
+template <typename TO, int ACT, int NC>
+__device__ __forceinline__ void finish(const LinearOut &o, int m, int n, int N, float (&v)[NC])
 {
-    if (o.bias) {
-        float b[8];
-        ld8(o.bias + n, b);
+    float r[NC], b[NC];
+    if (o.residual)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += b[i];
-    }
-    if (o.act != GDN_ACT_NONE) {
+        for (int e = 0; e < NC; e += 8)
+            if (n + e < N) ld8(static_cast<const TO *>(o.residual) + (size_t)m * o.r_row + n + e, reinterpret_cast<float(&)[8]>(r[e]));
+    if (o.bias)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = apply_act(v[i], o.act);
-    }
-    if (o.residual) {
-        float r[8];
-        ld8(static_cast<const TO *>(o.residual) + (size_t)m * o.r_row + n, r);
+        for (int e = 0; e < NC; e += 8)
+            if (n + e < N) ld8(o.bias + n + e, reinterpret_cast<float(&)[8]>(b[e]));
+    if (o.bias)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += r[i];
-    }
-    st8(static_cast<TO *>(o.y) + (size_t)m * o.y_row + n, v);
+        for (int i = 0; i < NC; ++i) v[i] += b[i];
+    if (ACT != GDN_ACT_NONE)
+#pragma unroll
+        for (int i = 0; i < NC; ++i) v[i] = apply_act<ACT>(v[i]);
+    if (o.residual)
+#pragma unroll
+        for (int i = 0; i < NC; ++i) v[i] += r[i];
+#pragma unroll
+    for (int e = 0; e < NC; e += 8)
+        if (n + e < N) st8(static_cast<TO *>(o.y) + (size_t)m * o.y_row + n + e, reinterpret_cast<float(&)[8]>(v[e]));
 }
+
+// ------------------------------------------------------------------ many rows: pairs of CTAs
+
+// Forms of the tensor-core and copy instructions for a pair of CTAs.
+__device__ __forceinline__ void pair_tmem_alloc(uint32_t smem_dst, uint32_t ncols)
+{
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_dst), "r"(ncols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void pair_tmem_dealloc(uint32_t taddr, uint32_t ncols)
+{
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void pair_mma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                 ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+}
+// Arrives once on the barrier at this offset in both CTAs when the products so far are done.
+__device__ __forceinline__ void pair_commit(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                 ::"r"(bar), "h"((uint16_t)3) : "memory");
+}
+// A box into this CTA's shared memory, counted on a barrier of the leader.
+__device__ __forceinline__ void pair_load_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t leader_bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3}], [%4];"
+                 ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(leader_bar) : "memory");
+}
+// Only reads of tensor memory come before it, which tcgen05's own fences order: at
+// cluster scope it would wait for the epilogue's stores (105 -> 9x us per 4,096 x 9,216 x 2,048).
+__device__ __forceinline__ void arrive_cluster(uint32_t cluster_bar)
+{
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+constexpr int PR_THREADS = 320;           // TMA warp, MMA warp, eight epilogue warps
+
+template <int BN>
+struct PairSmem {
+    static constexpr int STAGES = BN == 256 ? 6 : 8;
+    static constexpr uint32_t STAGE_BYTES = LN_A_BYTES + BN / 2 * LN_BK * 2;
+    alignas(1024) unsigned char stage[STAGES][STAGE_BYTES];
+    alignas(8) uint64_t full[STAGES], empty[STAGES], acc_full[2], acc_empty[2];
+    int last_it[STAGES];
+    uint32_t tmem;
+    int abort;
+};
+
+template <typename TO, int BN, int ACT>
+__global__ void __launch_bounds__(PR_THREADS, 1)
+    pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw, const LinearOut out, int M,
+                int N, int K)
+{
+    using Smem = PairSmem<BN>;
+    constexpr int STAGES = Smem::STAGES;
+    extern __shared__ unsigned char smem_raw[];
+    Smem &sm = *reinterpret_cast<Smem *>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = (int)blockIdx.x & 1, pair = (int)blockIdx.x >> 1, pairs = (int)gridDim.x >> 1;
+    const int m_tiles = (M + 255) / 256, tiles = m_tiles * ((N + BN - 1) / BN), slices = (K + LN_BK - 1) / LN_BK;
+    const volatile int &aborted = sm.abort;
+
+    if (tid == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(smem_u32(&sm.full[s]), 1);
+            mbar_init(smem_u32(&sm.empty[s]), 1);
+            sm.last_it[s] = -1;
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&sm.acc_full[b]), 1);
+            mbar_init(smem_u32(&sm.acc_empty[b]), 16);             // the epilogue warps of both CTAs
+        }
+        sm.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) pair_tmem_alloc(smem_u32(&sm.tmem), 2 * BN);
+    tc::fence_before_sync();
+    __syncthreads();
+    cluster_sync_all();                                // both CTAs' barriers exist
+    tc::fence_after_sync();
+    const uint32_t tm = sm.tmem;
+    grid_dep_wait();
+    grid_dep_launch();
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int it = 0;
+            for (int t = pair; t < tiles && !aborted; t += pairs) {
+                const int mt = t % m_tiles, nt = t / m_tiles;
+                for (int kb = 0; kb < slices; ++kb, ++it) {
+                    const int s = it % STAGES;
+                    if (it >= STAGES && !mbar_wait_bounded(smem_u32(&sm.empty[s]), (uint32_t)((it / STAGES - 1) & 1))) sm.abort = 1;
+                    if (aborted) break;
+                    const uint32_t dst = smem_u32(sm.stage[s]), bar = mapa_shared(smem_u32(&sm.full[s]), 0);
+                    if (rank == 0) mbar_arrive_expect_tx(smem_u32(&sm.full[s]), 2 * Smem::STAGE_BYTES);
+                    pair_load_2d(dst, &mx, kb * LN_BK, mt * 256 + rank * 128, bar);
+                    pair_load_2d(dst + LN_A_BYTES, &mw, kb * LN_BK, nt * BN + rank * (BN / 2), bar);
+                    sm.last_it[s] = it;
+                }
+            }
+            // every copy of the pair has landed before its CTAs leave: the leader waits, its partner meets it below
+            if (rank == 0)
+                for (int s = 0; s < STAGES; ++s)
+                    if (sm.last_it[s] >= 0 && !mbar_wait_bounded(smem_u32(&sm.full[s]), (uint32_t)((sm.last_it[s] / STAGES) & 1)))
+                        sm.abort = 1;
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            const uint32_t idesc = tc::instr_desc(tc::FMT_BF16, 256, BN);
+            int it = 0, ti = 0;
+            for (int t = pair; t < tiles && !aborted; t += pairs, ++ti) {
+                const int ab = ti & 1;
+                if (ti >= 2 && !mbar_wait_bounded(smem_u32(&sm.acc_empty[ab]), (uint32_t)(((ti >> 1) - 1) & 1))) sm.abort = 1;
+                tc::fence_after_sync();
+                const uint32_t d = tm + (uint32_t)(BN * ab);
+                for (int kb = 0; kb < slices; ++kb, ++it) {
+                    const int s = it % STAGES;
+                    if (!mbar_wait_bounded(smem_u32(&sm.full[s]), (uint32_t)((it / STAGES) & 1))) sm.abort = 1;
+                    if (aborted) break;
+                    tc::fence_after_sync();
+                    const uint64_t ad = tc::sw128_desc(smem_u32(sm.stage[s]));
+                    const uint64_t bd = tc::sw128_desc(smem_u32(sm.stage[s]) + LN_A_BYTES);
+#pragma unroll
+                    for (int k = 0; k < LN_BK / 16; ++k)
+                        pair_mma(d, ad + 2u * k, bd + 2u * k, idesc, (kb > 0 || k > 0) ? 1u : 0u);
+                    pair_commit(smem_u32(&sm.empty[s]));
+                }
+                if (aborted) break;
+                pair_commit(smem_u32(&sm.acc_full[ab]));
+            }
+        }
+    } else {
+        const int q = warp & 3, half = (warp - 2) >> 2;                // lanes 32 q.., half of the columns
+        int ti = 0;
+        for (int t = pair; t < tiles; t += pairs, ++ti) {
+            const int ab = ti & 1, mt = t % m_tiles, nt = t / m_tiles;
+            if (!mbar_wait_bounded(smem_u32(&sm.acc_full[ab]), (uint32_t)((ti >> 1) & 1))) sm.abort = 1;
+            if (aborted) break;
+            __syncwarp();
+            tc::fence_after_sync();
+            const int m = mt * 256 + rank * 128 + 32 * q + lane;
+#pragma unroll 1
+            for (int c = half * (BN / 2); c < (half + 1) * (BN / 2); c += 32) {
+                float v[32];
+                tc::tmem_ld32(tc::tmem_addr(tm + (uint32_t)(BN * ab), 32 * q, c), v);
+                tc::wait_ld();
+                if (m < M) finish<TO, ACT, 32>(out, m, nt * BN + c, N, v);
+                __syncwarp();
+            }
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) arrive_cluster(mapa_shared(smem_u32(&sm.acc_empty[ab]), 0));
+        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    cluster_sync_all();                                // nobody's barriers or tensor memory are used any more
+    tc::fence_after_sync();
+    if (warp == 1) pair_tmem_dealloc(tm, 2 * BN);
+    if (tid == 0 && sm.abort) atomicExch(&g_linear_error, (unsigned int)GDN_ERR_TIMEOUT);
+}
+
+// ------------------------------------------------------------------ few rows: split K
 
 template <int BN>
 struct LinearSmem {
-    static constexpr int STAGES = BN == 256 ? 4 : 6;
+    static constexpr int STAGES = 6;
     static constexpr uint32_t STAGE_BYTES = LN_A_BYTES + BN * LN_BK * 2;
     static constexpr int PART_LD = BN + 4;
     static_assert(LN_BM * PART_LD * 4 <= STAGES * STAGE_BYTES, "a partial tile fits the stages");
@@ -75,7 +252,7 @@ struct LinearSmem {
     int abort;
 };
 
-template <typename TO, int BN>
+template <typename TO, int BN, int ACT>
 __global__ void __launch_bounds__(LN_THREADS, 1)
     linear_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw, const LinearOut out,
                   int M, int N, int K, int splits)
@@ -193,11 +370,7 @@ __global__ void __launch_bounds__(LN_THREADS, 1)
                 tc::tmem_ld32(tc::tmem_addr(tm + (uint32_t)(BN * ab), 32 * q, c), v);
                 tc::wait_ld();
                 const int n = nt * BN + c;
-                if (m < M) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (n + 8 * e < N) finish8<TO>(out, m, n + 8 * e, *reinterpret_cast<float(*)[8]>(v + 8 * e));
-                }
+                if (m < M) finish<TO, ACT, 32>(out, m, n, N, v);
             }
             tc::fence_before_sync();
             mbar_arrive(smem_u32(&sm.acc_empty[ab]));
@@ -230,7 +403,7 @@ __global__ void __launch_bounds__(LN_THREADS, 1)
                         v[0] += a[r].x; v[1] += a[r].y; v[2] += a[r].z; v[3] += a[r].w;
                         v[4] += b[r].x; v[5] += b[r].y; v[6] += b[r].z; v[7] += b[r].w;
                     }
-                finish8<TO>(out, m, n, v);
+                finish<TO, ACT, 8>(out, m, n, N, v);
             }
         }
         cluster_sync_all();                            // no CTA leaves while others read its partial
@@ -243,43 +416,51 @@ __global__ void __launch_bounds__(LN_THREADS, 1)
 
 // ------------------------------------------------------------------ launcher
 
-template <int BN>
-constexpr size_t linear_smem() { return sizeof(LinearSmem<BN>) + 1024; }
+template <int BN> constexpr size_t linear_smem() { return sizeof(LinearSmem<BN>) + 1024; }
+template <int BN> constexpr size_t pair_smem() { return sizeof(PairSmem<BN>) + 1024; }
 
-// Set-up once per device: shared-memory attributes, and how many clusters of 2,
-// 4 and 8 CTAs can be resident at once.
+static cudaLaunchConfig_t cluster_config(cudaLaunchAttribute (&attr)[2], int grid, int threads, size_t smem, int cluster,
+                                         cudaStream_t s)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cfg;
+}
+
+// Set-up once per device: shared-memory attributes, and how many clusters can be
+// resident at once.
 struct LinearDevice {
-    int max_clusters[2][3];   // [BN == 128]
+    int split_clusters[3];                // of 2, 4 and 8 CTAs of linear_kernel
+    int pairs;                            // of pair_kernel
 };
 
-template <int BN>
-static bool linear_setup(int (&max_clusters)[3])
+template <typename F> static bool max_clusters(F kernel, int threads, size_t smem, int cluster, int *n)
 {
-    if (cudaFuncSetAttribute(linear_kernel<float, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)linear_smem<BN>()) != cudaSuccess ||
-        cudaFuncSetAttribute(linear_kernel<bf16, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)linear_smem<BN>()) != cudaSuccess)
-        return false;
-    for (int k = 0; k < 3; ++k) {
-        cudaLaunchConfig_t q = {};
-        q.gridDim = dim3(2 << k);
-        q.blockDim = dim3(LN_THREADS);
-        q.dynamicSmemBytes = linear_smem<BN>();
-        cudaLaunchAttribute qa[1];
-        qa[0].id = cudaLaunchAttributeClusterDimension;
-        qa[0].val.clusterDim.x = 2u << k;
-        qa[0].val.clusterDim.y = 1;
-        qa[0].val.clusterDim.z = 1;
-        q.attrs = qa;
-        q.numAttrs = 1;
-        int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, linear_kernel<bf16, BN>, &q) != cudaSuccess) {
-            cudaGetLastError();                        // a refused query: never split this far
-            n = 0;
-        }
-        max_clusters[k] = n;
-    }
-    return true;
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = cluster_config(attr, cluster, threads, smem, cluster, nullptr);
+    if (cudaOccupancyMaxActiveClusters(n, kernel, &cfg) == cudaSuccess) return true;
+    cudaGetLastError();                                // a refused query
+    *n = 0;
+    return false;
+}
+
+template <typename TO, int ACT> static bool linear_attributes()
+{
+    const cudaFuncAttribute at = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    return cudaFuncSetAttribute(linear_kernel<TO, 128, ACT>, at, (int)linear_smem<128>()) == cudaSuccess &&
+           cudaFuncSetAttribute(pair_kernel<TO, 128, ACT>, at, (int)pair_smem<128>()) == cudaSuccess &&
+           cudaFuncSetAttribute(pair_kernel<TO, 256, ACT>, at, (int)pair_smem<256>()) == cudaSuccess;
 }
 
 static const LinearDevice *linear_device()
@@ -291,42 +472,76 @@ static const LinearDevice *linear_device()
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
     std::lock_guard<std::mutex> lock(mu);
     if (!ready[dev]) {
-        if (!linear_setup<256>(info[dev].max_clusters[0]) || !linear_setup<128>(info[dev].max_clusters[1])) return nullptr;
+        if (!linear_attributes<float, 0>() || !linear_attributes<float, 1>() || !linear_attributes<float, 2>() ||
+            !linear_attributes<float, 3>() || !linear_attributes<bf16, 0>() || !linear_attributes<bf16, 1>() ||
+            !linear_attributes<bf16, 2>() || !linear_attributes<bf16, 3>())
+            return nullptr;
+        for (int k = 0; k < 3; ++k)
+            max_clusters(linear_kernel<bf16, 128, 0>, LN_THREADS, linear_smem<128>(), 2 << k, &info[dev].split_clusters[k]);
+        if (!max_clusters(pair_kernel<bf16, 256, 0>, PR_THREADS, pair_smem<256>(), 2, &info[dev].pairs) || info[dev].pairs < 1)
+            return nullptr;
         ready[dev] = true;
     }
     return &info[dev];
 }
 
-template <int BN>
-static cudaError_t launch_bn(const void *x, long long x_row, const void *w, const LinearOut &out, int M, int N, int K,
-                             gdn_dtype out_dt, cudaStream_t s, int n_sm, const int (&max_clusters)[3])
+struct LinearCall {
+    const void *x, *w;
+    long long x_row;
+    int M, N, K;
+    LinearOut out;
+    cudaStream_t s;
+};
+
+template <typename TO, int BN, int ACT>
+static cudaError_t launch_pairs(const LinearCall &c, const LinearDevice &dev)
 {
     CUtensorMap mx, mw;
-    if (!make_bf16_strided_map(&mx, x, M, K, x_row, LN_BM) || !make_bf16_strided_map(&mw, w, N, K, K, BN))
+    if (!make_bf16_strided_map(&mx, c.x, c.M, c.K, c.x_row, LN_BM) || !make_bf16_strided_map(&mw, c.w, c.N, c.K, c.K, BN / 2))
         return cudaErrorInvalidValue;
-    const int n_work = ((M + LN_BM - 1) / LN_BM) * ((N + BN - 1) / BN), kb_all = (K + LN_BK - 1) / LN_BK;
+    const int tiles = ((c.M + 255) / 256) * ((c.N + BN - 1) / BN);
+    cudaLaunchAttribute attr[2];
+    const cudaLaunchConfig_t cfg =
+        cluster_config(attr, 2 * (tiles < dev.pairs ? tiles : dev.pairs), PR_THREADS, pair_smem<BN>(), 2, c.s);
+    return cudaLaunchKernelEx(&cfg, pair_kernel<TO, BN, ACT>, mx, mw, c.out, c.M, c.N, c.K);
+}
+
+template <typename TO, int ACT>
+static cudaError_t launch_split(const LinearCall &c, const LinearDevice &dev, int n_sm)
+{
+    CUtensorMap mx, mw;
+    if (!make_bf16_strided_map(&mx, c.x, c.M, c.K, c.x_row, LN_BM) || !make_bf16_strided_map(&mw, c.w, c.N, c.K, c.K, 128))
+        return cudaErrorInvalidValue;
+    const int n_work = ((c.M + LN_BM - 1) / LN_BM) * ((c.N + 127) / 128), kb_all = (c.K + LN_BK - 1) / LN_BK;
     // split K while the tiles fill at most half of the SMs, and only as far as all
     // clusters of that size can be resident at once
     int splits = 1;
     while (splits < 8 && n_work * splits * 2 <= n_sm && splits * 2 <= kb_all &&
-           max_clusters[splits == 1 ? 0 : splits == 2 ? 1 : 2] >= n_work)
+           dev.split_clusters[splits == 1 ? 0 : splits == 2 ? 1 : 2] >= n_work)
         splits *= 2;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(splits > 1 ? n_work * splits : (n_work < n_sm ? n_work : n_sm));
-    cfg.blockDim = dim3(LN_THREADS);
-    cfg.dynamicSmemBytes = linear_smem<BN>();
-    cfg.stream = s;
     cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)splits;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = splits > 1 ? 2 : 1;
-    return out_dt == GDN_F32 ? cudaLaunchKernelEx(&cfg, linear_kernel<float, BN>, mx, mw, out, M, N, K, splits)
-                             : cudaLaunchKernelEx(&cfg, linear_kernel<bf16, BN>, mx, mw, out, M, N, K, splits);
+    const cudaLaunchConfig_t cfg = cluster_config(attr, splits > 1 ? n_work * splits : (n_work < n_sm ? n_work : n_sm),
+                                                  LN_THREADS, linear_smem<128>(), splits, c.s);
+    return cudaLaunchKernelEx(&cfg, linear_kernel<TO, 128, ACT>, mx, mw, c.out, c.M, c.N, c.K, splits);
+}
+
+template <typename TO, int ACT>
+static cudaError_t launch_act(const LinearCall &c, const LinearDevice &dev, int n_sm)
+{
+    const long long m2 = (c.M + 255) / 256, t256 = m2 * ((c.N + 255) / 256), t128 = m2 * ((c.N + 127) / 128);
+    if (c.M <= 128 || 2 * t128 <= dev.pairs) return launch_split<TO, ACT>(c, dev, n_sm);
+    return 2 * t256 > dev.pairs ? launch_pairs<TO, 256, ACT>(c, dev) : launch_pairs<TO, 128, ACT>(c, dev);
+}
+
+template <typename TO>
+static cudaError_t launch_out(const LinearCall &c, const LinearDevice &dev, int n_sm, gdn_activation act)
+{
+    switch (act) {
+        case GDN_ACT_SILU: return launch_act<TO, GDN_ACT_SILU>(c, dev, n_sm);
+        case GDN_ACT_GELU: return launch_act<TO, GDN_ACT_GELU>(c, dev, n_sm);
+        case GDN_ACT_SIGMOID: return launch_act<TO, GDN_ACT_SIGMOID>(c, dev, n_sm);
+        default: return launch_act<TO, GDN_ACT_NONE>(c, dev, n_sm);
+    }
 }
 
 cudaError_t launch_linear(const void *x, long long x_row, const void *w, const float *bias, const void *residual,
@@ -336,10 +551,8 @@ cudaError_t launch_linear(const void *x, long long x_row, const void *w, const f
     const int n_sm = sm_count();
     const LinearDevice *dev = linear_device();
     if (n_sm <= 0 || !dev) return cudaErrorInvalidDevice;
-    const LinearOut o = {bias, residual, y, r_row, y_row, (int)act};
-    if ((long long)((M + LN_BM - 1) / LN_BM) * ((N + 255) / 256) * 2 <= n_sm)
-        return launch_bn<128>(x, x_row, w, o, M, N, K, out_dt, s, n_sm, dev->max_clusters[1]);
-    return launch_bn<256>(x, x_row, w, o, M, N, K, out_dt, s, n_sm, dev->max_clusters[0]);
+    const LinearCall c = {x, w, x_row, M, N, K, {bias, residual, y, r_row, y_row}, s};
+    return out_dt == GDN_F32 ? launch_out<float>(c, *dev, n_sm, act) : launch_out<bf16>(c, *dev, n_sm, act);
 }
 
 // Device address of this file's error word, for gdn_device_error (NULL if the lookup fails).
