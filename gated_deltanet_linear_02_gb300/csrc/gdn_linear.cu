@@ -239,28 +239,32 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
 
 // ------------------------------------------------------------------ few rows: split K
 
-template <int BN>
+constexpr int LN_BN = 128, LN_MAX_STAGES = 12, LN_PART_LD = LN_BN + 4;
+constexpr uint32_t LN_B_BYTES = LN_BN * LN_BK * 2;
+constexpr uint32_t LN_RING = 212 * 1024;  // stages, with 16 KB behind the last one that a short A tile's products may read
+static_assert(LN_BM * LN_PART_LD * 4 <= LN_RING, "a partial tile fits the stages");
+
 struct LinearSmem {
-    static constexpr int STAGES = 6;
-    static constexpr uint32_t STAGE_BYTES = LN_A_BYTES + BN * LN_BK * 2;
-    static constexpr int PART_LD = BN + 4;
-    static_assert(LN_BM * PART_LD * 4 <= STAGES * STAGE_BYTES, "a partial tile fits the stages");
-    alignas(1024) unsigned char stage[STAGES][STAGE_BYTES];
-    alignas(8) uint64_t full[STAGES], empty[STAGES], acc_full[2], acc_empty[2];
-    int last_it[STAGES];
+    alignas(1024) unsigned char ring[LN_RING];
+    alignas(8) uint64_t full[LN_MAX_STAGES], empty[LN_MAX_STAGES], acc_full[2], acc_empty[2];
+    int last_round[LN_MAX_STAGES];
     uint32_t tmem;
     int abort;
 };
 
-template <typename TO, int BN, int ACT>
+// a_rows: rows of x that a stage holds, 128, or with fewer rows in all those, rounded up
+// to 8. The products read 128 rows all the same; what the others hold does not
+// matter, as each row of the tile has its own sums. Shorter stages, more of them:
+// more weights in flight.
+template <typename TO, int ACT>
 __global__ void __launch_bounds__(LN_THREADS, 1)
     linear_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw, const LinearOut out,
-                  int M, int N, int K, int splits)
+                  int M, int N, int K, int splits, int a_rows, int STAGES)
 {
-    using Smem = LinearSmem<BN>;
-    constexpr int STAGES = Smem::STAGES, PLD = Smem::PART_LD;
+    constexpr int BN = LN_BN, PLD = LN_PART_LD;
     extern __shared__ unsigned char smem_raw[];
-    Smem &sm = *reinterpret_cast<Smem *>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
+    LinearSmem &sm = *reinterpret_cast<LinearSmem *>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
+    const uint32_t a_bytes = (uint32_t)a_rows * LN_BK * 2, stage_bytes = a_bytes + LN_B_BYTES, ring = smem_u32(sm.ring);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int n_tiles = (N + BN - 1) / BN;
     const bool split = splits > 1;
@@ -279,7 +283,7 @@ __global__ void __launch_bounds__(LN_THREADS, 1)
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(smem_u32(&sm.full[s]), 1);
             mbar_init(smem_u32(&sm.empty[s]), 1);
-            sm.last_it[s] = -1;
+            sm.last_round[s] = -1;
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_u32(&sm.acc_full[b]), 1);
@@ -297,47 +301,50 @@ __global__ void __launch_bounds__(LN_THREADS, 1)
 
     if (warp == 0) {
         if (lane == 0) {
-            int it = 0;
+            int s = 0, round = 0;                      // stage, and how often the ring has gone round
             for (int w = w0; w < wend && !aborted; w += wstep) {
                 const int mt = w / n_tiles, nt = w % n_tiles;
-                for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                    const int s = it % STAGES;
-                    if (it >= STAGES && !mbar_wait_bounded(smem_u32(&sm.empty[s]), (uint32_t)((it / STAGES - 1) & 1)))
-                        sm.abort = 1;
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (round > 0 && !mbar_wait_bounded(smem_u32(&sm.empty[s]), (uint32_t)((round - 1) & 1))) sm.abort = 1;
                     if (aborted) break;
-                    const uint32_t dst = smem_u32(sm.stage[s]), bar = smem_u32(&sm.full[s]);
-                    mbar_arrive_expect_tx(bar, Smem::STAGE_BYTES);
+                    const uint32_t dst = ring + s * stage_bytes, bar = smem_u32(&sm.full[s]);
+                    mbar_arrive_expect_tx(bar, stage_bytes);
+                    tma_load_2d(dst + a_bytes, &mw, kb * LN_BK, nt * BN, bar);
                     tma_load_2d(dst, &mx, kb * LN_BK, mt * LN_BM, bar);
-                    tma_load_2d(dst + LN_A_BYTES, &mw, kb * LN_BK, nt * BN, bar);
-                    sm.last_it[s] = it;
+                    sm.last_round[s] = round;
+                    if (++s == STAGES) {
+                        s = 0;
+                        ++round;
+                    }
                 }
             }
             if (aborted)                               // copies in flight land before the CTA exits
-                for (int s = 0; s < STAGES; ++s)
-                    if (sm.last_it[s] >= 0)
-                        mbar_wait_bounded(smem_u32(&sm.full[s]), (uint32_t)((sm.last_it[s] / STAGES) & 1));
+                for (s = 0; s < STAGES; ++s)
+                    if (sm.last_round[s] >= 0) mbar_wait_bounded(smem_u32(&sm.full[s]), (uint32_t)(sm.last_round[s] & 1));
         }
     } else if (warp == 1) {
         if (lane == 0) {
             const uint32_t idesc = tc::instr_desc(tc::FMT_BF16, LN_BM, BN);
-            int it = 0, ti = 0;
+            int s = 0, round = 0, ti = 0;
             for (int w = w0; w < wend && !aborted; w += wstep, ++ti) {
                 const int ab = ti & 1;
                 if (ti >= 2 && !mbar_wait_bounded(smem_u32(&sm.acc_empty[ab]), (uint32_t)(((ti >> 1) - 1) & 1)))
                     sm.abort = 1;
                 tc::fence_after_sync();
                 const uint32_t d = tm + (uint32_t)(BN * ab);
-                for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                    const int s = it % STAGES;
-                    if (!mbar_wait_bounded(smem_u32(&sm.full[s]), (uint32_t)((it / STAGES) & 1))) sm.abort = 1;
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!mbar_wait_bounded(smem_u32(&sm.full[s]), (uint32_t)(round & 1))) sm.abort = 1;
                     if (aborted) break;
                     tc::fence_after_sync();
-                    const uint64_t ad = tc::sw128_desc(smem_u32(sm.stage[s]));
-                    const uint64_t bd = tc::sw128_desc(smem_u32(sm.stage[s]) + LN_A_BYTES);
+                    const uint64_t ad = tc::sw128_desc(ring + s * stage_bytes), bd = tc::sw128_desc(ring + s * stage_bytes + a_bytes);
 #pragma unroll
                     for (int k = 0; k < LN_BK / 16; ++k)
                         tc::mma_f16(d, ad + 2u * k, bd + 2u * k, idesc, (kb > kb0 || k > 0) ? 1u : 0u);
                     tc::mma_commit(smem_u32(&sm.empty[s]));
+                    if (++s == STAGES) {
+                        s = 0;
+                        ++round;
+                    }
                 }
                 if (aborted) break;
                 tc::mma_commit(smem_u32(&sm.acc_full[ab]));
@@ -348,8 +355,9 @@ __global__ void __launch_bounds__(LN_THREADS, 1)
         if (split) {                                   // this CTA's fp32 partial tile into shared memory
             if (!mbar_wait_bounded(smem_u32(&sm.acc_full[0]), 0)) sm.abort = 1;
             tc::fence_after_sync();
-            float *p = reinterpret_cast<float *>(sm.stage[0]) + row * PLD;
-            for (int c = 0; c < BN; c += 32) {
+            float *p = reinterpret_cast<float *>(sm.ring) + row * PLD;
+            const bool some = (w0 / n_tiles) * LN_BM + 32 * q < M;     // of this warp's rows
+            for (int c = 0; c < BN && some; c += 32) {
                 float v[32];
                 tc::tmem_ld32(tc::tmem_addr(tm, 32 * q, c), v);
                 tc::wait_ld();
@@ -377,12 +385,12 @@ __global__ void __launch_bounds__(LN_THREADS, 1)
         }
     }
     if (split) {
-        // CTA r of the cluster writes rows [r 128/S, (r+1) 128/S) of the tile, each the sum of the S partials
+        // each CTA of the cluster writes an even share of the tile's rows, each the sum of the S partials
         cluster_sync_all();
         if (warp >= 2 && !aborted) {
-            const int rows = LN_BM / splits, r0 = part * rows;
-            const int mt = w0 / n_tiles, nt = w0 % n_tiles;
-            const uint32_t base = smem_u32(sm.stage[0]);
+            const int mt = w0 / n_tiles, nt = w0 % n_tiles, there = min(LN_BM, M - mt * LN_BM);
+            const int r0 = there * part / splits, rows = there * (part + 1) / splits - r0;
+            const uint32_t base = ring;
             for (int f = tid - 64; f < rows * (BN / 8); f += 128) {
                 const int rr = r0 + f / (BN / 8), col = 8 * (f % (BN / 8));
                 const int m = mt * LN_BM + rr, n = nt * BN + col;
@@ -416,7 +424,8 @@ __global__ void __launch_bounds__(LN_THREADS, 1)
 
 // ------------------------------------------------------------------ launcher
 
-template <int BN> constexpr size_t linear_smem() { return sizeof(LinearSmem<BN>) + 1024; }
+constexpr size_t LN_SMEM = sizeof(LinearSmem) + 1024;
+static_assert(LN_SMEM <= 232448, "one CTA per SM");
 template <int BN> constexpr size_t pair_smem() { return sizeof(PairSmem<BN>) + 1024; }
 
 static cudaLaunchConfig_t cluster_config(cudaLaunchAttribute (&attr)[2], int grid, int threads, size_t smem, int cluster,
@@ -458,7 +467,7 @@ template <typename F> static bool max_clusters(F kernel, int threads, size_t sme
 template <typename TO, int ACT> static bool linear_attributes()
 {
     const cudaFuncAttribute at = cudaFuncAttributeMaxDynamicSharedMemorySize;
-    return cudaFuncSetAttribute(linear_kernel<TO, 128, ACT>, at, (int)linear_smem<128>()) == cudaSuccess &&
+    return cudaFuncSetAttribute(linear_kernel<TO, ACT>, at, (int)LN_SMEM) == cudaSuccess &&
            cudaFuncSetAttribute(pair_kernel<TO, 128, ACT>, at, (int)pair_smem<128>()) == cudaSuccess &&
            cudaFuncSetAttribute(pair_kernel<TO, 256, ACT>, at, (int)pair_smem<256>()) == cudaSuccess;
 }
@@ -477,7 +486,7 @@ static const LinearDevice *linear_device()
             !linear_attributes<bf16, 2>() || !linear_attributes<bf16, 3>())
             return nullptr;
         for (int k = 0; k < 3; ++k)
-            max_clusters(linear_kernel<bf16, 128, 0>, LN_THREADS, linear_smem<128>(), 2 << k, &info[dev].split_clusters[k]);
+            max_clusters(linear_kernel<bf16, 0>, LN_THREADS, LN_SMEM, 2 << k, &info[dev].split_clusters[k]);
         if (!max_clusters(pair_kernel<bf16, 256, 0>, PR_THREADS, pair_smem<256>(), 2, &info[dev].pairs) || info[dev].pairs < 1)
             return nullptr;
         ready[dev] = true;
@@ -510,7 +519,9 @@ template <typename TO, int ACT>
 static cudaError_t launch_split(const LinearCall &c, const LinearDevice &dev, int n_sm)
 {
     CUtensorMap mx, mw;
-    if (!make_bf16_strided_map(&mx, c.x, c.M, c.K, c.x_row, LN_BM) || !make_bf16_strided_map(&mw, c.w, c.N, c.K, c.K, 128))
+    const int a_rows = c.M < LN_BM ? (c.M + 7) & ~7 : LN_BM;
+    const int fit = (int)((LN_RING - LN_A_BYTES) / ((uint32_t)a_rows * LN_BK * 2 + LN_B_BYTES)), stages = fit < LN_MAX_STAGES ? fit : LN_MAX_STAGES;
+    if (!make_bf16_strided_map(&mx, c.x, c.M, c.K, c.x_row, a_rows) || !make_bf16_strided_map(&mw, c.w, c.N, c.K, c.K, LN_BN))
         return cudaErrorInvalidValue;
     const int n_work = ((c.M + LN_BM - 1) / LN_BM) * ((c.N + 127) / 128), kb_all = (c.K + LN_BK - 1) / LN_BK;
     // split K while the tiles fill at most half of the SMs, and only as far as all
@@ -521,8 +532,8 @@ static cudaError_t launch_split(const LinearCall &c, const LinearDevice &dev, in
         splits *= 2;
     cudaLaunchAttribute attr[2];
     const cudaLaunchConfig_t cfg = cluster_config(attr, splits > 1 ? n_work * splits : (n_work < n_sm ? n_work : n_sm),
-                                                  LN_THREADS, linear_smem<128>(), splits, c.s);
-    return cudaLaunchKernelEx(&cfg, linear_kernel<TO, 128, ACT>, mx, mw, c.out, c.M, c.N, c.K, splits);
+                                                  LN_THREADS, LN_SMEM, splits, c.s);
+    return cudaLaunchKernelEx(&cfg, linear_kernel<TO, ACT>, mx, mw, c.out, c.M, c.N, c.K, splits, a_rows, stages);
 }
 
 template <typename TO, int ACT>

@@ -60,7 +60,7 @@ static __device__ __noinline__ float2 pair_dot(const bf16 *x, const bf16 *w, int
     return sum;
 }
 
-// The same choice as below for tokens with near ties: neighbours are settled.
+// The same choice as below for tokens where dozens of logits are near one another.
 static __device__ __noinline__ void choose_settled(const float *logits, int E, int k, bool renorm, const bf16 *x, const bf16 *router, int lane,
                        int &id, float &weight)
 {
@@ -181,16 +181,19 @@ __device__ __forceinline__ void choose(const float (&v)[RT_SLOTS], int E, int k,
         if (there && fabsf(v[j]) < INFINITY) big = fmaxf(big, fabsf(v[j]));
     }
     big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
-    // the largest k and the one behind them; a lane offers the best that it has left
-    float best = 0.0f, prev = 0.0f;
+    // the largest k, and behind them those that are close to the last of them; a lane
+    // offers the best that it has left, lane i keeps the i-th
+    const float tie = 0x1p-13f * big;
+    float best = 0.0f, prev = 0.0f, kth = -INFINITY;
     bool close = false;
     id = 0;
     uint32_t left = 0;                                 // this lane's slots below E
 #pragma unroll
     for (int j = 0; j < RT_SLOTS; ++j) left |= (uint32_t)(lane + 32 * j < E) << j;
-    const int rounds = k < E ? k + 1 : k;
+    const int most = min(E, 32);
+    int n = 0;
 #pragma unroll 1
-    for (int i = 0; i < rounds; ++i) {
+    for (; n < most; ++n) {
         uint32_t mk = 0, mj = 0;
 #pragma unroll
         for (int j = RT_SLOTS - 1; j >= 0; --j)
@@ -200,18 +203,49 @@ __device__ __forceinline__ void choose(const float (&v)[RT_SLOTS], int E, int k,
             }
         const uint32_t top = __reduce_max_sync(0xffffffffu, mk);
         const uint32_t at = __reduce_min_sync(0xffffffffu, left != 0u && mk == top ? (uint32_t)lane + 32u * mj : 0xffffffffu);
-        if ((at & 31u) == (uint32_t)lane) left &= ~(1u << (at >> 5));
         const float val = top == 0u ? __uint_as_float(0x7fffffffu) : __uint_as_float((top & 0x80000000u) ? top ^ 0x80000000u : ~top);
-        close |= i > 0 && prev - val <= 0x1p-13f * big;
+        if (n >= k && !(kth - val <= tie)) break;
+        if ((at & 31u) == (uint32_t)lane) left &= ~(1u << (at >> 5));
+        close |= n > 0 && prev - val <= tie;
         prev = val;
-        if (lane == i && i < k) {
+        if (n < k) kth = val;
+        if (lane == n) {
             best = val;
             id = (int)at;
         }
     }
     if (close && big > 0.0f) {
-        choose_settled(v, E, k, renorm, x, router, lane, id, weight);
-        return;
+        if (n == 32 && E > 32) {                       // more neighbours than lanes
+            choose_settled(v, E, k, renorm, x, router, lane, id, weight);
+            return;
+        }
+        // in 48 bits those that are close to a neighbour, then every one's place among the n
+        const float up = __shfl_up_sync(0xffffffffu, best, 1), down = __shfl_down_sync(0xffffffffu, best, 1);
+        const bool near = lane < n && fabsf(best) < INFINITY && ((lane > 0 && up - best <= tie) || (lane + 1 < n && best - down <= tie));
+        float low = 0.0f;
+        for (uint32_t who = __ballot_sync(0xffffffffu, near); who; who &= who - 1) {
+            const int from = __ffs(who) - 1;
+            const float2 p = pair_dot(x, router + (size_t)__shfl_sync(0xffffffffu, id, from) * LD, lane);
+            if (lane == from) {
+                best = p.x;
+                low = p.y;
+            }
+        }
+        const uint32_t mine = sort_key(best);
+        int place = 0;
+#pragma unroll 1
+        for (int j = 0; j < n; ++j) {
+            const uint32_t kj = __shfl_sync(0xffffffffu, mine, j);
+            const float lj = __shfl_sync(0xffffffffu, low, j);
+            const int ej = __shfl_sync(0xffffffffu, id, j);
+            place += kj > mine || (kj == mine && (lj > low || (lj == low && ej < id)));
+        }
+        int from = 0;
+#pragma unroll 1
+        for (int j = 0; j < n; ++j)
+            if (__shfl_sync(0xffffffffu, place, j) == lane) from = j;
+        best = __shfl_sync(0xffffffffu, best, from);
+        id = __shfl_sync(0xffffffffu, id, from);
     }
     const float top = __shfl_sync(0xffffffffu, best, 0);
     const float ex = lane < k ? expf(best - top) : 0.0f;
