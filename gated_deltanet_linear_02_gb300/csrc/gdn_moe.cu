@@ -74,7 +74,10 @@ struct ExpertSmem {
     // 16-byte asynchronous copies. (A gather of four rows holds the TMA unit as long as a
     // whole weight tile: 32 of them a stage took 4,096 tokens 504 us.)
     static constexpr bool LOADERS = NT > 32;
-    static constexpr int THREADS = LOADERS ? 320 : 192;
+    // Epilogue: four warps, or eight that take every other 16 tokens (four took as long
+    // for a down unit as its copies).
+    static constexpr int EPI = LOADERS ? 2 : 1;
+    static constexpr int THREADS = LOADERS ? 448 : 192;
     static constexpr int H_BOX = NT <= 32 ? 16 : 64;      // rows of h per copy
     alignas(1024) unsigned char stage[STAGES][STAGE_BYTES];
     alignas(8) uint64_t full[STAGES], empty[STAGES], acc_full[2], acc_empty[2], info_full[EX_INFO], info_empty[EX_INFO];
@@ -127,11 +130,11 @@ __global__ void __launch_bounds__(ExpertSmem<NT>::THREADS, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_u32(&sm.acc_full[b]), 1);
-            mbar_init(smem_u32(&sm.acc_empty[b]), 4);
+            mbar_init(smem_u32(&sm.acc_empty[b]), 4 * Smem::EPI);
         }
         for (int i = 0; i < EX_INFO; ++i) {
             mbar_init(smem_u32(&sm.info_full[i]), 1);
-            mbar_init(smem_u32(&sm.info_empty[i]), Smem::LOADERS ? 9 : 5);
+            mbar_init(smem_u32(&sm.info_empty[i]), Smem::LOADERS ? 13 : 5);   // warp 1, loaders, epilogue
         }
         sm.abort = 0;
         fence_mbar_init();
@@ -174,6 +177,7 @@ __global__ void __launch_bounds__(ExpertSmem<NT>::THREADS, 1)
         // ---- units and copies
         const int tiles = sm.tile0[NE], units1 = tiles * FU, units = units1 + tiles * EX_DOWN_UNITS;
         int it = 0, next = 0;
+        const uint64_t once = evict_first_policy();    // weights pass through; rows of x and h are read again
         if (lane == 0) next = atomicAdd(ws.ticket, 1);
         for (int ui = 0;; ++ui) {
             const int u = __shfl_sync(0xffffffffu, next, 0);
@@ -230,9 +234,9 @@ __global__ void __launch_bounds__(ExpertSmem<NT>::THREADS, 1)
                 ya = (sh ? 0 : e * LD) + un.rows_at * 256;
                 yb = ya + 128;
                 slices = F / EX_BK;
-                if (lane == 0) {                       // the tile's h: four warps of each gate/up unit report it
+                if (lane == 0) {                       // the tile's h: every epilogue warp of each gate/up unit reports it
                     const uint64_t since = global_timer_ns();
-                    while (load_acquire(ws.ready + un.tile) < 4 * FU) {
+                    while (load_acquire(ws.ready + un.tile) < 4 * Smem::EPI * FU) {
                         __nanosleep(100);
                         if (global_timer_ns() - since > WAIT_LIMIT_NS) {
                             sm.abort = 1;
@@ -252,8 +256,8 @@ __global__ void __launch_bounds__(ExpertSmem<NT>::THREADS, 1)
                 const uint32_t dst = smem_u32(sm.stage[s]), bar = smem_u32(&sm.full[s]), b0 = dst + 2 * EX_A_BYTES;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(bar, bytes);
-                    tma_load_2d(dst, ma, kb * EX_BK, ya, bar);
-                    tma_load_2d(dst + EX_A_BYTES, mb, kb * EX_BK, yb, bar);
+                    tma_load_2d_hint(dst, ma, kb * EX_BK, ya, bar, once);
+                    tma_load_2d_hint(dst + EX_A_BYTES, mb, kb * EX_BK, yb, bar, once);
                     sm.last_it[s] = it;
                 }
                 __syncwarp();
@@ -303,7 +307,7 @@ __global__ void __launch_bounds__(ExpertSmem<NT>::THREADS, 1)
                 tc::mma_commit(smem_u32(&sm.acc_full[ab]));
             }
         }
-    } else if (warp >= 6) {
+    } else if (warp >= 6 && warp < 10) {
         // ---- token rows (LOADERS): 8 lanes bring the 128 bytes of a row, four rows at a time. A
         //      stage is reported two slices later, when its copies have landed.
         constexpr int LAG = 2;
@@ -354,7 +358,7 @@ __global__ void __launch_bounds__(ExpertSmem<NT>::THREADS, 1)
         for (int i = max(0, it - LAG); i < it && !aborted; ++i) report(i);
     } else {
         // ---- epilogue: thread = weight row (tensor-memory lane), columns = tokens
-        const int q = warp & 3, row = 32 * q + lane;
+        const int q = warp & 3, row = 32 * q + lane, c0 = warp >= 10 ? 16 : 0;
         for (int ui = 0; !aborted; ++ui) {
             const int slot = ui % EX_INFO, ab = ui & 1;
             if (!mbar_wait_sleep(smem_u32(&sm.info_full[slot]), (uint32_t)((ui / EX_INFO) & 1))) sm.abort = 1;
@@ -368,7 +372,7 @@ __global__ void __launch_bounds__(ExpertSmem<NT>::THREADS, 1)
             __syncwarp();
             tc::fence_after_sync();
             const uint32_t d0 = tc::tmem_addr(tm, 32 * q, 2 * NT * ab);
-            for (int c = 0; c < un.n; c += 16) {
+            for (int c = c0; c < un.n; c += 16 * Smem::EPI) {
                 float a[16], b[16];
                 tc::tmem_ld16(d0 + (uint32_t)c, a);
                 tc::tmem_ld16(d0 + (uint32_t)(NT + c), b);
@@ -378,6 +382,27 @@ __global__ void __launch_bounds__(ExpertSmem<NT>::THREADS, 1)
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
                         if (c + i < un.n) p[(size_t)i * F] = from_f<bf16>(silu_fast(a[i]) * b[i]);
+                } else if (NT > 32) {
+                    // y in 16 bits: fp16 scaled by the largest exponent of the token's 32 rows in
+                    // this warp, off by at most 2^-12 of that largest value. (bf16 would add as
+                    // much error as the output's own rounding; fp32 costs 2 x 150 MB at 4,096 tokens.)
+                    unsigned char keep = 0;            // lane i: scale of column i, lane 16 + i: of its other block
+                    __half *p = ws.y16 + (size_t)(un.row0 + c) * LD + un.rows_at * 256 + row;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int ea = (int)(__reduce_max_sync(0xffffffffu, __float_as_uint(a[i]) & 0x7fffffffu) >> 23);
+                        const int eb = (int)(__reduce_max_sync(0xffffffffu, __float_as_uint(b[i]) & 0x7fffffffu) >> 23);
+                        const int sa = ea == 255 ? 141 : max(ea, 20), sb = eb == 255 ? 141 : max(eb, 20);
+                        if (lane == i) keep = (unsigned char)sa;
+                        if (lane == 16 + i) keep = (unsigned char)sb;
+                        if (c + i < un.n) {
+                            p[(size_t)i * LD] = __float2half_rn(a[i] * __uint_as_float((uint32_t)(268 - sa) << 23));
+                            p[(size_t)i * LD + 128] = __float2half_rn(b[i] * __uint_as_float((uint32_t)(268 - sb) << 23));
+                        }
+                    }
+                    const int i = lane & 15;
+                    if (c + i < un.n)
+                        ws.scale[(size_t)(un.row0 + c + i) * (LD / 32) + un.rows_at * 8 + (lane >> 4) * 4 + q] = keep;
                 } else {
                     float *p = ws.y + (size_t)(un.row0 + c) * LD + un.rows_at * 256 + row;
 #pragma unroll
@@ -410,7 +435,39 @@ __global__ void __launch_bounds__(ExpertSmem<NT>::THREADS, 1)
 
 constexpr int CB_THREADS = LD / 8;
 
-template <typename TO>
+// 8 neighbouring outputs of a pair, as they are held.
+template <bool Y16> struct RawY;
+template <> struct RawY<false> {
+    float v[8];
+    __device__ __forceinline__ void load(const MoeWs &ws, size_t row, int c) { ld8(ws.y + row * LD + c, v); }
+    __device__ __forceinline__ void get(float (&y)[8]) const
+    {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = v[i];
+    }
+};
+template <> struct RawY<true> {
+    uint4 u;
+    unsigned char scale;
+    __device__ __forceinline__ void load(const MoeWs &ws, size_t row, int c)
+    {
+        u = *reinterpret_cast<const uint4 *>(ws.y16 + row * LD + c);
+        scale = ws.scale[row * (LD / 32) + c / 32];
+    }
+    __device__ __forceinline__ void get(float (&y)[8]) const
+    {
+        const float f = __uint_as_float((uint32_t)(scale - 14) << 23);             // 2^(scale - 141)
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+            y[2 * i] = v.x * f;
+            y[2 * i + 1] = v.y * f;
+        }
+    }
+};
+
+template <typename TO, bool Y16>
 __global__ void __launch_bounds__(CB_THREADS)
     moe_combine_kernel(const bf16 *x, long long x_row, const bf16 *sh_router, const int32_t *ids, const float *weights,
                        const void *residual, void *out, int M, int k, int shared, MoeWs ws)
@@ -426,9 +483,11 @@ __global__ void __launch_bounds__(CB_THREADS)
         row[tid] = r < 0 ? -1 : ws.offset[ids[m * k + tid]] + r;
         weight[tid] = weights[m * k + tid];
     }
-    float acc[8] = {}, ys[8];
+    constexpr int AHEAD = Y16 ? 8 : 4;
+    float acc[8] = {};
+    RawY<Y16> ys;
     if (residual) ld8(static_cast<const TO *>(residual) + m * LD + c, acc);
-    if (shared) ld8(ws.y + ((size_t)M * k + m) * LD + c, ys);
+    if (shared) ys.load(ws, (size_t)M * k + m, c);
     float s = 0.0f;
     if (sh_router) {                                   // the shared expert's gate
         float a[8], b[8];
@@ -441,17 +500,19 @@ __global__ void __launch_bounds__(CB_THREADS)
     }
     __syncthreads();
     float sum[8] = {};
-    for (int j = 0; j < k; j += 4) {                   // four rows in flight, added in slot order
-        float y[4][8];
+    for (int j = 0; j < k; j += AHEAD) {               // rows in flight, added in slot order
+        RawY<Y16> y[AHEAD];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (j + i < k && row[j + i] >= 0) ld8(ws.y + (size_t)row[j + i] * LD + c, y[i]);
+        for (int i = 0; i < AHEAD; ++i)
+            if (j + i < k && row[j + i] >= 0) y[i].load(ws, (size_t)row[j + i], c);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < AHEAD; ++i)
             if (j + i < k && row[j + i] >= 0) {
+                float v[8];
+                y[i].get(v);
                 const float w = weight[j + i];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) sum[e] = fmaf(w, y[i][e], sum[e]);
+                for (int e = 0; e < 8; ++e) sum[e] = fmaf(w, v[e], sum[e]);
             }
     }
     if (shared) {
@@ -462,8 +523,10 @@ __global__ void __launch_bounds__(CB_THREADS)
             for (int i = 0; i < CB_THREADS / 32; ++i) s += part[i];
             gate = 1.0f / (1.0f + expf(-s));
         }
+        float y[8];
+        ys.get(y);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum[i] = fmaf(gate, ys[i], sum[i]);
+        for (int i = 0; i < 8; ++i) sum[i] = fmaf(gate, y[i], sum[i]);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] += sum[i];
@@ -471,8 +534,6 @@ __global__ void __launch_bounds__(CB_THREADS)
 }
 
 // ------------------------------------------------------------------ launcher
-
-constexpr int MOE_FEW = 512;              // tokens up to which tiles hold 32 of them
 
 static bool moe_setup()
 {
@@ -503,6 +564,7 @@ cudaError_t launch_moe(const gdn_moe_params *p, const void *x, long long x_row, 
     const bool shared = p->sh_gate != nullptr;
     const size_t out_row = (size_t)LD * (out_dt == GDN_F32 ? 4 : 2);
     MoeWs ws = moe_workspace(p, M, workspace);
+    const bool small = M <= MOE_SMALL;                 // for the last window too: the workspace is laid out for it
     if (M <= MOE_FEW_TOKENS) return launch_moe_few(p, x, x_row, residual, out, M, ids, weights, ws, out_dt, s);
     ExpertMaps maps;
     if (!make_bf16_strided_map(&maps.gate, p->gate, (long long)E * F, LD, LD, 128) ||
@@ -520,7 +582,7 @@ cudaError_t launch_moe(const gdn_moe_params *p, const void *x, long long x_row, 
         const int32_t *idw = ids ? ids + (size_t)m0 * k : ws.ids;
         const float *ww = ids ? weights + (size_t)m0 * k : ws.weights;
         const size_t rows = (size_t)W * (k + (shared ? 1 : 0));
-        if (!make_bf16_strided_map(&maps.x, xw, W, LD, x_row, 1) || !make_bf16_strided_map(&maps.h, ws.h, rows, F, F, W <= MOE_FEW ? ExpertSmem<32>::H_BOX : ExpertSmem<MOE_TILE>::H_BOX))
+        if (!make_bf16_strided_map(&maps.x, xw, W, LD, x_row, 1) || !make_bf16_strided_map(&maps.h, ws.h, rows, F, F, small ? ExpertSmem<32>::H_BOX : ExpertSmem<MOE_TILE>::H_BOX))
             return cudaErrorInvalidValue;
         const int n_state = (int)ws.state_ints;
         cudaError_t e = launch_pdl(moe_zero_kernel, dim3((n_state + 1023) / 1024), dim3(256), 0, s, ws.state, n_state);
@@ -528,7 +590,7 @@ cudaError_t launch_moe(const gdn_moe_params *p, const void *x, long long x_row, 
         e = ids ? launch_pdl(moe_place_kernel, dim3((W * k + 255) / 256), dim3(256), 0, s, idw, W * k, k, E, ws.places)
                 : launch_route(p, xw, x_row, W, ws.ids, ws.weights, ws.places, s);
         if (e != cudaSuccess) return e;
-        e = W <= MOE_FEW ? launch_pdl(moe_experts_kernel<32>, dim3(n_sm), dim3(ExpertSmem<32>::THREADS),
+        e = small ? launch_pdl(moe_experts_kernel<32>, dim3(n_sm), dim3(ExpertSmem<32>::THREADS),
                                       sizeof(ExpertSmem<32>) + 1024, s, maps, xw, x_row, W, E, F, k, (int)shared, ws)
                          : launch_pdl(moe_experts_kernel<MOE_TILE>, dim3(n_sm), dim3(ExpertSmem<MOE_TILE>::THREADS),
                                       sizeof(ExpertSmem<MOE_TILE>) + 1024, s, maps, xw, x_row, W, E, F, k, (int)shared, ws);
@@ -536,10 +598,9 @@ cudaError_t launch_moe(const gdn_moe_params *p, const void *x, long long x_row, 
         const void *rw = residual ? static_cast<const char *>(residual) + m0 * out_row : nullptr;
         void *ow = static_cast<char *>(out) + m0 * out_row;
         const bf16 *shr = static_cast<const bf16 *>(p->sh_router);
-        e = out_dt == GDN_F32 ? launch_pdl(moe_combine_kernel<float>, dim3(W), dim3(CB_THREADS), 0, s, xw, x_row, shr, idw,
-                                           ww, rw, ow, W, k, (int)shared, ws)
-                              : launch_pdl(moe_combine_kernel<bf16>, dim3(W), dim3(CB_THREADS), 0, s, xw, x_row, shr, idw,
-                                           ww, rw, ow, W, k, (int)shared, ws);
+        auto combine = out_dt == GDN_F32 ? (small ? moe_combine_kernel<float, false> : moe_combine_kernel<float, true>)
+                                         : (small ? moe_combine_kernel<bf16, false> : moe_combine_kernel<bf16, true>);
+        e = launch_pdl(combine, dim3(W), dim3(CB_THREADS), 0, s, xw, x_row, shr, idw, ww, rw, ow, W, k, (int)shared, ws);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

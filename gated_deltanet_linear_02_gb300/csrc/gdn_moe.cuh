@@ -2,12 +2,15 @@
 // workspace of one call, and tensor-core and copy forms that only they use.
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include "gdn_layer.cuh"
 
 namespace gdn {
 
 constexpr int MOE_WINDOW = 8192;          // tokens that one pass over the experts takes, at most
 constexpr int MOE_TILE = 128;             // tokens of one product, at most
+constexpr int MOE_SMALL = 512;            // tokens up to which tiles hold 32 of them, and y is fp32
 constexpr int MOE_FEW_TOKENS = 4;         // tokens up to which the weights pass through the CUDA cores
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr)
@@ -15,6 +18,20 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr)
     float v;
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr));
     return v;
+}
+
+// A 2-D box (gdn_tma.cuh) that leaves L2 before what is read again.
+__device__ __forceinline__ uint64_t evict_first_policy()
+{
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ void tma_load_2d_hint(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar, uint64_t policy)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
+                 "[%0], [%1, {%2, %3}], [%4], %5;"
+                 ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "l"(policy) : "memory");
 }
 
 // Four rows y of a row-major matrix, 64 columns from x on, to four consecutive
@@ -56,7 +73,10 @@ struct MoeWs {
     int *ids;
     float *weights;
     bf16 *h;                              // [rows][F]
-    float *y;                             // [rows][2048]; few tokens: h in fp32, [rows][F]
+    float *y;                             // [rows][2048] outputs of the pairs. Few tokens: h in fp32, [rows][F];
+                                          // many: y16 and scale in its place
+    __half *y16;                          // [rows][2048], scaled by blocks of 32
+    unsigned char *scale;                 // [rows][64]: y = y16 * 2^(scale - 141)
     float *logits;                        // few tokens: [M][E + 1]
     size_t bytes;
 };
@@ -93,7 +113,10 @@ inline MoeWs moe_workspace(const gdn_moe_params *p, int M, void *base)
     w.ids = (int *)take(pairs * 4);
     w.weights = (float *)take(pairs * 4);
     w.h = (bf16 *)take(rows * p->ffn_dim * 2);
-    w.y = (float *)take(rows * (W <= MOE_FEW_TOKENS && p->ffn_dim > LD ? p->ffn_dim : LD) * 4);
+    const size_t y_row = W > MOE_SMALL ? LD * 2 + LD / 32 : (size_t)(W <= MOE_FEW_TOKENS && p->ffn_dim > LD ? p->ffn_dim : LD) * 4;
+    w.y = (float *)take(rows * y_row);
+    w.y16 = reinterpret_cast<__half *>(w.y);
+    w.scale = reinterpret_cast<unsigned char *>(w.y) + rows * LD * 2;
     w.logits = (float *)take(W <= MOE_FEW_TOKENS ? (size_t)W * (p->num_experts + 1) * 4 : 0);
     w.bytes = at;
     return w;
