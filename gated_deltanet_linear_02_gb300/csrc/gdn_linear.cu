@@ -105,7 +105,7 @@ __device__ __forceinline__ void pair_load_2d(uint32_t dst, const CUtensorMap *ma
                  ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(leader_bar) : "memory");
 }
 // Only reads of tensor memory come before it, which tcgen05's own fences order: at
-// cluster scope it would wait for the epilogue's stores (105 -> 9x us per 4,096 x 9,216 x 2,048).
+// cluster scope it would wait for the epilogue's stores.
 __device__ __forceinline__ void arrive_cluster(uint32_t cluster_bar)
 {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");

@@ -468,7 +468,7 @@ template <> struct RawY<true> {
 };
 
 template <typename TO, bool Y16>
-__global__ void __launch_bounds__(CB_THREADS)
+__global__ void __launch_bounds__(CB_THREADS, Y16 ? 4 : 1)
     moe_combine_kernel(const bf16 *x, long long x_row, const bf16 *sh_router, const int32_t *ids, const float *weights,
                        const void *residual, void *out, int M, int k, int shared, MoeWs ws)
 {
@@ -564,7 +564,7 @@ cudaError_t launch_moe(const gdn_moe_params *p, const void *x, long long x_row, 
     const bool shared = p->sh_gate != nullptr;
     const size_t out_row = (size_t)LD * (out_dt == GDN_F32 ? 4 : 2);
     MoeWs ws = moe_workspace(p, M, workspace);
-    const bool small = M <= MOE_SMALL;                 // for the last window too: the workspace is laid out for it
+    const bool small = moe_small(p, M);                // for the last window too: the workspace is laid out for it
     if (M <= MOE_FEW_TOKENS) return launch_moe_few(p, x, x_row, residual, out, M, ids, weights, ws, out_dt, s);
     ExpertMaps maps;
     if (!make_bf16_strided_map(&maps.gate, p->gate, (long long)E * F, LD, LD, 128) ||
@@ -585,10 +585,12 @@ cudaError_t launch_moe(const gdn_moe_params *p, const void *x, long long x_row, 
         if (!make_bf16_strided_map(&maps.x, xw, W, LD, x_row, 1) || !make_bf16_strided_map(&maps.h, ws.h, rows, F, F, small ? ExpertSmem<32>::H_BOX : ExpertSmem<MOE_TILE>::H_BOX))
             return cudaErrorInvalidValue;
         const int n_state = (int)ws.state_ints;
-        cudaError_t e = launch_pdl(moe_zero_kernel, dim3((n_state + 1023) / 1024), dim3(256), 0, s, ws.state, n_state);
+        cudaError_t e = cudaSuccess;
+        const bool one = !ids && W <= MOE_ROUTE_TILE;  // a single cluster routes, and clears the counters itself
+        if (!one) e = launch_pdl(moe_zero_kernel, dim3((n_state + 1023) / 1024), dim3(256), 0, s, ws.state, n_state);
         if (e != cudaSuccess) return e;
         e = ids ? launch_pdl(moe_place_kernel, dim3((W * k + 255) / 256), dim3(256), 0, s, idw, W * k, k, E, ws.places)
-                : launch_route(p, xw, x_row, W, ws.ids, ws.weights, ws.places, s);
+                : launch_route(p, xw, x_row, W, ws.ids, ws.weights, ws.places, one ? ws.state : nullptr, one ? n_state : 0, s);
         if (e != cudaSuccess) return e;
         e = small ? launch_pdl(moe_experts_kernel<32>, dim3(n_sm), dim3(ExpertSmem<32>::THREADS),
                                       sizeof(ExpertSmem<32>) + 1024, s, maps, xw, x_row, W, E, F, k, (int)shared, ws)

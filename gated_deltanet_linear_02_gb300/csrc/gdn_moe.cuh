@@ -10,7 +10,8 @@ namespace gdn {
 
 constexpr int MOE_WINDOW = 8192;          // tokens that one pass over the experts takes, at most
 constexpr int MOE_TILE = 128;             // tokens of one product, at most
-constexpr int MOE_SMALL = 512;            // tokens up to which tiles hold 32 of them, and y is fp32
+constexpr int MOE_SMALL = 16;             // tokens per expert, for even routing, up to which tiles hold 32 and y is fp32
+constexpr int MOE_ROUTE_TILE = 128;       // tokens of a cluster of the router
 constexpr int MOE_FEW_TOKENS = 4;         // tokens up to which the weights pass through the CUDA cores
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr)
@@ -81,6 +82,11 @@ struct MoeWs {
     size_t bytes;
 };
 
+inline bool moe_small(const gdn_moe_params *p, int M)
+{
+    return (long long)M * p->top_k <= (long long)MOE_SMALL * p->num_experts;
+}
+
 inline int moe_max_tiles(const gdn_moe_params *p, int W)
 {
     const long long pairs = (long long)W * p->top_k;
@@ -113,7 +119,7 @@ inline MoeWs moe_workspace(const gdn_moe_params *p, int M, void *base)
     w.ids = (int *)take(pairs * 4);
     w.weights = (float *)take(pairs * 4);
     w.h = (bf16 *)take(rows * p->ffn_dim * 2);
-    const size_t y_row = W > MOE_SMALL ? LD * 2 + LD / 32 : (size_t)(W <= MOE_FEW_TOKENS && p->ffn_dim > LD ? p->ffn_dim : LD) * 4;
+    const size_t y_row = W > MOE_FEW_TOKENS && !moe_small(p, M) ? LD * 2 + LD / 32 : (size_t)(W <= MOE_FEW_TOKENS && p->ffn_dim > LD ? p->ffn_dim : LD) * 4;
     w.y = (float *)take(rows * y_row);
     w.y16 = reinterpret_cast<__half *>(w.y);
     w.scale = reinterpret_cast<unsigned char *>(w.y) + rows * LD * 2;
@@ -123,7 +129,7 @@ inline MoeWs moe_workspace(const gdn_moe_params *p, int M, void *base)
 }
 
 cudaError_t launch_route(const gdn_moe_params *p, const void *x, long long x_row, int M, int32_t *ids, float *weights,
-                         const MoePlaces &places, cudaStream_t s);
+                         const MoePlaces &places, int *state, int n_state, cudaStream_t s);
 
 cudaError_t launch_moe_few(const gdn_moe_params *p, const void *x, long long x_row, const void *residual, void *out, int M,
                            const int32_t *ids, const float *weights, const MoeWs &ws, gdn_dtype out_dt, cudaStream_t s);

@@ -130,6 +130,13 @@ __global__ void __launch_bounds__(32 * (FW_MAX_WARPS + 1), 1) moe_few_kernel(con
     }
     if (tid == 0) sm.abort = 0;
     fence_mbar_init();
+    if (tid < 3 && shared) {                           // the shared expert's weights are needed whatever is chosen: to L2
+        const size_t all = (size_t)F * LD * 2, each = (all / gridDim.x + 16) & ~(size_t)15, at = blockIdx.x * each;
+        const bf16 *w = tid == 0 ? a.sh_gate : tid == 1 ? a.sh_up : a.sh_down;
+        if (at < all)
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;"
+                         ::"l"(reinterpret_cast<const unsigned char *>(w) + at), "r"((uint32_t)(all - at < each ? all - at : each)) : "memory");
+    }
     grid_dep_wait();
     grid_dep_launch();
     if (tid == 32 * warps) {

@@ -26,7 +26,7 @@ namespace gdn {
 
 __device__ unsigned int g_route_error;    // GDN_ERR_TIMEOUT if a bounded wait gave up
 
-constexpr int RT_BM = 128, RT_BK = 64, RT_THREADS = 512, RT_STAGES = 4;
+constexpr int RT_BM = MOE_ROUTE_TILE, RT_BK = 64, RT_THREADS = 512, RT_STAGES = 4;
 constexpr uint32_t RT_A_BYTES = RT_BM * RT_BK * 2;
 constexpr int RT_ACC_K = 256;             // K of one accumulator
 
@@ -42,7 +42,7 @@ static_assert(RT_BM * (RT_MAX_E + 4) * 4 <= sizeof(RouteSmem::stage), "partial l
 __global__ void __launch_bounds__(RT_THREADS, 1)
     route_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mr, const bf16 *x,
                  long long x_row, const bf16 *router, int M, int E, int N, int k, int renorm, int splits,
-                 int32_t *ids, float *weights, MoePlaces places)
+                 int32_t *ids, float *weights, MoePlaces places, int *state, int n_state)
 {
     extern __shared__ unsigned char smem_raw[];
     RouteSmem &sm = *reinterpret_cast<RouteSmem *>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
@@ -74,6 +74,10 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
     const uint32_t tm = sm.tmem;
     grid_dep_wait();
     grid_dep_launch();
+    // with a single cluster the counters that the choice adds to are cleared here: the barrier
+    // before the choice orders it
+    if (part == 0)
+        for (int i = tid; i < n_state; i += RT_THREADS) state[i] = 0;
 
     if (warp == 0) {
         if (lane == 0) {
@@ -192,7 +196,7 @@ static bool route_setup()
 }
 
 cudaError_t launch_route(const gdn_moe_params *p, const void *x, long long x_row, int M, int32_t *ids, float *weights,
-                         const MoePlaces &places, cudaStream_t s)
+                         const MoePlaces &places, int *state, int n_state, cudaStream_t s)
 {
     if (!route_setup()) return cudaErrorInvalidDevice;
     const int E = p->num_experts, N = (E + 15) & ~15;
@@ -215,13 +219,14 @@ cudaError_t launch_route(const gdn_moe_params *p, const void *x, long long x_row
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, route_kernel, mx, mr, (const bf16 *)x, x_row, (const bf16 *)p->router, M, E, N,
-                              p->top_k, p->norm_topk, splits, ids, weights, places);
+                              p->top_k, p->norm_topk, splits, ids, weights, places,
+                              state, n_state);
 }
 
 cudaError_t launch_route_only(const gdn_moe_params *p, const void *x, long long x_row, int M, int32_t *ids,
                               float *weights, cudaStream_t s)
 {
-    return launch_route(p, x, x_row, M, ids, weights, MoePlaces{}, s);
+    return launch_route(p, x, x_row, M, ids, weights, MoePlaces{}, nullptr, 0, s);
 }
 
 // Device address of this file's error word, for gdn_device_error (NULL if the lookup fails).

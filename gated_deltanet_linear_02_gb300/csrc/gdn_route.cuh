@@ -223,6 +223,8 @@ __device__ __forceinline__ void choose(const float (&v)[RT_SLOTS], int E, int k,
         const float up = __shfl_up_sync(0xffffffffu, best, 1), down = __shfl_down_sync(0xffffffffu, best, 1);
         const bool near = lane < n && fabsf(best) < INFINITY && ((lane > 0 && up - best <= tie) || (lane + 1 < n && best - down <= tie));
         float low = 0.0f;
+        for (uint32_t who = __ballot_sync(0xffffffffu, near); who; who &= who - 1)     // their rows, all at once
+            asm volatile("prefetch.global.L1 [%0];" ::"l"(router + (size_t)__shfl_sync(0xffffffffu, id, __ffs(who) - 1) * LD + lane * 64));
         for (uint32_t who = __ballot_sync(0xffffffffu, near); who; who &= who - 1) {
             const int from = __ffs(who) - 1;
             const float2 p = pair_dot(x, router + (size_t)__shfl_sync(0xffffffffu, id, from) * LD, lane);

@@ -181,6 +181,28 @@ def test_own_routing_is_the_router(ops, M):
     assert tl.relative(a, b.double()) < 1e-6
 
 
+@pytest.mark.parametrize("M", [2, 4, 20])
+@pytest.mark.parametrize("near", [3, 60])
+def test_own_routing_near_ties(ops, M, near):
+    """Router rows that differ in one last place: a few of them, and more than a warp has lanes."""
+    g = tl.gen(M + near)
+    W = tl.moe_weights(g, 64, 128)
+    for e in range(1, near):
+        W["router"][e] = W["router"][0]
+        W["router"][e, 7 * e] *= 1 + 2.0 ** -7
+    x = tl.rnd(g, M, D) + W["router"][0].float().mul(4).to(BF)      # those rows are the best of every token
+    check(ops, W, x, 4, F32, g=g)
+
+
+@pytest.mark.parametrize("M", [1, 9])
+@pytest.mark.parametrize("E,k,F", [(64, 16, 128), (4, 2, 8192), (20, 5, 2048)])
+def test_many_slots_and_wide_experts(ops, M, E, k, F):
+    g = tl.gen(M + E)
+    W = tl.moe_weights(g, E, F)
+    check(ops, W, tl.rnd(g, M, D), k, BF, residual=True, g=g)
+    check(ops, W, tl.rnd(g, 4, D), k, F32, g=g)
+
+
 @pytest.mark.parametrize("M", [3, 8, 40, 600])
 def test_rows_stay_apart(ops, M):
     g = tl.gen(M)
@@ -208,6 +230,21 @@ def test_residual_in_place_strides_and_empty(ops):
         ops.moe(p, x, r, residual=r)
         assert torch.equal(r, want)
     ops.moe(p, x[:0], r[:0])
+
+
+@pytest.mark.parametrize("scale", [1e-6, 1e6])
+def test_outputs_of_any_magnitude(ops, scale):
+    """The pairs' outputs of long calls are held in 16 bits with a scale of their own."""
+    g = tl.gen(12)
+    W = tl.moe_weights(g, 8, 128)
+    W["down"], W["sh_down"] = (W["down"].float() * scale).to(BF), (W["sh_down"].float() * scale).to(BF)
+    W["down"][3, 700] *= 2.0 ** 20                        # one dim far above the others
+    x = tl.rnd(g, 700, D)
+    out = check(ops, W, x, 2, F32, g=g)
+    ids, w = tl.route64(x, W["router"], 2, True)
+    ref = tl.moe64(W, x, ids, w)
+    rest = [d for d in range(D) if d // 32 != 700 // 32]  # outside its block nothing is lost
+    assert tl.relative(out[:, rest], ref[:, rest]) < BOUND[F32]
 
 
 def test_more_tokens_than_a_window(ops):
