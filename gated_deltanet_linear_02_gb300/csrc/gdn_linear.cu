@@ -46,6 +46,13 @@ __device__ __forceinline__ float apply_act(float v)
     return v;
 }
 
+// Brings the tensor maps near before the first copies need them.
+__device__ __forceinline__ void prefetch_maps(const CUtensorMap *a, const CUtensorMap *b)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(a)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(b)) : "memory");
+}
+
 // Epilogue of NC (8 or 32) neighbouring columns of row m, those below N; loads first.
 template <typename TO, int ACT, int NC>
 __device__ __forceinline__ void finish(const LinearOut &o, int m, int n, int N, float (&v)[NC])
@@ -151,6 +158,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
         fence_mbar_init();
     }
     if (warp == 1) pair_tmem_alloc(smem_u32(&sm.tmem), 2 * BN);
+    if (tid == 64) prefetch_maps(&mx, &mw);
     tc::fence_before_sync();
     __syncthreads();
     cluster_sync_all();                                // both CTAs' barriers exist
@@ -252,6 +260,46 @@ struct LinearSmem {
     int abort;
 };
 
+// The sums of a cluster's partial tiles for rows [r0, r0 + rows) of this CTA's tile: each
+// of 128 threads takes every 128th group of 8 columns, U groups at a time with all their
+// remote loads in flight, S >= splits.
+template <typename TO, int ACT, int S, int U>
+__device__ __forceinline__ void add_partials(const LinearOut &out, uint32_t part0, int splits, int r0, int rows, int m0,
+                                             int n0, int N, int t)
+{
+    constexpr int GROUPS = LN_BN / 8;
+    for (int f0 = t; f0 < rows * GROUPS; f0 += 128 * U) {
+        float4 a[U][S], b[U][S];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int f = f0 + 128 * u, rr = r0 + f / GROUPS, col = 8 * (f % GROUPS);
+            if (f < rows * GROUPS && n0 + col < N) {
+#pragma unroll
+                for (int r = 0; r < S; ++r)
+                    if (r < splits) {
+                        const uint32_t at = mapa_shared(part0 + (uint32_t)((rr * LN_PART_LD + col) * 4), (uint32_t)r);
+                        a[u][r] = ld_cluster_f32x4(at);
+                        b[u][r] = ld_cluster_f32x4(at + 16);
+                    }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int f = f0 + 128 * u, rr = r0 + f / GROUPS, col = 8 * (f % GROUPS);
+            if (f < rows * GROUPS && n0 + col < N) {
+                float v[8] = {a[u][0].x, a[u][0].y, a[u][0].z, a[u][0].w, b[u][0].x, b[u][0].y, b[u][0].z, b[u][0].w};
+#pragma unroll
+                for (int r = 1; r < S; ++r)
+                    if (r < splits) {
+                        v[0] += a[u][r].x; v[1] += a[u][r].y; v[2] += a[u][r].z; v[3] += a[u][r].w;
+                        v[4] += b[u][r].x; v[5] += b[u][r].y; v[6] += b[u][r].z; v[7] += b[u][r].w;
+                    }
+                finish<TO, ACT, 8>(out, m0 + rr, n0 + col, N, v);
+            }
+        }
+    }
+}
+
 // a_rows: rows of x that a stage holds, 128, or with fewer rows in all those, rounded up
 // to 8. The products read 128 rows all the same; what the others hold does not
 // matter, as each row of the tile has its own sums. Shorter stages, more of them:
@@ -279,6 +327,7 @@ __global__ void __launch_bounds__(LN_THREADS, 1)
         tc::tmem_alloc(smem_u32(&sm.tmem), 2 * BN);
         tc::tmem_relinquish();
     }
+    if (tid == 64) prefetch_maps(&mx, &mw);
     if (tid == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(smem_u32(&sm.full[s]), 1);
@@ -390,29 +439,9 @@ __global__ void __launch_bounds__(LN_THREADS, 1)
         if (warp >= 2 && !aborted) {
             const int mt = w0 / n_tiles, nt = w0 % n_tiles, there = min(LN_BM, M - mt * LN_BM);
             const int r0 = there * part / splits, rows = there * (part + 1) / splits - r0;
-            const uint32_t base = ring;
-            for (int f = tid - 64; f < rows * (BN / 8); f += 128) {
-                const int rr = r0 + f / (BN / 8), col = 8 * (f % (BN / 8));
-                const int m = mt * LN_BM + rr, n = nt * BN + col;
-                if (m >= M || n >= N) continue;
-                const uint32_t off = base + (uint32_t)((rr * PLD + col) * 4);
-                float4 a[8], b[8];                     // all remote loads in flight before the sum
-#pragma unroll
-                for (int r = 0; r < 8; ++r)
-                    if (r < splits) {
-                        const uint32_t at = mapa_shared(off, (uint32_t)r);
-                        a[r] = ld_cluster_f32x4(at);
-                        b[r] = ld_cluster_f32x4(at + 16);
-                    }
-                float v[8] = {a[0].x, a[0].y, a[0].z, a[0].w, b[0].x, b[0].y, b[0].z, b[0].w};
-#pragma unroll
-                for (int r = 1; r < 8; ++r)
-                    if (r < splits) {
-                        v[0] += a[r].x; v[1] += a[r].y; v[2] += a[r].z; v[3] += a[r].w;
-                        v[4] += b[r].x; v[5] += b[r].y; v[6] += b[r].z; v[7] += b[r].w;
-                    }
-                finish<TO, ACT, 8>(out, m, n, N, v);
-            }
+            if (splits <= 2) add_partials<TO, ACT, 2, 4>(out, ring, splits, r0, rows, mt * LN_BM, nt * BN, N, tid - 64);
+            else if (splits <= 4) add_partials<TO, ACT, 4, 2>(out, ring, splits, r0, rows, mt * LN_BM, nt * BN, N, tid - 64);
+            else add_partials<TO, ACT, 8, 1>(out, ring, splits, r0, rows, mt * LN_BM, nt * BN, N, tid - 64);
         }
         cluster_sync_all();                            // no CTA leaves while others read its partial
     }
@@ -450,7 +479,7 @@ static cudaLaunchConfig_t cluster_config(cudaLaunchAttribute (&attr)[2], int gri
 // Set-up once per device: shared-memory attributes, and how many clusters can be
 // resident at once.
 struct LinearDevice {
-    int split_clusters[3];                // of 2, 4 and 8 CTAs of linear_kernel
+    int split_clusters[9];                // of 2 to 8 CTAs of linear_kernel
     int pairs;                            // of pair_kernel
 };
 
@@ -485,8 +514,8 @@ static const LinearDevice *linear_device()
             !linear_attributes<float, 3>() || !linear_attributes<bf16, 0>() || !linear_attributes<bf16, 1>() ||
             !linear_attributes<bf16, 2>() || !linear_attributes<bf16, 3>())
             return nullptr;
-        for (int k = 0; k < 3; ++k)
-            max_clusters(linear_kernel<bf16, 0>, LN_THREADS, LN_SMEM, 2 << k, &info[dev].split_clusters[k]);
+        for (int k = 2; k <= 8; ++k)
+            max_clusters(linear_kernel<bf16, 0>, LN_THREADS, LN_SMEM, k, &info[dev].split_clusters[k]);
         if (!max_clusters(pair_kernel<bf16, 256, 0>, PR_THREADS, pair_smem<256>(), 2, &info[dev].pairs) || info[dev].pairs < 1)
             return nullptr;
         ready[dev] = true;
@@ -524,12 +553,10 @@ static cudaError_t launch_split(const LinearCall &c, const LinearDevice &dev, in
     if (!make_bf16_strided_map(&mx, c.x, c.M, c.K, c.x_row, a_rows) || !make_bf16_strided_map(&mw, c.w, c.N, c.K, c.K, LN_BN))
         return cudaErrorInvalidValue;
     const int n_work = ((c.M + LN_BM - 1) / LN_BM) * ((c.N + 127) / 128), kb_all = (c.K + LN_BK - 1) / LN_BK;
-    // split K while the tiles fill at most half of the SMs, and only as far as all
-    // clusters of that size can be resident at once
-    int splits = 1;
-    while (splits < 8 && n_work * splits * 2 <= n_sm && splits * 2 <= kb_all &&
-           dev.split_clusters[splits == 1 ? 0 : splits == 2 ? 1 : 2] >= n_work)
-        splits *= 2;
+    // split K as far as the SMs reach, every CTA has a slice, and all clusters of that
+    // size can be resident at once
+    int splits = 8;
+    while (splits > 1 && ((long long)n_work * splits > n_sm || splits > kb_all || dev.split_clusters[splits] < n_work)) --splits;
     cudaLaunchAttribute attr[2];
     const cudaLaunchConfig_t cfg = cluster_config(attr, splits > 1 ? n_work * splits : (n_work < n_sm ? n_work : n_sm),
                                                   LN_THREADS, LN_SMEM, splits, c.s);
