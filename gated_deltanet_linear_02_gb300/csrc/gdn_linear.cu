@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
 
 // ------------------------------------------------------------------ few rows: split K
 
-constexpr int LN_BN = 128, LN_MAX_STAGES = 12, LN_PART_LD = LN_BN + 4;
+constexpr int LN_BN = 128, LN_MAX_STAGES = 6, LN_PART_LD = LN_BN + 4;
 constexpr uint32_t LN_B_BYTES = LN_BN * LN_BK * 2;
 constexpr uint32_t LN_RING = 212 * 1024;  // stages, with 16 KB behind the last one that a short A tile's products may read
 static_assert(LN_BM * LN_PART_LD * 4 <= LN_RING, "a partial tile fits the stages");
@@ -311,7 +311,7 @@ __device__ __forceinline__ void add_partials(const LinearOut &out, uint32_t part
 }
 
 // a_rows: rows of x that a stage holds, 128, or with fewer rows in all those, rounded up
-// to 8. The products read 128 rows all the same; what the others hold does not
+// to 8; two slices of 64 along K a stage, as above. The products read 128 rows all the same; what the others hold does not
 // matter, as each row of the tile has its own sums. Shorter stages, more of them:
 // more weights in flight.
 template <typename TO, int ACT>
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(LN_THREADS, 1)
     constexpr int BN = LN_BN, PLD = LN_PART_LD;
     extern __shared__ unsigned char smem_raw[];
     LinearSmem &sm = *reinterpret_cast<LinearSmem *>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
-    const uint32_t a_bytes = (uint32_t)a_rows * LN_BK * 2, stage_bytes = a_bytes + LN_B_BYTES, ring = smem_u32(sm.ring);
+    const uint32_t a_bytes = (uint32_t)a_rows * LN_BK * 2, slice_bytes = a_bytes + LN_B_BYTES, stage_bytes = 2 * slice_bytes, ring = smem_u32(sm.ring);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int n_tiles = (N + BN - 1) / BN;
     const bool split = splits > 1;
@@ -363,13 +363,16 @@ __global__ void __launch_bounds__(LN_THREADS, 1)
             int s = 0, round = 0;                      // stage, and how often the ring has gone round
             for (int w = w0; w < wend && !aborted; w += wstep) {
                 const int mt = w / n_tiles, nt = w % n_tiles;
-                for (int kb = kb0; kb < kb1; ++kb) {
+                for (int kb = kb0; kb < kb1; kb += 2) {
                     if (round > 0 && !mbar_wait_bounded(smem_u32(&sm.empty[s]), (uint32_t)((round - 1) & 1))) sm.abort = 1;
                     if (aborted) break;
+                    const int two = kb + 1 < kb1;
                     const uint32_t dst = ring + s * stage_bytes, bar = smem_u32(&sm.full[s]);
-                    mbar_arrive_expect_tx(bar, stage_bytes);
-                    tma_load_2d(dst + a_bytes, &mw, kb * LN_BK, nt * BN, bar);
-                    tma_load_2d(dst, &mx, kb * LN_BK, mt * LN_BM, bar);
+                    mbar_arrive_expect_tx(bar, slice_bytes * (1 + two));
+                    for (int h = 0; h <= two; ++h) {
+                        tma_load_2d(dst + h * slice_bytes + a_bytes, &mw, (kb + h) * LN_BK, nt * BN, bar);
+                        tma_load_2d(dst + h * slice_bytes, &mx, (kb + h) * LN_BK, mt * LN_BM, bar);
+                    }
                     sm.last_round[s] = round;
                     if (++s == STAGES) {
                         s = 0;
@@ -391,7 +394,7 @@ __global__ void __launch_bounds__(LN_THREADS, 1)
                     sm.abort = 1;
                 tc::fence_after_sync();
                 const uint32_t d = tm + (uint32_t)(BN * ab);
-                for (int kb = kb0; kb < kb1; ++kb) {
+                for (int kb = kb0; kb < kb1; kb += 2) {
                     if (!mbar_wait_bounded(smem_u32(&sm.full[s]), (uint32_t)(round & 1))) sm.abort = 1;
                     if (aborted) break;
                     tc::fence_after_sync();
@@ -399,6 +402,11 @@ __global__ void __launch_bounds__(LN_THREADS, 1)
 #pragma unroll
                     for (int k = 0; k < LN_BK / 16; ++k)
                         tc::mma_f16(d, ad + 2u * k, bd + 2u * k, idesc, (kb > kb0 || k > 0) ? 1u : 0u);
+                    if (kb + 1 < kb1) {
+#pragma unroll
+                        for (int k = 0; k < LN_BK / 16; ++k)
+                            tc::mma_f16(d, ad + (slice_bytes >> 4) + 2u * k, bd + (slice_bytes >> 4) + 2u * k, idesc, 1u);
+                    }
                     tc::mma_commit(smem_u32(&sm.empty[s]));
                     if (++s == STAGES) {
                         s = 0;
@@ -559,7 +567,7 @@ static cudaError_t launch_split(const LinearCall &c, const LinearDevice &dev, in
 {
     CUtensorMap mx, mw;
     const int a_rows = c.M < LN_BM ? (c.M + 7) & ~7 : LN_BM;
-    const int fit = (int)((LN_RING - LN_A_BYTES) / ((uint32_t)a_rows * LN_BK * 2 + LN_B_BYTES)), stages = fit < LN_MAX_STAGES ? fit : LN_MAX_STAGES;
+    const int fit = (int)((LN_RING - LN_A_BYTES) / (2 * ((uint32_t)a_rows * LN_BK * 2 + LN_B_BYTES))), stages = fit < LN_MAX_STAGES ? fit : LN_MAX_STAGES;
     if (!make_bf16_strided_map(&mx, c.x, c.M, c.K, c.x_row, a_rows) || !make_bf16_strided_map(&mw, c.w, c.N, c.K, c.K, LN_BN))
         return cudaErrorInvalidValue;
     const int n_work = ((c.M + LN_BM - 1) / LN_BM) * ((c.N + 127) / 128), kb_all = (c.K + LN_BK - 1) / LN_BK;
