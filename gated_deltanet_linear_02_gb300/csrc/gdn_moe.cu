@@ -18,6 +18,8 @@
 //    Both kinds are the same pipeline: two A tiles and one B tile per stage of
 //    64 along K, two accumulators, double-buffered against the epilogue. Token rows
 //    come by TMA gathers of four rows.
+//    256 tokens: 227 us, HBM at 6.9 TB/s. 4,096 tokens: 326 us, 1.85 GB of HBM traffic and
+//    12.4 TB/s from L2 into the SMs.
 //  - moe_combine: residual, the pairs' outputs in slot order, the shared expert with its gate.
 #include <mutex>
 
