@@ -14,13 +14,6 @@ constexpr int MOE_SMALL = 16;             // tokens per expert, for even routing
 constexpr int MOE_ROUTE_TILE = 128;       // tokens of a cluster of the router
 constexpr int MOE_FEW_TOKENS = 4;         // tokens up to which the weights pass through the CUDA cores
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr)
-{
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr));
-    return v;
-}
-
 // A 2-D box (gdn_tma.cuh) that leaves L2 before what is read again.
 __device__ __forceinline__ uint64_t evict_first_policy()
 {

@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(32 * (FW_MAX_WARPS + 1), 1) moe_few_kernel(con
         float v[RT_SLOTS], w;
         int id;
 #pragma unroll
-        for (int j = 0; j < RT_SLOTS; ++j) v[j] = lane + 32 * j < a.E ? a.logits[(size_t)warp * (a.E + 1) + lane + 32 * j] : 0.0f;
+        for (int j = 0; j < RT_SLOTS; ++j) v[j] = expert_of(lane, j) < a.E ? a.logits[(size_t)warp * (a.E + 1) + expert_of(lane, j)] : 0.0f;
         choose(v, a.E, k, a.renorm != 0, a.x + (size_t)warp * a.x_row, a.router, lane, id, w);
         if (lane < k) {
             sm.id[warp * k + lane] = id;

@@ -13,8 +13,9 @@
 // The choice is exact: where two of the first k + 1 logits are closer than 2^-13 of
 // the largest magnitude (the error bound is far below), the warp sums theirs again
 // in pairs of fp32 (48 bits; products of bf16 are exact).
-// Ties go to the lowest index. NaN ranks below everything. 256 tokens 17 us, 4,096
-// 21 us, a few 6.5: latency of the copies, the cluster, the rounds and the near ties (6 us).
+// Ties go to the lowest index. NaN ranks below everything. 256 tokens 16.5 us, 4,096
+// 21.6 us, a few 6.5: the products are done after 1.7 us, the partial logits of a CTA's
+// tokens take 5 (131 KB from the other SMs), the choice 2, near ties 4.
 #include <mutex>
 
 #include "gdn_layer.cuh"
@@ -150,18 +151,20 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
             float v[RT_SLOTS];
 #pragma unroll
             for (int j = 0; j < RT_SLOTS; ++j) v[j] = 0.0f;
-            for (int r0 = 0; r0 < splits; r0 += 4) {   // 32 loads in flight
-                float u[4][RT_SLOTS];
+            // all loads in flight, 16 bytes each (a quarter of the requests to the other SMs)
+            const bool low = 4 * lane < N, high = 128 + 4 * lane < N;
+            float4 p[8], u[8];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const uint32_t at = mapa_shared(base + (uint32_t)(t * PLD + lane) * 4u, (uint32_t)(r0 + r));
+            for (int r = 0; r < 8; ++r) {
+                p[r] = u[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                const uint32_t at = mapa_shared(base + (uint32_t)(t * PLD + 4 * lane) * 4u, (uint32_t)min(r, splits - 1));
+                if (r < splits && low) p[r] = ld_cluster_f32x4(at);
+                if (r < splits && high) u[r] = ld_cluster_f32x4(at + 512u);
+            }
 #pragma unroll
-                    for (int j = 0; j < RT_SLOTS; ++j) u[r][j] = lane + 32 * j < E ? ld_cluster_f32(at + 128u * j) : 0.0f;
-                }
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-#pragma unroll
-                    for (int j = 0; j < RT_SLOTS; ++j) v[j] += u[r][j];
+            for (int r = 0; r < 8; ++r) {
+                v[0] += p[r].x; v[1] += p[r].y; v[2] += p[r].z; v[3] += p[r].w;
+                v[4] += u[r].x; v[5] += u[r].y; v[6] += u[r].z; v[7] += u[r].w;
             }
             int id;
             float w;

@@ -9,6 +9,13 @@ namespace gdn {
 constexpr int RT_MAX_E = GDN_MOE_MAX_EXPERTS;
 constexpr int RT_SLOTS = RT_MAX_E / 32;   // logits per lane
 
+// A lane holds experts 4 lane .. 4 lane + 3 (slots 0 to 3) and 128 + 4 lane .. (slots 4 to 7), so
+// that logits come 16 bytes at a time. A larger slot is a larger expert.
+static_assert(RT_SLOTS == 8, "two vectors of four logits a lane");
+__device__ __forceinline__ int expert_of(int lane, int j) { return (j >> 2) * 128 + lane * 4 + (j & 3); }
+__device__ __forceinline__ int lane_of(int e) { return (e >> 2) & 31; }
+__device__ __forceinline__ int slot_of(int e) { return (e >> 7) * 4 + (e & 3); }
+
 // Order-preserving keys of floats; NaN is the smallest, -0 is +0.
 __device__ __forceinline__ uint32_t sort_key(float x)
 {
@@ -70,7 +77,7 @@ static __device__ __noinline__ void choose_settled(const float *logits, int E, i
     for (int j = 0; j < RT_SLOTS; ++j) v[j] = logits[j];
 #pragma unroll
     for (int j = 0; j < RT_SLOTS; ++j) {
-        const bool there = lane + 32 * j < E;
+        const bool there = expert_of(lane, j) < E;
         key[j] = there ? sort_key(v[j]) : 0u;
         if (there && fabsf(v[j]) < INFINITY) big = fmaxf(big, fabsf(v[j]));
     }
@@ -92,34 +99,34 @@ static __device__ __noinline__ void choose_settled(const float *logits, int E, i
             uint32_t mk = 0;
 #pragma unroll
             for (int j = 0; j < RT_SLOTS; ++j)
-                if (!(taken >> j & 1u) && lane + 32 * j < E) mk = max(mk, key[j]);
+                if (!(taken >> j & 1u) && expert_of(lane, j) < E) mk = max(mk, key[j]);
             const uint32_t top = __reduce_max_sync(0xffffffffu, mk);
             uint32_t ml = 0;                           // settled: the larger low part among equal high ones
             if (settled) {
 #pragma unroll
                 for (int j = 0; j < RT_SLOTS; ++j)
-                    if (!(taken >> j & 1u) && lane + 32 * j < E && key[j] == top) ml = max(ml, sort_key(lo[j]));
+                    if (!(taken >> j & 1u) && expert_of(lane, j) < E && key[j] == top) ml = max(ml, sort_key(lo[j]));
                 ml = __reduce_max_sync(0xffffffffu, ml);
             }
             uint32_t at = 0xffffffffu;
 #pragma unroll
             for (int j = RT_SLOTS - 1; j >= 0; --j)
-                if (!(taken >> j & 1u) && lane + 32 * j < E && key[j] == top && (!settled || sort_key(lo[j]) == ml))
-                    at = (uint32_t)(lane + 32 * j);
+                if (!(taken >> j & 1u) && expert_of(lane, j) < E && key[j] == top && (!settled || sort_key(lo[j]) == ml))
+                    at = (uint32_t)expert_of(lane, j);
             at = __reduce_min_sync(0xffffffffu, at);
             float val = 0.0f;
 #pragma unroll
             for (int j = 0; j < RT_SLOTS; ++j)
-                if ((int)at == lane + 32 * j) {
+                if ((int)at == expert_of(lane, j)) {
                     val = v[j];
                     taken |= 1u << j;
                 }
-            val = __shfl_sync(0xffffffffu, val, (int)(at & 31u));
+            val = __shfl_sync(0xffffffffu, val, lane_of((int)at));
             if (i > 0 && prev - val <= 0x1p-13f * big) {
                 close = true;
                 border |= i == k;
-                if ((prev_at & 31) == lane) near |= 1u << (prev_at >> 5);
-                if ((int)(at & 31u) == lane) near |= 1u << (at >> 5);
+                if (lane_of(prev_at) == lane) near |= 1u << slot_of(prev_at);
+                if (lane_of((int)at) == lane) near |= 1u << slot_of((int)at);
             }
             prev = val;
             prev_at = (int)at;
@@ -138,7 +145,7 @@ static __device__ __noinline__ void choose_settled(const float *logits, int E, i
         if (border) {
 #pragma unroll
             for (int j = 0; j < RT_SLOTS; ++j)
-                if (lane + 32 * j < E && !(v[j] < kth - 0x1p-13f * big) && v[j] <= kth) near |= 1u << j;
+                if (expert_of(lane, j) < E && !(v[j] < kth - 0x1p-13f * big) && v[j] <= kth) near |= 1u << j;
         }
 #pragma unroll
         for (int j = 0; j < RT_SLOTS; ++j) {
@@ -146,7 +153,7 @@ static __device__ __noinline__ void choose_settled(const float *logits, int E, i
             while (who) {
                 const int from = __ffs(who) - 1;
                 who &= who - 1;
-                const float2 p = pair_dot(x, router + (size_t)(from + 32 * j) * LD, lane);
+                const float2 p = pair_dot(x, router + (size_t)expert_of(from, j) * LD, lane);
                 if (lane == from) {
                     v[j] = p.x;
                     key[j] = sort_key(p.x);
@@ -162,12 +169,12 @@ static __device__ __noinline__ void choose_settled(const float *logits, int E, i
         sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < RT_SLOTS; ++j)
-            if (lane + 32 * j < E) sum += expf(v[j] - top);
+            if (expert_of(lane, j) < E) sum += expf(v[j] - top);
     }
     weight = ex / warp_sum(sum);
 }
 
-// The k largest of the warp's logits v[j] (expert lane + 32 j; whatever past E):
+// The k largest of the warp's logits v[j] (expert_of(lane, j); whatever past E):
 // lane i < k gets the i-th expert and its weight.
 __device__ __forceinline__ void choose(const float (&v)[RT_SLOTS], int E, int k, bool renorm, const bf16 *x,
                                        const bf16 *router, int lane, int &id, float &weight)
@@ -176,7 +183,7 @@ __device__ __forceinline__ void choose(const float (&v)[RT_SLOTS], int E, int k,
     float big = 0.0f;
 #pragma unroll
     for (int j = 0; j < RT_SLOTS; ++j) {
-        const bool there = lane + 32 * j < E;
+        const bool there = expert_of(lane, j) < E;
         key[j] = there ? sort_key(v[j]) : 0u;
         if (there && fabsf(v[j]) < INFINITY) big = fmaxf(big, fabsf(v[j]));
     }
@@ -189,7 +196,7 @@ __device__ __forceinline__ void choose(const float (&v)[RT_SLOTS], int E, int k,
     id = 0;
     uint32_t left = 0;                                 // this lane's slots below E
 #pragma unroll
-    for (int j = 0; j < RT_SLOTS; ++j) left |= (uint32_t)(lane + 32 * j < E) << j;
+    for (int j = 0; j < RT_SLOTS; ++j) left |= (uint32_t)(expert_of(lane, j) < E) << j;
     const int most = min(E, 32);
     int n = 0;
 #pragma unroll 1
@@ -202,10 +209,10 @@ __device__ __forceinline__ void choose(const float (&v)[RT_SLOTS], int E, int k,
                 mj = (uint32_t)j;
             }
         const uint32_t top = __reduce_max_sync(0xffffffffu, mk);
-        const uint32_t at = __reduce_min_sync(0xffffffffu, left != 0u && mk == top ? (uint32_t)lane + 32u * mj : 0xffffffffu);
+        const uint32_t at = __reduce_min_sync(0xffffffffu, left != 0u && mk == top ? (uint32_t)expert_of(lane, (int)mj) : 0xffffffffu);
         const float val = top == 0u ? __uint_as_float(0x7fffffffu) : __uint_as_float((top & 0x80000000u) ? top ^ 0x80000000u : ~top);
         if (n >= k && !(kth - val <= tie)) break;
-        if ((at & 31u) == (uint32_t)lane) left &= ~(1u << (at >> 5));
+        if (lane_of((int)at) == lane) left &= ~(1u << slot_of((int)at));
         close |= n > 0 && prev - val <= tie;
         prev = val;
         if (n < k) kth = val;
@@ -256,7 +263,7 @@ __device__ __forceinline__ void choose(const float (&v)[RT_SLOTS], int E, int k,
         sum = 0.0f;
 #pragma unroll 1
         for (int j = 0; j < RT_SLOTS; ++j)
-            if (lane + 32 * j < E) sum += expf(v[j] - top);
+            if (expert_of(lane, j) < E) sum += expf(v[j] - top);
     }
     weight = ex / warp_sum(sum);
 }
