@@ -424,6 +424,7 @@ __global__ void __launch_bounds__(LN_THREADS, 1)
         const int q = warp & 3, row = 32 * q + lane;
         if (split) {                                   // this CTA's fp32 partial tile into shared memory
             if (!mbar_wait_bounded(smem_u32(&sm.acc_full[0]), 0)) sm.abort = 1;
+            __syncwarp();
             tc::fence_after_sync();
             float *p = reinterpret_cast<float *>(sm.ring) + row * PLD;
             const bool some = (w0 / n_tiles) * LN_BM + 32 * q < M;     // of this warp's rows
@@ -441,6 +442,7 @@ __global__ void __launch_bounds__(LN_THREADS, 1)
             const int ab = ti & 1, mt = w / n_tiles, nt = w % n_tiles;
             if (!mbar_wait_bounded(smem_u32(&sm.acc_full[ab]), (uint32_t)((ti >> 1) & 1))) sm.abort = 1;
             if (aborted) break;
+            __syncwarp();                              // tensor memory is read by whole warps
             tc::fence_after_sync();
             const int m = mt * LN_BM + row;
             for (int c = 0; c < BN; c += 32) {
@@ -449,6 +451,7 @@ __global__ void __launch_bounds__(LN_THREADS, 1)
                 tc::wait_ld();
                 const int n = nt * BN + c;
                 if (m < M) finish<TO, ACT, 32>(out, m, n, N, v);
+                __syncwarp();
             }
             tc::fence_before_sync();
             mbar_arrive(smem_u32(&sm.acc_empty[ab]));
