@@ -43,6 +43,10 @@ __device__ __forceinline__ void st8(bf16 *p, const float (&x)[8])
         make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
 }
 
+// Whether the CTA has given up, one answer for the whole warp: another warp may set the flag
+// between two lanes' reads, and lanes that disagree must not come to a step that all take together.
+__device__ __forceinline__ bool warp_gave_up(const volatile int &aborted) { return __any_sync(0xffffffffu, aborted != 0); }
+
 // Row-major bf16 matrix [rows][cols], row_stride elements from row to row (a
 // multiple of 8), read in boxes of 64 columns x box_rows rows in the 128-byte
 // swizzle; elements past either end read as zero. False if the driver's encoder

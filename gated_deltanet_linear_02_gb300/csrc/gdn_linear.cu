@@ -233,8 +233,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
         for (int t = pair; t < tiles; t += pairs, ++ti) {
             const int ab = ti & 1, mt = t % m_tiles, nt = t / m_tiles;
             if (!mbar_wait_bounded(smem_u32(&sm.acc_full[ab]), (uint32_t)((ti >> 1) & 1))) sm.abort = 1;
-            if (aborted) break;
-            __syncwarp();
+            if (warp_gave_up(aborted)) break;
             tc::fence_after_sync();
             const int m = mt * 256 + rank * 128 + 32 * q + lane;
 #pragma unroll 1
@@ -441,8 +440,7 @@ __global__ void __launch_bounds__(LN_THREADS, 1)
         for (int w = w0; w < wend && !split; w += wstep, ++ti) {
             const int ab = ti & 1, mt = w / n_tiles, nt = w % n_tiles;
             if (!mbar_wait_bounded(smem_u32(&sm.acc_full[ab]), (uint32_t)((ti >> 1) & 1))) sm.abort = 1;
-            if (aborted) break;
-            __syncwarp();                              // tensor memory is read by whole warps
+            if (warp_gave_up(aborted)) break;          // tensor memory is read by whole warps
             tc::fence_after_sync();
             const int m = mt * LN_BM + row;
             for (int c = 0; c < BN; c += 32) {

@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(ExpertSmem<NT>::THREADS, 1)
             if (ui >= EX_INFO && !mbar_wait_bounded(smem_u32(&sm.info_empty[slot]), (uint32_t)((ui / EX_INFO - 1) & 1)))
                 sm.abort = 1;
             Unit un = {-1, 0, 0, 0, 0, 0, 0};
-            if (u < units && !aborted) {
+            if (!warp_gave_up(aborted) && u < units) {
                 un.kind = u >= units1;
                 const int per = un.kind ? EX_DOWN_UNITS : FU, v = un.kind ? u - units1 : u;
                 int lo = 0, hi = NE;                   // the expert: tile0[lo] <= v / per < tile0[hi]
@@ -253,8 +253,7 @@ __global__ void __launch_bounds__(ExpertSmem<NT>::THREADS, 1)
                 const int s = it % STAGES;
                 if (it >= STAGES && !mbar_wait_bounded(smem_u32(&sm.empty[s]), (uint32_t)((it / STAGES - 1) & 1)))
                     sm.abort = 1;
-                __syncwarp();
-                if (aborted) break;
+                if (warp_gave_up(aborted)) break;
                 const uint32_t dst = smem_u32(sm.stage[s]), bar = smem_u32(&sm.full[s]), b0 = dst + 2 * EX_A_BYTES;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(bar, bytes);
@@ -320,10 +319,10 @@ __global__ void __launch_bounds__(ExpertSmem<NT>::THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sm.full[i % STAGES]));
         };
-        for (int ui = 0; !aborted; ++ui) {
+        for (int ui = 0;; ++ui) {
             const int slot = ui % EX_INFO;
             if (!mbar_wait_sleep(smem_u32(&sm.info_full[slot]), (uint32_t)((ui / EX_INFO) & 1))) sm.abort = 1;
-            if (aborted) break;
+            if (warp_gave_up(aborted)) break;
             const Unit un = sm.info[slot];
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sm.info_empty[slot]));
@@ -342,7 +341,7 @@ __global__ void __launch_bounds__(ExpertSmem<NT>::THREADS, 1)
                 const int s = it % STAGES;
                 if (it >= STAGES && !mbar_wait_bounded(smem_u32(&sm.empty[s]), (uint32_t)((it / STAGES - 1) & 1)))
                     sm.abort = 1;
-                if (aborted) break;
+                if (warp_gave_up(aborted)) break;
                 const uint32_t b0 = smem_u32(sm.stage[s]) + 2 * EX_A_BYTES;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -357,21 +356,21 @@ __global__ void __launch_bounds__(ExpertSmem<NT>::THREADS, 1)
             }
         }
         cp_async_wait<0>();
-        for (int i = max(0, it - LAG); i < it && !aborted; ++i) report(i);
+        if (!warp_gave_up(aborted))
+            for (int i = max(0, it - LAG); i < it; ++i) report(i);
     } else {
         // ---- epilogue: thread = weight row (tensor-memory lane), columns = tokens
         const int q = warp & 3, row = 32 * q + lane, c0 = warp >= 10 ? 16 : 0;
-        for (int ui = 0; !aborted; ++ui) {
+        for (int ui = 0;; ++ui) {
             const int slot = ui % EX_INFO, ab = ui & 1;
             if (!mbar_wait_sleep(smem_u32(&sm.info_full[slot]), (uint32_t)((ui / EX_INFO) & 1))) sm.abort = 1;
-            if (aborted) break;
+            if (warp_gave_up(aborted)) break;
             const Unit un = sm.info[slot];
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sm.info_empty[slot]));
             if (un.kind < 0) break;
             if (!mbar_wait_sleep(smem_u32(&sm.acc_full[ab]), (uint32_t)((ui >> 1) & 1))) sm.abort = 1;
-            if (aborted) break;
-            __syncwarp();
+            if (warp_gave_up(aborted)) break;
             tc::fence_after_sync();
             const uint32_t d0 = tc::tmem_addr(tm, 32 * q, 2 * NT * ab);
             for (int c = c0; c < un.n; c += 16 * Smem::EPI) {

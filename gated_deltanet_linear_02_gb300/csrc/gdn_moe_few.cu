@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(32 * (FW_MAX_WARPS + 1), 1) moe_few_kernel(con
             for (int u = lo + warp; u < hi; u += warps) {
                 if (tid == 0 && more < 0 && u + 2 * warps >= hi) more = atomicAdd(a.state, 1);
                 const uint32_t slot = arrived();
-                if (aborted) break;
+                if (warp_gave_up(aborted)) break;
                 const int f = u / distinct, i = u - f * distinct;
                 const uint32_t gw = slot + 16 * lane;
                 for (int p = sm.begin[i]; p < sm.begin[i + 1]; ++p) {
@@ -354,6 +354,7 @@ __global__ void __launch_bounds__(32 * (FW_MAX_WARPS + 1), 1) moe_few_kernel(con
         }
     if (warp < warps) {
         if (!STAGED) __threadfence();
+        __syncwarp();
         asm volatile("bar.sync 2, %0;" ::"r"(32 * warps) : "memory");
         // ---- output dims; a lane keeps its share of every token's sums
         const int group = warp / FW_GROUP, row0 = (warp % FW_GROUP) * FW_DIMS;
@@ -362,9 +363,10 @@ __global__ void __launch_bounds__(32 * (FW_MAX_WARPS + 1), 1) moe_few_kernel(con
             const int d0 = d_lo + b * dims, n = min(dims, d_hi - d0);
             float acc[FW_DIMS][MOE_FEW_TOKENS] = {};
             if (group < groups)
-                for (int i = (group + groups - step % groups) % groups; i < distinct && !aborted; i += groups) {
+                for (int i = (group + groups - step % groups) % groups; i < distinct; i += groups) {
                     const int q = step + i, s = q % slots;
                     if (!mbar_wait_bounded(smem_u32(&sm.row_full[s]), (uint32_t)((q / slots) & 1))) sm.abort = 1;
+                    if (warp_gave_up(aborted)) break;
                     const uint32_t rows = smem_u32(ring) + s * slot_bytes + (uint32_t)(row0 * F + lane * 8) * 2;
                     for (int p = sm.begin[i]; p < sm.begin[i + 1]; ++p) {
                         const int at = sm.pair[p] * F, m = sm.token[p];

@@ -120,10 +120,11 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
         }
     } else if (warp >= 4 && warp < 8) {
         if (!mbar_wait_bounded(smem_u32(&sm.done), 0)) sm.abort = 1;
+        const bool lost = warp_gave_up(aborted);
         tc::fence_after_sync();
         const int q = warp & 3, row = 32 * q + lane;
         float *p = reinterpret_cast<float *>(sm.stage[0]) + row * PLD;
-        if (!aborted)
+        if (!lost)
             for (int c = 0; c < N; c += 16) {
                 float v[16];
                 tc::tmem_ld16(tc::tmem_addr(tm, 32 * q, c), v);
@@ -147,7 +148,7 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
         const uint32_t base = smem_u32(sm.stage[0]);
         for (int t = part * rows + warp; t < (part + 1) * rows; t += RT_THREADS / 32) {
             const int m = tile * RT_BM + t;
-            if (m >= M || aborted) break;
+            if (m >= M || warp_gave_up(aborted)) break;
             float v[RT_SLOTS];
 #pragma unroll
             for (int j = 0; j < RT_SLOTS; ++j) v[j] = 0.0f;
