@@ -66,7 +66,7 @@ cudaError_t launch_route_only(const gdn_moe_params *, const void *, long long, i
 void *route_error_word();
 size_t moe_workspace_bytes(const gdn_moe_params *, int);
 cudaError_t launch_moe(const gdn_moe_params *, const void *, long long, const void *, void *, int, const int32_t *,
-                       const float *, void *, gdn_dtype, cudaStream_t);
+                       const float *, void *, gdn_dtype, bool, cudaStream_t);
 void *moe_error_word();
 void *few_error_word();
 cudaError_t launch_wait_timeout(cudaStream_t s);
@@ -728,13 +728,14 @@ size_t gdn_moe_workspace_size(const gdn_moe_params *p, int M)
     return moe_workspace_bytes(p, M);
 }
 
-gdn_status gdn_moe(const gdn_moe_params *p, const void *x, long long x_row_stride, const void *residual, void *out,
-                   int M, const int32_t *ids, const float *weights, void *workspace, size_t workspace_bytes,
-                   gdn_dtype out_dt, void *stream)
+static gdn_status moe_call(const gdn_moe_params *p, const void *x, long long x_row_stride, const void *residual, void *out,
+                           int M, const int32_t *ids, const float *weights, void *workspace, size_t workspace_bytes,
+                           gdn_dtype out_dt, bool lose_route, void *stream)
 {
     if (!ok_dtype(out_dt)) return fail(GDN_ERR_INVALID_ARG, "unknown output dtype");
     gdn_status st = check_moe_sizes(p, M);
     if (st != GDN_OK || M == 0) return st;
+    if (lose_route && M <= 4) return fail(GDN_ERR_INVALID_ARG, "M must be above 4");
     if ((ids == nullptr) != (weights == nullptr)) return fail(GDN_ERR_INVALID_ARG, "ids and weights go together");
     if ((p->sh_gate == nullptr) != (p->sh_up == nullptr) || (p->sh_gate == nullptr) != (p->sh_down == nullptr) ||
         (p->sh_gate == nullptr && p->sh_router != nullptr))
@@ -762,8 +763,23 @@ gdn_status gdn_moe(const gdn_moe_params *p, const void *x, long long x_row_strid
     for (const auto &t : in)
         if (overlap(workspace, need, t.q, t.n)) return fail(GDN_ERR_INVALID_ARG, "the workspace overlaps an input");
     if (overlap(workspace, need, out, no)) return fail(GDN_ERR_INVALID_ARG, "the workspace overlaps out");
-    cudaError_t e = launch_moe(p, x, x_row_stride, residual, out, M, ids, weights, workspace, out_dt, (cudaStream_t)stream);
+    cudaError_t e = launch_moe(p, x, x_row_stride, residual, out, M, ids, weights, workspace, out_dt, lose_route,
+                               (cudaStream_t)stream);
     return e == cudaSuccess ? GDN_OK : cuda_fail(e, "gdn_moe");
+}
+
+gdn_status gdn_moe(const gdn_moe_params *p, const void *x, long long x_row_stride, const void *residual, void *out,
+                   int M, const int32_t *ids, const float *weights, void *workspace, size_t workspace_bytes,
+                   gdn_dtype out_dt, void *stream)
+{
+    return moe_call(p, x, x_row_stride, residual, out, M, ids, weights, workspace, workspace_bytes, out_dt, false, stream);
+}
+
+gdn_status gdn_selftest_moe_lost_route(const gdn_moe_params *p, const void *x, long long x_row_stride,
+                                       const void *residual, void *out, int M, void *workspace, size_t workspace_bytes,
+                                       gdn_dtype out_dt, void *stream)
+{
+    return moe_call(p, x, x_row_stride, residual, out, M, nullptr, nullptr, workspace, workspace_bytes, out_dt, true, stream);
 }
 
 gdn_status gdn_device_error(void *stream)

@@ -557,7 +557,7 @@ static bool moe_setup()
 size_t moe_workspace_bytes(const gdn_moe_params *p, int M) { return moe_workspace(p, M, nullptr).bytes; }
 
 cudaError_t launch_moe(const gdn_moe_params *p, const void *x, long long x_row, const void *residual, void *out, int M,
-                       const int32_t *ids, const float *weights, void *workspace, gdn_dtype out_dt, cudaStream_t s)
+                       const int32_t *ids, const float *weights, void *workspace, gdn_dtype out_dt, bool lose_route, cudaStream_t s)
 {
     const int n_sm = sm_count();
     if (n_sm <= 0 || !moe_setup()) return cudaErrorInvalidDevice;
@@ -591,7 +591,7 @@ cudaError_t launch_moe(const gdn_moe_params *p, const void *x, long long x_row, 
         if (!one) e = launch_pdl(moe_zero_kernel, dim3((n_state + 1023) / 1024), dim3(256), 0, s, ws.state, n_state);
         if (e != cudaSuccess) return e;
         e = ids ? launch_pdl(moe_place_kernel, dim3((W * k + 255) / 256), dim3(256), 0, s, idw, W * k, k, E, ws.places)
-                : launch_route(p, xw, x_row, W, ws.ids, ws.weights, ws.places, one ? ws.state : nullptr, one ? n_state : 0, s);
+                : launch_route(p, xw, x_row, W, ws.ids, ws.weights, ws.places, one ? ws.state : nullptr, one ? n_state : 0, lose_route, s);
         if (e != cudaSuccess) return e;
         e = small ? launch_pdl(moe_experts_kernel<32>, dim3(n_sm), dim3(ExpertSmem<32>::THREADS),
                                       sizeof(ExpertSmem<32>) + 1024, s, maps, xw, x_row, W, E, F, k, (int)shared, ws)

@@ -122,7 +122,7 @@ inline MoeWs moe_workspace(const gdn_moe_params *p, int M, void *base)
 }
 
 cudaError_t launch_route(const gdn_moe_params *p, const void *x, long long x_row, int M, int32_t *ids, float *weights,
-                         const MoePlaces &places, int *state, int n_state, cudaStream_t s);
+                         const MoePlaces &places, int *state, int n_state, bool lose, cudaStream_t s);
 
 cudaError_t launch_moe_few(const gdn_moe_params *p, const void *x, long long x_row, const void *residual, void *out, int M,
                            const int32_t *ids, const float *weights, const MoeWs &ws, gdn_dtype out_dt, cudaStream_t s);

@@ -16,6 +16,10 @@
 // Ties go to the lowest index. NaN ranks below everything. 256 tokens 16.5 us, 4,096
 // 21.6 us, a few 6.5: the products are done after 1.7 us, the partial logits of a CTA's
 // tokens take 5 (131 KB from the other SMs), the choice 2, near ties 4.
+//
+// Where a wait of a cluster gave up, its tokens are marked as nobody's (id -1), so that the kernels
+// behind find no index that was not written. `lose` makes that happen, for the library's self-test:
+// the products' completion is not announced, and every wait for it runs out.
 #include <mutex>
 
 #include "gdn_layer.cuh"
@@ -27,6 +31,13 @@
 namespace gdn {
 
 __device__ unsigned int g_route_error;    // GDN_ERR_TIMEOUT if a bounded wait gave up
+
+__device__ __forceinline__ int ld_cluster_s32(uint32_t addr)
+{
+    int v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
 
 constexpr int RT_BM = MOE_ROUTE_TILE, RT_BK = 64, RT_THREADS = 512, RT_STAGES = 4;
 constexpr uint32_t RT_A_BYTES = RT_BM * RT_BK * 2;
@@ -44,7 +55,7 @@ static_assert(RT_BM * (RT_MAX_E + 4) * 4 <= sizeof(RouteSmem::stage), "partial l
 __global__ void __launch_bounds__(RT_THREADS, 1)
     route_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mr, const bf16 *x,
                  long long x_row, const bf16 *router, int M, int E, int N, int k, int renorm, int splits,
-                 int32_t *ids, float *weights, MoePlaces places, int *state, int n_state)
+                 int32_t *ids, float *weights, MoePlaces places, int *state, int n_state, int lose)
 {
     extern __shared__ unsigned char smem_raw[];
     RouteSmem &sm = *reinterpret_cast<RouteSmem *>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
@@ -116,7 +127,7 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
                     tc::mma_f16(d, ad + 2u * kk, bd + 2u * kk, idesc, (in > 0 || kk > 0) ? 1u : 0u);
                 tc::mma_commit(smem_u32(&sm.empty[s]));
             }
-            if (!aborted) tc::mma_commit(smem_u32(&sm.done));
+            if (!aborted && !lose) tc::mma_commit(smem_u32(&sm.done));
         }
     } else if (warp >= 4 && warp < 8) {
         if (!mbar_wait_bounded(smem_u32(&sm.done), 0)) sm.abort = 1;
@@ -148,7 +159,9 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
         const uint32_t base = smem_u32(sm.stage[0]);
         for (int t = part * rows + warp; t < (part + 1) * rows; t += RT_THREADS / 32) {
             const int m = tile * RT_BM + t;
-            if (m >= M || warp_gave_up(aborted)) break;
+            if (m >= M) break;
+            // whether any CTA of the cluster has given up: its partial logits may not be there
+            const int lost = ld_cluster_s32(mapa_shared(smem_u32(&sm.abort), (uint32_t)min(lane, splits - 1)));
             float v[RT_SLOTS];
 #pragma unroll
             for (int j = 0; j < RT_SLOTS; ++j) v[j] = 0.0f;
@@ -166,6 +179,14 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
             for (int r = 0; r < 8; ++r) {
                 v[0] += p[r].x; v[1] += p[r].y; v[2] += p[r].z; v[3] += p[r].w;
                 v[4] += u[r].x; v[5] += u[r].y; v[6] += u[r].z; v[7] += u[r].w;
+            }
+            if (__any_sync(0xffffffffu, lost)) {       // nobody's token: what follows must not take these for indices
+                if (lane < k) {
+                    ids[(size_t)m * k + lane] = -1;
+                    weights[(size_t)m * k + lane] = 0.0f;
+                    if (places.count) places.rank[(size_t)m * k + lane] = -1;
+                }
+                continue;
             }
             int id;
             float w;
@@ -201,7 +222,7 @@ static bool route_setup()
 }
 
 cudaError_t launch_route(const gdn_moe_params *p, const void *x, long long x_row, int M, int32_t *ids, float *weights,
-                         const MoePlaces &places, int *state, int n_state, cudaStream_t s)
+                         const MoePlaces &places, int *state, int n_state, bool lose, cudaStream_t s)
 {
     if (!route_setup()) return cudaErrorInvalidDevice;
     const int E = p->num_experts, N = (E + 15) & ~15;
@@ -225,13 +246,13 @@ cudaError_t launch_route(const gdn_moe_params *p, const void *x, long long x_row
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, route_kernel, mx, mr, (const bf16 *)x, x_row, (const bf16 *)p->router, M, E, N,
                               p->top_k, p->norm_topk, splits, ids, weights, places,
-                              state, n_state);
+                              state, n_state, (int)lose);
 }
 
 cudaError_t launch_route_only(const gdn_moe_params *p, const void *x, long long x_row, int M, int32_t *ids,
                               float *weights, cudaStream_t s)
 {
-    return launch_route(p, x, x_row, M, ids, weights, MoePlaces{}, nullptr, 0, s);
+    return launch_route(p, x, x_row, M, ids, weights, MoePlaces{}, nullptr, 0, false, s);
 }
 
 // Device address of this file's error word, for gdn_device_error (NULL if the lookup fails).

@@ -127,6 +127,8 @@ def lib() -> ctypes.CDLL:
         L.gdn_prefill_workspace_size.argtypes = [_int, _int, _int, _int]
         L.gdn_selftest_wait_timeout.restype = _int
         L.gdn_selftest_wait_timeout.argtypes = [_vp]
+        L.gdn_selftest_moe_lost_route.restype = _int
+        L.gdn_selftest_moe_lost_route.argtypes = [_vp, _vp, _ll, _vp, _vp, _int, _vp, _sz, _int, _vp]
         L.gdn_device_error.restype = _int
         L.gdn_device_error.argtypes = [_vp]
         L.gdn_get_device_error.restype = _int
@@ -754,6 +756,17 @@ def selftest_wait_timeout(stream=None) -> None:
     """gdn_selftest_wait_timeout: enqueue the kernel whose bounded wait runs
     out (about 2 s); the next device_error() then reports GDN_ERR_TIMEOUT."""
     _check(lib().gdn_selftest_wait_timeout(_stream(stream)), "gdn_selftest_wait_timeout")
+
+
+def selftest_moe_lost_route(params: gdn_moe_params, x, out, residual=None, stream=None) -> None:
+    """gdn_selftest_moe_lost_route: moe() of more than 4 tokens whose router's wait runs out (about
+    2 s): out = residual + the shared expert, and the next device_error() reports GDN_ERR_TIMEOUT."""
+    M, dev = x.shape[0], _on_current(x.device, "selftest_moe_lost_route")
+    ws = _workspace(max(moe_workspace_size(params, M), 256), dev, stream)
+    xp, xr = _rows(x, "x", M, N_EMBD, dev, torch.bfloat16)
+    _check(lib().gdn_selftest_moe_lost_route(params._ref, xp, xr, _dense(residual, "residual", (M, N_EMBD), dev, out.dtype),
+                                             _dense(out, "out", (M, N_EMBD), dev), M, ws.data_ptr(), ws.nbytes, _act_dtype(out),
+                                             _raw_stream(stream, dev)), "gdn_selftest_moe_lost_route")
 
 
 def static_scratch_bytes() -> int:

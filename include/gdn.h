@@ -625,7 +625,9 @@ typedef struct {
  * The order is that of the exact logits: neighbours closer than 2^-13 of the
  * token's largest logit are settled in 48 bits. Only router, num_experts, top_k and
  * norm_topk of the parameters are used. 0 <= M <= 2^24. Errors:
- * GDN_ERR_INVALID_ARG, GDN_ERR_CUDA.
+ * GDN_ERR_INVALID_ARG, GDN_ERR_CUDA. A bounded device wait that gives up is reported
+ * afterwards by gdn_device_error; tokens that it left without a choice have ids of -1 and
+ * weights of 0.
  */
 gdn_status gdn_moe_route(const gdn_moe_params *p, const void *x, long long x_row_stride, int M, int32_t *ids,
                          float *weights, void *stream);
@@ -683,6 +685,14 @@ gdn_status gdn_get_device_error(void *workspace, void *stream);
  * GDN_ERR_TIMEOUT (and clears it) and the context stays usable. Errors:
  * GDN_ERR_CUDA. */
 gdn_status gdn_selftest_wait_timeout(void *stream);
+
+/* The same for a wait inside a longer call: gdn_moe of M > 4 tokens whose router never hears
+ * that its products are done. After the limit (2 s per window of 8,192 tokens) every token
+ * counts as routed to no expert, the rest of the call runs (out = residual + the shared
+ * expert), and gdn_device_error reports GDN_ERR_TIMEOUT. Arguments and errors as gdn_moe. */
+gdn_status gdn_selftest_moe_lost_route(const gdn_moe_params *p, const void *x, long long x_row_stride,
+                                       const void *residual, void *out, int M, void *workspace, size_t workspace_bytes,
+                                       gdn_dtype out_dt, void *stream);
 
 /* Human-readable name of a status (static storage). */
 const char *gdn_status_string(gdn_status s);
