@@ -112,6 +112,13 @@ __device__ __forceinline__ void lds8f(uint32_t addr, float (&x)[8])
     x[4] = __uint_as_float(b.x); x[5] = __uint_as_float(b.y); x[6] = __uint_as_float(b.z); x[7] = __uint_as_float(b.w);
 }
 
+// One value of h, for CTAs that poll it: a strong store, as the polls are strong loads (a weak
+// one would race with them).
+__device__ __forceinline__ void store_relaxed(float *p, float v)
+{
+    asm volatile("st.relaxed.gpu.global.f32 [%0], %1;" ::"l"(p), "f"(v) : "memory");
+}
+
 template <typename TO, bool STAGED>
 __global__ void __launch_bounds__(32 * (FW_MAX_WARPS + 1), 1) moe_few_kernel(const FewArgs a)
 {
@@ -276,7 +283,7 @@ __global__ void __launch_bounds__(32 * (FW_MAX_WARPS + 1), 1) moe_few_kernel(con
                     const float gs = warp_sum(sg[0] + sg[1]), us = warp_sum(su[0] + su[1]);
                     if (lane == 0) {                   // with its weight; a NaN as the common one
                         const float h = sm.weight[pr] * (silu_f(gs) * us);
-                        __stcg(a.h + (size_t)pr * F + f, h == h ? h : __uint_as_float(0x7fffffffu));
+                        store_relaxed(a.h + (size_t)pr * F + f, h == h ? h : __uint_as_float(0x7fffffffu));
                     }
                 }
                 __syncwarp();
