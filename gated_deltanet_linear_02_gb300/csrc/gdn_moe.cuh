@@ -71,7 +71,7 @@ struct MoeWs {
                                           // many: y16 and scale in its place
     __half *y16;                          // [rows][2048], scaled by blocks of 32
     unsigned char *scale;                 // [rows][64]: y = y16 * 2^(scale - 141)
-    float *logits;                        // few tokens: [M][E + 1]
+    float *logits;                        // few tokens: [M][E + 1], and their sums of magnitudes
     size_t bytes;
 };
 
@@ -116,7 +116,7 @@ inline MoeWs moe_workspace(const gdn_moe_params *p, int M, void *base)
     w.y = (float *)take(rows * y_row);
     w.y16 = reinterpret_cast<__half *>(w.y);
     w.scale = reinterpret_cast<unsigned char *>(w.y) + rows * LD * 2;
-    w.logits = (float *)take(W <= MOE_FEW_TOKENS ? (size_t)W * (p->num_experts + 1) * 4 : 0);
+    w.logits = (float *)take(W <= MOE_FEW_TOKENS ? (size_t)W * (p->num_experts + 1) * 8 : 0);
     w.bytes = at;
     return w;
 }

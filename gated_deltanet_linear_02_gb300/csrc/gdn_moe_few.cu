@@ -27,12 +27,15 @@ namespace gdn {
 __device__ unsigned int g_few_error;      // GDN_ERR_TIMEOUT if a bounded wait gave up
 
 constexpr int FW_LOGIT_WARPS = 4;
+__host__ __device__ constexpr int few_logit_blocks(int experts) { return experts / FW_LOGIT_WARPS + 1; }     // of the logits and the shared expert's gate
+static_assert(few_logit_blocks(GDN_MOE_MAX_EXPERTS) <= 96, "three a lane");
 
 // What h holds until it is written: a NaN that no computation gives (a computed NaN is
 // stored as another one). Reading h and waiting for it are one: no counter, no fence.
 constexpr uint32_t FW_NOT_YET = 0xffffffffu;
 
-// logits [M][E + 1], the last one the shared expert's
+// logits [M][E + 1], the last one the shared expert's; behind them for each token the largest sum of magnitudes of
+// each CTA's experts (finite ones: the others belong to logits that are not finite either), [M][gridDim.x]
 __global__ void __launch_bounds__(32 * FW_LOGIT_WARPS)
     moe_few_logits_kernel(const bf16 *x, long long x_row, const bf16 *router, const bf16 *sh_router, int M, int E,
                           int first, float *logits, int *state, uint4 *h, int h_vectors)
@@ -44,24 +47,38 @@ __global__ void __launch_bounds__(32 * FW_LOGIT_WARPS)
     if (blockIdx.x == 0 && threadIdx.x < 2) state[threadIdx.x] = 0;
     for (int i = blockIdx.x * 32 * FW_LOGIT_WARPS + threadIdx.x; i < h_vectors; i += gridDim.x * 32 * FW_LOGIT_WARPS)
         h[i] = make_uint4(FW_NOT_YET, FW_NOT_YET, FW_NOT_YET, FW_NOT_YET);
-    if (e > E || (e == E && sh_router == nullptr)) return;
-    const bf16 *w = (e == E ? sh_router : router + (size_t)e * LD) + lane * 8;
+    if (first + (int)blockIdx.x * FW_LOGIT_WARPS > E) return;
+    __shared__ float mags[MOE_FEW_TOKENS][FW_LOGIT_WARPS];
+    const bool there = e < E || (e == E && sh_router != nullptr);
+    const bf16 *w = (e < E ? router + (size_t)e * LD : sh_router) + lane * 8;
     uint4 u[LD / 256];
 #pragma unroll
-    for (int c = 0; c < LD / 256; ++c) u[c] = *reinterpret_cast<const uint4 *>(w + c * 256);
+    for (int c = 0; c < LD / 256; ++c) u[c] = there ? *reinterpret_cast<const uint4 *>(w + c * 256) : make_uint4(0u, 0u, 0u, 0u);
     for (int m = 0; m < M; ++m) {
         const bf16 *xm = x + (size_t)m * x_row + lane * 8;
-        float s[4] = {};
+        float s[4] = {}, t[4] = {};
 #pragma unroll
         for (int c = 0; c < LD / 256; ++c) {
             float a[8], b[8];
             unpack8(u[c], a);
             ld8(xm + c * 256, b);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s[i & 3] = fmaf(a[i], b[i], s[i & 3]);
+            for (int i = 0; i < 8; ++i) {
+                const float p = __fmul_rn(a[i], b[i]);         // exact
+                s[i & 3] = __fadd_rn(s[i & 3], p);
+                t[i & 3] = __fadd_rn(t[i & 3], fabsf(p));
+            }
         }
-        const float l = warp_sum((s[0] + s[1]) + (s[2] + s[3]));
-        if (lane == 0) logits[(size_t)m * (E + 1) + e] = l;
+        const float l = warp_sum((s[0] + s[1]) + (s[2] + s[3])), mag = warp_sum((t[0] + t[1]) + (t[2] + t[3]));
+        if (lane == 0) {
+            if (there) logits[(size_t)m * (E + 1) + e] = l;
+            mags[m][warp] = e < E && mag < INFINITY ? mag : 0.0f;
+        }
+    }
+    __syncthreads();
+    if (first == 0 && threadIdx.x < M) {               // not for a given routing
+        const float *t = mags[threadIdx.x];
+        logits[(size_t)M * (E + 1) + threadIdx.x * gridDim.x + blockIdx.x] = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
     }
 }
 
@@ -162,11 +179,18 @@ __global__ void __launch_bounds__(32 * (FW_MAX_WARPS + 1), 1) moe_few_kernel(con
             sm.weight[tid] = a.weights[tid];
         }
     } else if (warp < M) {
-        float v[RT_SLOTS], w;
+        // a logit is 23 additions deep (16 in a chain, 2, 5), each off by at most 2^-24 of its sum of
+        // magnitudes: 2^-18 of the largest such sum for a difference
+        float v[RT_SLOTS], mag = 0.0f, w;
         int id;
 #pragma unroll
         for (int j = 0; j < RT_SLOTS; ++j) v[j] = expert_of(lane, j) < a.E ? a.logits[(size_t)warp * (a.E + 1) + expert_of(lane, j)] : 0.0f;
-        choose(v, a.E, k, a.renorm != 0, a.x + (size_t)warp * a.x_row, a.router, lane, id, w);
+        const int blocks = few_logit_blocks(a.E);
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+            if (lane + 32 * i < blocks) mag = fmaxf(mag, a.logits[(size_t)M * (a.E + 1) + warp * blocks + lane + 32 * i]);
+        mag = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mag)));
+        choose(v, a.E, k, a.renorm != 0, 0x1p-18f * mag, a.x + (size_t)warp * a.x_row, a.router, lane, id, w);
         if (lane < k) {
             sm.id[warp * k + lane] = id;
             sm.weight[warp * k + lane] = w;
@@ -460,7 +484,7 @@ cudaError_t launch_moe_few(const gdn_moe_params *p, const void *x, long long x_r
     const int n_sm = sm_count();
     if (n_sm <= 0 || !few_setup()) return cudaErrorInvalidDevice;
     const int E = p->num_experts, first = ids ? E : 0;          // with a given routing only the shared expert's gate
-    cudaError_t e = launch_pdl(moe_few_logits_kernel, dim3((E + 1 - first + FW_LOGIT_WARPS - 1) / FW_LOGIT_WARPS + (ids ? 31 : 0)),
+    cudaError_t e = launch_pdl(moe_few_logits_kernel, dim3(ids ? 32 : few_logit_blocks(E)),
                                dim3(32 * FW_LOGIT_WARPS), 0, s, (const bf16 *)x, x_row, (const bf16 *)p->router,
                                (const bf16 *)p->sh_router, M, E, first, ws.logits, ws.state, (uint4 *)ws.y,
                                M * (p->top_k + (p->sh_gate ? 1 : 0)) * (p->ffn_dim / 4));

@@ -10,9 +10,12 @@
 // terms). They meet in distributed shared memory, where each CTA has 128 / S
 // tokens: a warp per token holds 8 logits a lane and takes the largest k times.
 //
-// The choice is exact: where two of the first k + 1 logits are closer than 2^-13 of
-// the largest magnitude (the error bound is far below), the warp sums theirs again
-// in pairs of fp32 (48 bits; products of bf16 are exact).
+// The choice is exact: where two of the first k + 1 logits are closer than a bound on their
+// error, the warp sums theirs again in pairs of fp32 (48 bits; products of bf16 are exact).
+// The bound: an accumulator takes 16 steps, each off by at most 2^-23 of its sum of magnitudes,
+// and up to 8 roundings of 2^-24 join them: 1.25 2^-19 of sum |x_i r_i| in all, twice that for a
+// difference. That sum is at most |x| |r| in each part of K; warps that the products leave
+// idle take the norms from the stages as they pass (of r the largest).
 // Ties go to the lowest index. NaN ranks below everything. 256 tokens 16.5 us, 4,096
 // 21.6 us, a few 6.5: the products are done after 1.7 us, the partial logits of a CTA's
 // tokens take 5 (131 KB from the other SMs), the choice 2, near ties 4.
@@ -47,9 +50,57 @@ struct RouteSmem {
     alignas(1024) unsigned char stage[RT_STAGES][RT_A_BYTES + RT_MAX_E * RT_BK * 2];
     alignas(8) uint64_t full[RT_STAGES], empty[RT_STAGES], done;
     int last_it[RT_STAGES];
+    float x_squares[RT_BM];               // sums of squares of this part of the tokens' rows
+    uint32_t row_norm;                    // bits of the largest norm of this part of the router's rows
     uint32_t tmem;
     int abort;
 };
+constexpr int RT_NORM_WARP = 8, RT_NORM_WARPS = 8;       // a thread per router row
+static_assert(32 * RT_NORM_WARPS == RT_MAX_E && 32 * (RT_NORM_WARP + RT_NORM_WARPS) == RT_THREADS, "a thread per router row");
+
+// The norm of n bf16 values from their sum of squares; where that left fp32's range, a bound on it
+// from the largest magnitude (bits `top`). 0 if a value is not finite: then so is the
+// logit, and there is nothing to settle.
+__device__ __forceinline__ bool in_range(float squares) { return squares > 0x1p-80f && squares < 0x1p100f; }
+__device__ __forceinline__ float norm_of(float squares, uint32_t top, int n)
+{
+    if (in_range(squares)) return sqrtf(squares);
+    return top >= 0x7f80u ? 0.0f : sqrtf((float)n) * __uint_as_float(top << 16);
+}
+// The sum of squares of 8 values, to 1 in 128: four products and sums of pairs in bf16, then fp32.
+__device__ __forceinline__ float squares(uint4 u)
+{
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    uint32_t t;
+    asm("mul.rn.bf16x2 %0, %1, %1;" : "=r"(t) : "r"(w[0]));
+#pragma unroll
+    for (int i = 1; i < 4; ++i) asm("fma.rn.bf16x2 %0, %1, %1, %0;" : "+r"(t) : "r"(w[i]));
+    return __uint_as_float(t << 16) + __uint_as_float(t & 0xFFFF0000u);
+}
+__device__ __forceinline__ uint32_t top_bits(uint4 u)
+{
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    uint32_t t = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t = max(t, max(w[i] & 0x7fffu, w[i] >> 16 & 0x7fffu));
+    return t;
+}
+
+// The bound where the squares of part of a row left fp32's range (zeros too): by the whole row, in memory.
+static __device__ __noinline__ float bound_of(const bf16 *x, float r_norm, int splits, int lane)
+{
+    float q = 0.0f;
+    uint32_t top = 0;
+    for (int c = 0; c < LD; c += 256) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(x + c + lane * 8);
+        q += squares(u);
+        top = max(top, top_bits(u));
+    }
+    const float norm = norm_of(warp_sum(q), __reduce_max_sync(0xffffffffu, top), LD);
+    return norm == 0.0f ? 0.0f : norm * sqrtf((float)splits) * __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(r_norm)));
+}
+constexpr float RT_TIE = 0x1.5p-18f;      // 1.25 2^-18 and what the norms' own roundings take
+
 static_assert(RT_BM * (RT_MAX_E + 4) * 4 <= sizeof(RouteSmem::stage), "partial logits fit the stages");
 
 __global__ void __launch_bounds__(RT_THREADS, 1)
@@ -74,10 +125,11 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
     if (tid == 0) {
         for (int s = 0; s < RT_STAGES; ++s) {
             mbar_init(smem_u32(&sm.full[s]), 1);
-            mbar_init(smem_u32(&sm.empty[s]), 1);
+            mbar_init(smem_u32(&sm.empty[s]), 1 + RT_NORM_WARPS);
             sm.last_it[s] = -1;
         }
         mbar_init(smem_u32(&sm.done), 1);
+        sm.row_norm = 0u;
         sm.abort = 0;
         fence_mbar_init();
     }
@@ -132,6 +184,7 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
     } else if (warp >= 4 && warp < 8) {
         if (!mbar_wait_bounded(smem_u32(&sm.done), 0)) sm.abort = 1;
         const bool lost = warp_gave_up(aborted);
+        asm volatile("bar.sync 1, %0;" ::"n"(128 + 32 * RT_NORM_WARPS) : "memory");       // the norms are done with the stages
         tc::fence_after_sync();
         const int q = warp & 3, row = 32 * q + lane;
         float *p = reinterpret_cast<float *>(sm.stage[0]) + row * PLD;
@@ -153,15 +206,50 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
                     reinterpret_cast<float4 *>(p + c)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
             }
     }
+    const int rows = RT_BM / splits;
+    if (warp >= RT_NORM_WARP) {
+        const int e = tid - 32 * RT_NORM_WARP;
+        const int row = e >> 1, half = (e & 1) << 2;   // of x: half a row a thread
+        float q = 0.0f, qx = 0.0f;
+        for (int it = 0; it < kbn; ++it) {
+            const int s = it % RT_STAGES;
+            if (!mbar_wait_sleep(smem_u32(&sm.full[s]), (uint32_t)((it / RT_STAGES) & 1))) sm.abort = 1;
+            if (warp_gave_up(aborted)) break;
+            // 16 bytes at a time, in an order that keeps the lanes off each other's banks
+            const unsigned char *r = sm.stage[s] + RT_A_BYTES + e * (RT_BK * 2), *rx = sm.stage[s] + row * (RT_BK * 2);
+            if (e < E)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) q += squares(*reinterpret_cast<const uint4 *>(r + ((j ^ (e & 7)) << 4)));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) qx += squares(*reinterpret_cast<const uint4 *>(rx + (((j | half) ^ (row & 7)) << 4)));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm.empty[s]));
+        }
+        __syncwarp();
+        asm volatile("bar.arrive 1, %0;" ::"n"(128 + 32 * RT_NORM_WARPS) : "memory");
+        qx += __shfl_xor_sync(0xffffffffu, qx, 1);
+        if (half == 0) sm.x_squares[row] = qx;
+        float norm = norm_of(q, 0u, 0);
+        if (e < E && !(norm > 0.0f)) {                 // squares out of range
+            uint32_t top = 0;
+            for (int c = 0; c < kbn * RT_BK; c += 8)
+                top = max(top, top_bits(*reinterpret_cast<const uint4 *>(router + (size_t)e * LD + kb0 * RT_BK + c)));
+            norm = norm_of(0.0f, top, kbn * RT_BK);
+        }
+        const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(norm));
+        if (lane == 0) atomicMax(&sm.row_norm, most);
+    }
     cluster_sync_all();
     {
-        const int rows = RT_BM / splits;
         const uint32_t base = smem_u32(sm.stage[0]);
         for (int t = part * rows + warp; t < (part + 1) * rows; t += RT_THREADS / 32) {
             const int m = tile * RT_BM + t;
             if (m >= M) break;
             // whether any CTA of the cluster has given up: its partial logits may not be there
-            const int lost = ld_cluster_s32(mapa_shared(smem_u32(&sm.abort), (uint32_t)min(lane, splits - 1)));
+            const uint32_t peer = (uint32_t)min(lane, splits - 1);
+            const int lost = ld_cluster_s32(mapa_shared(smem_u32(&sm.abort), peer));
+            const float r_norm = __int_as_float(ld_cluster_s32(mapa_shared(smem_u32(&sm.row_norm), peer)));
+            const float x_sq = __int_as_float(ld_cluster_s32(mapa_shared(smem_u32(&sm.x_squares[t]), peer)));
             float v[RT_SLOTS];
 #pragma unroll
             for (int j = 0; j < RT_SLOTS; ++j) v[j] = 0.0f;
@@ -190,7 +278,9 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
             }
             int id;
             float w;
-            choose(v, E, k, renorm != 0, x + (size_t)m * x_row, router, lane, id, w);
+            float bound = warp_sum(lane < splits ? sqrtf(x_sq) * r_norm : 0.0f);
+            if (__any_sync(0xffffffffu, !in_range(x_sq))) bound = bound_of(x + (size_t)m * x_row, r_norm, splits, lane);
+            choose(v, E, k, renorm != 0, RT_TIE * bound, x + (size_t)m * x_row, router, lane, id, w);
             if (lane < k) {
                 ids[(size_t)m * k + lane] = id;
                 weights[(size_t)m * k + lane] = w;

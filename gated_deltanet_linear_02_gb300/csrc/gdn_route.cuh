@@ -68,20 +68,15 @@ static __device__ __noinline__ float2 pair_dot(const bf16 *x, const bf16 *w, int
 }
 
 // The same choice as below for tokens where dozens of logits are near one another.
-static __device__ __noinline__ void choose_settled(const float *logits, int E, int k, bool renorm, const bf16 *x, const bf16 *router, int lane,
-                       int &id, float &weight)
+static __device__ __noinline__ void choose_settled(const float *logits, int E, int k, bool renorm, float tie, const bf16 *x,
+                                                   const bf16 *router, int lane, int &id, float &weight)
 {
     uint32_t key[RT_SLOTS];
-    float v[RT_SLOTS], big = 0.0f;
+    float v[RT_SLOTS];
 #pragma unroll
     for (int j = 0; j < RT_SLOTS; ++j) v[j] = logits[j];
 #pragma unroll
-    for (int j = 0; j < RT_SLOTS; ++j) {
-        const bool there = expert_of(lane, j) < E;
-        key[j] = there ? sort_key(v[j]) : 0u;
-        if (there && fabsf(v[j]) < INFINITY) big = fmaxf(big, fabsf(v[j]));
-    }
-    big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
+    for (int j = 0; j < RT_SLOTS; ++j) key[j] = expert_of(lane, j) < E ? sort_key(v[j]) : 0u;
     float lo[RT_SLOTS];
 #pragma unroll
     for (int j = 0; j < RT_SLOTS; ++j) lo[j] = 0.0f;
@@ -122,7 +117,7 @@ static __device__ __noinline__ void choose_settled(const float *logits, int E, i
                     taken |= 1u << j;
                 }
             val = __shfl_sync(0xffffffffu, val, lane_of((int)at));
-            if (i > 0 && prev - val <= 0x1p-13f * big) {
+            if (i > 0 && prev - val <= tie) {
                 close = true;
                 border |= i == k;
                 if (lane_of(prev_at) == lane) near |= 1u << slot_of(prev_at);
@@ -138,14 +133,14 @@ static __device__ __noinline__ void choose_settled(const float *logits, int E, i
                 }
             }
         }
-        if (settled || !close || !(big > 0.0f)) break;
+        if (settled || !close || !(tie > 0.0f)) break;
         // in 48 bits: the neighbours among the first k, and where the last of them is
         // close to the next, every expert that may be in its place
         settled = true;
         if (border) {
 #pragma unroll
             for (int j = 0; j < RT_SLOTS; ++j)
-                if (expert_of(lane, j) < E && !(v[j] < kth - 0x1p-13f * big) && v[j] <= kth) near |= 1u << j;
+                if (expert_of(lane, j) < E && !(v[j] < kth - tie) && v[j] <= kth) near |= 1u << j;
         }
 #pragma unroll
         for (int j = 0; j < RT_SLOTS; ++j) {
@@ -175,22 +170,18 @@ static __device__ __noinline__ void choose_settled(const float *logits, int E, i
 }
 
 // The k largest of the warp's logits v[j] (expert_of(lane, j); whatever past E):
-// lane i < k gets the i-th expert and its weight.
-__device__ __forceinline__ void choose(const float (&v)[RT_SLOTS], int E, int k, bool renorm, const bf16 *x,
+// lane i < k gets the i-th expert and its weight. `tie` bounds how far the difference of two of
+// these logits is from the exact one, so that closer ones may be in the wrong order; it follows
+// the sums of magnitudes that the logits are sums of, which may be any multiple of the
+// logits themselves. 0: all logits are 0 or not finite, nothing is to be settled.
+__device__ __forceinline__ void choose(const float (&v)[RT_SLOTS], int E, int k, bool renorm, float tie, const bf16 *x,
                                        const bf16 *router, int lane, int &id, float &weight)
 {
     uint32_t key[RT_SLOTS];
-    float big = 0.0f;
 #pragma unroll
-    for (int j = 0; j < RT_SLOTS; ++j) {
-        const bool there = expert_of(lane, j) < E;
-        key[j] = there ? sort_key(v[j]) : 0u;
-        if (there && fabsf(v[j]) < INFINITY) big = fmaxf(big, fabsf(v[j]));
-    }
-    big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
+    for (int j = 0; j < RT_SLOTS; ++j) key[j] = expert_of(lane, j) < E ? sort_key(v[j]) : 0u;
     // the largest k, and behind them those that are close to the last of them; a lane
     // offers the best that it has left, lane i keeps the i-th
-    const float tie = 0x1p-13f * big;
     float best = 0.0f, prev = 0.0f, kth = -INFINITY;
     bool close = false;
     id = 0;
@@ -221,9 +212,9 @@ __device__ __forceinline__ void choose(const float (&v)[RT_SLOTS], int E, int k,
             id = (int)at;
         }
     }
-    if (close && big > 0.0f) {
+    if (close && tie > 0.0f) {
         if (n == 32 && E > 32) {                       // more neighbours than lanes
-            choose_settled(v, E, k, renorm, x, router, lane, id, weight);
+            choose_settled(v, E, k, renorm, tie, x, router, lane, id, weight);
             return;
         }
         // in 48 bits those that are close to a neighbour, then every one's place among the n

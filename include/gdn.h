@@ -622,8 +622,10 @@ typedef struct {
  * number), and their weights softmax(l) (with norm_topk over the chosen ones).
  *   x        [M][2048] bf16 with its row stride
  *   ids      [M][top_k] int32          weights [M][top_k] fp32
- * The order is that of the exact logits: neighbours closer than 2^-13 of the
- * token's largest logit are settled in 48 bits. Only router, num_experts, top_k and
+ * The order is that of the exact logits, however large the terms that cancel in them (as long as
+ * the terms stay within fp32's normal numbers): logits closer than a bound on their error, which
+ * follows the sum of the terms' magnitudes, are settled in 48 bits of that sum. The weights come
+ * from fp32 logits, off by at most 2^-18 |x| |router[e]|. Only router, num_experts, top_k and
  * norm_topk of the parameters are used. 0 <= M <= 2^24. Errors:
  * GDN_ERR_INVALID_ARG, GDN_ERR_CUDA. A bounded device wait that gives up is reported
  * afterwards by gdn_device_error; tokens that it left without a choice have ids of -1 and
