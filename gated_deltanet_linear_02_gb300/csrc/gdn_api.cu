@@ -64,7 +64,7 @@ cudaError_t launch_linear(const void *, long long, const void *, const float *, 
 void *linear_error_word();
 cudaError_t launch_route_only(const gdn_moe_params *, const void *, long long, int, int32_t *, float *, cudaStream_t);
 void *route_error_word();
-size_t moe_workspace_bytes(const gdn_moe_params *, int);
+size_t moe_workspace_bytes(const gdn_moe_params *, int), moe_call_bytes(const gdn_moe_params *, int);
 cudaError_t launch_moe(const gdn_moe_params *, const void *, long long, const void *, void *, int, const int32_t *,
                        const float *, void *, gdn_dtype, bool, cudaStream_t);
 void *moe_error_word();
@@ -747,7 +747,7 @@ static gdn_status moe_call(const gdn_moe_params *p, const void *x, long long x_r
         return fail(GDN_ERR_INVALID_ARG, "a tensor is NULL or not 16-byte aligned, or the row stride is below 2048 or not a multiple of 8");
     const size_t no = (size_t)M * GDN_HIDDEN * elem_size(out_dt), nx = rx.bytes(M), np = (size_t)M * p->top_k * 4;
     const size_t nf = (size_t)p->ffn_dim * GDN_HIDDEN * 2, ne = (size_t)p->num_experts * nf;
-    const size_t need = moe_workspace_bytes(p, M);
+    const size_t need = moe_call_bytes(p, M);
     struct { const void *q; size_t n; } in[] = {
         {x, nx}, {p->gate, ne}, {p->up, ne}, {p->down, ne}, {p->sh_gate, p->sh_gate ? nf : 0}, {p->sh_up, p->sh_up ? nf : 0},
         {p->sh_down, p->sh_down ? nf : 0}, {p->sh_router, p->sh_router ? GDN_HIDDEN * 2 : 0},

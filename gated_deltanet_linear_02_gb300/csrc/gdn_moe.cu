@@ -554,7 +554,17 @@ static bool moe_setup()
     return true;
 }
 
-size_t moe_workspace_bytes(const gdn_moe_params *p, int M) { return moe_workspace(p, M, nullptr).bytes; }
+// What a call of M tokens takes, and what every call of up to M does: rows shrink where the
+// form changes, so the most is taken by M or by the last token number of a form below it.
+size_t moe_call_bytes(const gdn_moe_params *p, int M) { return moe_workspace(p, M, nullptr).bytes; }
+size_t moe_workspace_bytes(const gdn_moe_params *p, int M)
+{
+    const int last[] = {MOE_FEW_TOKENS, MOE_SMALL * p->num_experts / p->top_k};
+    size_t most = moe_call_bytes(p, M);
+    for (const int m : last)
+        if (m < M && moe_call_bytes(p, m) > most) most = moe_call_bytes(p, m);
+    return most;
+}
 
 cudaError_t launch_moe(const gdn_moe_params *p, const void *x, long long x_row, const void *residual, void *out, int M,
                        const int32_t *ids, const float *weights, void *workspace, gdn_dtype out_dt, bool lose_route, cudaStream_t s)

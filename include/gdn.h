@@ -657,8 +657,9 @@ gdn_status gdn_moe(const gdn_moe_params *p, const void *x, long long x_row_strid
                    int M, const int32_t *ids, const float *weights, void *workspace, size_t workspace_bytes,
                    gdn_dtype out_dt, void *stream);
 
-/* Bytes of workspace gdn_moe needs; 0 if the sizes are out of range. It stops
- * growing at 8,192 tokens. Pure host arithmetic. */
+/* Bytes of workspace that gdn_moe needs for any number of tokens up to M, so one made
+ * for the largest call serves the smaller ones; 0 if the sizes are out of range. It never shrinks
+ * as M grows, and stops growing at 8,192 tokens. Pure host arithmetic. */
 size_t gdn_moe_workspace_size(const gdn_moe_params *p, int M);
 
 /* Bytes of workspace gdn_prefill needs for these sizes (0 if the arguments are
