@@ -108,6 +108,13 @@ template <int N> __device__ __forceinline__ void cp_async_wait()
 }
 __device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
+// The largest exponent (biased, plus 1) of the warp's finite values: with one more in the exponent
+// the others wrap round to 0.
+__device__ __forceinline__ int top_exponent(float v)
+{
+    return (int)(__reduce_max_sync(0xffffffffu, (__float_as_uint(v) + 0x00800000u) & 0x7fffffffu) >> 23);
+}
+
 template <int NT>
 __global__ void __launch_bounds__(ExpertSmem<NT>::THREADS, 1)
     moe_experts_kernel(const __grid_constant__ ExpertMaps maps, const bf16 *x, long long x_row, int M, int E, int F, int k, int shared, MoeWs ws)
@@ -384,16 +391,15 @@ __global__ void __launch_bounds__(ExpertSmem<NT>::THREADS, 1)
                     for (int i = 0; i < 16; ++i)
                         if (c + i < un.n) p[(size_t)i * F] = from_f<bf16>(silu_fast(a[i]) * b[i]);
                 } else if (NT > 32) {
-                    // y in 16 bits: fp16 scaled by the largest exponent of the token's 32 rows in
-                    // this warp, off by at most 2^-12 of that largest value. (bf16 would add as
-                    // much error as the output's own rounding; fp32 costs 2 x 150 MB at 4,096 tokens.)
+                    // y in 16 bits: fp16 scaled by the largest exponent among the token's 32 rows in this
+                    // warp that are finite (the others stay what they are under any scale), off by at most
+                    // 2^-11 of that largest value. (bf16 would add as much error as the output's own
+                    // rounding; fp32 costs 2 x 150 MB at 4,096 tokens.)
                     unsigned char keep = 0;            // lane i: scale of column i, lane 16 + i: of its other block
                     __half *p = ws.y16 + (size_t)(un.row0 + c) * LD + un.rows_at * 256 + row;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        const int ea = (int)(__reduce_max_sync(0xffffffffu, __float_as_uint(a[i]) & 0x7fffffffu) >> 23);
-                        const int eb = (int)(__reduce_max_sync(0xffffffffu, __float_as_uint(b[i]) & 0x7fffffffu) >> 23);
-                        const int sa = ea == 255 ? 141 : max(ea, 20), sb = eb == 255 ? 141 : max(eb, 20);
+                        const int sa = max(top_exponent(a[i]), 21) - 1, sb = max(top_exponent(b[i]), 21) - 1;
                         if (lane == i) keep = (unsigned char)sa;
                         if (lane == 16 + i) keep = (unsigned char)sb;
                         if (c + i < un.n) {
