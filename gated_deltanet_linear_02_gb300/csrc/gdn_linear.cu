@@ -66,15 +66,20 @@ __device__ __forceinline__ float gelu(float v)
     return v * (v < 0.0f ? h : 1.0f - h);
 }
 
-// exp and the division by special functions: a few 2^-23 of the result. Beyond fp32's
-// exponents the limits come out (silu and sigmoid of -100: 0).
-template <int ACT>
+// For bf16 outputs exp and the division by special functions, whose error grows with |v|, by
+// 2^-23 (4 + 2 |v|) of the value at most, far below the output's rounding; 0 where the denominator
+// passes 2^126 (silu and sigmoid below -87.3). For fp32 outputs within 2^-21 down to fp32's last
+// numbers, by exp(-|v|), which does not overflow. 4,001 x 9,216 x 2,048 with SiLU to
+// fp32: 128 us (with the functions of bf16 127), 96 rows 13.1 (13.0).
+template <typename TO, int ACT>
 __device__ __forceinline__ float apply_act(float v)
 {
-    if (ACT == GDN_ACT_SILU) return __fdividef(v, 1.0f + __expf(-v));
     if (ACT == GDN_ACT_GELU) return gelu(v);
-    if (ACT == GDN_ACT_SIGMOID) return __fdividef(1.0f, 1.0f + __expf(-v));
-    return v;
+    if (ACT == GDN_ACT_NONE) return v;
+    const float top = ACT == GDN_ACT_SILU ? v : 1.0f;
+    if (sizeof(TO) == 2) return __fdividef(top, 1.0f + __expf(-v));
+    const float e = expf(-fabsf(v));
+    return top * __fdividef(v < 0.0f ? e : 1.0f, 1.0f + e);         // the denominator is at most 2
 }
 
 // Brings the tensor maps near before the first copies need them.
@@ -102,7 +107,7 @@ __device__ __forceinline__ void finish(const LinearOut &o, int m, int n, int N, 
         for (int i = 0; i < NC; ++i) v[i] += b[i];
     if (ACT != GDN_ACT_NONE)
 #pragma unroll
-        for (int i = 0; i < NC; ++i) v[i] = apply_act<ACT>(v[i]);
+        for (int i = 0; i < NC; ++i) v[i] = apply_act<TO, ACT>(v[i]);
     if (o.residual)
 #pragma unroll
         for (int i = 0; i < NC; ++i) v[i] += r[i];

@@ -576,8 +576,9 @@ gdn_status gdn_add_norm(const gdn_norm_params *p, const void *x, long long x_row
                         long long x_out_row_stride, void *h, long long h_row_stride, int M, gdn_dtype stream_dt,
                         gdn_dtype act, void *stream);
 
-/* GELU is the exact one, v / 2 * erfc(-v / sqrt(2)), off by at most (v^2 + 6) 2^-23 of its value
- * before the output's rounding (0 below -13.2, where it leaves fp32's normal numbers). */
+/* What each adds to the output's rounding, relative to its value: silu v / (1 + exp(-v)) and sigmoid
+ * 2^-21 for fp32 outputs, 2^-23 (4 + 2 |v|) for bf16 ones (0 below -87.3); gelu, the exact one,
+ * v / 2 * erfc(-v / sqrt(2)), 2^-23 (v^2 + 6) (0 below -13.2, where it leaves fp32's normal numbers). */
 typedef enum { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1, GDN_ACT_GELU = 2, GDN_ACT_SIGMOID = 3 } gdn_activation;
 
 /*
