@@ -205,7 +205,19 @@ struct Rows {
                (row >= width || (once && row == 0));
     }
 };
-bool overlap(const Rows &a, const Rows &b, int M) { return a.p && b.p && overlap(a.p, a.bytes(M), b.p, b.bytes(M)); }
+// Whether M rows of each share an element. Rows the same distance apart (blocks of columns of one
+// buffer) do not where each block ends before the other's next row begins; others
+// count as overlapping where their address ranges do.
+bool overlap(const Rows &a, const Rows &b, int M)
+{
+    if (!a.p || !b.p || !overlap(a.p, a.bytes(M), b.p, b.bytes(M))) return false;
+    const size_t step = (size_t)a.row * elem_size(a.dt), wa = (size_t)a.width * elem_size(a.dt),
+                 wb = (size_t)b.width * elem_size(b.dt);
+    if (M == 1 || step == 0 || step != (size_t)b.row * elem_size(b.dt)) return true;
+    const uintptr_t pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
+    const size_t at = pb >= pa ? (pb - pa) % step : (step - (pa - pb) % step) % step;    // of b's rows behind a's
+    return at < wa || at + wb > step;
+}
 bool same_rows(const Rows &a, const Rows &b) { return a.p == b.p && a.row == b.row && a.dt == b.dt; }
 
 gdn_status check_moe_route(const gdn_moe_params *p)

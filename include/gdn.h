@@ -541,7 +541,9 @@ size_t gdn_attn_paged_workspace_size(const gdn_paged_batch *batch, const gdn_kv_
 /* ---------------------------------------------------------------------------
  * Around the mixers: the residual stream and its norms, the dense products that
  * have no entry point of their own, and the mixture-of-experts feed-forward.
- * The residual stream is GDN_HIDDEN (2048) wide.
+ * The residual stream is GDN_HIDDEN (2048) wide. Blocks of columns of one buffer may be inputs
+ * and outputs of one call: rows that have the same stride and share no element do not overlap. With
+ * different strides address ranges count.
  * ------------------------------------------------------------------------- */
 
 /* Parameters of gdn_add_norm: device fp32 weights, applied as w. */
