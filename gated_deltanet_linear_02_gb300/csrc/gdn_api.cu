@@ -686,6 +686,10 @@ gdn_status gdn_add_norm(const gdn_norm_params *p, const void *x, long long x_row
     if ((overlap(ro, rx, M) && !same_rows(ro, rx)) || overlap(ro, rd, M) || overlap(ro, rg, M) || overlap(ro, rh, M) ||
         (overlap(rh, rd, M) && !same_rows(rh, rd)) || overlap(rh, rx, M) || overlap(rh, rg, M))
         return fail(GDN_ERR_INVALID_ARG, "an output overlaps another tensor");
+    const float *const norm_weights[] = {p->norm_w, p->post_w};
+    for (const float *w : norm_weights)
+        if (w && ((x_out && overlap(x_out, ro.bytes(M), w, GDN_HIDDEN * 4)) || (h && overlap(h, rh.bytes(M), w, GDN_HIDDEN * 4))))
+            return fail(GDN_ERR_INVALID_ARG, "an output overlaps a norm weight");
     cudaError_t e = launch_add_norm(p, x, x_row_stride, delta, delta_row_stride, gate, gate_row_stride, x_out,
                                     x_out_row_stride, h, h_row_stride, M, stream_dt, act, (cudaStream_t)stream);
     return e == cudaSuccess ? GDN_OK : cuda_fail(e, "gdn_add_norm");
