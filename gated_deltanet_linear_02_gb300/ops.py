@@ -590,7 +590,7 @@ def _rows(t, name: str, M: int, width: int, device, dtype=None):
     if t.shape == (M, width) and t.device == device and (dtype is None or t.dtype is dtype):
         row, last = t.stride()
         if last == 1:
-            return t.data_ptr(), row if M > 1 or row == 0 else width
+            return t.data_ptr(), row if M > 1 else width   # a single row has no next one
     _refuse(t, name, (M, width), device, dtype)
     raise ValueError(f"{name} must be dense in its last dimension")
 

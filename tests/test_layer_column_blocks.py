@@ -63,3 +63,19 @@ def test_blocks_that_share_columns_are_refused(ops):
     # other distances from row to row: by the address ranges
     abi.refused(ops, abi.linear(ops, xr=512, y=at(0) + 2 * 256, yr=1024), "overlaps")
     abi.refused(ops, abi.linear(ops, xr=512, y=at(0) + 2 * 256, yr=512, dt=ops.GDN_F32), "overlaps")
+
+
+@gpu
+def test_one_row_of_any_stride(ops):
+    """A single row has no next one: its stride does not matter."""
+    g = tl.gen(4)
+    v, w = tl.rnd(g, D), tl.rnd(g, 64, D, scale=0.02)
+    p = ops.make_norm_params(torch.ones(D, device="cuda"))
+    want, got = (torch.empty(1, D, dtype=BF, device="cuda") for _ in range(2))
+    ops.add_norm(p, v[None], None, None, want)
+    ops.add_norm(p, v.expand(4, D)[:1], None, None, got)
+    assert torch.equal(got, want)
+    y, z = (torch.empty(1, 64, dtype=BF, device="cuda") for _ in range(2))
+    ops.linear(v[None], w, y)
+    ops.linear(v.expand(4, D)[:1], w, z)
+    assert torch.equal(y, z)
