@@ -650,8 +650,13 @@ gdn_status gdn_moe_route(const gdn_moe_params *p, const void *x, long long x_row
  *   workspace device scratch, 256-byte aligned, of gdn_moe_workspace_size(p, M)
  *             bytes; contents need no initialisation. Calls that share one must be
  *             ordered on a stream
- * fp32 sums and epilogues; rounded to bf16 once, by at most half a step, are the
- * hidden activations silu(.) * (.), which enter a bf16 product. A row of x affects
+ * fp32 sums and epilogues, with two roundings between, whatever out_dt is:
+ *  - above 4 tokens the hidden activations silu(.) * (.) are rounded to bf16, by at most half a
+ *    step (silu adds what gdn_linear's does for bf16); they enter a bf16 product;
+ *  - where M * top_k > 16 * num_experts, the outputs of the pairs (token, expert), the shared
+ *    expert among them, are held in fp16 scaled by blocks of 32 dims: off by at most 2^-11 of the
+ *    largest finite value of their block.
+ * A row of x affects
  * its own output alone, whatever it holds. 0 <= M <= 2^24. Errors:
  * GDN_ERR_INVALID_ARG, GDN_ERR_WORKSPACE, GDN_ERR_CUDA (also when the driver's
  * tensor-map encoder is unavailable). A bounded device wait that gives up is
