@@ -766,7 +766,7 @@ static gdn_status moe_call(const gdn_moe_params *p, const void *x, long long x_r
     const size_t need = moe_call_bytes(p, M);
     struct { const void *q; size_t n; } in[] = {
         {x, nx}, {p->gate, ne}, {p->up, ne}, {p->down, ne}, {p->sh_gate, p->sh_gate ? nf : 0}, {p->sh_up, p->sh_up ? nf : 0},
-        {p->sh_down, p->sh_down ? nf : 0}, {p->sh_router, p->sh_router ? GDN_HIDDEN * 2 : 0},
+        {p->sh_down, p->sh_down ? nf : 0}, {p->sh_router, p->sh_router ? (size_t)GDN_HIDDEN * 2 : 0},
         {p->router, p->router ? (size_t)p->num_experts * GDN_HIDDEN * 2 : 0}, {ids, ids ? np : 0}, {weights, ids ? np : 0},
         {residual, residual && residual != out ? no : 0}};
     for (const auto &t : in)

@@ -60,9 +60,9 @@ __device__ __forceinline__ void store4(bf16 *p, float4 v)
 
 __device__ __forceinline__ float silu_f(float x) { return x / (1.0f + expf(-x)); }
 
-// SiLU with the fast exponential and division intrinsics (a few ulp). Used only
-// where the result becomes a tf32 tensor-core operand, whose rounding is about
-// 1e3 times coarser.
+// SiLU with the fast exponential and division intrinsics (2^-23 (4 + 2 |x|) of its value; 0
+// below -87.3). Used only where the result becomes a bf16 tensor-core operand, whose
+// rounding is coarser by far.
 __device__ __forceinline__ float silu_fast(float x) { return __fdividef(x, 1.0f + __expf(-x)); }
 
 // softplus with a linear tail above 20, the same reading the oracle takes.

@@ -17,7 +17,7 @@
 //    that were handed out before it, so it never waits for a CTA that is not running.
 //    Both kinds are the same pipeline: two A tiles and one B tile per stage of
 //    64 along K, two accumulators, double-buffered against the epilogue. Token rows
-//    come by TMA gathers of four rows.
+//    come by TMA gathers of four rows (tiles of 32 tokens) or by asynchronous copies (of 128).
 //    256 tokens: 227 us, HBM at 6.9 TB/s. 4,096 tokens: 326 us, 1.85 GB of HBM traffic and
 //    12.4 TB/s from L2 into the SMs.
 //  - moe_combine: residual, the pairs' outputs in slot order, the shared expert with its gate.

@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(32 * FW_LOGIT_WARPS)
     }
 }
 
-// Two CTAs per SM: one computes and synchronises while the other's rows are in flight.
+// One CTA per SM, with as many warps as their slots leave room for.
 constexpr int FW_MAX_WARPS = 16, FW_MIN_WARPS = 8;
 constexpr uint32_t FW_SLOT = 8192;        // a row of gate and one of up; two slots a warp
 constexpr int FW_ROW_SLOTS = 12;          // down rows on their way, at most, in the same memory
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(32 * (FW_MAX_WARPS + 1), 1) moe_few_kernel(con
     //      add their sums up in the end (always in the same order).
     const int d_lo = (int)((long long)LD * sm.dims / grid), d_hi = (int)((long long)LD * (sm.dims + 1) / grid);
     const int fit = (int)(2 * FW_SLOT / (2 * (uint32_t)F)), dims = min(min(fit, FW_DIMS * FW_GROUP), max(1, d_hi - d_lo));
-    const int blocks = (d_hi - d_lo + dims - 1) / dims, steps = blocks * distinct;
+    const int blocks = (d_hi - d_lo + dims - 1) / dims;
     const uint32_t slot_bytes = (uint32_t)dims * F * 2;
     // a multiple of the groups: a slot is always the same group's (a barrier tells a phase
     // only from the one before it)
@@ -445,9 +445,6 @@ __global__ void __launch_bounds__(32 * (FW_MAX_WARPS + 1), 1) moe_few_kernel(con
             asm volatile("bar.sync 2, %0;" ::"r"(32 * warps) : "memory");
             step += distinct;
         }
-        if (distinct == 0)                             // nobody's token
-            for (int i = blockIdx.x * 32 * warps + tid; i < M * LD; i += grid * 32 * warps)
-                static_cast<TO *>(a.out)[i] = a.residual ? static_cast<const TO *>(a.residual)[i] : from_f<TO>(0.0f);
         if (aborted) {                                 // copies in flight land before the CTA exits
             while (reads < fills) {
                 const uint32_t n = reads++;
