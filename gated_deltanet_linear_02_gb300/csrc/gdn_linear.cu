@@ -15,9 +15,11 @@
 //  - linear_kernel, for few rows: tiles of 128 rows x 128 columns, each tile's K range
 //    split over the CTAs of a cluster, whose partial tiles meet in distributed
 //    shared memory (always in the same order).
-// 4,001 x 9,216 x 2,048 with bias and SiLU: 93 us, 1.62 PFLOP/s, bound by what L2 brings to
-// the SMs (12.7 TB/s); 8,192^3: 1.73 PFLOP/s. One row, 2,048 -> 9,216: 9.4 us (4 TB/s), 4,096 -> 2,048:
-// 6.1 us; there the start, the issue of the products and the cluster's exchange bind.
+// 4,001 x 9,216 x 2,048 with bias and SiLU: 104 us, 1.45 PFLOP/s; 93 to 96 us in short runs, before
+// power caps the clock, where it is bound by what L2 brings to the SMs (12.7 TB/s). 8,192^3, short
+// runs: 1.73 PFLOP/s. One row, 2,048 -> 9,216: 9.8 us (3.8 TB/s), 4,096 -> 2,048: 6.3 us; there the start,
+// the issue of the products and the cluster's exchange bind. Between 129 and some 3,000 rows tiles are few
+// and whole waves of them are half empty: 768 x 2,048 x 4,096 19.8 us.
 #include <mutex>
 
 #include "gdn_layer.cuh"
@@ -618,6 +620,10 @@ static cudaError_t launch_split(const LinearCall &c, const LinearDevice &dev, in
     return cudaLaunchKernelEx(&cfg, linear_kernel<TO, ACT>, mx, mw, c.out, c.M, c.N, c.K, splits, a_rows, stages);
 }
 
+// The form. Tiles of 256 columns once they are more than half of what the pairs hold, else of 128, which
+// then fit one wave: 768 x 2,048 x 4,096 24.3 us with 256 and 19.8 with 128, 1,536 x 2,048 x 4,096 25.1 and
+// 35.2. Split K by lone CTAs up to half of that wave: 256 x 2,048 x 4,096 12.0 us; from there
+// to the whole wave it is within 10% either way (384 rows 14.5 in both, 1,024 18.2 here against 20.0).
 template <typename TO, int ACT>
 static cudaError_t launch_act(const LinearCall &c, const LinearDevice &dev, int n_sm)
 {

@@ -11,9 +11,8 @@
 //    a time, while the others wait for the whole of h, whose values say themselves
 //    that they are there. A CTA that has done its share of h takes another one if there is
 //    any left, so that it never waits for work of a CTA that is not running.
-// One token of 8 of 256 experts and a shared one: 18.7 us with the weights partly in L2, 20.7
-// without (8.4 at the copy's rate): 4 us logits, 4 choice and lists, 8 h, 1.5 until h is there, 4 outputs. Four
-// tokens 51 us of 29. What it took: atomics on one address return every
+// One token of 8 of 256 experts and a shared one: 20.9 us (8.5 at the copy's rate): 4 us logits, 4 choice
+// and lists, 8 h, 1.5 until h is there, 4 outputs. Four tokens 52.8 us of 29. What it took: atomics on one address return every
 // 4 ns or so, so a counter that every warp asks for each row pair cost more than the sweep;
 // rows in registers instead of slots made the warps load and compute in step (3.9 TB/s);
 // one producer for all row pairs fell behind (0.4 us of serial work per 8 KB).

@@ -16,9 +16,9 @@
 // and up to 8 roundings of 2^-24 join them: 1.25 2^-19 of sum |x_i r_i| in all, twice that for a
 // difference. That sum is at most |x| |r| in each part of K; warps that the products leave
 // idle take the norms from the stages as they pass (of r the largest).
-// Ties go to the lowest index. NaN ranks below everything. 256 tokens 16.5 us, 4,096
-// 21.6 us, a few 6.5: the products are done after 1.7 us, the partial logits of a CTA's
-// tokens take 5 (131 KB from the other SMs), the choice 2, near ties 4.
+// Ties go to the lowest index. NaN ranks below everything. 256 tokens 17.9 us, 4,096
+// 22.9 us, 4 tokens 8.2: the products are done after 1.7 us, the partial logits of a CTA's
+// tokens take 5 (131 KB from the other SMs), the choice 2, near ties 4, the bound's norms 1.
 //
 // Where a wait of a cluster gave up, its tokens are marked as nobody's (id -1), so that the kernels
 // behind find no index that was not written. `lose` makes that happen, for the library's self-test:
