@@ -41,11 +41,12 @@ struct LinearOut {
 };
 
 // v / 2 * erfc(-v / sqrt 2) for any v, relative to its value (1 + erf cancels for negative v, and is 0
-// from -5.5 on). With t = |v| / sqrt 2: erfc(t) = exp(-t^2) u q(u), u = 1 / (1 + 0.55 t), as u
-// brings t in [0, inf) to (0, 1]; q is a polynomial of degree 9, least squares on 1 / u erfcx(t)
-// over |v| <= 14 with weights that even the relative error out (below 2^-27). exp(-v^2 / 2) by
-// the special function (its argument is off by v^2 2^-24), u with a Newton step behind it. 4,001 x
-// 9,216 x 2,048: 99 us; with erfcf 133, with 1 + erff 102.
+// from -5.5 on). With t = |v| / sqrt 2, in the form of Hastings' approximations (Abramowitz and
+// Stegun 7.1.26): erfc(t) = exp(-t^2) u q(u), u = 1 / (1 + 0.55 t), which brings t in [0, inf) to (0, 1].
+// q is a polynomial of degree 9 fitted here, least squares on exp(t^2) erfc(t) / u over |v| <= 14 with
+// weights that even the relative error out (below 2^-27). exp(-v^2 / 2) by the special function (its
+// argument is off by v^2 2^-24), u with a Newton step behind it. 4,001 x 9,216 x 2,048: 99 us;
+// with erfcf 133, with 1 + erff 102.
 __device__ __forceinline__ float gelu(float v)
 {
     const float a = fminf(fabsf(v), 14.0f);            // NaN comes back with the product below

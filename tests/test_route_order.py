@@ -96,3 +96,18 @@ def test_rows_that_decide_nothing(ops, M):
     rid = torch.sort(logits, dim=-1, descending=True, stable=True)[1][:, :K]
     assert torch.equal(ids[rest].long(), rid)
     assert ids[3].tolist() == list(range(K)) and w[[2, 3]].isnan().all()
+
+
+@pytest.mark.parametrize("E", [24, 256])
+@pytest.mark.parametrize("M", [3, 200])
+def test_equal_sums_of_different_terms(ops, E, M):
+    """Router rows that are permutations of one another, tokens whose elements are all the same:
+    every logit is the same number, and the lowest indices are taken."""
+    g = tl.gen(E)
+    row = tl.rnd(g, D, scale=0.03)
+    router = torch.stack([row[torch.randperm(D, generator=g, device="cuda")] for _ in range(E)])
+    x = tl.rnd(g, M, 1).expand(M, D).contiguous()
+    ids, w = torch.empty(M, K, dtype=torch.int32, device="cuda"), torch.empty(M, K, device="cuda")
+    ops.moe_route(ops.make_moe_params(router, top_k=K), x, ids, w)
+    assert ops.device_error() == ops.GDN_OK
+    assert (ids == torch.arange(K, device="cuda")).all() and ((w - 1 / K).abs() <= 2.0 ** -24).all()
